@@ -16,6 +16,9 @@ LIB_PATH = os.environ.get("TOKTIER_LIBRARY") or os.path.join(HERE, "libtoktier.s
 
 TOKTIER_GPT2, TOKTIER_CL100K, TOKTIER_O200K, TOKTIER_DEEPSEEK = 1, 2, 3, 4
 TOKTIER_IGNORE_MERGES = 1
+TOKTIER_F32, TOKTIER_F16, TOKTIER_BF16 = 1, 2, 3
+TOKTIER_MAX_VOCAB = 1 << 21
+TYPES = {torch.float32: TOKTIER_F32, torch.float16: TOKTIER_F16, torch.bfloat16: TOKTIER_BF16}
 FAMILIES = {"gpt2": TOKTIER_GPT2, "cl100k": TOKTIER_CL100K, "o200k": TOKTIER_O200K,
             "deepseek": TOKTIER_DEEPSEEK}
 STATUS = {0: "TOKTIER_OK", 1: "TOKTIER_E_INVALID_ARG", 2: "TOKTIER_E_BAD_FAMILY", 3: "TOKTIER_E_BAD_MERGES",
@@ -29,7 +32,10 @@ EXPORTS = ("toktier_load_vocab", "toktier_load_vocab_ex", "toktier_free_vocab", 
            "toktier_pretokenize_batch", "toktier_repair_scratch_bytes", "toktier_repair_append",
            "toktier_plan_create", "toktier_plan_create_bucket", "toktier_plan_launch", "toktier_plan_free",
            "toktier_last_status", "toktier_status_string", "toktier_last_hip_error",
-           "toktier_unicode_table_sha256")
+           "toktier_unicode_table_sha256",
+           "toktier_embed", "toktier_embed_backward_workspace_bytes", "toktier_embed_backward",
+           "toktier_cross_entropy_workspace_bytes", "toktier_cross_entropy", "toktier_cross_entropy_backward",
+           "toktier_sample_workspace_bytes", "toktier_sample")
 
 # kernel launches of one encode call, in stream order (TOKTIER_K_* in toktier.h)
 KERNELS = ("summary", "pieces", "tiles", "giant_seams", "bpe", "bpe_giant", "emit")
@@ -86,6 +92,15 @@ def lib():
     L.toktier_repair_scratch_bytes.argtypes = [vp, u64, u64p]
     L.toktier_repair_append.argtypes = [vp, vp, u64, u64, vp, vp, u64, vp, vp, u64, u64p, vp, u64, vp,
                                         ctypes.POINTER(RepairInfo)]
+    f32 = ctypes.c_float
+    L.toktier_embed.argtypes = [vp, i32, u32, u32, u64, vp, u64, f32, vp, i32, u64, vp]
+    L.toktier_embed_backward_workspace_bytes.argtypes = [u64, u32, u32, u64p]
+    L.toktier_embed_backward.argtypes = [vp, i32, u64, vp, u64, f32, vp, i32, u32, u32, u64, i32, vp, u64, vp]
+    L.toktier_cross_entropy_workspace_bytes.argtypes = [u32, u32, u64p]
+    L.toktier_cross_entropy.argtypes = [vp, i32, u32, u32, u64, vp, vp, vp, vp, f32, vp, u64, vp, u64, vp]
+    L.toktier_cross_entropy_backward.argtypes = [vp, i32, u32, u32, u64, vp, vp, vp, f32, vp, u64, vp]
+    L.toktier_sample_workspace_bytes.argtypes = [u32, u32, u64p]
+    L.toktier_sample.argtypes = [vp, i32, u32, u32, u64, vp, u64, vp, vp, vp, vp, vp, vp, vp, vp, u64, vp]
     for f in ("toktier_status_string",):
         getattr(L, f).argtypes = [i32]
         getattr(L, f).restype = ctypes.c_char_p
@@ -432,6 +447,157 @@ def toktier_last_status(workspace, stream=None):
 
 def toktier_unicode_table_sha256():
     return lib().toktier_unicode_table_sha256().decode()
+
+
+# ---------------------------------------------------------------------------------------------
+# token operators (embedding lookup and gradient, next-token cross entropy, sampling)
+#
+# Tensors live on the current device; matrices are 2-D with unit stride inside a row (views with a row
+# stride are fine), IDs are int32 (read as uint32: -1 names no row).  A tensor of another kind is refused
+# with TOKTIER_E_INVALID_ARG here, since the library only sees its address.
+
+def _refuse(what, why):
+    raise ToktierError(1, f"{what}: {why}")
+
+
+def _on_device(t, what, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index != torch.cuda.current_device():
+        _refuse(what, f"{name} is not a tensor on the current device")
+
+
+def _matrix(t, what, name):
+    """(pointer, type, rows, columns, row stride) of a matrix argument."""
+    _on_device(t, what, name)
+    if t.dim() != 2 or t.dtype not in TYPES or (t.size(1) > 1 and t.stride(1) != 1):
+        _refuse(what, f"{name} is not a 2-D float32, float16 or bfloat16 tensor with unit stride in a row")
+    rows, cols = t.shape
+    return _ptr(t), TYPES[t.dtype], rows, cols, t.stride(0) if rows > 1 else cols
+
+
+def _vector(t, what, name, n, dtypes, optional=False):
+    if t is None and optional:
+        return None
+    _on_device(t, what, name)
+    if t.dim() != 1 or t.dtype not in dtypes or t.numel() != n or not t.is_contiguous():
+        _refuse(what, f"{name} is not a contiguous tensor of {n} x {dtypes[0]}")
+    return _ptr(t)
+
+
+def _scratch(t, what):
+    _on_device(t, what, "workspace")
+    if t.dtype != torch.uint8 or not t.is_contiguous():
+        _refuse(what, "workspace is not a contiguous uint8 tensor")
+    return _ptr(t), t.numel()
+
+
+_IDS, _FLOAT = (torch.int32, torch.uint32), (torch.float32,)
+
+
+def toktier_embed(table, ids, out, scale=1.0, stream=None):
+    """out[t] = scale * table[ids[t]], zeros where ids[t] is no row of the table.  table: [n_vocab, dim],
+    ids: int32 [n], out: [n, dim]; the types of table and out may differ."""
+    what = "toktier_embed"
+    tp, tt_, n_vocab, dim, ts = _matrix(table, what, "table")
+    op, ot, n, odim, os_ = _matrix(out, what, "out")
+    if odim != dim:
+        _refuse(what, f"out has {odim} columns, table {dim}")
+    _check(lib().toktier_embed(tp, tt_, n_vocab, dim, ts, _vector(ids, what, "ids", n, _IDS), n, float(scale), op, ot,
+                               os_, _stream(stream)), what)
+
+
+def toktier_embed_backward_workspace_bytes(n_tokens, n_vocab, dim):
+    out = ctypes.c_uint64()
+    _check(lib().toktier_embed_backward_workspace_bytes(int(n_tokens), int(n_vocab), int(dim), ctypes.byref(out)),
+           "toktier_embed_backward_workspace_bytes")
+    return out.value
+
+
+def toktier_embed_backward(grad_out, ids, grad_table, workspace, scale=1.0, accumulate=False, stream=None):
+    """grad_table[r] = scale * (sum of grad_out[t] over ids[t] = r), every row written, or added to what
+    grad_table holds when accumulate is True.  grad_out: [n, dim], ids: int32 [n], grad_table: [n_vocab, dim];
+    workspace: uint8 of toktier_embed_backward_workspace_bytes(n, n_vocab, dim)."""
+    what = "toktier_embed_backward"
+    gp, gt, n, dim, gs = _matrix(grad_out, what, "grad_out")
+    tp, tt_, n_vocab, tdim, ts = _matrix(grad_table, what, "grad_table")
+    if tdim != dim:
+        _refuse(what, f"grad_table has {tdim} columns, grad_out {dim}")
+    wp, wn = _scratch(workspace, what)
+    _check(lib().toktier_embed_backward(gp, gt, gs, _vector(ids, what, "ids", n, _IDS), n, float(scale), tp, tt_,
+                                        n_vocab, dim, ts, int(bool(accumulate)), wp, wn, _stream(stream)), what)
+
+
+def toktier_cross_entropy_workspace_bytes(n_rows, n_vocab):
+    out = ctypes.c_uint64()
+    _check(lib().toktier_cross_entropy_workspace_bytes(int(n_rows), int(n_vocab), ctypes.byref(out)),
+           "toktier_cross_entropy_workspace_bytes")
+    return out.value
+
+
+def _grad_logits(grad_logits, logits, what):
+    gp, gt, rows, cols, gs = _matrix(grad_logits, what, "grad_logits")
+    if grad_logits.shape != logits.shape or grad_logits.dtype != logits.dtype:
+        _refuse(what, "grad_logits differs from logits in shape or type")
+    return gp, gs
+
+
+def toktier_cross_entropy(logits, targets, loss, lse, workspace, grad_logits=None, grad_loss=None, grad_scale=1.0,
+                          stream=None):
+    """loss[i] = lse[i] - logits[i, targets[i]] (0 where targets[i] is no ID), lse[i] = logsumexp(logits[i]) and,
+    where grad_logits is given (logits itself is allowed), its gradient times grad_scale * grad_loss[i] in the
+    same pass.  logits, grad_logits: [n, n_vocab]; targets: int32 [n]; loss, lse, grad_loss: float32 [n]."""
+    what = "toktier_cross_entropy"
+    xp, xt, n, n_vocab, xs = _matrix(logits, what, "logits")
+    gp, gs = _grad_logits(grad_logits, logits, what) if grad_logits is not None else (None, 0)
+    wp, wn = _scratch(workspace, what)
+    _check(lib().toktier_cross_entropy(xp, xt, n, n_vocab, xs, _vector(targets, what, "targets", n, _IDS),
+                                       _vector(loss, what, "loss", n, _FLOAT), _vector(lse, what, "lse", n, _FLOAT),
+                                       _vector(grad_loss, what, "grad_loss", n, _FLOAT, True), float(grad_scale),
+                                       gp, gs, wp, wn, _stream(stream)), what)
+
+
+def toktier_cross_entropy_backward(logits, targets, lse, grad_logits, grad_loss=None, grad_scale=1.0, stream=None):
+    """The gradient alone, from the lse that toktier_cross_entropy wrote for these logits."""
+    what = "toktier_cross_entropy_backward"
+    xp, xt, n, n_vocab, xs = _matrix(logits, what, "logits")
+    gp, gs = _grad_logits(grad_logits, logits, what)
+    _check(lib().toktier_cross_entropy_backward(xp, xt, n, n_vocab, xs, _vector(targets, what, "targets", n, _IDS),
+                                                _vector(lse, what, "lse", n, _FLOAT),
+                                                _vector(grad_loss, what, "grad_loss", n, _FLOAT, True),
+                                                float(grad_scale), gp, gs, _stream(stream)), what)
+
+
+def toktier_sample_workspace_bytes(n_rows, n_vocab):
+    out = ctypes.c_uint64()
+    _check(lib().toktier_sample_workspace_bytes(int(n_rows), int(n_vocab), ctypes.byref(out)),
+           "toktier_sample_workspace_bytes")
+    return out.value
+
+
+def toktier_sample(logits, uniform, out_ids, out_logprobs, workspace, temperature=None, top_k=None, top_p=None,
+                   min_p=None, mask=None, stream=None):
+    """One ID per row of logits [n, n_vocab] from the given random numbers, with per-row settings (None: off).
+    uniform, temperature, top_p, min_p: float32 [n]; top_k: int32 [n]; out_ids: int32 [n] (-1: nothing to choose
+    from); out_logprobs: float32 [n] or None; mask: int32 [n or 1, >= ceil(n_vocab / 32)], bit j & 31 of word
+    j >> 5 allows ID j, one row for all or one each."""
+    what = "toktier_sample"
+    xp, xt, n, n_vocab, xs = _matrix(logits, what, "logits")
+    mp, ms = None, 0
+    if mask is not None:
+        _on_device(mask, what, "mask")
+        if (mask.dim() != 2 or mask.dtype not in _IDS or mask.size(0) not in (1, n) or mask.size(1) * 32 < n_vocab or
+                (mask.size(1) > 1 and mask.stride(1) != 1)):
+            _refuse(what, "mask is not an int32 tensor of [rows or 1, ceil(n_vocab / 32)] with unit stride in a row")
+        mp, ms = _ptr(mask), mask.stride(0) if mask.size(0) > 1 else 0
+    wp, wn = _scratch(workspace, what)
+    _check(lib().toktier_sample(xp, xt, n, n_vocab, xs, mp, ms,
+                                _vector(temperature, what, "temperature", n, _FLOAT, True),
+                                _vector(top_k, what, "top_k", n, _IDS, True),
+                                _vector(top_p, what, "top_p", n, _FLOAT, True),
+                                _vector(min_p, what, "min_p", n, _FLOAT, True),
+                                _vector(uniform, what, "uniform", n, _FLOAT),
+                                _vector(out_ids, what, "out_ids", n, _IDS),
+                                _vector(out_logprobs, what, "out_logprobs", n, _FLOAT, True), wp, wn,
+                                _stream(stream)), what)
 
 
 class Tokenizer:

@@ -3,7 +3,7 @@
     python -m exact_bpe_tokenization_amd.build
 
 Each .hip source is compiled separately (in parallel) with hipcc for gfx950, then linked into one
-shared library.  Packed fp32 instructions are disabled (the library computes only integers).
+shared library.  Packed fp32 instructions are disabled.
 """
 import concurrent.futures
 import os
@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtoktier.so")
-SOURCES = ["pretok.hip", "bpe.hip", "tiles.hip", "added.hip", "toktier.hip", "repair.hip"]
+SOURCES = ["pretok.hip", "bpe.hip", "tiles.hip", "added.hip", "toktier.hip", "repair.hip", "embed.hip", "loss.hip",
+           "sample.hip"]
 ARCH = "gfx950"
 
 

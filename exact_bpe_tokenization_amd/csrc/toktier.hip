@@ -13,6 +13,7 @@
 
 #include "../../include/toktier.h"
 #include "internal.h"
+#include "ops.h"
 
 static_assert(tt::FAMILY_GPT2 == TOKTIER_GPT2 && tt::FAMILY_O200K == TOKTIER_O200K &&
               tt::FAMILY_DEEPSEEK == TOKTIER_DEEPSEEK, "family codes");
@@ -29,6 +30,10 @@ static int hip_fail(hipError_t e)
     g_hip_err = hipGetErrorString(e);
     (void)hipGetLastError();   // clear the sticky error
     return TOKTIER_E_HIP;
+}
+
+namespace tt {
+int hip_status(hipError_t e) { return e == hipSuccess ? TOKTIER_OK : hip_fail(e); }   // for the other sources
 }
 
 #define HIP_TRY(x)                                 \

@@ -369,6 +369,116 @@ int toktier_plan_create_bucket(const toktier_vocab *v, const uint8_t *bytes, con
 int toktier_plan_launch(toktier_plan *p, void *stream, uint64_t *out_n_tokens);
 int toktier_plan_free(toktier_plan *p);
 
+/*
+ * Token operators: what a model does with the IDs at either end, on the same device and stream as the
+ * encoder -- embedding lookup and its gradient (IDs in), next-token cross entropy and its gradient, and
+ * sampling of the next ID (IDs out).
+ *   - They take no vocabulary handle: n_vocab is the caller's number of IDs (<= TOKTIER_MAX_VOCAB).
+ *   - Matrices are row-major device memory with unit stride inside a row; `stride` counts elements from
+ *     one row to the next and is at least the row's length.  Any alignment that is a multiple of the
+ *     element's size will do; what lies between rows is neither read nor written.
+ *   - IDs are uint32 as the encoder writes them.  An ID that is not below n_vocab (0xFFFFFFFF by custom)
+ *     names no row: padding for the lookup, an ignored position for the loss.
+ *   - Work is enqueued on `stream` (hipStream_t as void*, NULL = default) of the current device; nothing
+ *     is allocated or waited for, so every call can be captured into a HIP graph.  A workspace is
+ *     caller-owned scratch, 256-byte aligned, its contents on entry do not matter, and it must not be
+ *     shared by two calls in flight.
+ *   - Results depend on the arguments alone: repeated calls give the same bits.
+ * Errors of every call: E_INVALID_ARG (null pointer, unknown type, bad size, stride or alignment,
+ * overlapping output), E_CAPACITY (workspace too small), E_HIP; arguments are checked before any device
+ * work.  Zero rows or tokens are valid.
+ */
+enum {
+    TOKTIER_F32 = 1,
+    TOKTIER_F16 = 2,
+    TOKTIER_BF16 = 3
+};
+
+/* Largest n_vocab: every ID the encoder writes lies below it (256 + TOKTIER_MAX_MERGES IDs and added ones). */
+#define TOKTIER_MAX_VOCAB (1u << 21)
+
+/*
+ * Embedding lookup: out[t, 0..dim) = scale * table[ids[t], 0..dim); a row of zeros where ids[t] >= n_vocab.
+ *   table   device, n_vocab rows of dim elements of table_type.
+ *   ids     device, uint32[n_tokens]; n_tokens < 2^32 - 1.
+ *   out     device, n_tokens rows of dim elements of out_type (any of the three, whatever the table's);
+ *           the product is rounded once, from 32 bits.
+ */
+int toktier_embed(const void *table, int table_type, uint32_t n_vocab, uint32_t dim, uint64_t table_stride,
+                  const uint32_t *ids, uint64_t n_tokens, float scale, void *out, int out_type,
+                  uint64_t out_stride, void *stream);
+
+/*
+ * Gradient of the lookup: grad_table[r, :] = scale * (sum of grad_out[t, :] over the tokens with ids[t] = r),
+ * summed in 32 bits in an order fixed by the token order (tokens are sorted by ID; no floating-point
+ * atomics), rounded once.
+ *   accumulate  0: all n_vocab rows are written, those of absent IDs with zeros.  1: the sums are added to
+ *               grad_table's values; rows of absent IDs are left alone.
+ *   workspace   device, toktier_embed_backward_workspace_bytes(n_tokens, n_vocab, dim) bytes.
+ * grad_type and table_type may differ (16-bit gradients into a 32-bit table, for instance).
+ */
+int toktier_embed_backward_workspace_bytes(uint64_t n_tokens, uint32_t n_vocab, uint32_t dim, uint64_t *out_bytes);
+int toktier_embed_backward(const void *grad_out, int grad_type, uint64_t grad_stride, const uint32_t *ids,
+                           uint64_t n_tokens, float scale, void *grad_table, int table_type, uint32_t n_vocab,
+                           uint32_t dim, uint64_t table_stride, int accumulate, void *workspace,
+                           uint64_t workspace_bytes, void *stream);
+
+/*
+ * Next-token cross entropy, and in the same pass its gradient.  For row i with target y = targets[i]:
+ *   lse[i]  = log(sum_j exp(logits[i, j]))
+ *   loss[i] = lse[i] - logits[i, y]                            (0 where y >= n_vocab)
+ *   grad_logits[i, j] = c_i * (exp(logits[i, j] - lse[i]) - [j == y])   (zeros where y >= n_vocab)
+ *   c_i = grad_scale * (grad_loss ? grad_loss[i] : 1)          (the mean over N positions: c_i = 1 / N)
+ * Logits of -inf have probability 0.  A row of nothing else has lse -inf, loss +inf and a gradient of
+ * zeros; a NaN or +inf in a row makes its lse, loss and gradient NaN (an ignored row keeps loss 0 and a
+ * gradient of zeros).
+ *   targets      device, uint32[n_rows].
+ *   loss, lse    device, float[n_rows].
+ *   grad_loss    device, float[n_rows], or NULL.
+ *   grad_logits  device, n_rows rows of n_vocab elements of `type`, or NULL for the loss alone; may be
+ *                `logits` itself with the same stride (in place), else must not overlap it.
+ *   workspace    device, toktier_cross_entropy_workspace_bytes(n_rows, n_vocab) bytes.
+ */
+int toktier_cross_entropy_workspace_bytes(uint32_t n_rows, uint32_t n_vocab, uint64_t *out_bytes);
+int toktier_cross_entropy(const void *logits, int type, uint32_t n_rows, uint32_t n_vocab, uint64_t stride,
+                          const uint32_t *targets, float *loss, float *lse, const float *grad_loss,
+                          float grad_scale, void *grad_logits, uint64_t grad_stride, void *workspace,
+                          uint64_t workspace_bytes, void *stream);
+
+/* The gradient alone, later, from the lse that toktier_cross_entropy wrote for the same logits. */
+int toktier_cross_entropy_backward(const void *logits, int type, uint32_t n_rows, uint32_t n_vocab, uint64_t stride,
+                                   const uint32_t *targets, const float *lse, const float *grad_loss,
+                                   float grad_scale, void *grad_logits, uint64_t grad_stride, void *stream);
+
+/*
+ * Sampling of one ID per row with temperature, top-k, top-p and min-p from given random numbers.  With
+ * x the row's logits, those of -inf or NaN and those whose mask bit is 0 being out of the choice, sorted by
+ * (x descending, ID ascending), and w_j = exp((x_j - max x) / temperature):
+ *   top-k   keeps the first k;
+ *   top-p   keeps, of those, the shortest prefix whose mass reaches top_p * (mass of all of those);
+ *   min-p   keeps, of those, the ones with w_j >= min_p;
+ * the first is always kept.  out_ids[i] is the smallest ID whose kept mass, summed over IDs in ascending
+ * order, exceeds uniform[i] * (mass of all kept), out_logprobs[i] the logarithm of its share of that mass.
+ * A row with nothing to choose from gives ID 0xFFFFFFFF and -inf.  A logit of +inf outweighs every finite
+ * one.  The masses are sums of 64-bit integers (w_j is computed in 64-bit floating point and rounded to
+ * a multiple of 2^-45, coarser only for more than 2^18 IDs), so they are exact sums in any order.
+ * Per-row settings, each device [n_rows] or NULL for "off":
+ *   temperature  float; <= 0 or NaN: the largest logit (the lowest ID of equals), log-probability 0; NULL: 1.
+ *   top_k        uint32; 0: off.
+ *   top_p        float; >= 1 or NaN: off; <= 0: the first alone.
+ *   min_p        float; <= 0 or NaN: off; >= 1: the largest and its equals.
+ *   uniform      float in [0, 1), required; values outside are taken as the nearest inside, NaN as 0.
+ *   mask         device, uint32 words, bit (j & 31) of word j >> 5 for ID j (1: allowed), row i at
+ *                mask + i * mask_stride (in words; 0: one mask for all rows); NULL: all allowed.
+ *   out_ids      device, uint32[n_rows].   out_logprobs  device, float[n_rows], or NULL.
+ *   workspace    device, toktier_sample_workspace_bytes(n_rows, n_vocab) bytes.
+ */
+int toktier_sample_workspace_bytes(uint32_t n_rows, uint32_t n_vocab, uint64_t *out_bytes);
+int toktier_sample(const void *logits, int type, uint32_t n_rows, uint32_t n_vocab, uint64_t stride,
+                   const uint32_t *mask, uint64_t mask_stride, const float *temperature, const uint32_t *top_k,
+                   const float *top_p, const float *min_p, const float *uniform, uint32_t *out_ids,
+                   float *out_logprobs, void *workspace, uint64_t workspace_bytes, void *stream);
+
 /* Static English text for a status code. */
 const char *toktier_status_string(int status);
 
