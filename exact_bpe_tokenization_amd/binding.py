@@ -460,34 +460,48 @@ def _refuse(what, why):
     raise ToktierError(1, f"{what}: {why}")
 
 
-def _on_device(t, what, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index != torch.cuda.current_device():
-        _refuse(what, f"{name} is not a tensor on the current device")
+def _here(stream):
+    """(current device, raw stream) of a call: these calls are short, so torch's own quick lookup is used
+    where it is there."""
+    if not torch.cuda.is_initialized():   # then no tensor is on a device: the checks say so
+        return None, None
+    dev = torch.cuda.current_device()
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return dev, raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
+    return dev, _stream(stream)
 
 
-def _matrix(t, what, name):
+def _matrix(t, dev, what, name):
     """(pointer, type, rows, columns, row stride) of a matrix argument."""
-    _on_device(t, what, name)
-    if t.dim() != 2 or t.dtype not in TYPES or (t.size(1) > 1 and t.stride(1) != 1):
-        _refuse(what, f"{name} is not a 2-D float32, float16 or bfloat16 tensor with unit stride in a row")
-    rows, cols = t.shape
-    return _ptr(t), TYPES[t.dtype], rows, cols, t.stride(0) if rows > 1 else cols
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _refuse(what, f"{name} is not a tensor on the current device")
+    kind, shape = TYPES.get(t.dtype), t.shape
+    if kind is None or len(shape) != 2:
+        _refuse(what, f"{name} is not a 2-D float32, float16 or bfloat16 tensor")
+    rows, cols = shape
+    row_stride, stride = t.stride()
+    if stride != 1 and cols > 1:
+        _refuse(what, f"the rows of {name} do not have unit stride")
+    return t.data_ptr(), kind, rows, cols, row_stride if rows > 1 else cols
 
 
-def _vector(t, what, name, n, dtypes, optional=False):
-    if t is None and optional:
-        return None
-    _on_device(t, what, name)
-    if t.dim() != 1 or t.dtype not in dtypes or t.numel() != n or not t.is_contiguous():
+def _vector(t, dev, what, name, n, dtypes):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _refuse(what, f"{name} is not a tensor on the current device")
+    if t.dtype not in dtypes or t.shape != (n,) or not t.is_contiguous():
         _refuse(what, f"{name} is not a contiguous tensor of {n} x {dtypes[0]}")
-    return _ptr(t)
+    return t.data_ptr()
 
 
-def _scratch(t, what):
-    _on_device(t, what, "workspace")
-    if t.dtype != torch.uint8 or not t.is_contiguous():
-        _refuse(what, "workspace is not a contiguous uint8 tensor")
-    return _ptr(t), t.numel()
+def _optional(t, dev, what, name, n, dtypes):
+    return None if t is None else _vector(t, dev, what, name, n, dtypes)
+
+
+def _scratch(t, dev, what):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != torch.uint8 or not t.is_contiguous():
+        _refuse(what, "workspace is not a contiguous uint8 tensor on the current device")
+    return t.data_ptr(), t.numel()
 
 
 _IDS, _FLOAT = (torch.int32, torch.uint32), (torch.float32,)
@@ -497,12 +511,13 @@ def toktier_embed(table, ids, out, scale=1.0, stream=None):
     """out[t] = scale * table[ids[t]], zeros where ids[t] is no row of the table.  table: [n_vocab, dim],
     ids: int32 [n], out: [n, dim]; the types of table and out may differ."""
     what = "toktier_embed"
-    tp, tt_, n_vocab, dim, ts = _matrix(table, what, "table")
-    op, ot, n, odim, os_ = _matrix(out, what, "out")
+    dev, st = _here(stream)
+    tp, tt_, n_vocab, dim, ts = _matrix(table, dev, what, "table")
+    op, ot, n, odim, os_ = _matrix(out, dev, what, "out")
     if odim != dim:
         _refuse(what, f"out has {odim} columns, table {dim}")
-    _check(lib().toktier_embed(tp, tt_, n_vocab, dim, ts, _vector(ids, what, "ids", n, _IDS), n, float(scale), op, ot,
-                               os_, _stream(stream)), what)
+    _check(lib().toktier_embed(tp, tt_, n_vocab, dim, ts, _vector(ids, dev, what, "ids", n, _IDS), n, float(scale), op, ot,
+                               os_, st), what)
 
 
 def toktier_embed_backward_workspace_bytes(n_tokens, n_vocab, dim):
@@ -517,13 +532,14 @@ def toktier_embed_backward(grad_out, ids, grad_table, workspace, scale=1.0, accu
     grad_table holds when accumulate is True.  grad_out: [n, dim], ids: int32 [n], grad_table: [n_vocab, dim];
     workspace: uint8 of toktier_embed_backward_workspace_bytes(n, n_vocab, dim)."""
     what = "toktier_embed_backward"
-    gp, gt, n, dim, gs = _matrix(grad_out, what, "grad_out")
-    tp, tt_, n_vocab, tdim, ts = _matrix(grad_table, what, "grad_table")
+    dev, st = _here(stream)
+    gp, gt, n, dim, gs = _matrix(grad_out, dev, what, "grad_out")
+    tp, tt_, n_vocab, tdim, ts = _matrix(grad_table, dev, what, "grad_table")
     if tdim != dim:
         _refuse(what, f"grad_table has {tdim} columns, grad_out {dim}")
-    wp, wn = _scratch(workspace, what)
-    _check(lib().toktier_embed_backward(gp, gt, gs, _vector(ids, what, "ids", n, _IDS), n, float(scale), tp, tt_,
-                                        n_vocab, dim, ts, int(bool(accumulate)), wp, wn, _stream(stream)), what)
+    wp, wn = _scratch(workspace, dev, what)
+    _check(lib().toktier_embed_backward(gp, gt, gs, _vector(ids, dev, what, "ids", n, _IDS), n, float(scale), tp, tt_,
+                                        n_vocab, dim, ts, int(bool(accumulate)), wp, wn, st), what)
 
 
 def toktier_cross_entropy_workspace_bytes(n_rows, n_vocab):
@@ -533,8 +549,8 @@ def toktier_cross_entropy_workspace_bytes(n_rows, n_vocab):
     return out.value
 
 
-def _grad_logits(grad_logits, logits, what):
-    gp, gt, rows, cols, gs = _matrix(grad_logits, what, "grad_logits")
+def _grad_logits(grad_logits, logits, dev, what):
+    gp, gt, rows, cols, gs = _matrix(grad_logits, dev, what, "grad_logits")
     if grad_logits.shape != logits.shape or grad_logits.dtype != logits.dtype:
         _refuse(what, "grad_logits differs from logits in shape or type")
     return gp, gs
@@ -546,24 +562,27 @@ def toktier_cross_entropy(logits, targets, loss, lse, workspace, grad_logits=Non
     where grad_logits is given (logits itself is allowed), its gradient times grad_scale * grad_loss[i] in the
     same pass.  logits, grad_logits: [n, n_vocab]; targets: int32 [n]; loss, lse, grad_loss: float32 [n]."""
     what = "toktier_cross_entropy"
-    xp, xt, n, n_vocab, xs = _matrix(logits, what, "logits")
-    gp, gs = _grad_logits(grad_logits, logits, what) if grad_logits is not None else (None, 0)
-    wp, wn = _scratch(workspace, what)
-    _check(lib().toktier_cross_entropy(xp, xt, n, n_vocab, xs, _vector(targets, what, "targets", n, _IDS),
-                                       _vector(loss, what, "loss", n, _FLOAT), _vector(lse, what, "lse", n, _FLOAT),
-                                       _vector(grad_loss, what, "grad_loss", n, _FLOAT, True), float(grad_scale),
-                                       gp, gs, wp, wn, _stream(stream)), what)
+    dev, st = _here(stream)
+    xp, xt, n, n_vocab, xs = _matrix(logits, dev, what, "logits")
+    gp, gs = _grad_logits(grad_logits, logits, dev, what) if grad_logits is not None else (None, 0)
+    wp, wn = _scratch(workspace, dev, what)
+    _check(lib().toktier_cross_entropy(xp, xt, n, n_vocab, xs, _vector(targets, dev, what, "targets", n, _IDS),
+                                       _vector(loss, dev, what, "loss", n, _FLOAT),
+                                       _vector(lse, dev, what, "lse", n, _FLOAT),
+                                       _optional(grad_loss, dev, what, "grad_loss", n, _FLOAT), float(grad_scale),
+                                       gp, gs, wp, wn, st), what)
 
 
 def toktier_cross_entropy_backward(logits, targets, lse, grad_logits, grad_loss=None, grad_scale=1.0, stream=None):
     """The gradient alone, from the lse that toktier_cross_entropy wrote for these logits."""
     what = "toktier_cross_entropy_backward"
-    xp, xt, n, n_vocab, xs = _matrix(logits, what, "logits")
-    gp, gs = _grad_logits(grad_logits, logits, what)
-    _check(lib().toktier_cross_entropy_backward(xp, xt, n, n_vocab, xs, _vector(targets, what, "targets", n, _IDS),
-                                                _vector(lse, what, "lse", n, _FLOAT),
-                                                _vector(grad_loss, what, "grad_loss", n, _FLOAT, True),
-                                                float(grad_scale), gp, gs, _stream(stream)), what)
+    dev, st = _here(stream)
+    xp, xt, n, n_vocab, xs = _matrix(logits, dev, what, "logits")
+    gp, gs = _grad_logits(grad_logits, logits, dev, what)
+    _check(lib().toktier_cross_entropy_backward(xp, xt, n, n_vocab, xs, _vector(targets, dev, what, "targets", n, _IDS),
+                                                _vector(lse, dev, what, "lse", n, _FLOAT),
+                                                _optional(grad_loss, dev, what, "grad_loss", n, _FLOAT),
+                                                float(grad_scale), gp, gs, st), what)
 
 
 def toktier_sample_workspace_bytes(n_rows, n_vocab):
@@ -580,24 +599,25 @@ def toktier_sample(logits, uniform, out_ids, out_logprobs, workspace, temperatur
     from); out_logprobs: float32 [n] or None; mask: int32 [n or 1, >= ceil(n_vocab / 32)], bit j & 31 of word
     j >> 5 allows ID j, one row for all or one each."""
     what = "toktier_sample"
-    xp, xt, n, n_vocab, xs = _matrix(logits, what, "logits")
+    dev, st = _here(stream)
+    xp, xt, n, n_vocab, xs = _matrix(logits, dev, what, "logits")
     mp, ms = None, 0
     if mask is not None:
-        _on_device(mask, what, "mask")
-        if (mask.dim() != 2 or mask.dtype not in _IDS or mask.size(0) not in (1, n) or mask.size(1) * 32 < n_vocab or
+        if (not isinstance(mask, torch.Tensor) or mask.get_device() != dev or mask.dim() != 2 or
+                mask.dtype not in _IDS or mask.size(0) not in (1, n) or mask.size(1) * 32 < n_vocab or
                 (mask.size(1) > 1 and mask.stride(1) != 1)):
-            _refuse(what, "mask is not an int32 tensor of [rows or 1, ceil(n_vocab / 32)] with unit stride in a row")
-        mp, ms = _ptr(mask), mask.stride(0) if mask.size(0) > 1 else 0
-    wp, wn = _scratch(workspace, what)
+            _refuse(what, "mask is not an int32 tensor of [rows or 1, ceil(n_vocab / 32)] on the current device with "
+                          "unit stride in a row")
+        mp, ms = mask.data_ptr(), mask.stride(0) if mask.size(0) > 1 else 0
+    wp, wn = _scratch(workspace, dev, what)
     _check(lib().toktier_sample(xp, xt, n, n_vocab, xs, mp, ms,
-                                _vector(temperature, what, "temperature", n, _FLOAT, True),
-                                _vector(top_k, what, "top_k", n, _IDS, True),
-                                _vector(top_p, what, "top_p", n, _FLOAT, True),
-                                _vector(min_p, what, "min_p", n, _FLOAT, True),
-                                _vector(uniform, what, "uniform", n, _FLOAT),
-                                _vector(out_ids, what, "out_ids", n, _IDS),
-                                _vector(out_logprobs, what, "out_logprobs", n, _FLOAT, True), wp, wn,
-                                _stream(stream)), what)
+                                _optional(temperature, dev, what, "temperature", n, _FLOAT),
+                                _optional(top_k, dev, what, "top_k", n, _IDS),
+                                _optional(top_p, dev, what, "top_p", n, _FLOAT),
+                                _optional(min_p, dev, what, "min_p", n, _FLOAT),
+                                _vector(uniform, dev, what, "uniform", n, _FLOAT),
+                                _vector(out_ids, dev, what, "out_ids", n, _IDS),
+                                _optional(out_logprobs, dev, what, "out_logprobs", n, _FLOAT), wp, wn, st), what)
 
 
 class Tokenizer:

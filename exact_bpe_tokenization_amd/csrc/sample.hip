@@ -1,33 +1,173 @@
 // sample.hip -- sampling of one ID per row: temperature, top-k, top-p, min-p, given random numbers.
 //
 // Every filter keeps a prefix of the order (logit descending, ID ascending), so the kept set is one pair: a
-// logit (as an order-preserving 32-bit key) and how many of its equals, lowest IDs first.  Counts find the
-// top-k pair and masses the top-p pair, by the same search over histograms of key digits.  Masses are
+// logit (as an integer key of the same order) and how many of its equals, lowest IDs first.  Masses are
 // sums of 64-bit integers, w = 2^y rounded to a multiple of 2^-S with y = (x - max) log2(e) / temperature in
 // 64-bit floating point: exact in any order, so neither atomics nor the split of a row over threads can
 // change an ID.
+//
+// One workgroup per row; a wavefront owns a contiguous segment of it, in registers where the row fits.
+//   1. keys and the largest of them;
+//   2. for top-k and top-p, a histogram over 4,095 bins of the key (sign, exponent, 7 mantissa bits) with
+//      counts and masses; a scan from the top finds the bin where a filter ends, and a digit search over
+//      that bin's keys the exact key and its equals (nothing to search for bfloat16, whose bins hold one key);
+//   3. the ID by the running mass over IDs: per wavefront, then inside the one wavefront that holds it.
+#include <type_traits>
+
 #include "ops.h"
 
 namespace tt {
 namespace {
 
-constexpr int THREADS = 1024, WAVES = THREADS / 64;
-constexpr uint32_t SLAB = THREADS * VEC;                      // elements of one round of the workgroup's vectors
-constexpr uint32_t MAX_SLABS = TOKTIER_MAX_VOCAB / SLAB;
-constexpr uint32_t BINS = 2048;
-constexpr uint32_t NO_ID = 0xFFFFFFFFu;
+#define INLINE __attribute__((always_inline))   // of a lambda: the keys it sees stay in registers
 
-// Order-preserving key of a logit; 0 for one that is out of the choice (-inf, NaN).
-__device__ __forceinline__ uint32_t logit_key(float x)
+constexpr uint32_t NO_ID = 0xFFFFFFFFu;
+constexpr int BINS = 4096, HALF = BINS / 2 - 1;   // bins of a sign; bin 0 holds the largest keys
+constexpr int DIGIT = 11, DIGITS = 1 << DIGIT;
+
+// A key is the logit's sign and magnitude bits as an integer: the order of the logits, -0 equal to +0.
+// Bins: magnitudes below 2^-9 share the middle one, those from 2^7 on the outermost, and between them a bin
+// has 128 per octave.
+template <class T> struct Keys;
+template <> struct Keys<__bf16> {
+    static constexpr int INF = 0x7F80, LOW = 0x3B00, SHIFT = 0;
+    static __device__ __forceinline__ float value(int k)
+    {
+        const uint32_t m = (uint32_t)(k < 0 ? -k : k);
+        return __builtin_bit_cast(float, m << 16 | ((uint32_t)k & 0x80000000u));
+    }
+};
+template <> struct Keys<_Float16> {
+    static constexpr int INF = 0x7C00, LOW = 0x1800, SHIFT = 3;
+    static __device__ __forceinline__ float value(int k)
+    {
+        const uint32_t m = (uint32_t)(k < 0 ? -k : k);
+        const float f = (float)__builtin_bit_cast(_Float16, (uint16_t)m);
+        return k < 0 ? -f : f;
+    }
+};
+template <> struct Keys<float> {
+    static constexpr int INF = 0x7F800000, LOW = 118 << 23, SHIFT = 16;
+    static __device__ __forceinline__ float value(int k)
+    {
+        const uint32_t m = (uint32_t)(k < 0 ? -k : k);
+        return __builtin_bit_cast(float, m | ((uint32_t)k & 0x80000000u));
+    }
+};
+
+template <class T> __device__ __forceinline__ int bin_of(int k)
 {
-    if (!(x > -__builtin_inff())) return 0;
-    const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.f);   // -0 and +0 are equals
-    return (int32_t)b < 0 ? ~b : b | 0x80000000u;
+    using K = Keys<T>;
+    const int sign = k >> 31, mag = (k ^ sign) - sign;
+    int m = (mag - (K::LOW - (1 << K::SHIFT))) >> K::SHIFT;
+    m = m < 0 ? 0 : m > HALF ? HALF : m;
+    return HALF - ((m ^ sign) - sign);
 }
 
-__device__ __forceinline__ float key_logit(uint32_t k)
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+// Eight keys: packed in pairs for the 16-bit types.
+template <class T> struct Vec8 {
+    u32x4 a;
+    __device__ __forceinline__ s16x2 pair(int i) const
+    {
+        const uint32_t w = a[i];   // (a bit cast of the vector's element itself would read element 0)
+        return __builtin_bit_cast(s16x2, w);
+    }
+    __device__ __forceinline__ int at(int e) const
+    {
+        return (e & 1) ? (int)a[e >> 1] >> 16 : (int)(int16_t)(a[e >> 1] & 0xFFFFu);
+    }
+    __device__ __forceinline__ int pick(int e) const   // at(), for an index known at run time only
+    {
+        const uint32_t w = e & 4 ? (e & 2 ? a[3] : a[2]) : (e & 2 ? a[1] : a[0]);
+        return (e & 1) ? (int)w >> 16 : (int)(int16_t)(w & 0xFFFFu);
+    }
+    __device__ __forceinline__ void hide(int e) { a[e >> 1] = (e & 1) ? (a[e >> 1] & 0xFFFFu) | 0x80000000u : (a[e >> 1] & 0xFFFF0000u) | 0x8000u; }
+    __device__ __forceinline__ int max() const
+    {
+        s16x2 m = pair(0);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, pair(i));
+        return m.x > m.y ? m.x : m.y;
+    }
+    // logits to keys, in place
+    __device__ __forceinline__ void order()
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const s16x2 b = pair(i), sign = b >> 15;
+            const s16x2 m = __builtin_bit_cast(s16x2, a[i] & 0x7FFF7FFFu);
+            a[i] = __builtin_bit_cast(uint32_t, (m ^ sign) - sign);
+        }
+    }
+    __device__ __forceinline__ void bins(int (&b)[VEC]) const
+    {
+        using K = Keys<T>;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const s16x2 k = pair(i), sign = k >> 15;
+            const u16x2 mag = __builtin_bit_cast(u16x2, __builtin_elementwise_max(k, (s16x2)-k));
+            u16x2 m = __builtin_elementwise_sub_sat(mag, (u16x2)(unsigned short)(K::LOW - (1 << K::SHIFT)));
+            m = __builtin_elementwise_min((u16x2)(m >> K::SHIFT), (u16x2)(unsigned short)HALF);
+            const s16x2 t = (s16x2)(short)HALF - ((__builtin_bit_cast(s16x2, m) ^ sign) - sign);
+            b[2 * i] = t.x;
+            b[2 * i + 1] = t.y;
+        }
+    }
+};
+template <> struct Vec8<float> {
+    u32x4 a, b;
+    __device__ __forceinline__ int at(int e) const { return e < 4 ? (int)a[e] : (int)b[e - 4]; }
+    __device__ __forceinline__ int pick(int e) const
+    {
+        const uint32_t l = e & 2 ? (e & 1 ? a[3] : a[2]) : (e & 1 ? a[1] : a[0]);
+        const uint32_t h = e & 2 ? (e & 1 ? b[3] : b[2]) : (e & 1 ? b[1] : b[0]);
+        return (int)(e & 4 ? h : l);
+    }
+    __device__ __forceinline__ void set(int e, int v)
+    {
+        if (e < 4) a[e] = (uint32_t)v;
+        else b[e - 4] = (uint32_t)v;
+    }
+    __device__ __forceinline__ void hide(int e) { set(e, (int)0x80000000); }
+    __device__ __forceinline__ int max() const
+    {
+        int m = at(0);
+#pragma unroll
+        for (int e = 1; e < VEC; ++e) m = at(e) > m ? at(e) : m;
+        return m;
+    }
+    __device__ __forceinline__ void order()
+    {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int x = at(e), sign = x >> 31;
+            set(e, ((x & 0x7FFFFFFF) ^ sign) - sign);
+        }
+    }
+    __device__ __forceinline__ void bins(int (&out)[VEC]) const
+    {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out[e] = bin_of<float>(at(e));
+    }
+};
+
+// Keys of a bin: lo .. hi.
+template <class T> __device__ __forceinline__ void bin_range(int b, int &lo, int &hi)
 {
-    return __builtin_bit_cast(float, (int32_t)k < 0 ? k & 0x7FFFFFFFu : ~k);
+    using K = Keys<T>;
+    const int s = HALF - b, m = s < 0 ? -s : s;
+    const int a = m == 0 ? -(K::LOW - 1) : K::LOW + ((m - 1) << K::SHIFT);
+    const int z = m == 0 ? K::LOW - 1 : m == HALF ? K::INF : K::LOW + (m << K::SHIFT) - 1;
+    lo = s < 0 ? -z : a;
+    hi = s < 0 ? -a : z;
+}
+// bfloat16: one key per bin, but for the middle and the outermost ones
+template <class T> __device__ __forceinline__ bool bin_exact(int b)
+{
+    return __is_same(T, __bf16) && b != HALF && b != 0 && b != 2 * HALF;
 }
 
 // Weights of one row.  2^y = 2^n 2^f with n the nearest integer: 2^f on [-1/2, 1/2] by the polynomial of degree
@@ -35,17 +175,15 @@ __device__ __forceinline__ float key_logit(uint32_t k)
 // adding 2^(52 - S) and reading the low bits.
 struct Weights {
     double c, max, magic;
-    uint32_t max_key;
+    int max_key;
 
     __device__ __forceinline__ uint64_t one() const
     {
         return __builtin_bit_cast(uint64_t, 1.0 + magic) - __builtin_bit_cast(uint64_t, magic);
     }
-    __device__ __forceinline__ uint64_t of(uint32_t key) const
+    __device__ __forceinline__ uint64_t of(int key, float x) const
     {
-        if (key == max_key) return one();
-        const double y = ((double)key_logit(key) - max) * c;
-        if (key == 0 || !(y > -64.0)) return 0;
+        const double y = ((double)x - max) * c;
         const double n = __builtin_rint(y), f = y - n;
         double p = 7.072585949269224e-09;
         p = __builtin_fma(p, f, 1.0208690299958306e-07);
@@ -59,17 +197,9 @@ struct Weights {
         p = __builtin_fma(p, f, 0.69314718055995);
         p = __builtin_fma(p, f, 1.0);
         const double w = __builtin_amdgcn_ldexp(p, (int)n);
-        return __builtin_bit_cast(uint64_t, w + magic) - __builtin_bit_cast(uint64_t, magic);
+        const uint64_t q = __builtin_bit_cast(uint64_t, w + magic) - __builtin_bit_cast(uint64_t, magic);
+        return key == max_key ? one() : y > -64.0 ? q : 0ull;   // the largest may be +inf; y may be -inf or NaN
     }
-};
-
-struct Shared {
-    uint64_t hist[BINS];
-    uint64_t slab[MAX_SLABS];
-    uint64_t wave[WAVES];
-    uint64_t found_above;
-    uint32_t found;
-    uint32_t found_key;
 };
 
 template <class V> __device__ __forceinline__ V wave_scan(V v)
@@ -81,275 +211,522 @@ template <class V> __device__ __forceinline__ V wave_scan(V v)
     }
     return v;
 }
+template <class V> __device__ __forceinline__ V wave_sum(V v)
+{
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
 
-// Inclusive sum over the workgroup's threads; total: over all.
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, Shared &sh, uint64_t &total)
+template <int WAVES> struct Shared {
+    uint64_t mass[BINS];                                     // per bin; for the draw, the weight of its key
+    union {
+        uint32_t count[BINS];
+        uint64_t digit[DIGITS];
+    };
+    uint64_t wave[WAVES];
+    uint64_t above, inside;
+    uint32_t found;
+    int key;
+};
+
+// Sum over the threads below this one; total: over all.
+template <int WAVES> __device__ __forceinline__ uint64_t block_before(uint64_t v, Shared<WAVES> &sh, uint64_t &total)
 {
     const uint32_t wave = threadIdx.x >> 6;
-    v = wave_scan(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 63) sh.wave[wave] = v;
+    const uint64_t incl = wave_scan(v);
+    if ((threadIdx.x & 63) == 63) sh.wave[wave] = incl;
     __syncthreads();
     uint64_t base = 0;
     total = 0;
-#pragma unroll
+#pragma unroll 4
     for (uint32_t w = 0; w < WAVES; ++w) {
         const uint64_t s = sh.wave[w];
         if (w < wave) base += s;
         total += s;
     }
-    return base + v;
+    __syncthreads();
+    return base + incl - v;
 }
 
-template <class T> struct Row {
+// The first of n bins (value(b), b ascending) at which the running sum reaches target(total), the sum before it
+// and the bin's own value.  n / threads consecutive bins per thread.  False when the total is below target.
+template <int N, int WAVES, class F, class G>
+__device__ __forceinline__ bool find_bin(Shared<WAVES> &sh, F value, G target_of, uint32_t &bin, uint64_t &above,
+                                         uint64_t &inside, uint64_t &target)
+{
+    constexpr int PER = N / (WAVES * 64);
+    uint64_t v[PER], sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        v[i] = value(threadIdx.x * PER + i);
+        sum += v[i];
+    }
+    uint64_t run = block_before(sum, sh, total);
+    target = target_of(total);
+    if (target > total) return false;
+    if (run < target && target <= run + sum) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (run < target && target <= run + v[i]) {
+                sh.found = threadIdx.x * PER + i;
+                sh.above = run;
+                sh.inside = v[i];
+            }
+            run += v[i];
+        }
+    }
+    __syncthreads();
+    bin = sh.found;
+    above = sh.above;
+    inside = sh.inside;
+    __syncthreads();
+    return true;
+}
+
+// One row.  NV > 0: its keys stay in registers (NV vectors per thread at most); NV == 0: every pass reads them.
+template <class T, int WAVES, int NV> struct Row {
+    static constexpr int HELD = NV ? NV : 1;
     const T *x;
     const uint32_t *mask;
-    uint32_t n;
+    uint32_t n, nv, first;   // elements, vectors per thread, this thread's first element
+    bool nan;                // a positive NaN may be among the keys of a 16-bit type
+    using V = Vec8<T>;
+    V held[HELD];
 
-    // keys of the eight elements from j on (j a multiple of eight below n)
-    __device__ __forceinline__ void keys(uint32_t j, uint32_t (&k)[VEC]) const
+    __device__ __forceinline__ uint32_t at(uint32_t i) const { return first + i * (64 * VEC); }
+
+    __device__ __forceinline__ Vec8<T> raw(uint32_t j) const
     {
-        float v[VEC];
-        load_part(x + j, n - j, -__builtin_inff(), v);
-        const uint32_t bits = mask ? mask[j >> 5] >> (j & 31u) : 0xFFu;
+        Vec8<T> v;
+        if (j + VEC <= n) {
+            if constexpr (sizeof(T) == 4) {
+                v.a = *(const u32x4_row *)(x + j);
+                v.b = *(const u32x4_row *)(x + j + 4);
+            } else {
+                v.a = *(const u32x4_row *)(x + j);
+            }
+        } else {
+            uint32_t e[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) k[e] = (bits >> e) & 1u ? logit_key(v[e]) : 0u;
+            for (int k = 0; k < VEC; ++k) {
+                if constexpr (sizeof(T) == 4) e[k] = j + k < n ? __builtin_bit_cast(uint32_t, x[j + k]) : 0xFF800000u;
+                else e[k] = j + k < n ? (uint32_t)__builtin_bit_cast(uint16_t, x[j + k]) : 0x8000u | (uint32_t)Keys<T>::INF;
+            }
+            if constexpr (sizeof(T) == 4) {
+                v.a = u32x4{e[0], e[1], e[2], e[3]};
+                v.b = u32x4{e[4], e[5], e[6], e[7]};
+            } else {
+                v.a = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+            }
+        }
+        return v;
+    }
+    __device__ __forceinline__ void finish(Vec8<T> &v, uint32_t j) const
+    {
+        v.order();
+        if (nan || sizeof(T) == 4) drop_nan(v);
+        if (mask && j < n) {
+            const uint32_t bits = mask[j >> 5] >> (j & 31u);
+            if ((bits & 0xFFu) != 0xFFu) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (!((bits >> e) & 1u)) v.hide(e);
+            }
+        }
+    }
+    static __device__ __forceinline__ void drop_nan(Vec8<T> &v)
+    {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (v.at(e) > Keys<T>::INF) v.hide(e);
+    }
+    __device__ __forceinline__ void load()
+    {
+        if constexpr (NV > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (i < (int)nv) held[i] = raw(at(i));
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (i < (int)nv) finish(held[i], at(i));
+        }
+    }
+    // Keeps the compiler from carrying what it derived from the keys in one pass over to the next: those
+    // values would need several times the registers of the keys themselves.
+    static __device__ __forceinline__ void forget(V &v)
+    {
+        asm volatile("" : "+v"(v.a));
+        if constexpr (sizeof(T) == 4) asm volatile("" : "+v"(v.b));
+    }
+    // f(index of the first element, keys) over this thread's vectors, ascending
+    template <class F> __device__ __forceinline__ void each(F f)
+    {
+        if constexpr (NV > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (i < (int)nv) {
+                    forget(held[i]);
+                    f(at(i), held[i]);
+                }
+        } else {
+            for (uint32_t i = 0; i < nv; ++i) {
+                Vec8<T> v = raw(at(i));
+                finish(v, at(i));
+                f(at(i), v);
+            }
+        }
     }
 };
 
-// The bin of sh.hist where the sum from the highest bin down reaches `target` (1 .. the sum of all), and the
-// sum above it.
-__device__ __forceinline__ uint32_t find_bin(Shared &sh, uint64_t target, uint64_t &above)
+// The index at which the running sum (over IDs) of the elements' measure exceeds target(total), and its key.
+// sum(vector, index): a vector's, 0 at once where no lane has any; element(vector, index, e): one element's.
+// Per wavefront first; then only the wavefront that holds it looks closer.
+template <int WAVES, class R, class S, class E, class G>
+__device__ __forceinline__ uint32_t locate(R &row, Shared<WAVES> &sh, S sum_of, E element, G target_of, uint64_t &total, int &key)
 {
-    const uint32_t hi = BINS - 1 - 2 * threadIdx.x;
-    const uint64_t a = sh.hist[hi], b = sh.hist[hi - 1];
-    uint64_t total;
-    const uint64_t incl = block_scan(a + b, sh, total), before = incl - a - b;
-    if (before < target && target <= incl) {
-        const bool second = before + a < target;
-        sh.found = second ? hi - 1 : hi;
-        sh.found_above = second ? before + a : before;
+    const uint32_t wave = threadIdx.x >> 6;
+    uint64_t sum = 0;
+    row.each([&](uint32_t j, const auto &v) INLINE { sum += sum_of(v, j); });
+    sum = wave_sum(sum);
+    if ((threadIdx.x & 63) == 0) sh.wave[wave] = sum;
+    __syncthreads();
+    uint64_t before = 0;
+    total = 0;
+#pragma unroll 4
+    for (uint32_t w = 0; w < WAVES; ++w) {
+        const uint64_t s = sh.wave[w];
+        if (w < wave) before += s;
+        total += s;
     }
-    __syncthreads();
-    above = sh.found_above;
-    const uint32_t bin = sh.found;
-    __syncthreads();
-    return bin;
-}
-
-// The first index (ascending) at which the running sum of measure(key, index) exceeds `target`; the target is
-// target(total of all).
-template <class T, class M, class G>
-__device__ __forceinline__ uint32_t locate(const Row<T> &row, Shared &sh, M measure, G target_of, uint64_t &total,
-                                           uint32_t &key_at)
-{
-    const uint32_t slabs = (row.n + SLAB - 1) / SLAB;
-    if (threadIdx.x < MAX_SLABS) sh.slab[threadIdx.x] = 0;
-    __syncthreads();
-    for (uint32_t s = 0; s < slabs; ++s) {
-        const uint32_t j = s * SLAB + threadIdx.x * VEC;
-        uint64_t sum = 0;
-        if (j < row.n) {
-            uint32_t k[VEC];
-            row.keys(j, k);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) sum += measure(k[e], j + e);
-        }
-        if (__ballot(sum != 0)) {
-            sum = wave_scan(sum);
-            if ((threadIdx.x & 63) == 63) atomicAdd((unsigned long long *)&sh.slab[s], (unsigned long long)sum);
-        }
-    }
-    __syncthreads();
-    uint64_t v = threadIdx.x < slabs ? sh.slab[threadIdx.x] : 0;
-    uint64_t incl = block_scan(v, sh, total);
     const uint64_t target = target_of(total);
-    if (incl - v <= target && target < incl) {
-        sh.found = threadIdx.x;
-        sh.found_above = incl - v;
-    }
-    __syncthreads();
-    const uint32_t s = sh.found;
-    const uint64_t base = sh.found_above;
-    const uint32_t j = s * SLAB + threadIdx.x * VEC;
-    uint32_t k[VEC] = {};
-    v = 0;
-    if (j < row.n) {
-        row.keys(j, k);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v += measure(k[e], j + e);
-    }
-    uint64_t all;
-    incl = base + block_scan(v, sh, all);
-    if (incl - v <= target && target < incl) {
-        uint64_t run = incl - v;
-        uint32_t at = NO_ID, kk = 0;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            run += measure(k[e], j + e);
-            if (at == NO_ID && run > target) {
-                at = j + e;
-                kk = k[e];
+    if (before <= target && target < before + sum) {
+        // by thread: the vector in which its share of the wavefront's running sum passes the target
+        typename R::V hit{};
+        uint64_t hit_at = 0, run = before;
+        uint32_t hit_j = NO_ID;
+        row.each([&](uint32_t j, const auto &v) INLINE {
+            const uint64_t mine = sum_of(v, j);
+            if (!__any(mine != 0)) return;
+            const uint64_t incl = run + wave_scan(mine);
+            if (incl - mine <= target && target < incl) {
+                hit = v;
+                hit_at = incl - mine;
+                hit_j = j;
+            }
+            run = __shfl(incl, 63);
+        });
+        if (hit_j != NO_ID) {
+#pragma unroll 1
+            for (int e = 0; e < VEC; ++e) {
+                hit_at += element(hit, hit_j, e);
+                if (hit_at > target) {
+                    sh.found = hit_j + e;
+                    sh.key = hit.pick(e);
+                    break;
+                }
             }
         }
-        sh.found = at;
-        sh.found_key = kk;
     }
     __syncthreads();
-    const uint32_t r = sh.found;
-    key_at = sh.found_key;
+    const uint32_t id = sh.found;
+    key = sh.key;
     __syncthreads();
-    return r;
+    return id;
 }
 
-template <class T>
-__global__ __launch_bounds__(THREADS) void k_sample(const T *__restrict__ logits, uint32_t n_vocab, uint64_t stride,
-                                                    const uint32_t *__restrict__ mask, uint64_t mask_stride,
-                                                    const float *__restrict__ temperature,
-                                                    const uint32_t *__restrict__ top_k, const float *__restrict__ top_p,
-                                                    const float *__restrict__ min_p, const float *__restrict__ uniform,
-                                                    uint32_t *__restrict__ out_ids, float *__restrict__ out_logprobs,
-                                                    double magic)
+template <class T, int WAVES, int NV>
+__global__ __launch_bounds__(WAVES * 64) void k_sample(const T *__restrict__ logits, uint32_t n_vocab, uint64_t stride,
+                                                       const uint32_t *__restrict__ mask, uint64_t mask_stride,
+                                                       const float *__restrict__ temperature,
+                                                       const uint32_t *__restrict__ top_k, const float *__restrict__ top_p,
+                                                       const float *__restrict__ min_p, const float *__restrict__ uniform,
+                                                       uint32_t *__restrict__ out_ids, float *__restrict__ out_logprobs,
+                                                       double magic)
 {
-    __shared__ Shared sh;
-    // levels of the key search: digits of 11, 11 and 10 bits; a 16-bit type has nothing below the second
-    constexpr int LEVELS = sizeof(T) == 4 ? 3 : 2;
+    using K = Keys<T>;
+    using V = Vec8<T>;
+    constexpr int THREADS = WAVES * 64;
+    constexpr bool TABLE = __is_same(T, __bf16);   // a weight per bin
+    __shared__ Shared<WAVES> sh;
     const uint64_t r = blockIdx.x;
-    const Row<T> row{logits + r * stride, mask ? mask + r * mask_stride : nullptr, n_vocab};
+    Row<T, WAVES, NV> row;
+    row.x = logits + r * stride;
+    row.mask = mask ? mask + r * mask_stride : nullptr;
+    row.n = n_vocab;
+    row.nv = (n_vocab + THREADS * VEC - 1) / (THREADS * VEC);
+    row.first = (threadIdx.x >> 6) * (row.nv * 64 * VEC) + (threadIdx.x & 63) * VEC;
+    row.nan = false;
+    row.load();
     const float temp = temperature ? temperature[r] : 1.f;
+    const uint32_t k = top_k ? top_k[r] : 0;
+    const float p = top_p ? top_p[r] : 1.f, mp = min_p ? min_p[r] : 0.f, u_in = uniform[r];
 
-    // largest key with its lowest index, and how many are in the choice
-    uint64_t best = 0;
-    uint32_t valid = 0;
-    for (uint32_t j = threadIdx.x * VEC; j < n_vocab; j += SLAB) {
-        uint32_t k[VEC];
-        row.keys(j, k);
+    // 1. the largest key, of each thread and of all
+    int mine, top;
+    for (;;) {
+        mine = (int)0x80000000;
+        row.each([&](uint32_t, const V &v) INLINE {
+            const int m = v.max();
+            mine = m > mine ? m : mine;
+        });
+        int m = mine;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            valid += k[e] != 0;
-            const uint64_t b = (uint64_t)k[e] << 32 | ~(j + e);
-            if (b > best) best = b;
+        for (int d = 32; d; d >>= 1) {
+            const int o = __shfl_xor(m, d);
+            m = o > m ? o : m;
+        }
+        if ((threadIdx.x & 63) == 0) sh.wave[threadIdx.x >> 6] = (uint32_t)m;
+        __syncthreads();
+        top = (int)(uint32_t)sh.wave[0];
+#pragma unroll 4
+        for (int w = 0; w < WAVES; ++w) top = (int)(uint32_t)sh.wave[w] > top ? (int)(uint32_t)sh.wave[w] : top;
+        __syncthreads();
+        if (sizeof(T) == 4 || top <= K::INF) break;
+        row.nan = true;   // NaN of 16 bits: take them out and look again
+        if constexpr (NV > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (i < (int)row.nv) row.drop_nan(row.held[i]);
         }
     }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        const uint64_t o = __shfl_xor(best, d);
-        best = o > best ? o : best;
-    }
-    uint64_t total;
-    block_scan(valid, sh, total);
-    valid = (uint32_t)total;
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) sh.wave[threadIdx.x >> 6] = best;
-    __syncthreads();
-    for (int w = 0; w < WAVES; ++w) best = sh.wave[w] > best ? sh.wave[w] : best;
-    __syncthreads();
-    const uint32_t max_key = (uint32_t)(best >> 32);
-    uint32_t k = top_k ? top_k[r] : 0;
-    if (k == 0 || k > valid) k = valid;
-    if (k <= 1 || !(temp > 0.f)) {   // nothing, or the first alone
+    constexpr int LOWEST = -K::INF + 1;   // the smallest key in the choice
+    if (top < LOWEST) {                   // nothing to choose from
         if (threadIdx.x == 0) {
-            out_ids[r] = valid ? ~(uint32_t)best : NO_ID;
-            if (out_logprobs) out_logprobs[r] = valid ? 0.f : -__builtin_inff();
+            out_ids[r] = NO_ID;
+            if (out_logprobs) out_logprobs[r] = -__builtin_inff();
         }
         return;
     }
-    const Weights wt{1.4426950408889634 / (double)temp, (double)key_logit(max_key), magic, max_key};
+    const bool first_alone = k == 1 || !(temp > 0.f);
+    const Weights wt{1.4426950408889634 / (double)temp, (double)K::value(top), magic, top};
+    auto weight = [&](int key) INLINE { return wt.of(key, K::value(key)); };
 
-    // kept so far: keys above key_f, and of those equal to it the first `ties`
-    uint32_t key_f = 1, ties = 0xFFFFFFFFu, count_f = 0;   // (all)
-    auto digit_shift = [](int level) { return level == 0 ? 21 : level == 1 ? 10 : 0; };
-    // One search: measure(key) summed per digit over the keys >= floor, level by level.  `floor_excess` is what
-    // the equals of `floor` beyond its ties would add.
-    auto search = [&](auto measure, uint32_t floor, uint64_t floor_excess, auto target_of, uint64_t &above_all,
-                      uint64_t &target, uint64_t &in_bin) {
-        uint32_t prefix = 0;
-        above_all = 0;
-        target = 0;
-        for (int level = 0; level < LEVELS; ++level) {
-            const int shift = digit_shift(level);
-            const uint32_t dmask = level == 2 ? 1023u : 2047u;
-            const int pshift = level == 0 ? 0 : digit_shift(level - 1);
-            for (uint32_t b = threadIdx.x; b < BINS; b += THREADS) sh.hist[b] = 0;
+    // 2. kept so far: keys above key_f, and of those equal to it (count_f of them) the first `ties`
+    int key_f = first_alone ? top : LOWEST;
+    uint64_t ties = 1, count_f = first_alone ? 2 : 0;   // count_f 0: no filter so far, all are kept
+    const bool need_k = !first_alone && k != 0 && k < n_vocab, need_p = !first_alone && p < 1.f;
+    if (need_k || need_p) {
+        int floor = LOWEST;
+        bool found;
+        uint32_t bin_k = BINS;
+        uint64_t above, inside, target;
+        auto count_of = [&](int i) INLINE { return (uint64_t)sh.count[i]; };
+        auto target_k = [&](uint64_t) INLINE { return (uint64_t)k; };
+        auto clear_counts = [&]() INLINE {
+            for (int b = threadIdx.x; b < BINS; b += THREADS) sh.count[b] = 0;
             __syncthreads();
-            for (uint32_t j = threadIdx.x * VEC; j < n_vocab; j += SLAB) {
-                uint32_t kk[VEC];
-                row.keys(j, kk);
+        };
+        // Two rounds for a small k: k threads with a key >= f hold at least k such keys, so nothing below the
+        // k-th largest of the threads' own largest keys (or its bin's lowest key) can be kept.
+        for (int round = need_k && k <= THREADS / 2 ? 0 : 1;; ++round) {
+            if (need_p && round)
+                for (int b = threadIdx.x; b < BINS; b += THREADS) sh.mass[b] = 0;
+            clear_counts();
+            if (round == 0) {
+                if (mine >= LOWEST) atomicAdd(&sh.count[bin_of<T>(mine)], 1u);
+            } else {
+                row.each([&](uint32_t, const V &v) INLINE {
+                    if (!__any(v.max() >= floor)) return;
+                    int b[VEC];
+                    v.bins(b);
+                    bool more = false;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (kk[e] >= floor && (level == 0 || kk[e] >> pshift == prefix))
-                        atomicAdd((unsigned long long *)&sh.hist[(kk[e] >> shift) & dmask],
-                                  (unsigned long long)measure(kk[e]));
+                    for (int e = 0; e < VEC; ++e)
+                        if (v.at(e) >= floor) {
+                            atomicAdd(&sh.count[b[e]], 1u);
+                            more |= !bin_exact<T>(b[e]);
+                        }
+                    if (need_p && __any(more)) {
+#pragma unroll 1
+                        for (int e = 0; e < VEC; ++e) {
+                            const int key = v.pick(e), bin = bin_of<T>(key);
+                            if (key >= floor && !bin_exact<T>(bin))
+                                atomicAdd((unsigned long long *)&sh.mass[bin], (unsigned long long)weight(key));
+                        }
+                    }
+                });
             }
             __syncthreads();
-            if (threadIdx.x == 0 && floor_excess && (level == 0 || floor >> pshift == prefix))
-                sh.hist[(floor >> shift) & dmask] -= floor_excess;
-            __syncthreads();
-            if (level == 0) {
-                uint64_t all;
-                block_scan(sh.hist[2 * threadIdx.x] + sh.hist[2 * threadIdx.x + 1], sh, all);
-                target = target_of(all);
-                __syncthreads();
+            found = need_k && find_bin<BINS>(sh, count_of, target_k, bin_k, above, inside, target);
+            if (round) break;
+            if (found) {
+                int hi;
+                bin_range<T>((int)bin_k, floor, hi);
+                floor = floor < LOWEST ? LOWEST : floor;
             }
-            uint64_t above;
-            const uint32_t bin = find_bin(sh, target - above_all, above);
-            above_all += above;
-            in_bin = sh.hist[bin];
-            __syncthreads();
-            prefix = level == 0 ? bin : prefix << (level == 2 ? 10 : 11) | bin;
         }
-        // the digits below the last level are zeros, of a negative number ones
-        const int low = digit_shift(LEVELS - 1);
-        return low && !(prefix >> (31 - low)) ? prefix << low | ((1u << low) - 1u) : prefix << low;
-    };
+        if (need_p && TABLE) {
+#pragma unroll 1
+            for (int b = threadIdx.x; b < BINS - 1; b += THREADS)
+                if (bin_exact<T>(b) && sh.count[b]) {
+                    int lo, hi;
+                    bin_range<T>(b, lo, hi);
+                    sh.mass[b] = sh.count[b] * weight(lo);
+                }
+            __syncthreads();
+        }
+        // Stage 0 by counts, stage 1 by masses: the bin where the filter ends, then the exact key in it, by the
+        // running sum over the digits of hi - key, highest digit first (overwrites the counts).
+        const bool cut_k = found;
+        uint64_t excess = 0, mass_k = 0;   // mass of what lies beyond the ties of key_f; of the kept part of bin_k
+        int from = LOWEST;
+        for (int stage = cut_k ? 0 : 1; stage < (need_p ? 2 : 1); ++stage) {
+            uint32_t bin = bin_k;
+            if (stage) {
+                find_bin<BINS>(sh, [&](int i) INLINE {
+                    return !cut_k || i < (int)bin_k ? sh.mass[i] : i == (int)bin_k ? mass_k : 0ull;
+                }, [&](uint64_t all) INLINE {
+                    const double t = __builtin_ceil((double)p * (double)all);
+                    const uint64_t q = t > 1.0 ? (uint64_t)t : 1ull;
+                    return q < all ? q : all;
+                }, bin, above, inside, target);
+            }
+            int lo, hi;
+            bin_range<T>((int)bin, lo, hi);
+            uint64_t left = target - above;   // to be reached inside the bin
+            const int key_k = key_f;
+            const bool last = stage && cut_k && bin == bin_k;
+            if (last && from < key_k) from = key_k;
+            key_f = lo;
+            if (!bin_exact<T>((int)bin)) {
+                const int bits = 32 - __builtin_clz((uint32_t)(hi - lo));
+                int shift = (bits + DIGIT - 1) / DIGIT * DIGIT;
+                uint32_t prefix = 0;
+                while (shift > 0) {
+                    const int up = shift;
+                    shift -= DIGIT;
+                    for (int b = threadIdx.x; b < DIGITS; b += THREADS) sh.digit[b] = 0;
+                    __syncthreads();
+                    auto add = [&](int key, uint64_t amount) INLINE {
+                        const uint32_t d = (uint32_t)(hi - key);
+                        if ((up < 32 ? d >> up : 0u) == prefix)
+                            atomicAdd((unsigned long long *)&sh.digit[(d >> shift) & (DIGITS - 1)], (unsigned long long)amount);
+                    };
+                    row.each([&](uint32_t, const V &v) INLINE {
+                        if (!__any(v.max() >= lo)) return;
+#pragma unroll 1
+                        for (int e = 0; e < VEC; ++e) {
+                            const int key = v.pick(e);
+                            if (key >= lo && key <= hi && key >= from) add(key, stage ? weight(key) : 1ull);
+                        }
+                    });
+                    if (threadIdx.x == 0 && last && excess) add(key_k, 0ull - excess);
+                    __syncthreads();
+                    uint32_t digit;
+                    uint64_t a, t;
+                    find_bin<DIGITS>(sh, [&](int i) INLINE { return sh.digit[i]; }, [&](uint64_t) INLINE { return left; }, digit, a,
+                                     inside, t);
+                    left -= a;
+                    prefix = prefix << DIGIT | digit;
+                }
+                key_f = hi - (int)prefix;
+            }
+            if (stage == 0) {
+                ties = left;
+                count_f = inside;
+                if (need_p) {   // what its bin holds below key_f, and of its equals beyond the ties, is no longer kept
+                    const uint64_t w = weight(key_f);
+                    excess = (count_f - ties) * w;
+                    mass_k = ties * w;
+                    if (!bin_exact<T>((int)bin)) {
+                        uint64_t part = 0;
+                        row.each([&](uint32_t, const V &v) INLINE {
+                            if (!__any(v.max() >= key_f)) return;
+#pragma unroll 1
+                            for (int e = 0; e < VEC; ++e) {
+                                const int key = v.pick(e);
+                                if (key >= key_f && key <= hi) part += weight(key);
+                            }
+                        });
+                        block_before(part, sh, mass_k);
+                        mass_k -= excess;
+                    }
+                }
+            } else {
+                const uint64_t w = weight(key_f), need = (left + w - 1) / w;
+                if (last && key_f == key_k) {
+                    ties = need < ties ? need : ties;
+                } else {
+                    count_f = inside / w;
+                    ties = need;
+                }
+            }
+        }
+    }
+    uint32_t id = NO_ID;   // the last index whose key may equal key_f
+    uint64_t total;
+    int key_at;
+    if (ties < count_f)
+        id = locate<WAVES>(row, sh, [&](const V &v, uint32_t) INLINE {
+            uint64_t n = 0;
+            if (__any(v.max() >= key_f)) {
+                uint32_t c = 0;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) c += v.at(e) == key_f;
+                n = c;
+            }
+            return n;
+        }, [&](const V &v, uint32_t, int e) INLINE { return (uint64_t)(v.pick(e) == key_f); },
+        [&](uint64_t) INLINE { return ties - 1; }, total, key_at);
+    if (first_alone) {
+        if (threadIdx.x == 0) {
+            out_ids[r] = id;
+            if (out_logprobs) out_logprobs[r] = 0.f;
+        }
+        return;
+    }
 
-    uint64_t above, target, in_bin;
-    uint64_t excess = 0;
-    if (k < valid) {
-        key_f = search([](uint32_t) { return 1ull; }, 1u, 0, [&](uint64_t) { return (uint64_t)k; }, above, target, in_bin);
-        ties = k - (uint32_t)above;
-        count_f = (uint32_t)in_bin;
-        excess = (uint64_t)(count_f - ties) * wt.of(key_f);
-    }
-    const float p = top_p ? top_p[r] : 1.f;
-    if (p < 1.f) {
-        const uint32_t key_k = key_f;
-        const uint32_t key = search([&](uint32_t kk) { return wt.of(kk); }, key_k, excess, [&](uint64_t all) {
-            const double t = __builtin_ceil((double)p * (double)all);
-            const uint64_t u = t > 1.0 ? (uint64_t)t : 1ull;
-            return u < all ? u : all;
-        }, above, target, in_bin);
-        const uint64_t w = wt.of(key);
-        const uint32_t need = (uint32_t)((target - above + w - 1) / w);
-        if (key != key_k || count_f == 0) {
-            count_f = (uint32_t)(in_bin / w);
-            ties = need;
-        } else {
-            ties = need < ties ? need : ties;
-        }
-        key_f = key;
-    }
-    uint32_t cut = NO_ID;   // the last index whose key may equal key_f
-    uint32_t dummy;
-    if (ties < count_f) {
-        uint64_t t;
-        cut = locate(row, sh, [&](uint32_t kk, uint32_t) { return (uint64_t)(kk == key_f); },
-                     [&](uint64_t) { return (uint64_t)ties - 1; }, t, dummy);
-    }
-    const float mp = min_p ? min_p[r] : 0.f;
+    // 3. the draw
+    const uint32_t cut = id;
     const uint64_t one = wt.one();
     const uint64_t w_min = mp >= 1.f ? one : mp > 0.f ? (uint64_t)__builtin_ceil((double)mp * (double)one) : 0;
-    const float u_in = uniform[r];
     const double u = u_in > 0.f ? (double)fminf(u_in, 0x1.fffffep-1f) : 0.0;
-    uint32_t key_at;
-    const uint32_t id = locate(row, sh, [&](uint32_t kk, uint32_t j) {
-        if (kk < key_f || (kk == key_f && j > cut)) return (uint64_t)0;
-        const uint64_t w = wt.of(kk);
-        return w >= w_min ? w : (uint64_t)0;
-    }, [&](uint64_t all) { return (uint64_t)(u * (double)all); }, total, key_at);
+    if (TABLE) {   // the weights of the kept bins, so that no element needs its own exponential
+        __syncthreads();
+#pragma unroll 1
+        for (int b = threadIdx.x; b < BINS - 1; b += THREADS) {
+            int lo, hi;
+            bin_range<T>(b, lo, hi);
+            if (bin_exact<T>(b) && lo <= top) {
+                const uint64_t w = lo >= key_f ? weight(lo) : 0;
+                sh.mass[b] = w >= w_min ? w : 0;
+            }
+        }
+        __syncthreads();
+    }
+    auto kept = [&](int key, uint32_t j) INLINE { return key > key_f || (key == key_f && j <= cut); };
+    auto element = [&](const V &v, uint32_t j, int e) INLINE {
+        const int key = v.pick(e);
+        const uint64_t w = weight(key);
+        return kept(key, j + e) && w >= w_min ? w : 0ull;
+    };
+    id = locate<WAVES>(row, sh, [&](const V &v, uint32_t j) INLINE {
+        uint64_t sum = 0;
+        if (!__any(v.max() >= key_f)) return sum;
+        bool each = !TABLE;
+        if (TABLE) {
+            int b[VEC];
+            v.bins(b);
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const bool in = kept(v.at(e), j + e);
+                odd |= in && !bin_exact<T>(b[e]);
+                if (in) sum += sh.mass[b[e]];
+            }
+            each = __any(odd);
+            if (each) sum = 0;
+        }
+        if (each) {
+#pragma unroll 1
+            for (int e = 0; e < VEC; ++e) sum += element(v, j, e);
+        }
+        return sum;
+    }, element, [&](uint64_t all) INLINE { return (uint64_t)(u * (double)all); }, total, key_at);
     if (threadIdx.x == 0) {
         out_ids[r] = id;
-        if (out_logprobs) out_logprobs[r] = (float)log((double)wt.of(key_at) / (double)total);
+        if (out_logprobs) out_logprobs[r] = (float)log((double)weight(key_at) / (double)total);
     }
 }
 
@@ -395,8 +772,16 @@ extern "C" int toktier_sample(const void *logits, int type, uint32_t n_rows, uin
     const double magic = weight_magic(n_vocab);
     with_type(type, [&](auto t) {
         using T = decltype(t);
-        k_sample<T><<<n_rows, THREADS, 0, (hipStream_t)stream>>>((const T *)logits, n_vocab, stride, mask, mask_stride, temperature, top_k,
-                                                                 top_p, min_p, uniform, out_ids, out_logprobs, magic);
+        auto launch = [&](auto waves, auto nv) {
+            k_sample<T, decltype(waves)::value, decltype(nv)::value><<<n_rows, decltype(waves)::value * 64, 0, (hipStream_t)stream>>>(
+                (const T *)logits, n_vocab, stride, mask, mask_stride, temperature, top_k, top_p, min_p, uniform, out_ids, out_logprobs,
+                magic);
+        };
+        constexpr bool F32 = sizeof(T) == 4;
+        const uint32_t nv = (n_vocab + 1024 * VEC - 1) / (1024 * VEC);
+        if (n_vocab <= 256 * VEC * 4) launch(std::integral_constant<int, 4>{}, std::integral_constant<int, F32 ? 0 : 4>{});
+        else if (!F32 && nv <= 5) launch(std::integral_constant<int, 16>{}, std::integral_constant<int, F32 ? 0 : 5>{});
+        else launch(std::integral_constant<int, 16>{}, std::integral_constant<int, 0>{});
     });
     return hip_status(hipGetLastError());
 }
