@@ -44,16 +44,21 @@ __global__ __launch_bounds__(256) void k_embed(const TI *__restrict__ table, uin
 // gradient: tokens sorted by ID (stable, so equal IDs keep the token order), then one sum per run of
 // equal IDs.
 //
-// Sort: least-significant-digit radix sort in one or two passes of up to 11 bits.  Each pass is a
-// histogram per block and a stable scatter: a wavefront owns a contiguous part of its block, so the rank
-// of an element is (block base + counts of the block's earlier wavefronts + the wavefront's own count so
-// far + equal digits in lower lanes, from one ballot per digit bit).
+// Sort: least-significant-digit radix sort in one or two passes of up to 11 bits.  A wavefront owns a
+// contiguous part of its block, so the rank of an element is (places of lower digits and earlier blocks +
+// counts of the block's earlier wavefronts + the wavefront's own count so far + equal digits in lower lanes,
+// from one ballot per digit bit).  Up to SORT_ONE tokens one block does every pass in one launch; more take a
+// histogram launch and a scatter launch per pass.
+//
+// The launches of the sort leave most of the chip idle, so where rows of absent IDs have to become zeros and
+// most of the rows are absent, the zeros are written by further blocks of these launches.
 constexpr int SORT_WAVES = 8, SORT_THREADS = SORT_WAVES * 64;
-constexpr uint32_t SORT_MAX_BLOCKS = 128;
+constexpr int R_MANY = 8, R_ONE = 16;   // elements per thread
+constexpr uint32_t SORT_ONE = SORT_THREADS * R_ONE;
 constexpr uint32_t MAX_BINS = 2048;
 
 struct SortPlan {
-    uint32_t bits, passes, dbits, bins, rounds, blocks;
+    uint32_t bits, passes, dbits, bins, groups, blocks;   // a block sorts `groups` groups of 512 x R_MANY elements
 };
 
 SortPlan sort_plan(uint64_t n_tokens, uint32_t n_vocab)
@@ -63,30 +68,176 @@ SortPlan sort_plan(uint64_t n_tokens, uint32_t n_vocab)
     p.passes = p.bits <= 11 ? 1 : 2;
     p.dbits = (p.bits + p.passes - 1) / p.passes;
     p.bins = 1u << p.dbits;
-    const uint64_t per = (uint64_t)SORT_THREADS * SORT_MAX_BLOCKS;
-    p.rounds = (uint32_t)((n_tokens + per - 1) / per);
-    if (p.rounds < 8) p.rounds = 8;
-    p.blocks = (uint32_t)((n_tokens + (uint64_t)SORT_THREADS * p.rounds - 1) / ((uint64_t)SORT_THREADS * p.rounds));
+    // every block reads all blocks' histograms, so there are at most 256 of them
+    const uint64_t group = SORT_THREADS * R_MANY;
+    p.groups = (uint32_t)((n_tokens + group * 256 - 1) / (group * 256));
+    if (p.groups < 1) p.groups = 1;
+    p.blocks = (uint32_t)((n_tokens + group * p.groups - 1) / (group * p.groups));
     return p;
 }
 
-__device__ __forceinline__ uint32_t sort_key(const uint32_t *keys, bool first, uint32_t i, uint32_t n_vocab)
+// Rows of zeros: `rows` rows of row_bytes (a multiple of 2) from p, stride bytes apart, none of them past `end`.
+struct Zeros {
+    uint8_t *p;
+    uint64_t row_bytes, stride, end;
+    uint32_t rows, per_block, from;   // from: the launch's first row
+};
+
+__device__ __forceinline__ void zero_block(const Zeros &z, uint32_t block)
 {
-    const uint32_t k = keys[i];
-    return first ? min(k, n_vocab) : k;
+    const uint64_t r0 = z.from + (uint64_t)block * z.per_block;
+    for (uint32_t q = 0; q < z.per_block && r0 + q < z.rows; ++q) {
+        const uint64_t at = (r0 + q) * z.stride, left = z.end - at;
+        const uint64_t n = z.row_bytes < left ? z.row_bytes : left;
+        uint8_t *row = z.p + at;
+        for (uint64_t c = threadIdx.x * 16ull; c < n; c += blockDim.x * 16ull) {
+            if (c + 16 <= n) {
+                *(u32x4_row *)(row + c) = u32x4{0, 0, 0, 0};
+            } else {
+                for (uint64_t d = c; d < n; d += 2) *(uint16_t *)(row + d) = 0;
+            }
+        }
+    }
 }
 
-__global__ __launch_bounds__(SORT_THREADS) void k_sort_hist(const uint32_t *__restrict__ keys, int first, uint32_t n,
-                                                            uint32_t n_vocab, uint32_t shift, uint32_t bins,
-                                                            uint32_t rounds, uint32_t *__restrict__ hist)
+struct SortLds {
+    uint32_t cnt[SORT_WAVES][MAX_BINS];   // per wavefront: counts, then next output places
+    uint32_t wsum[SORT_WAVES];
+};
+
+// One pass over this block's elements [base, base + groups * 512 * R) of n.  hist: the counts of every block
+// ([blocks][bins]), or NULL where this block is the only one.
+template <int R>
+__device__ __forceinline__ void sort_pass(SortLds &sh, const uint32_t *keys, const uint32_t *pos, bool first, uint32_t n,
+                                          uint32_t n_vocab, uint32_t shift, uint32_t dbits, uint32_t groups, uint32_t block,
+                                          uint32_t blocks, const uint32_t *hist, uint32_t *keys_out, uint32_t *pos_out)
+{
+    const uint32_t bins = 1u << dbits, tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+    const uint64_t base = ((uint64_t)block * SORT_WAVES + wave) * (64 * R) * groups + lane;
+    uint32_t key[R];
+    auto load = [&](uint32_t g) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint64_t i = base + ((uint64_t)g * R + r) * 64;
+            key[r] = i < n ? keys[i] : 0xFFFFFFFFu;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) key[r] = min(key[r], n_vocab);   // an ID without a row; also what lies past the end
+    };
+    load(0);
+    for (uint32_t b = lane * 4; b < bins; b += 256) *(u32x4 *)&sh.cnt[wave][b] = u32x4{0, 0, 0, 0};
+    __syncthreads();
+    for (uint32_t g = 0;;) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (base + ((uint64_t)g * R + r) * 64 < n) atomicAdd(&sh.cnt[wave][(key[r] >> shift) & (bins - 1)], 1u);
+        if (++g == groups) break;
+        load(g);
+    }
+    __syncthreads();
+    // first place of every bin in this block: all elements of lower bins, and of this bin in earlier blocks and
+    // wavefronts.  A thread owns four consecutive bins (`bins` is a multiple of 4).
+    const uint32_t b0 = tid * 4;
+    u32x4 all = 0, before = 0, sum;
+    if (b0 < bins) {
+        if (hist) {
+#pragma unroll 8
+            for (uint32_t k = 0; k < blocks; ++k) {
+                const u32x4 v = *(const u32x4 *)&hist[(uint64_t)k * bins + b0];
+                all += v;
+                if (k < block) before += v;
+            }
+        } else {
+#pragma unroll
+            for (int w = 0; w < SORT_WAVES; ++w) all += *(u32x4 *)&sh.cnt[w][b0];
+        }
+    }
+    sum[0] = all[0];
+    sum[1] = sum[0] + all[1];
+    sum[2] = sum[1] + all[2];
+    sum[3] = sum[2] + all[3];
+    const uint32_t incl = wave_incl_sum(sum[3]);
+    if (lane == 63) sh.wsum[wave] = incl;
+    __syncthreads();
+    uint32_t at = incl - sum[3];
+#pragma unroll
+    for (uint32_t w = 0; w < SORT_WAVES; ++w) at += w < wave ? sh.wsum[w] : 0;
+    if (b0 < bins) {
+        u32x4 place = before + at;
+        place[1] += sum[0];
+        place[2] += sum[1];
+        place[3] += sum[2];
+#pragma unroll
+        for (int w = 0; w < SORT_WAVES; ++w) {
+            const u32x4 c = *(u32x4 *)&sh.cnt[w][b0];
+            *(u32x4 *)&sh.cnt[w][b0] = place;
+            place += c;
+        }
+    }
+    __syncthreads();
+    for (uint32_t g = 0; g < groups; ++g) {
+        if (groups > 1) load(g);
+        uint32_t from[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint64_t i = base + ((uint64_t)g * R + r) * 64;
+            from[r] = first || i >= n ? (uint32_t)i : pos[i];
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = base + ((uint64_t)g * R + r) * 64 < n;
+            const uint32_t d = (key[r] >> shift) & (bins - 1);
+            uint64_t same = __ballot(in);
+            for (uint32_t b = 0; b < dbits; ++b) {
+                const uint64_t one = __ballot((d >> b) & 1u);
+                same &= (d >> b) & 1u ? one : ~one;
+            }
+            const uint32_t rank = __popcll(same & ((1ull << lane) - 1ull));
+            const uint32_t place = sh.cnt[wave][d];
+            __builtin_amdgcn_wave_barrier();
+            if (in) {
+                if (rank == 0) sh.cnt[wave][d] = place + __popcll(same);
+                keys_out[place + rank] = key[r];
+                pos_out[place + rank] = from[r];
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+}
+
+__global__ __launch_bounds__(SORT_THREADS) void k_sort_one(const uint32_t *__restrict__ ids, uint32_t n, uint32_t n_vocab,
+                                                           uint32_t passes, uint32_t dbits, uint32_t *keys0, uint32_t *pos0,
+                                                           uint32_t *keys1, uint32_t *pos1, Zeros z)
+{
+    __shared__ __align__(16) SortLds sh;
+    if (blockIdx.x > 0) return zero_block(z, blockIdx.x - 1);
+    sort_pass<R_ONE>(sh, ids, nullptr, true, n, n_vocab, 0, dbits, 1, 0, 1, nullptr, keys0, pos0);
+    if (passes == 1) return;
+    __threadfence_block();
+    __syncthreads();
+    sort_pass<R_ONE>(sh, keys0, pos0, false, n, n_vocab, dbits, dbits, 1, 0, 1, nullptr, keys1, pos1);
+}
+
+__global__ __launch_bounds__(SORT_THREADS) void k_sort_hist(const uint32_t *__restrict__ keys, uint32_t n, uint32_t n_vocab,
+                                                            uint32_t shift, uint32_t bins, uint32_t groups, uint32_t blocks,
+                                                            uint32_t *__restrict__ hist, Zeros z)
 {
     __shared__ uint32_t h[MAX_BINS];
+    if (blockIdx.x >= blocks) return zero_block(z, blockIdx.x - blocks);
     for (uint32_t b = threadIdx.x; b < bins; b += SORT_THREADS) h[b] = 0;
     __syncthreads();
-    const uint64_t base = (uint64_t)blockIdx.x * (SORT_THREADS * rounds);
-    for (uint32_t r = 0; r < rounds; ++r) {
-        const uint64_t i = base + (uint64_t)r * SORT_THREADS + threadIdx.x;
-        if (i < n) atomicAdd(&h[(sort_key(keys, first, (uint32_t)i, n_vocab) >> shift) & (bins - 1)], 1u);
+    const uint64_t base = (uint64_t)blockIdx.x * (SORT_THREADS * R_MANY) * groups + threadIdx.x;
+    for (uint32_t g = 0; g < groups; ++g) {
+        uint32_t key[R_MANY];
+#pragma unroll
+        for (int r = 0; r < R_MANY; ++r) {
+            const uint64_t i = base + ((uint64_t)g * R_MANY + r) * SORT_THREADS;
+            key[r] = i < n ? keys[i] : 0;
+        }
+#pragma unroll
+        for (int r = 0; r < R_MANY; ++r)
+            if (base + ((uint64_t)g * R_MANY + r) * SORT_THREADS < n)
+                atomicAdd(&h[(min(key[r], n_vocab) >> shift) & (bins - 1)], 1u);
     }
     __syncthreads();
     for (uint32_t b = threadIdx.x; b < bins; b += SORT_THREADS) hist[(uint64_t)blockIdx.x * bins + b] = h[b];
@@ -95,85 +246,22 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_hist(const uint32_t *__re
 __global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(const uint32_t *__restrict__ keys,
                                                                const uint32_t *__restrict__ pos, int first, uint32_t n,
                                                                uint32_t n_vocab, uint32_t shift, uint32_t dbits,
-                                                               uint32_t rounds, const uint32_t *__restrict__ hist,
+                                                               uint32_t groups, uint32_t blocks,
+                                                               const uint32_t *__restrict__ hist,
                                                                uint32_t *__restrict__ keys_out,
-                                                               uint32_t *__restrict__ pos_out)
+                                                               uint32_t *__restrict__ pos_out, Zeros z)
 {
-    __shared__ uint32_t cnt[SORT_WAVES][MAX_BINS];   // per wavefront: counts, then next output places
-    __shared__ uint32_t wsum[SORT_WAVES];
-    const uint32_t bins = 1u << dbits, tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
-    for (uint32_t b = lane; b < bins; b += 64) cnt[wave][b] = 0;
-    __syncthreads();
-    const uint64_t base = (uint64_t)blockIdx.x * (SORT_THREADS * rounds) + (uint64_t)wave * 64 * rounds;
-    for (uint32_t r = 0; r < rounds; ++r) {
-        const uint64_t i = base + r * 64 + lane;
-        if (i < n) atomicAdd(&cnt[wave][(sort_key(keys, first, (uint32_t)i, n_vocab) >> shift) & (bins - 1)], 1u);
-    }
-    __syncthreads();
-    // first place of every bin in this block: all elements of lower bins, and of this bin in earlier blocks.
-    // A thread owns up to four consecutive bins.
-    uint32_t tot[MAX_BINS / SORT_THREADS], before[MAX_BINS / SORT_THREADS], sum = 0;
-    constexpr uint32_t PER = MAX_BINS / SORT_THREADS;
-#pragma unroll
-    for (uint32_t q = 0; q < PER; ++q) {
-        const uint32_t b = tid * PER + q;
-        uint32_t all = 0, bef = 0;
-        if (b < bins)
-            for (uint32_t k = 0; k < gridDim.x; ++k) {
-                const uint32_t v = hist[(uint64_t)k * bins + b];
-                all += v;
-                if (k < blockIdx.x) bef += v;
-            }
-        tot[q] = all;
-        before[q] = bef;
-        sum += all;
-    }
-    const uint32_t incl = wave_incl_sum(sum);
-    if (lane == 63) wsum[wave] = incl;
-    __syncthreads();
-    uint32_t at = incl - sum;
-    for (uint32_t w = 0; w < wave; ++w) at += wsum[w];
-#pragma unroll
-    for (uint32_t q = 0; q < PER; ++q) {
-        const uint32_t b = tid * PER + q;
-        if (b < bins) {
-            uint32_t place = at + before[q];
-            for (int w = 0; w < SORT_WAVES; ++w) {
-                const uint32_t c = cnt[w][b];
-                cnt[w][b] = place;
-                place += c;
-            }
-        }
-        at += tot[q];
-    }
-    __syncthreads();
-    for (uint32_t r = 0; r < rounds; ++r) {
-        const uint64_t i = base + r * 64 + lane;
-        const bool in = i < n;
-        const uint32_t key = in ? sort_key(keys, first, (uint32_t)i, n_vocab) : 0;
-        const uint32_t d = (key >> shift) & (bins - 1);
-        uint64_t same = __ballot(in);
-        for (uint32_t b = 0; b < dbits; ++b) {
-            const uint64_t one = __ballot((d >> b) & 1u);
-            same &= (d >> b) & 1u ? one : ~one;
-        }
-        if (in) {
-            const uint32_t rank = __popcll(same & ((1ull << lane) - 1ull)), count = __popcll(same);
-            const uint32_t place = cnt[wave][d];
-            __builtin_amdgcn_wave_barrier();
-            if (rank == 0) cnt[wave][d] = place + count;
-            keys_out[place + rank] = key;
-            pos_out[place + rank] = first ? (uint32_t)i : pos[i];
-        }
-        __builtin_amdgcn_wave_barrier();
-    }
+    __shared__ __align__(16) SortLds sh;
+    if (blockIdx.x >= blocks) return zero_block(z, blockIdx.x - blocks);
+    sort_pass<R_MANY>(sh, keys, pos, first, n, n_vocab, shift, dbits, groups, blockIdx.x, blocks, hist, keys_out, pos_out);
 }
 
-// Sums.  The sorted tokens are cut into chunks of C; a wavefront takes one chunk and 512 columns and adds
-// up each run of equal IDs in registers.  A run inside a chunk is a finished row; one that crosses a
-// chunk's border leaves a partial sum (slot 0: the run entered from the chunk before, slot 1: it starts
-// here and goes on), joined in chunk order by k_embed_join.
+// Sums.  The sorted tokens are cut into chunks; a wavefront takes one chunk and 512 columns and adds up
+// each run of equal IDs in registers, eight rows in flight.  A run inside a chunk is a finished row; one
+// that crosses a chunk's border leaves a partial sum (slot 0: the run entered from the chunk before, slot 1:
+// it starts here and goes on), joined in chunk order by k_embed_join.
 constexpr uint32_t COLS = 64 * VEC;
+constexpr int ROWS = 8;
 
 template <class TT>
 __device__ __forceinline__ void put_row(TT *__restrict__ row, uint32_t n, float scale, bool accumulate,
@@ -191,7 +279,7 @@ __device__ __forceinline__ void put_row(TT *__restrict__ row, uint32_t n, float 
     store_part(row, n, x);
 }
 
-constexpr int ZROWS = 16;   // table rows that a wavefront looks after when absent IDs get zeros
+constexpr int ZROWS = 16;   // table rows that a wavefront looks after when absent IDs get zeros here
 
 template <class TG, class TT>
 __global__ __launch_bounds__(256) void k_embed_sum(const TG *__restrict__ grad, uint64_t gstride,
@@ -199,47 +287,44 @@ __global__ __launch_bounds__(256) void k_embed_sum(const TG *__restrict__ grad, 
                                                    uint32_t n, uint32_t n_vocab, uint32_t dim, uint32_t chunk,
                                                    uint32_t n_chunks, uint32_t ncb, float scale, int accumulate,
                                                    TT *__restrict__ table, uint64_t tstride, float *__restrict__ part,
-                                                   uint32_t dpad)
+                                                   uint32_t dpad, uint32_t absent_units)
 {
     const uint32_t lane = threadIdx.x & 63u;
-    const uint64_t unit = __builtin_amdgcn_readfirstlane((uint32_t)(blockIdx.x * 4u + (threadIdx.x >> 6)));
-    if (unit < (uint64_t)n_chunks * ncb) {
-        const uint32_t ch = (uint32_t)(unit / ncb), c = (uint32_t)(unit % ncb) * COLS + lane * VEC;
+    const uint32_t unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4u + (threadIdx.x >> 6)), sums = n_chunks * ncb;
+    if (unit < sums) {
+        const uint32_t ch = unit / ncb, c = unit % ncb * COLS + lane * VEC;
         const uint32_t i0 = ch * chunk, len = min(chunk, n - i0);
         const uint32_t my = min(lane, len - 1);
         const uint32_t key_l = keys[i0 + my], pos_l = pos[i0 + my];
+        const uint32_t prev = i0 > 0 ? keys[i0 - 1] : 0xFFFFFFFFu, next_ch = i0 + len < n ? keys[i0 + len] : 0xFFFFFFFFu;
         const uint32_t live = __popcll(__ballot(lane < len && key_l < n_vocab));   // those without a row sort last
         if (live == 0) return;
-        const bool enters = i0 > 0 && keys[i0 - 1] == (uint32_t)__builtin_amdgcn_readlane((int)key_l, 0);
-        const bool leaves = i0 + len < n && keys[i0 + len] == (uint32_t)__builtin_amdgcn_readlane((int)key_l, (int)len - 1);
+        const bool enters = prev == (uint32_t)__builtin_amdgcn_readlane((int)key_l, 0);
+        const bool leaves = next_ch == (uint32_t)__builtin_amdgcn_readlane((int)key_l, (int)len - 1);
         const uint32_t m = c < dim ? dim - c : 0;
         float acc[VEC] = {};
         uint32_t run0 = 0;
-        for (uint32_t i = 0; i < live; i += 4) {
-            float x[4][VEC];
+        for (uint32_t i = 0; i < live; i += ROWS) {
+            Vec<TG> x[ROWS];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < ROWS; ++u) {
                 const uint32_t p = (uint32_t)__builtin_amdgcn_readlane((int)pos_l, (int)min(i + u, live - 1));
-                if (m) load_part(grad + p * gstride + c, m, 0.f, x[u]);
+                if (i + u < live && m) x[u] = load_some(grad + p * gstride + c, m);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < ROWS; ++u) {
                 const uint32_t j = i + u;
                 if (j >= live) break;
                 const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)key_l, (int)j);
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) acc[k] += x[u][k];
+                for (int k = 0; k < VEC; ++k) acc[k] += vec_at(x[u], k);
                 const bool last = j + 1 == len;
                 const uint32_t next = (uint32_t)__builtin_amdgcn_readlane((int)key_l, (int)min(j + 1, len - 1));
                 if (last || next != key) {
-                    const bool from = run0 == 0 && enters, on = last && leaves;
+                    const bool in = run0 == 0 && enters, on = last && leaves;
                     if (m) {
-                        if (from || on) {
-                            float *q = part + ((uint64_t)ch * 2 + (from ? 0 : 1)) * dpad + c;
-                            store_vec(q, acc);
-                        } else {
-                            put_row(table + key * tstride + c, m, scale, accumulate, acc);
-                        }
+                        if (in || on) store_vec(part + ((uint64_t)ch * 2 + (in ? 0 : 1)) * dpad + c, acc);
+                        else put_row(table + key * tstride + c, m, scale, accumulate, acc);
                     }
 #pragma unroll
                     for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
@@ -249,14 +334,14 @@ __global__ __launch_bounds__(256) void k_embed_sum(const TG *__restrict__ grad, 
         }
         return;
     }
-    if (accumulate) return;
-    // rows of absent IDs: a lane looks its row up in the sorted keys, then the wavefront writes zeros
-    const uint64_t r0 = (unit - (uint64_t)n_chunks * ncb) * ZROWS;
-    if (r0 >= n_vocab) return;
+    // rows of absent IDs (launched where they are not zeros already): a lane looks its row up in the sorted
+    // keys, then the wavefront writes zeros
+    if (unit - sums >= absent_units) return;
+    const uint64_t r0 = (uint64_t)(unit - sums) * ZROWS;
     const uint32_t row = (uint32_t)r0 + (lane % ZROWS);
     uint32_t lo = 0, hi = n;
     while (lo < hi) {
-        const uint32_t mid = (lo + hi) >> 1;
+        const uint32_t mid = lo + (hi - lo) / 2;
         if (keys[mid] < row) lo = mid + 1;
         else hi = mid;
     }
@@ -277,40 +362,43 @@ __global__ __launch_bounds__(256) void k_embed_join(const uint32_t *__restrict__
                                                     uint64_t tstride, const float *__restrict__ part, uint32_t dpad)
 {
     const uint32_t lane = threadIdx.x & 63u;
-    const uint64_t unit = __builtin_amdgcn_readfirstlane((uint32_t)(blockIdx.x * 4u + (threadIdx.x >> 6)));
-    if (unit >= (uint64_t)n_chunks * ncb) return;
-    const uint32_t ch = (uint32_t)(unit / ncb), c = (uint32_t)(unit % ncb) * COLS + lane * VEC;
+    const uint32_t unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4u + (threadIdx.x >> 6));
+    if (unit >= n_chunks * ncb) return;
+    const uint32_t ch = unit / ncb, c = unit % ncb * COLS + lane * VEC;
     const uint32_t i0 = ch * chunk, end = i0 + chunk;
     if (end >= n) return;
-    const uint32_t key = keys[end - 1];
-    if (key >= n_vocab || keys[end] != key) return;                   // no run leaves this chunk
-    if (keys[i0] == key && i0 > 0 && keys[i0 - 1] == key) return;     // it started in an earlier chunk
-    if (c >= dim) return;
-    float acc[VEC];
-    load_part(part + ((uint64_t)ch * 2 + 1) * dpad + c, VEC, 0.f, acc);
-    for (uint32_t h = ch + 1; h < n_chunks && keys[h * chunk] == key; ++h) {
-        float x[VEC];
-        load_part(part + (uint64_t)h * 2 * dpad + c, VEC, 0.f, x);
+    const uint32_t prev = i0 > 0 ? keys[i0 - 1] : 0xFFFFFFFFu, head = keys[i0], key = keys[end - 1], next = keys[end];
+    if (key >= n_vocab || next != key) return;       // no run leaves this chunk
+    if (head == key && prev == key) return;          // it started in an earlier chunk
+    float acc[VEC] = {};
+    if (c < dim) load_part(part + ((uint64_t)ch * 2 + 1) * dpad + c, VEC, 0.f, acc);
+    // the chunks that the run enters: 64 heads are compared at once, and eight partial sums are in flight
+    for (uint32_t h0 = ch + 1; h0 < n_chunks; h0 += 64) {
+        const uint32_t h = h0 + lane;
+        const uint64_t same = __ballot(h < n_chunks && keys[(uint64_t)min(h, n_chunks - 1) * chunk] == key);
+        const uint32_t count = ~same ? (uint32_t)__builtin_ctzll(~same) : 64u;
+        if (c < dim)
+            for (uint32_t q = 0; q < count; q += ROWS) {
+                Vec<float> x[ROWS];
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) acc[k] += x[k];
+                for (int u = 0; u < ROWS; ++u)
+                    if (q + u < count) x[u] = load_vec(part + (uint64_t)(h0 + q + u) * 2 * dpad + c);
+#pragma unroll
+                for (int u = 0; u < ROWS; ++u)
+                    if (q + u < count)
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k) acc[k] += vec_at(x[u], k);
+            }
+        if (count < 64) break;
     }
-    put_row(table + key * tstride + c, dim - c, scale, accumulate, acc);
+    if (c < dim) put_row(table + key * tstride + c, dim - c, scale, accumulate, acc);
 }
 
-template <class TT>
-__global__ __launch_bounds__(256) void k_zero_rows(TT *__restrict__ table, uint32_t n_vocab, uint32_t dim,
-                                                   uint64_t tstride)
-{
-    const float zero[VEC] = {};
-    for (uint32_t c = threadIdx.x * VEC; c < dim; c += 256 * VEC)
-        store_part(table + blockIdx.x * tstride + c, dim - c, zero);
-}
-
-constexpr uint32_t CHUNK = 64;
+__global__ __launch_bounds__(SORT_THREADS) void k_zero_rows(Zeros z) { zero_block(z, blockIdx.x); }
 
 struct BackwardLayout {
     SortPlan sort;
-    uint32_t n_chunks, ncb, dpad;
+    uint32_t chunk, n_chunks, ncb, dpad;
     uint64_t keys[2], pos[2], hist, part, total;
 };
 
@@ -318,9 +406,13 @@ BackwardLayout backward_layout(uint64_t n_tokens, uint32_t n_vocab, uint32_t dim
 {
     BackwardLayout L;
     L.sort = sort_plan(n_tokens, n_vocab);
-    L.n_chunks = (uint32_t)((n_tokens + CHUNK - 1) / CHUNK);
     L.ncb = (dim + COLS - 1) / COLS;
     L.dpad = (dim + VEC - 1) / VEC * VEC;
+    // tokens per chunk: 64 (fewest partial sums), fewer where that would leave the chip with under 4,096
+    // wavefronts, eight per CU and SIMD pair
+    L.chunk = 64;
+    while (L.chunk > 8 && n_tokens * L.ncb < 4096ull * L.chunk) L.chunk /= 2;
+    L.n_chunks = (uint32_t)((n_tokens + L.chunk - 1) / L.chunk);
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t o = at;
@@ -335,6 +427,24 @@ BackwardLayout backward_layout(uint64_t n_tokens, uint32_t n_vocab, uint32_t dim
     L.part = take(8ull * L.n_chunks * L.dpad);
     L.total = at < 256 ? 256 : at;
     return L;
+}
+
+// The rows of a table as zeros to write: whole where they are contiguous, cut into pieces of 64 KiB.
+Zeros zeros_of(void *table, uint32_t size, uint32_t n_vocab, uint32_t dim, uint64_t stride)
+{
+    Zeros z;
+    z.p = (uint8_t *)table;
+    z.row_bytes = (uint64_t)dim * size;
+    z.stride = stride * size;
+    z.end = z.stride * n_vocab;
+    z.rows = n_vocab;
+    if (z.row_bytes == z.stride) {
+        z.row_bytes = z.stride = 65536;
+        z.rows = (uint32_t)((z.end + 65535) / 65536);
+    }
+    z.per_block = z.row_bytes >= 65536 ? 1 : (uint32_t)(65536 / z.row_bytes);
+    z.from = 0;
+    return z;
 }
 
 bool sizes_ok(uint64_t n_tokens, uint32_t n_vocab, uint32_t dim)
@@ -401,12 +511,10 @@ extern "C" int toktier_embed_backward(const void *grad_out, int grad_type, uint6
         if (!apart(grad_table, tb, grad_out, gb) || !apart(grad_table, tb, ids, 4 * n_tokens)) return TOKTIER_E_INVALID_ARG;
     }
     hipStream_t s = (hipStream_t)stream;
+    Zeros z = zeros_of(grad_table, elem_size(table_type), n_vocab, dim, table_stride);
     if (n_tokens == 0) {
         if (accumulate) return TOKTIER_OK;
-        with_type(table_type, [&](auto tt_) {
-            using TT = decltype(tt_);
-            k_zero_rows<TT><<<n_vocab, 256, 0, s>>>((TT *)grad_table, n_vocab, dim, table_stride);
-        });
+        k_zero_rows<<<(z.rows + z.per_block - 1) / z.per_block, SORT_THREADS, 0, s>>>(z);
         return hip_status(hipGetLastError());
     }
     const BackwardLayout L = backward_layout(n_tokens, n_vocab, dim);
@@ -414,36 +522,58 @@ extern "C" int toktier_embed_backward(const void *grad_out, int grad_type, uint6
     if (!apart(workspace, L.total, grad_table, tb) || !apart(workspace, L.total, ids, 4 * n_tokens) ||
         !apart(workspace, L.total, grad_out, extent(grad_type, n_tokens, dim, grad_stride)))
         return TOKTIER_E_INVALID_ARG;
+    const uint64_t sums = (uint64_t)L.n_chunks * L.ncb;
+    if (sums > 0x7FFFFFFFull) return TOKTIER_E_INVALID_ARG;
     uint8_t *ws = (uint8_t *)workspace;
     const uint32_t n = (uint32_t)n_tokens;
-    uint32_t *hist = (uint32_t *)(ws + L.hist);
-    const uint32_t *keys = ids, *pos = nullptr;
-    for (uint32_t p = 0; p < L.sort.passes; ++p) {
-        const uint32_t shift = p * L.sort.dbits;
-        uint32_t *ko = (uint32_t *)(ws + L.keys[p]), *po = (uint32_t *)(ws + L.pos[p]);
-        k_sort_hist<<<L.sort.blocks, SORT_THREADS, 0, s>>>(keys, p == 0, n, n_vocab, shift, L.sort.bins, L.sort.rounds, hist);
-        k_sort_scatter<<<L.sort.blocks, SORT_THREADS, 0, s>>>(keys, pos, p == 0, n, n_vocab, shift, L.sort.dbits,
-                                                              L.sort.rounds, hist, ko, po);
-        keys = ko;
-        pos = po;
+    // fewer tokens than rows: all rows become zeros beside the sort, and those of present IDs are written
+    // again; else only the absent ones, after it
+    const bool early = !accumulate && n < n_vocab;
+    uint32_t *hist = (uint32_t *)(ws + L.hist), *keys[2], *pos[2];
+    for (int p = 0; p < 2; ++p) {
+        keys[p] = (uint32_t *)(ws + L.keys[p]);
+        pos[p] = (uint32_t *)(ws + L.pos[p]);
+    }
+    uint32_t zrows = z.rows;
+    auto zero_blocks = [&](uint32_t launch, uint32_t launches) {   // this launch's share of the zeros
+        if (!early) return 0u;
+        const uint32_t share = (zrows + launches - 1) / launches;
+        z.from = share * launch < zrows ? share * launch : zrows;
+        z.rows = share < zrows - z.from ? z.from + share : zrows;
+        return (z.rows - z.from + z.per_block - 1) / z.per_block;
+    };
+    const uint32_t last = L.sort.passes - 1;
+    if (n <= SORT_ONE) {
+        const uint32_t zb = zero_blocks(0, 1);
+        k_sort_one<<<1 + zb, SORT_THREADS, 0, s>>>(ids, n, n_vocab, L.sort.passes, L.sort.dbits, keys[0], pos[0], keys[1], pos[1], z);
+    } else {
+        for (uint32_t p = 0; p <= last; ++p) {
+            const uint32_t *ki = p ? keys[0] : ids, *pi = p ? pos[0] : nullptr, shift = p * L.sort.dbits, launches = 2 * L.sort.passes;
+            const uint32_t zh = zero_blocks(2 * p, launches);
+            k_sort_hist<<<L.sort.blocks + zh, SORT_THREADS, 0, s>>>(ki, n, n_vocab, shift, L.sort.bins, L.sort.groups, L.sort.blocks,
+                                                                    hist, z);
+            const uint32_t zs = zero_blocks(2 * p + 1, launches);
+            k_sort_scatter<<<L.sort.blocks + zs, SORT_THREADS, 0, s>>>(ki, pi, p == 0, n, n_vocab, shift, L.sort.dbits, L.sort.groups,
+                                                                       L.sort.blocks, hist, keys[p], pos[p], z);
+        }
     }
     float *part = (float *)(ws + L.part);
-    const uint64_t sums = (uint64_t)L.n_chunks * L.ncb, zeros = accumulate ? 0 : (n_vocab + ZROWS - 1) / ZROWS;
-    const uint64_t blocks = (sums + zeros + 3) / 4, jblocks = (sums + 3) / 4;
-    if (blocks > 0x3FFFFFFFull) return TOKTIER_E_INVALID_ARG;
+    const uint64_t absent = accumulate || early ? 0 : (n_vocab + ZROWS - 1) / ZROWS;
+    const uint32_t blocks = (uint32_t)((sums + absent + 3) / 4), jblocks = (uint32_t)((sums + 3) / 4);
     with_type(grad_type, [&](auto tg) {
         with_type(table_type, [&](auto tt_) {
             using TG = decltype(tg);
             using TT = decltype(tt_);
-            k_embed_sum<TG, TT><<<(uint32_t)blocks, 256, 0, s>>>((const TG *)grad_out, grad_stride, keys, pos, n, n_vocab, dim, CHUNK,
-                                                                 L.n_chunks, L.ncb, scale, accumulate, (TT *)grad_table,
-                                                                 table_stride, part, L.dpad);
+            k_embed_sum<TG, TT><<<blocks, 256, 0, s>>>((const TG *)grad_out, grad_stride, keys[last], pos[last], n, n_vocab, dim, L.chunk,
+                                                       L.n_chunks, L.ncb, scale, accumulate, (TT *)grad_table, table_stride, part, L.dpad,
+                                                       (uint32_t)absent);
         });
     });
-    with_type(table_type, [&](auto tt_) {
-        using TT = decltype(tt_);
-        k_embed_join<TT><<<(uint32_t)jblocks, 256, 0, s>>>(keys, n, n_vocab, dim, CHUNK, L.n_chunks, L.ncb, scale, accumulate,
-                                                           (TT *)grad_table, table_stride, part, L.dpad);
-    });
+    if (L.n_chunks > 1)
+        with_type(table_type, [&](auto tt_) {
+            using TT = decltype(tt_);
+            k_embed_join<TT><<<jblocks, 256, 0, s>>>(keys[last], n, n_vocab, dim, L.chunk, L.n_chunks, L.ncb, scale, accumulate,
+                                                     (TT *)grad_table, table_stride, part, L.dpad);
+        });
     return hip_status(hipGetLastError());
 }

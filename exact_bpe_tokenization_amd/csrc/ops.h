@@ -73,6 +73,27 @@ template <class T> __device__ __forceinline__ void load_part(const T *p, uint32_
     for (int k = 0; k < VEC; ++k) x[k] = k < (int)n ? (float)p[k] : fill;
 }
 
+// the same as a vector, zeros past the end
+template <class T> __device__ __forceinline__ Vec<T> load_some(const T *p, uint32_t n)
+{
+    if (n >= VEC) return load_vec(p);
+    float x[VEC];
+    load_part(p, n, 0.f, x);
+    Vec<T> v;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        if constexpr (sizeof(T) == 4) {
+            const float f = x[k];
+            if (k < 4) v.a[k] = __builtin_bit_cast(uint32_t, f);
+            else v.b[k - 4] = __builtin_bit_cast(uint32_t, f);
+        } else {
+            const uint32_t h = __builtin_bit_cast(uint16_t, (T)x[k]);
+            v.a[k >> 1] = (k & 1) ? v.a[k >> 1] | h << 16 : h;
+        }
+    }
+    return v;
+}
+
 template <class T> __device__ __forceinline__ void store_part(T *p, uint32_t n, const float (&x)[VEC])
 {
     if (n >= VEC) {
