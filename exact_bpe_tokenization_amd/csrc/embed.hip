@@ -105,21 +105,21 @@ struct SortLds {
     uint32_t wsum[SORT_WAVES];
 };
 
-// One pass over this block's elements [base, base + groups * 512 * R) of n.  hist: the counts of every block
+// One pass over this block's elements, `groups` groups of `rounds` (at most R) per thread.  hist: the counts of every block
 // ([blocks][bins]), or NULL where this block is the only one.
 template <int R>
 __device__ __forceinline__ void sort_pass(SortLds &sh, const uint32_t *keys, const uint32_t *pos, bool first, uint32_t n,
-                                          uint32_t n_vocab, uint32_t shift, uint32_t dbits, uint32_t groups, uint32_t block,
-                                          uint32_t blocks, const uint32_t *hist, uint32_t *keys_out, uint32_t *pos_out)
+                                          uint32_t n_vocab, uint32_t shift, uint32_t dbits, uint32_t rounds, uint32_t groups,
+                                          uint32_t block, uint32_t blocks, const uint32_t *hist, uint32_t *keys_out, uint32_t *pos_out)
 {
     const uint32_t bins = 1u << dbits, tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
-    const uint64_t base = ((uint64_t)block * SORT_WAVES + wave) * (64 * R) * groups + lane;
+    const uint64_t base = ((uint64_t)block * SORT_WAVES + wave) * (64 * rounds) * groups + lane;
     uint32_t key[R];
     auto load = [&](uint32_t g) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const uint64_t i = base + ((uint64_t)g * R + r) * 64;
-            key[r] = i < n ? keys[i] : 0xFFFFFFFFu;
+            const uint64_t i = base + ((uint64_t)g * rounds + r) * 64;
+            key[r] = r < (int)rounds && i < n ? keys[i] : 0xFFFFFFFFu;
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) key[r] = min(key[r], n_vocab);   // an ID without a row; also what lies past the end
@@ -130,7 +130,8 @@ __device__ __forceinline__ void sort_pass(SortLds &sh, const uint32_t *keys, con
     for (uint32_t g = 0;;) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            if (base + ((uint64_t)g * R + r) * 64 < n) atomicAdd(&sh.cnt[wave][(key[r] >> shift) & (bins - 1)], 1u);
+            if (r < (int)rounds && base + ((uint64_t)g * rounds + r) * 64 < n)
+                atomicAdd(&sh.cnt[wave][(key[r] >> shift) & (bins - 1)], 1u);
         if (++g == groups) break;
         load(g);
     }
@@ -180,12 +181,13 @@ __device__ __forceinline__ void sort_pass(SortLds &sh, const uint32_t *keys, con
         uint32_t from[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const uint64_t i = base + ((uint64_t)g * R + r) * 64;
-            from[r] = first || i >= n ? (uint32_t)i : pos[i];
+            const uint64_t i = base + ((uint64_t)g * rounds + r) * 64;
+            from[r] = first || r >= (int)rounds || i >= n ? (uint32_t)i : pos[i];
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const bool in = base + ((uint64_t)g * R + r) * 64 < n;
+            if (r >= (int)rounds) break;
+            const bool in = base + ((uint64_t)g * rounds + r) * 64 < n;
             const uint32_t d = (key[r] >> shift) & (bins - 1);
             uint64_t same = __ballot(in);
             for (uint32_t b = 0; b < dbits; ++b) {
@@ -206,16 +208,16 @@ __device__ __forceinline__ void sort_pass(SortLds &sh, const uint32_t *keys, con
 }
 
 __global__ __launch_bounds__(SORT_THREADS) void k_sort_one(const uint32_t *__restrict__ ids, uint32_t n, uint32_t n_vocab,
-                                                           uint32_t passes, uint32_t dbits, uint32_t *keys0, uint32_t *pos0,
+                                                           uint32_t passes, uint32_t dbits, uint32_t rounds, uint32_t *keys0, uint32_t *pos0,
                                                            uint32_t *keys1, uint32_t *pos1, Zeros z)
 {
     __shared__ __align__(16) SortLds sh;
     if (blockIdx.x > 0) return zero_block(z, blockIdx.x - 1);
-    sort_pass<R_ONE>(sh, ids, nullptr, true, n, n_vocab, 0, dbits, 1, 0, 1, nullptr, keys0, pos0);
+    sort_pass<R_ONE>(sh, ids, nullptr, true, n, n_vocab, 0, dbits, rounds, 1, 0, 1, nullptr, keys0, pos0);
     if (passes == 1) return;
     __threadfence_block();
     __syncthreads();
-    sort_pass<R_ONE>(sh, keys0, pos0, false, n, n_vocab, dbits, dbits, 1, 0, 1, nullptr, keys1, pos1);
+    sort_pass<R_ONE>(sh, keys0, pos0, false, n, n_vocab, dbits, dbits, rounds, 1, 0, 1, nullptr, keys1, pos1);
 }
 
 __global__ __launch_bounds__(SORT_THREADS) void k_sort_hist(const uint32_t *__restrict__ keys, uint32_t n, uint32_t n_vocab,
@@ -253,7 +255,7 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(const uint32_t *_
 {
     __shared__ __align__(16) SortLds sh;
     if (blockIdx.x >= blocks) return zero_block(z, blockIdx.x - blocks);
-    sort_pass<R_MANY>(sh, keys, pos, first, n, n_vocab, shift, dbits, groups, blockIdx.x, blocks, hist, keys_out, pos_out);
+    sort_pass<R_MANY>(sh, keys, pos, first, n, n_vocab, shift, dbits, R_MANY, groups, blockIdx.x, blocks, hist, keys_out, pos_out);
 }
 
 // Sums.  The sorted tokens are cut into chunks; a wavefront takes one chunk and 512 columns and adds up
@@ -261,7 +263,7 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(const uint32_t *_
 // that crosses a chunk's border leaves a partial sum (slot 0: the run entered from the chunk before, slot 1:
 // it starts here and goes on), joined in chunk order by k_embed_join.
 constexpr uint32_t COLS = 64 * VEC;
-constexpr int ROWS = 8;
+constexpr int ROWS = 8, PARTS = 16;   // rows, and partial sums, of a wavefront in flight
 
 template <class TT>
 __device__ __forceinline__ void put_row(TT *__restrict__ row, uint32_t n, float scale, bool accumulate,
@@ -372,19 +374,19 @@ __global__ __launch_bounds__(256) void k_embed_join(const uint32_t *__restrict__
     if (head == key && prev == key) return;          // it started in an earlier chunk
     float acc[VEC] = {};
     if (c < dim) load_part(part + ((uint64_t)ch * 2 + 1) * dpad + c, VEC, 0.f, acc);
-    // the chunks that the run enters: 64 heads are compared at once, and eight partial sums are in flight
+    // the chunks that the run enters: 64 heads are compared at once, and their partial sums loaded together
     for (uint32_t h0 = ch + 1; h0 < n_chunks; h0 += 64) {
         const uint32_t h = h0 + lane;
         const uint64_t same = __ballot(h < n_chunks && keys[(uint64_t)min(h, n_chunks - 1) * chunk] == key);
         const uint32_t count = ~same ? (uint32_t)__builtin_ctzll(~same) : 64u;
         if (c < dim)
-            for (uint32_t q = 0; q < count; q += ROWS) {
-                Vec<float> x[ROWS];
+            for (uint32_t q = 0; q < count; q += PARTS) {
+                Vec<float> x[PARTS];
 #pragma unroll
-                for (int u = 0; u < ROWS; ++u)
+                for (int u = 0; u < PARTS; ++u)
                     if (q + u < count) x[u] = load_vec(part + (uint64_t)(h0 + q + u) * 2 * dpad + c);
 #pragma unroll
-                for (int u = 0; u < ROWS; ++u)
+                for (int u = 0; u < PARTS; ++u)
                     if (q + u < count)
 #pragma unroll
                         for (int k = 0; k < VEC; ++k) acc[k] += vec_at(x[u], k);
@@ -545,7 +547,8 @@ extern "C" int toktier_embed_backward(const void *grad_out, int grad_type, uint6
     const uint32_t last = L.sort.passes - 1;
     if (n <= SORT_ONE) {
         const uint32_t zb = zero_blocks(0, 1);
-        k_sort_one<<<1 + zb, SORT_THREADS, 0, s>>>(ids, n, n_vocab, L.sort.passes, L.sort.dbits, keys[0], pos[0], keys[1], pos[1], z);
+        k_sort_one<<<1 + zb, SORT_THREADS, 0, s>>>(ids, n, n_vocab, L.sort.passes, L.sort.dbits,
+                                                      (n + SORT_THREADS - 1) / SORT_THREADS, keys[0], pos[0], keys[1], pos[1], z);
     } else {
         for (uint32_t p = 0; p <= last; ++p) {
             const uint32_t *ki = p ? keys[0] : ids, *pi = p ? pos[0] : nullptr, shift = p * L.sort.dbits, launches = 2 * L.sort.passes;
