@@ -431,7 +431,10 @@ BackwardLayout backward_layout(uint64_t n_tokens, uint32_t n_vocab, uint32_t dim
     return L;
 }
 
-// The rows of a table as zeros to write: whole where they are contiguous, cut into pieces of 64 KiB.
+// The rows of a table as zeros to write; contiguous rows are cut into pieces of 16 KiB, one per block
+// (538 MB in 88 us; 96 us in pieces of 64 KiB).
+constexpr uint64_t PIECE = 16384;
+
 Zeros zeros_of(void *table, uint32_t size, uint32_t n_vocab, uint32_t dim, uint64_t stride)
 {
     Zeros z;
@@ -441,10 +444,10 @@ Zeros zeros_of(void *table, uint32_t size, uint32_t n_vocab, uint32_t dim, uint6
     z.end = z.stride * n_vocab;
     z.rows = n_vocab;
     if (z.row_bytes == z.stride) {
-        z.row_bytes = z.stride = 65536;
-        z.rows = (uint32_t)((z.end + 65535) / 65536);
+        z.row_bytes = z.stride = PIECE;
+        z.rows = (uint32_t)((z.end + PIECE - 1) / PIECE);
     }
-    z.per_block = z.row_bytes >= 65536 ? 1 : (uint32_t)(65536 / z.row_bytes);
+    z.per_block = z.row_bytes >= PIECE ? 1 : (uint32_t)(PIECE / z.row_bytes);
     z.from = 0;
     return z;
 }

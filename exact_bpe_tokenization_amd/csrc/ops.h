@@ -38,26 +38,30 @@ template <class T> __device__ __forceinline__ float vec_at(const Vec<T> &v, int 
     }
 }
 
-// Eight floats rounded (to nearest even) to T and stored.
-template <class T> __device__ __forceinline__ void store_vec(T *p, const float (&x)[VEC])
+// Eight floats rounded (to nearest even) to T.
+template <class T> __device__ __forceinline__ Vec<T> to_vec(const float (&x)[VEC])
 {
+    Vec<T> v;
     if constexpr (sizeof(T) == 4) {
-        u32x4 a, b;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            a[k] = __builtin_bit_cast(uint32_t, x[k]);
-            b[k] = __builtin_bit_cast(uint32_t, x[k + 4]);
+            v.a[k] = __builtin_bit_cast(uint32_t, x[k]);
+            v.b[k] = __builtin_bit_cast(uint32_t, x[k + 4]);
         }
-        *(u32x4_row *)p = a;
-        *(u32x4_row *)(p + 4) = b;
     } else {
-        u32x4 a;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            a[k] = (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k]) |
-                   (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k + 1]) << 16;
-        *(u32x4_row *)p = a;
+            v.a[k] = (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k]) |
+                     (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k + 1]) << 16;
     }
+    return v;
+}
+
+template <class T> __device__ __forceinline__ void store_vec(T *p, const float (&x)[VEC])
+{
+    const Vec<T> v = to_vec<T>(x);
+    *(u32x4_row *)p = v.a;
+    if constexpr (sizeof(T) == 4) *(u32x4_row *)(p + 4) = v.b;
 }
 
 // Up to eight elements (n of them) where a row ends inside a vector.
@@ -79,19 +83,7 @@ template <class T> __device__ __forceinline__ Vec<T> load_some(const T *p, uint3
     if (n >= VEC) return load_vec(p);
     float x[VEC];
     load_part(p, n, 0.f, x);
-    Vec<T> v;
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-        if constexpr (sizeof(T) == 4) {
-            const float f = x[k];
-            if (k < 4) v.a[k] = __builtin_bit_cast(uint32_t, f);
-            else v.b[k - 4] = __builtin_bit_cast(uint32_t, f);
-        } else {
-            const uint32_t h = __builtin_bit_cast(uint16_t, (T)x[k]);
-            v.a[k >> 1] = (k & 1) ? v.a[k >> 1] | h << 16 : h;
-        }
-    }
-    return v;
+    return to_vec<T>(x);
 }
 
 template <class T> __device__ __forceinline__ void store_part(T *p, uint32_t n, const float (&x)[VEC])
@@ -103,6 +95,15 @@ template <class T> __device__ __forceinline__ void store_part(T *p, uint32_t n, 
 #pragma unroll
     for (int k = 0; k < VEC; ++k)
         if (k < (int)n) p[k] = (T)x[k];
+}
+
+// store_part past the caches, for what no kernel of this call reads again
+template <class T> __device__ __forceinline__ void stream_part(T *p, uint32_t n, const float (&x)[VEC])
+{
+    if (n < VEC) return store_part(p, n, x);
+    Vec<T> v = to_vec<T>(x);
+    __builtin_nontemporal_store(v.a, (u32x4_row *)p);
+    if constexpr (sizeof(T) == 4) __builtin_nontemporal_store(v.b, (u32x4_row *)(p + 4));
 }
 
 // ---------------------------------------------------------------------------------------------
