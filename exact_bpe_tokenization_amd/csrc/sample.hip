@@ -1,17 +1,16 @@
 // sample.hip -- sampling of one ID per row: temperature, top-k, top-p, min-p, given random numbers.
 //
 // Every filter keeps a prefix of the order (logit descending, ID ascending), so the kept set is one pair: a
-// logit (as an integer key of the same order) and how many of its equals, lowest IDs first.  Masses are
-// sums of 64-bit integers, w = 2^y rounded to a multiple of 2^-S with y = (x - max) log2(e) / temperature in
-// 64-bit floating point: exact in any order, so neither atomics nor the split of a row over threads can
-// change an ID.
+// logit (as an integer key of the same order) and the last ID that may have it.  Masses are sums of 64-bit
+// integers, w = 2^y rounded to a multiple of 2^-S with y = (x - max) log2(e) / temperature in 64-bit floating
+// point: exact in any order, so neither atomics nor the split of a row over threads can change an ID.
 //
-// One workgroup per row; a wavefront owns a contiguous segment of it, in registers where the row fits.
-//   1. keys and the largest of them;
-//   2. for top-k and top-p, a histogram over 4,095 bins of the key (sign, exponent, 7 mantissa bits) with
-//      counts and masses; a scan from the top finds the bin where a filter ends, and a digit search over
-//      that bin's keys the exact key and its equals (nothing to search for bfloat16, whose bins hold one key);
-//   3. the ID by the running mass over IDs: per wavefront, then inside the one wavefront that holds it.
+// A row goes through four phases:
+//   keys    the largest key, and a histogram of the keys over 4,095 bins (sign, exponent, 7 mantissa bits);
+//   border  the bins in which top-k (by counts) and top-p (by masses) end;
+//   cells   per cell of consecutive IDs, the mass of what lies above the border, and a list of what lies in it;
+//   draw    the list sorted gives the exact border; the running mass over the cells, then inside one, gives the ID.
+// A bin of bfloat16 holds one key, so that its mass is its count times one weight and its list is not needed.
 #include <type_traits>
 
 #include "ops.h"
@@ -19,11 +18,14 @@
 namespace tt {
 namespace {
 
-#define INLINE __attribute__((always_inline))   // of a lambda: the keys it sees stay in registers
+#define INLINE __attribute__((always_inline))   // of a lambda
 
 constexpr uint32_t NO_ID = 0xFFFFFFFFu;
 constexpr int BINS = 4096, HALF = BINS / 2 - 1;   // bins of a sign; bin 0 holds the largest keys
-constexpr int DIGIT = 11, DIGITS = 1 << DIGIT;
+constexpr int DIGIT = 12;
+constexpr uint32_t LIST = 2048;                   // elements that a border may have to be sorted
+constexpr uint32_t ODD = 512;                     // bfloat16: listed elements of bins with several keys
+constexpr uint32_t MAX_CELLS = 256;               // of 8,192 elements
 
 // A key is the logit's sign and magnitude bits as an integer: the order of the logits, -0 equal to +0.
 // Bins: magnitudes below 2^-9 share the middle one, those from 2^7 on the outermost, and between them a bin
@@ -64,8 +66,24 @@ template <class T> __device__ __forceinline__ int bin_of(int k)
     return HALF - ((m ^ sign) - sign);
 }
 
+// Keys of a bin: lo .. hi.
+template <class T> __device__ __forceinline__ void bin_range(int b, int &lo, int &hi)
+{
+    using K = Keys<T>;
+    const int s = HALF - b, m = s < 0 ? -s : s;
+    const int a = m == 0 ? -(K::LOW - 1) : K::LOW + ((m - 1) << K::SHIFT);
+    const int z = m == 0 ? K::LOW - 1 : m == HALF ? K::INF : K::LOW + (m << K::SHIFT) - 1;
+    lo = s < 0 ? -z : a;
+    hi = s < 0 ? -a : z;
+}
+// bfloat16: one key per bin, but for the middle and the outermost ones
+template <class T> __device__ __forceinline__ bool bin_exact(int b)
+{
+    const int s = b - HALF, m = s < 0 ? -s : s;
+    return __is_same(T, __bf16) && (uint32_t)(m - 1) < (uint32_t)(HALF - 1);
+}
+
 typedef short s16x2 __attribute__((ext_vector_type(2)));
-typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 // Eight keys: packed in pairs for the 16-bit types.
 template <class T> struct Vec8 {
@@ -75,16 +93,19 @@ template <class T> struct Vec8 {
         const uint32_t w = a[i];   // (a bit cast of the vector's element itself would read element 0)
         return __builtin_bit_cast(s16x2, w);
     }
-    __device__ __forceinline__ int at(int e) const
-    {
-        return (e & 1) ? (int)a[e >> 1] >> 16 : (int)(int16_t)(a[e >> 1] & 0xFFFFu);
-    }
-    __device__ __forceinline__ int pick(int e) const   // at(), for an index known at run time only
+    __device__ __forceinline__ int pick(int e) const   // e known at run time only
     {
         const uint32_t w = e & 4 ? (e & 2 ? a[3] : a[2]) : (e & 2 ? a[1] : a[0]);
         return (e & 1) ? (int)w >> 16 : (int)(int16_t)(w & 0xFFFFu);
     }
-    __device__ __forceinline__ void hide(int e) { a[e >> 1] = (e & 1) ? (a[e >> 1] & 0xFFFFu) | 0x80000000u : (a[e >> 1] & 0xFFFF0000u) | 0x8000u; }
+    __device__ __forceinline__ int at(int e) const
+    {
+        return (e & 1) ? (int)a[e >> 1] >> 16 : (int)(int16_t)(a[e >> 1] & 0xFFFFu);
+    }
+    __device__ __forceinline__ void hide(int e)
+    {
+        a[e >> 1] = (e & 1) ? (a[e >> 1] & 0xFFFFu) | 0x80000000u : (a[e >> 1] & 0xFFFF0000u) | 0x8000u;
+    }
     __device__ __forceinline__ int max() const
     {
         s16x2 m = pair(0);
@@ -100,20 +121,6 @@ template <class T> struct Vec8 {
             const s16x2 b = pair(i), sign = b >> 15;
             const s16x2 m = __builtin_bit_cast(s16x2, a[i] & 0x7FFF7FFFu);
             a[i] = __builtin_bit_cast(uint32_t, (m ^ sign) - sign);
-        }
-    }
-    __device__ __forceinline__ void bins(int (&b)[VEC]) const
-    {
-        using K = Keys<T>;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const s16x2 k = pair(i), sign = k >> 15;
-            const u16x2 mag = __builtin_bit_cast(u16x2, __builtin_elementwise_max(k, (s16x2)-k));
-            u16x2 m = __builtin_elementwise_sub_sat(mag, (u16x2)(unsigned short)(K::LOW - (1 << K::SHIFT)));
-            m = __builtin_elementwise_min((u16x2)(m >> K::SHIFT), (u16x2)(unsigned short)HALF);
-            const s16x2 t = (s16x2)(short)HALF - ((__builtin_bit_cast(s16x2, m) ^ sign) - sign);
-            b[2 * i] = t.x;
-            b[2 * i + 1] = t.y;
         }
     }
 };
@@ -147,28 +154,7 @@ template <> struct Vec8<float> {
             set(e, ((x & 0x7FFFFFFF) ^ sign) - sign);
         }
     }
-    __device__ __forceinline__ void bins(int (&out)[VEC]) const
-    {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) out[e] = bin_of<float>(at(e));
-    }
 };
-
-// Keys of a bin: lo .. hi.
-template <class T> __device__ __forceinline__ void bin_range(int b, int &lo, int &hi)
-{
-    using K = Keys<T>;
-    const int s = HALF - b, m = s < 0 ? -s : s;
-    const int a = m == 0 ? -(K::LOW - 1) : K::LOW + ((m - 1) << K::SHIFT);
-    const int z = m == 0 ? K::LOW - 1 : m == HALF ? K::INF : K::LOW + (m << K::SHIFT) - 1;
-    lo = s < 0 ? -z : a;
-    hi = s < 0 ? -a : z;
-}
-// bfloat16: one key per bin, but for the middle and the outermost ones
-template <class T> __device__ __forceinline__ bool bin_exact(int b)
-{
-    return __is_same(T, __bf16) && b != HALF && b != 0 && b != 2 * HALF;
-}
 
 // Weights of one row.  2^y = 2^n 2^f with n the nearest integer: 2^f on [-1/2, 1/2] by the polynomial of degree
 // 10 that interpolates it at the Chebyshev nodes (relative error below 2^-51), the multiple of 2^-S by
@@ -202,6 +188,13 @@ struct Weights {
     }
 };
 
+// A kernel runs most of its code once per row, so fetching instructions costs more than issuing them: what is
+// used in several places is a function of its own.
+template <class T> __device__ __attribute__((noinline)) uint64_t weight_of(double c, double max, double magic, int max_key, int key)
+{
+    return Weights{c, max, magic, max_key}.of(key, Keys<T>::value(key));
+}
+
 template <class V> __device__ __forceinline__ V wave_scan(V v)
 {
 #pragma unroll
@@ -211,231 +204,872 @@ template <class V> __device__ __forceinline__ V wave_scan(V v)
     }
     return v;
 }
-template <class V> __device__ __forceinline__ V wave_sum(V v)
-{
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-}
 
-template <int WAVES> struct Shared {
-    uint64_t mass[BINS];                                     // per bin; for the draw, the weight of its key
+template <int WAVES> struct Lds {
+    uint64_t mass[BINS];         // masses, or weights, per bin; weights of the list
     union {
         uint32_t count[BINS];
-        uint64_t digit[DIGITS];
+        uint64_t list[LIST];     // key above, inverted ID below: the order is that of the numbers, descending
     };
+    uint64_t cell[MAX_CELLS];    // mass of what is kept
+    uint32_t border[MAX_CELLS];  // elements in the border's bins
     uint64_t wave[WAVES];
     uint64_t above, inside;
-    uint32_t found;
+    uint32_t found, n_list, n_odd;
     int key;
+    uint32_t odd[ODD];
 };
 
 // Sum over the threads below this one; total: over all.
-template <int WAVES> __device__ __forceinline__ uint64_t block_before(uint64_t v, Shared<WAVES> &sh, uint64_t &total)
+typedef __attribute__((address_space(3))) uint64_t lds_u64;
+
+template <int WAVES> __device__ __attribute__((noinline)) ulonglong2 block_sums(uint64_t v, lds_u64 *wave_sums)
 {
     const uint32_t wave = threadIdx.x >> 6;
     const uint64_t incl = wave_scan(v);
-    if ((threadIdx.x & 63) == 63) sh.wave[wave] = incl;
+    if ((threadIdx.x & 63) == 63) wave_sums[wave] = incl;
     __syncthreads();
-    uint64_t base = 0;
-    total = 0;
+    uint64_t base = 0, all = 0;
 #pragma unroll 4
     for (uint32_t w = 0; w < WAVES; ++w) {
-        const uint64_t s = sh.wave[w];
+        const uint64_t s = wave_sums[w];
         if (w < wave) base += s;
-        total += s;
+        all += s;
     }
     __syncthreads();
-    return base + incl - v;
+    return ulonglong2{base + incl - v, all};
 }
 
-// The first of n bins (value(b), b ascending) at which the running sum reaches target(total), the sum before it
-// and the bin's own value.  n / threads consecutive bins per thread.  False when the total is below target.
-template <int N, int WAVES, class F, class G>
-__device__ __forceinline__ bool find_bin(Shared<WAVES> &sh, F value, G target_of, uint32_t &bin, uint64_t &above,
-                                         uint64_t &inside, uint64_t &target)
+template <int WAVES> __device__ __forceinline__ uint64_t block_before(uint64_t v, uint64_t *wave_sums, uint64_t &total)
 {
-    constexpr int PER = N / (WAVES * 64);
-    uint64_t v[PER], sum = 0, total;
+    const ulonglong2 r = block_sums<WAVES>(v, (lds_u64 *)wave_sums);
+    total = r.y;
+    return r.x;
+}
+
+// One row's logits, mask and settings.
+template <class T> struct Row {
+    using V = Vec8<T>;
+    const T *x;
+    const uint32_t *mask;
+    uint32_t n;
+    float temp, p, min_p, u;
+    uint32_t k;
+
+    __device__ __forceinline__ V raw(uint32_t j) const
+    {
+        V v;
+        if (j + VEC <= n) {
+            v.a = *(const u32x4_row *)(x + j);
+            if constexpr (sizeof(T) == 4) v.b = *(const u32x4_row *)(x + j + 4);
+        } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        v[i] = value(threadIdx.x * PER + i);
-        sum += v[i];
+            for (int e = 0; e < VEC; ++e) {
+                if constexpr (sizeof(T) == 4) {
+                    v.set(e, j + e < n ? __builtin_bit_cast(int, x[j + e]) : (int)0xFF800000u);
+                } else {
+                    const uint32_t h = j + e < n ? (uint32_t)__builtin_bit_cast(uint16_t, x[j + e]) : 0x8000u | (uint32_t)Keys<T>::INF;
+                    v.a[e >> 1] = (e & 1) ? v.a[e >> 1] | h << 16 : h;
+                }
+            }
+        }
+        return v;
     }
-    uint64_t run = block_before(sum, sh, total);
+    __device__ __forceinline__ void finish(V &v, uint32_t j) const
+    {
+        v.order();
+        if (__any(v.max() > Keys<T>::INF)) {   // NaN
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (v.at(e) > Keys<T>::INF) v.hide(e);
+        }
+        if (mask && j < n) {
+            const uint32_t bits = mask[j >> 5] >> (j & 31u);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (!((bits >> e) & 1u)) v.hide(e);
+        }
+    }
+};
+
+
+// Where the filters end.  Bins before lo are kept, bins after hi are not; those from lo to hi are the border.
+struct Border {
+    int lo, hi;
+    bool hard;        // too many elements for the list: see general_row
+    bool listed;      // the border's elements are sorted; else it is one key, of which the first `ties` of `count` are kept
+    bool by_k, by_p;  // listed: limits on their number, on their mass
+    uint64_t left_k, left_p;   // (left_p 0: top-p of what left_k keeps)
+    int key;
+    uint64_t ties, count;
+};
+
+// ---- keys: over cells [c0, c1), this thread's largest key and the vector where it first met it
+template <class T, int WAVES>
+__device__ __forceinline__ void scan_keys(const Row<T> &row, Lds<WAVES> &sh, uint32_t c0, uint32_t c1, bool hist, int &mine,
+                                          uint32_t &mine_j)
+{
+    using V = Vec8<T>;
+    using K = Keys<T>;
+    constexpr uint32_t AHEAD = 4, CELL = WAVES * 64 * VEC;
+    mine = (int)0x80000000;
+    mine_j = 0;
+#pragma unroll 1
+    for (uint32_t c = c0; c < c1; c += AHEAD) {
+        V v[AHEAD];
+#pragma unroll
+        for (uint32_t q = 0; q < AHEAD; ++q)
+            if (c + q < c1) v[q] = row.raw((c + q) * CELL + threadIdx.x * VEC);
+#pragma unroll
+        for (uint32_t q = 0; q < AHEAD; ++q)
+            if (c + q < c1) {
+                const uint32_t j = (c + q) * CELL + threadIdx.x * VEC;
+                row.finish(v[q], j);
+                const int m = v[q].max();
+                if (m > mine) {
+                    mine = m;
+                    mine_j = j;
+                }
+                if (hist) {
+                    bool odd = false;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const int key = v[q].at(e), b = bin_of<T>(key);
+                        const bool in = key > -K::INF;
+                        if (in) atomicAdd(&sh.count[b], 1u);
+                        if (__is_same(T, __bf16)) odd |= in & !bin_exact<T>(b);
+                    }
+                    if (__is_same(T, __bf16) && __any(odd)) {
+#pragma unroll 1
+                        for (int e = 0; e < VEC; ++e) {
+                            const int key = v[q].pick(e);
+                            if ((key > -K::INF) & !bin_exact<T>(bin_of<T>(key))) {
+                                const uint32_t at = atomicAdd(&sh.n_odd, 1u);
+                                if (at < ODD) sh.odd[at] = (uint32_t)key;
+                            }
+                        }
+                    }
+                }
+            }
+    }
+}
+
+// The largest key of the workgroup with its lowest index, as one number: the order of keys, then of inverted indexes.
+template <class T, int WAVES>
+__device__ __forceinline__ uint64_t block_best(const Row<T> &row, Lds<WAVES> &sh, int mine, uint32_t mine_j)
+{
+    uint32_t e0 = 0;
+    if (mine > -Keys<T>::INF) {
+        Vec8<T> v = row.raw(mine_j);
+        row.finish(v, mine_j);
+#pragma unroll
+        for (int e = VEC - 1; e >= 0; --e)
+            if (v.at(e) == mine) e0 = e;
+    }
+    uint64_t best = (uint64_t)((uint32_t)mine ^ 0x80000000u) << 32 | ~(mine_j + e0);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        const uint64_t o = __shfl_xor(best, d);
+        best = o > best ? o : best;
+    }
+    if ((threadIdx.x & 63) == 0) sh.wave[threadIdx.x >> 6] = best;
+    __syncthreads();
+#pragma unroll 4
+    for (int w = 0; w < WAVES; ++w) {
+        const uint64_t o = sh.wave[w];
+        best = o > best ? o : best;
+    }
+    __syncthreads();
+    return best;
+}
+
+// The first bin at which the running sum of value(bin) reaches target(total), the sum before it and its own;
+// false where the total is below the target.
+template <int WAVES, class F, class G>
+__device__ __forceinline__ bool find_bin(Lds<WAVES> &sh, F value, G target_of, uint32_t &bin, uint64_t &before, uint64_t &inside,
+                                         uint64_t &target)
+{
+    constexpr int PER = BINS / (WAVES * 64);
+    const int b0 = threadIdx.x * PER;
+    uint64_t sum = 0, total;
+#pragma unroll 4
+    for (int i = 0; i < PER; ++i) sum += value(b0 + i);
+    uint64_t run = block_before<WAVES>(sum, sh.wave, total);
     target = target_of(total);
     if (target > total) return false;
     if (run < target && target <= run + sum) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (run < target && target <= run + v[i]) {
-                sh.found = threadIdx.x * PER + i;
+#pragma unroll 1
+        for (int i = 0;; ++i) {
+            const uint64_t v = value(b0 + i);
+            if (target <= run + v) {
+                sh.found = b0 + i;
                 sh.above = run;
-                sh.inside = v[i];
+                sh.inside = v;
+                break;
             }
-            run += v[i];
+            run += v;
         }
     }
     __syncthreads();
     bin = sh.found;
-    above = sh.above;
+    before = sh.above;
     inside = sh.inside;
     __syncthreads();
     return true;
 }
 
-// One row.  NV > 0: its keys stay in registers (NV vectors per thread at most); NV == 0: every pass reads them.
-template <class T, int WAVES, int NV> struct Row {
-    static constexpr int HELD = NV ? NV : 1;
-    const T *x;
-    const uint32_t *mask;
-    uint32_t n, nv, first;   // elements, vectors per thread, this thread's first element
-    bool nan;                // a positive NaN may be among the keys of a 16-bit type
-    using V = Vec8<T>;
-    V held[HELD];
-
-    __device__ __forceinline__ uint32_t at(uint32_t i) const { return first + i * (64 * VEC); }
-
-    __device__ __forceinline__ Vec8<T> raw(uint32_t j) const
-    {
-        Vec8<T> v;
-        if (j + VEC <= n) {
-            if constexpr (sizeof(T) == 4) {
-                v.a = *(const u32x4_row *)(x + j);
-                v.b = *(const u32x4_row *)(x + j + 4);
-            } else {
-                v.a = *(const u32x4_row *)(x + j);
-            }
-        } else {
-            uint32_t e[VEC];
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                if constexpr (sizeof(T) == 4) e[k] = j + k < n ? __builtin_bit_cast(uint32_t, x[j + k]) : 0xFF800000u;
-                else e[k] = j + k < n ? (uint32_t)__builtin_bit_cast(uint16_t, x[j + k]) : 0x8000u | (uint32_t)Keys<T>::INF;
-            }
-            if constexpr (sizeof(T) == 4) {
-                v.a = u32x4{e[0], e[1], e[2], e[3]};
-                v.b = u32x4{e[4], e[5], e[6], e[7]};
-            } else {
-                v.a = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
-            }
-        }
-        return v;
-    }
-    __device__ __forceinline__ void finish(Vec8<T> &v, uint32_t j) const
-    {
-        v.order();
-        if (nan || sizeof(T) == 4) drop_nan(v);
-        if (mask && j < n) {
-            const uint32_t bits = mask[j >> 5] >> (j & 31u);
-            if ((bits & 0xFFu) != 0xFFu) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (!((bits >> e) & 1u)) v.hide(e);
-            }
-        }
-    }
-    static __device__ __forceinline__ void drop_nan(Vec8<T> &v)
-    {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            if (v.at(e) > Keys<T>::INF) v.hide(e);
-    }
-    __device__ __forceinline__ void load()
-    {
-        if constexpr (NV > 0) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i < (int)nv) held[i] = raw(at(i));
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i < (int)nv) finish(held[i], at(i));
-        }
-    }
-    // Keeps the compiler from carrying what it derived from the keys in one pass over to the next: those
-    // values would need several times the registers of the keys themselves.
-    static __device__ __forceinline__ void forget(V &v)
-    {
-        asm volatile("" : "+v"(v.a));
-        if constexpr (sizeof(T) == 4) asm volatile("" : "+v"(v.b));
-    }
-    // f(index of the first element, keys) over this thread's vectors, ascending
-    template <class F> __device__ __forceinline__ void each(F f)
-    {
-        if constexpr (NV > 0) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i < (int)nv) {
-                    forget(held[i]);
-                    f(at(i), held[i]);
-                }
-        } else {
-            for (uint32_t i = 0; i < nv; ++i) {
-                Vec8<T> v = raw(at(i));
-                finish(v, at(i));
-                f(at(i), v);
-            }
-        }
-    }
-};
-
-// The index at which the running sum (over IDs) of the elements' measure exceeds target(total), and its key.
-// sum(vector, index): a vector's, 0 at once where no lane has any; element(vector, index, e): one element's.
-// Per wavefront first; then only the wavefront that holds it looks closer.
-template <int WAVES, class R, class S, class E, class G>
-__device__ __forceinline__ uint32_t locate(R &row, Shared<WAVES> &sh, S sum_of, E element, G target_of, uint64_t &total, int &key)
+__device__ __forceinline__ uint64_t share_of(float p, uint64_t all)   // the mass that top-p has to reach, 1 .. all
 {
-    const uint32_t wave = threadIdx.x >> 6;
-    uint64_t sum = 0;
-    row.each([&](uint32_t j, const auto &v) INLINE { sum += sum_of(v, j); });
-    sum = wave_sum(sum);
-    if ((threadIdx.x & 63) == 0) sh.wave[wave] = sum;
-    __syncthreads();
-    uint64_t before = 0;
-    total = 0;
-#pragma unroll 4
-    for (uint32_t w = 0; w < WAVES; ++w) {
-        const uint64_t s = sh.wave[w];
-        if (w < wave) before += s;
-        total += s;
-    }
-    const uint64_t target = target_of(total);
-    if (before <= target && target < before + sum) {
-        // by thread: the vector in which its share of the wavefront's running sum passes the target
-        typename R::V hit{};
-        uint64_t hit_at = 0, run = before;
-        uint32_t hit_j = NO_ID;
-        row.each([&](uint32_t j, const auto &v) INLINE {
-            const uint64_t mine = sum_of(v, j);
-            if (!__any(mine != 0)) return;
-            const uint64_t incl = run + wave_scan(mine);
-            if (incl - mine <= target && target < incl) {
-                hit = v;
-                hit_at = incl - mine;
-                hit_j = j;
-            }
-            run = __shfl(incl, 63);
-        });
-        if (hit_j != NO_ID) {
-#pragma unroll 1
-            for (int e = 0; e < VEC; ++e) {
-                hit_at += element(hit, hit_j, e);
-                if (hit_at > target) {
-                    sh.found = hit_j + e;
-                    sh.key = hit.pick(e);
-                    break;
-                }
-            }
-        }
-    }
-    __syncthreads();
-    const uint32_t id = sh.found;
-    key = sh.key;
-    __syncthreads();
-    return id;
+    const double t = __builtin_ceil((double)p * (double)all);
+    const uint64_t q = t > 1.0 ? (uint64_t)t : 1ull;
+    return q < all ? q : all;
 }
 
-template <class T, int WAVES, int NV>
+// ---- border, from sh.count; fill_masses() brings the masses into sh.mass where they are needed
+template <class T, int WAVES, class W, class M>
+__device__ __forceinline__ Border find_border(const Row<T> &row, Lds<WAVES> &sh, W weight, M fill_masses)
+{
+    Border r{};
+    r.lo = r.hi = BINS;
+    bool need_k = row.k != 0 && row.k < row.n;
+    const bool need_p = row.p < 1.f;
+    uint32_t bin_k = BINS, bin;
+    uint64_t above_k = 0, count_k = 0, before, inside, target;
+    const uint64_t k = row.k;
+    if (need_k)
+        need_k = find_bin<WAVES>(sh, [&](int b) INLINE { return (uint64_t)sh.count[b]; }, [&](uint64_t) INLINE { return k; }, bin_k,
+                                 above_k, count_k, target);
+    if (!need_k && !need_p) return r;
+    if (need_k && (above_k + count_k <= LIST || !need_p)) {
+        r.hi = (int)bin_k;
+        r.by_k = true;
+        if (above_k + count_k <= LIST) {   // all that top-k may keep goes to the list
+            r.lo = 0;
+            r.listed = true;
+            r.by_p = need_p;
+            r.left_k = k;
+            return r;
+        }
+        r.lo = r.hi;
+        r.left_k = r.ties = k - above_k;
+        r.count = count_k;
+    } else {
+        fill_masses(bin_k);
+        uint64_t mass_k = 0;
+        if (need_k) {
+            if (!bin_exact<T>((int)bin_k)) {
+                r.hard = true;
+                return r;
+            }
+            int lo, hi;
+            bin_range<T>((int)bin_k, lo, hi);
+            mass_k = (k - above_k) * weight(lo);
+        }
+        find_bin<WAVES>(sh, [&](int b) INLINE { return b < (int)bin_k ? sh.mass[b] : b == (int)bin_k ? mass_k : 0ull; },
+                        [&](uint64_t all) INLINE { return share_of(row.p, all); }, bin, before, inside, target);
+        r.lo = r.hi = (int)bin;
+        r.by_p = true;
+        r.left_p = target - before;
+        r.count = sh.count[bin];
+    }
+    int lo, hi;
+    bin_range<T>(r.lo, lo, hi);
+    r.key = lo;
+    r.listed = !bin_exact<T>(r.lo);
+    if (r.listed) {
+        r.hard = r.count > LIST;
+    } else if (r.by_p) {
+        const uint64_t w = weight(lo);
+        r.ties = (r.left_p + w - 1) / w;
+    }
+    __syncthreads();   // the counts have been read: the list may take their place
+    return r;
+}
+
+// ---- cells [c0, c1): adds to sh.cell, sh.border and sh.list
+template <class T, int WAVES, class W>
+__device__ __forceinline__ void scan_cells(const Row<T> &row, Lds<WAVES> &sh, const Weights &wt, const Border &b, uint64_t w_min,
+                                           uint32_t c0, uint32_t c1, W weight)
+{
+    using V = Vec8<T>;
+    using K = Keys<T>;
+    constexpr bool TABLE = __is_same(T, __bf16);
+    constexpr uint32_t AHEAD = 4, CELL = WAVES * 64 * VEC;
+    int lowest = -K::INF + 1;
+    if (b.hi < BINS) {
+        int h;
+        bin_range<T>(b.hi, lowest, h);
+        lowest = lowest > -K::INF ? lowest : -K::INF + 1;
+    }
+    if (TABLE) {   // the weights of the bins above the border, so that no element needs its own exponential
+#pragma unroll 1
+        for (int i = threadIdx.x; i < BINS - 1; i += WAVES * 64) {
+            int l, h;
+            bin_range<T>(i, l, h);
+            uint64_t w = 0;
+            if ((i < b.lo) & (l <= wt.max_key) & bin_exact<T>(i)) w = weight(l);
+            sh.mass[i] = w >= w_min ? w : 0;
+        }
+        __syncthreads();
+    }
+#pragma unroll 1
+    for (uint32_t c = c0; c < c1; c += AHEAD) {
+        V v[AHEAD];
+#pragma unroll
+        for (uint32_t q = 0; q < AHEAD; ++q)
+            if (c + q < c1) v[q] = row.raw((c + q) * CELL + threadIdx.x * VEC);
+#pragma unroll
+        for (uint32_t q = 0; q < AHEAD; ++q)
+            if (c + q < c1) {
+                const uint32_t j = (c + q) * CELL + threadIdx.x * VEC;
+                row.finish(v[q], j);
+                if (!__any(v[q].max() >= lowest)) continue;
+                uint64_t sum = 0;
+                uint32_t in_border = 0;
+                bool slow = !TABLE;
+                if (TABLE) {
+                    uint64_t w[VEC];
+                    bool odd = false;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const int key = v[q].at(e), bin = bin_of<T>(key);
+                        w[e] = sh.mass[bin];
+                        in_border += (bin >= b.lo) & (key >= lowest);
+                        odd |= (key >= lowest) & !bin_exact<T>(bin);
+                    }
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) sum += w[e];
+                    slow = __any(odd | (b.listed & (in_border != 0)));
+                    if (slow) in_border = 0;
+                }
+                if (slow) {
+#pragma unroll 1
+                    for (int e = 0; e < VEC; ++e) {
+                        const int key = v[q].pick(e), bin = bin_of<T>(key);
+                        const bool in = key >= lowest;
+                        if (in & (bin >= b.lo)) {
+                            ++in_border;
+                            if (b.listed) {
+                                const uint32_t at = atomicAdd(&sh.n_list, 1u);
+                                if (at < LIST) sh.list[at] = (uint64_t)((uint32_t)key ^ 0x80000000u) << 32 | ~(j + e);
+                            }
+                        }
+                        const bool own = in & (bin < b.lo) & !bin_exact<T>(bin);
+                        if (__any(own)) {
+                            const uint64_t w = wt.of(key, K::value(key));
+                            sum += own && w >= w_min ? w : 0;
+                        }
+                    }
+                }
+                if (__any(in_border != 0)) {
+                    const uint32_t all = wave_incl_sum(in_border);
+                    if ((threadIdx.x & 63) == 63) atomicAdd(&sh.border[c + q], all);
+                }
+                if (__any(sum != 0)) {
+                    const uint64_t all = wave_scan(sum);
+                    if ((threadIdx.x & 63) == 63) atomicAdd((unsigned long long *)&sh.cell[c + q], (unsigned long long)all);
+                }
+            }
+    }
+}
+
+// Sorts the first n (at most LIST) of sh.list, descending; a power of two from n on is padded with zeros.
+template <int WAVES> __device__ __forceinline__ void sort_list(Lds<WAVES> &sh, uint32_t n)
+{
+    uint32_t size = 2;
+    while (size < n) size *= 2;
+    for (uint32_t i = n + threadIdx.x; i < size; i += WAVES * 64) sh.list[i] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (uint32_t run = 2; run <= size; run *= 2)
+#pragma unroll 1
+        for (uint32_t stride = run / 2; stride; stride /= 2) {
+#pragma unroll 1
+            for (uint32_t t = threadIdx.x; t < size / 2; t += WAVES * 64) {
+                const uint32_t i = 2 * t - (t & (stride - 1)), o = i + stride;
+                const uint64_t a = sh.list[i], b = sh.list[o];
+                if ((a < b) == ((i & run) == 0)) {
+                    sh.list[i] = b;
+                    sh.list[o] = a;
+                }
+            }
+            // pairs less than 64 apart stay inside the 128 elements of one wavefront
+            const uint32_t next = stride > 1 ? stride / 2 : run;
+            if (stride >= 64 || next >= 64) __syncthreads();
+            else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+    __syncthreads();
+}
+
+// The cell, or the thread, at which the running sum exceeds the target: every thread brings its part.
+template <int WAVES>
+__device__ __forceinline__ uint32_t find_part(Lds<WAVES> &sh, uint64_t part, uint64_t target, uint64_t &before)
+{
+    uint64_t total;
+    const uint64_t run = block_before<WAVES>(part, sh.wave, total);
+    if (run <= target && target < run + part) {
+        sh.found = threadIdx.x;
+        sh.above = run;
+    }
+    __syncthreads();
+    const uint32_t at = sh.found;
+    before = sh.above;
+    __syncthreads();
+    return at;
+}
+
+// ---- draw
+template <class T, int WAVES, class W>
+__device__ __forceinline__ void draw(const Row<T> &row, Lds<WAVES> &sh, const Border &b, uint64_t w_min, W weight, uint32_t *out_id,
+                                     float *out_logprob)
+{
+    using K = Keys<T>;
+    using V = Vec8<T>;
+    constexpr uint32_t THREADS = WAVES * 64, CELL = THREADS * VEC, CELL_SHIFT = __builtin_ctz(CELL);
+    const uint32_t cells = (row.n + CELL - 1) / CELL, tid = threadIdx.x;
+    int key_f = -K::INF + 1;
+    uint32_t cut = NO_ID;
+    auto kept_weight = [&](int key) INLINE {
+        const uint64_t w = weight(key);
+        return w >= w_min ? w : 0ull;
+    };
+    if (b.listed) {
+        const uint32_t n = sh.n_list;
+        sort_list(sh, n);
+        // each thread's consecutive elements, their weights in sh.mass
+        const uint32_t per = (n + THREADS - 1) / THREADS, i0 = tid * per;
+        const uint32_t limit = b.by_k && b.left_k < n ? (uint32_t)b.left_k : n;
+        uint64_t mine = 0, all;
+#pragma unroll 1
+        for (uint32_t i = i0; i < i0 + per && i < limit; ++i) {
+            const uint64_t w = weight((int)((uint32_t)(sh.list[i] >> 32) ^ 0x80000000u));
+            sh.mass[i] = w;
+            mine += w;
+        }
+        uint64_t run = block_before<WAVES>(mine, sh.wave, all);
+        const uint64_t target = !b.by_p ? ~0ull : b.left_p ? b.left_p : share_of(row.p, all);
+        if (tid == 0) sh.found = 0;
+        __syncthreads();
+        uint32_t kept = 0;
+#pragma unroll 1
+        for (uint32_t i = i0; i < i0 + per && i < limit && run < target; ++i) {
+            const uint64_t w = sh.mass[i];
+            ++kept;
+            run += w;
+            if (w >= w_min) atomicAdd((unsigned long long *)&sh.cell[~(uint32_t)sh.list[i] >> CELL_SHIFT], (unsigned long long)w);
+        }
+        if (kept) atomicMax(&sh.found, i0 + kept);
+        __syncthreads();
+        const uint64_t last = sh.list[sh.found - 1];
+        key_f = (int)((uint32_t)(last >> 32) ^ 0x80000000u);
+        cut = ~(uint32_t)last;
+        __syncthreads();
+    } else if (b.hi < BINS) {
+        key_f = b.key;
+        const uint64_t w = kept_weight(key_f);
+        uint64_t full = tid < cells ? sh.border[tid] : 0;
+        if (b.ties < b.count) {   // the last of the equals that are kept: its cell, then its place there
+            uint64_t before, before_thread;
+            const uint32_t c = find_part(sh, full, b.ties - 1, before);
+            const uint32_t j = c * CELL + tid * VEC;
+            V v = row.raw(j);
+            row.finish(v, j);
+            uint32_t equal = 0;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) equal += v.at(e) == key_f;
+            const uint32_t t = find_part(sh, (uint64_t)equal, b.ties - 1 - before, before_thread);
+            if (tid == t) {
+                uint64_t at = before + before_thread;
+#pragma unroll 1
+                for (int e = 0; e < VEC; ++e)
+                    if (v.pick(e) == key_f && ++at == b.ties) sh.found = j + e;
+            }
+            __syncthreads();
+            cut = sh.found;
+            __syncthreads();
+            full = tid < c ? full : tid == c ? b.ties - before : 0;
+        }
+        if (tid < cells) sh.cell[tid] += full * w;
+        __syncthreads();
+    }
+    // the cell, the thread's vector in it, the element
+    uint64_t total, before, before_thread;
+    const uint64_t mass = tid < cells ? sh.cell[tid] : 0;
+    block_before<WAVES>(mass, sh.wave, total);
+    const double u = row.u > 0.f ? (double)fminf(row.u, 0x1.fffffep-1f) : 0.0;
+    uint64_t target = (uint64_t)(u * (double)total);
+    const uint32_t c = find_part(sh, mass, target, before), j = c * CELL + tid * VEC;
+    target -= before;
+    V v = row.raw(j);
+    row.finish(v, j);
+    uint64_t sum = 0;
+    auto amount = [&](int e) INLINE {
+        const int key = v.pick(e);
+        const bool in = (key > key_f) | ((key == key_f) & (j + e <= cut));
+        return __any(in) ? (in ? kept_weight(key) : 0ull) : 0ull;
+    };
+    if (__any(v.max() >= key_f)) {
+#pragma unroll 1
+        for (int e = 0; e < VEC; ++e) sum += amount(e);
+    }
+    const uint32_t t = find_part(sh, sum, target, before_thread);
+    if (tid == t) {
+        uint64_t run = before_thread;
+#pragma unroll 1
+        for (int e = 0; e < VEC; ++e) {
+            const uint64_t w = amount(e);
+            run += w;
+            if (run > target) {
+                *out_id = j + e;
+                if (out_logprob) *out_logprob = (float)log((double)w / (double)total);
+                break;
+            }
+        }
+    }
+}
+
+// Any row, by one search: histograms over bins and then over digits of the key, for counts and for masses, and
+// the ID by running masses.  For borders with more elements than the list holds.
+template <class T, int WAVES>
+__device__ __attribute__((noinline)) void general_row(const Row<T> &in, Lds<WAVES> &sh, double magic, uint32_t *out_id, float *out_logprob)
+{
+    using K = Keys<T>;
+    using V = Vec8<T>;
+    constexpr uint32_t THREADS = WAVES * 64;
+    constexpr bool TABLE = __is_same(T, __bf16);   // a weight per bin
+    const Row<T> row = in;
+    const uint32_t n_vocab = row.n;
+    const uint32_t tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    // a wavefront's segment: nv * 512 consecutive elements, a vector of each lane per step
+    const uint32_t nv = (n_vocab + THREADS * VEC - 1) / (THREADS * VEC), first = wave * (nv * 64 * VEC) + lane * VEC;
+    const float temp = row.temp, p = row.p, mp = row.min_p, u_in = row.u;
+    const uint32_t k = row.k;
+
+    // 1. the largest key, of each thread and of all
+    int mine, top;
+#pragma unroll 1
+    for (;;) {
+        constexpr uint32_t AHEAD = sizeof(T) == 4 ? 4 : 8;   // vectors of a thread in flight
+        mine = (int)0x80000000;
+#pragma unroll 1
+        for (uint32_t i = 0; i < nv; i += AHEAD) {
+            V v[AHEAD];
+#pragma unroll
+            for (uint32_t q = 0; q < AHEAD; ++q)
+                if (i + q < nv) v[q] = row.raw(first + (i + q) * (64 * VEC));
+#pragma unroll
+            for (uint32_t q = 0; q < AHEAD; ++q)
+                if (i + q < nv) {
+                    row.finish(v[q], first + (i + q) * (64 * VEC));
+                    const int m = v[q].max();
+                    mine = m > mine ? m : mine;
+                }
+        }
+        int m = mine;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) {
+            const int o = __shfl_xor(m, d);
+            m = o > m ? o : m;
+        }
+        if (lane == 0) sh.wave[wave] = (uint32_t)m;
+        __syncthreads();
+        top = (int)0x80000000;
+#pragma unroll 1
+        for (int w = 0; w < WAVES; ++w) top = (int)(uint32_t)sh.wave[w] > top ? (int)(uint32_t)sh.wave[w] : top;
+        __syncthreads();
+        break;
+    }
+    constexpr int LOWEST = -K::INF + 1;   // the smallest key in the choice
+    if (top < LOWEST) {                   // nothing to choose from
+        if (tid == 0) {
+            *out_id = NO_ID;
+            if (out_logprob) *out_logprob = -__builtin_inff();
+        }
+        return;
+    }
+    const Weights wt{1.4426950408889634 / (double)temp, (double)K::value(top), magic, top};
+    auto weight = [&](int key) { return weight_of<T>(wt.c, wt.max, wt.magic, wt.max_key, key); };
+    const bool first_alone = k == 1 || !(temp > 0.f);
+    const bool need_k = !first_alone && k != 0 && k < n_vocab, need_p = !first_alone && p < 1.f;
+
+    // Kept so far: keys above key_f, and of those equal to it (count_f of them) the first `ties`, which are those
+    // up to index `cut`; count_f 0: no filter, all are kept.
+    int key_f = first_alone ? top : LOWEST;
+    uint64_t ties = 1, count_f = first_alone ? 2 : 0;
+    uint32_t cut = NO_ID;
+    // A step is one pass over elements lo <= key <= hi, each with an amount: 1, or its weight.
+    enum { FLOOR, BIN, DIGITS, NTH, DRAW };
+    int step = first_alone ? NTH : need_k ? (k <= THREADS / 2 ? FLOOR : BIN) : need_p ? BIN : DRAW;
+    bool by_mass = !need_k;                            // of a search: top-p's
+    int lo = first_alone ? top : LOWEST, hi = K::INF;  // of the pass
+    int shift = 0, above_shift = 0;                    // of DIGITS: which digit of hi - key
+    uint32_t prefix = 0;
+    uint64_t target = 0, excess = 0;                   // excess: what the equals of top-k's key beyond its ties weigh
+    int key_k = K::INF + 1;
+    // of NTH and DRAW: 0 per wavefront, 1 per thread inside a wavefront's segment, 2 per element inside a thread's
+    int level = 0;
+    uint32_t begin = first, stride_v = 64 * VEC, count_v = nv, from = 0, until = n_vocab;
+    uint64_t base = 0, total = 0;
+    const uint64_t min_p_weight = mp >= 1.f ? wt.one() : mp > 0.f ? (uint64_t)__builtin_ceil((double)mp * (double)wt.one()) : 0;
+#pragma unroll 1
+    for (;;) {
+        const bool hist = step <= DIGITS;
+        const bool weighted = step == DRAW || (by_mass && (step == BIN || step == DIGITS));
+        const uint64_t w_min = step == DRAW ? min_p_weight : 0;
+        uint64_t sum = 0;
+        int key_in = 0;
+        if (hist || (TABLE && step == DRAW && level == 0)) {
+#pragma unroll 1
+            for (uint32_t b = tid; b < BINS; b += THREADS) {
+                uint64_t w = 0;
+                if (TABLE && !hist) {   // the draw takes the weights of bins with one key from a table
+                    int l, h;
+                    bin_range<T>((int)b, l, h);
+                    if ((l >= key_f) & (l <= top)) w = weight(l);
+                    w = w >= w_min ? w : 0;
+                }
+                sh.mass[b] = w;
+            }
+            __syncthreads();
+        }
+        if (step == FLOOR) {
+            // k threads with a key >= f hold at least k such keys, so nothing below the k-th largest of the
+            // threads' own largest keys (or its bin's lowest key) can be among the first k
+            if (mine >= LOWEST) atomicAdd((unsigned long long *)&sh.mass[bin_of<T>(mine)], 1ull);
+        } else {
+            V next = row.raw(begin);
+#pragma unroll 1
+            for (uint32_t i = 0; i < count_v; ++i) {
+                const uint32_t j = begin + i * stride_v;
+                V v = next;
+                if (i + 1 < count_v) next = row.raw(j + stride_v);
+                row.finish(v, j);
+                if (!__any(v.max() >= lo)) continue;
+#pragma unroll 1
+                for (int e = 0; e < VEC; ++e) {
+                    const int key = v.pick(e);
+                    const uint32_t at = j + e;
+                    const bool in = (key >= lo) & (key <= hi) & ((key != key_f) | (at <= cut)) & (at >= from) & (at < until);
+                    if (!__any(in)) continue;
+                    const int b = bin_of<T>(key);
+                    uint64_t amount = 1;
+                    if (weighted) {
+                        bool own = true;
+                        if (TABLE) {
+                            if (step == DRAW) amount = sh.mass[b];
+                            own = in & !bin_exact<T>(b);   // (an exact bin's histogram holds counts until it is complete)
+                        }
+                        if (__any(own)) {
+                            const uint64_t w = wt.of(key, K::value(key));
+                            amount = own ? (w >= w_min ? w : 0) : amount;
+                        }
+                    }
+                    if (hist) {
+                        const uint32_t d = (uint32_t)(hi - key);
+                        if (in & (step == BIN || (above_shift < 32 ? d >> above_shift : 0u) == prefix))
+                            atomicAdd((unsigned long long *)&sh.mass[step == BIN ? (uint32_t)b : (d >> shift) & (BINS - 1)],
+                                      (unsigned long long)amount);
+                    } else if (in) {
+                        sum += amount;
+                        key_in = key;
+                    }
+                }
+            }
+        }
+        // sums in the order of the histogram's bins, or of the threads' elements
+        constexpr uint32_t PER = BINS / THREADS;
+        if (hist) {
+            __syncthreads();
+            if (weighted && excess && tid == 0) {
+                const uint32_t d = (uint32_t)(hi - key_k);
+                if (step == BIN) sh.mass[bin_of<T>(key_k)] -= TABLE && bin_exact<T>(bin_of<T>(key_k)) ? count_f - ties : excess;
+                else if ((key_k >= lo) & (key_k <= hi) & ((above_shift < 32 ? d >> above_shift : 0u) == prefix))
+                    sh.mass[(d >> shift) & (BINS - 1)] -= excess;
+            }
+            __syncthreads();
+#pragma unroll 1
+            for (uint32_t q = 0; q < PER; ++q) {
+                const uint32_t b = tid * PER + q;
+                uint64_t c = sh.mass[b];
+                if (TABLE && weighted && step == BIN && c && bin_exact<T>((int)b)) {
+                    int l, h;
+                    bin_range<T>((int)b, l, h);
+                    c *= weight(l);
+                    sh.mass[b] = c;
+                }
+                sum += c;
+            }
+        }
+        const uint64_t incl = wave_scan(sum);
+        if (lane == 63) sh.wave[wave] = incl;
+        __syncthreads();
+        uint64_t run = incl - sum, all = 0;
+#pragma unroll 1
+        for (uint32_t w = 0; w < WAVES; ++w) {
+            const uint64_t s = sh.wave[w];
+            run += w < wave ? s : 0;
+            all += s;
+        }
+        if (hist) {
+            if (step == FLOOR || step == BIN) {
+                target = k;
+                if (weighted) {
+                    const double t = __builtin_ceil((double)p * (double)all);
+                    target = t > 1.0 ? (uint64_t)t : 1ull;
+                    target = target < all ? target : all;
+                }
+            }
+            const bool enough = target <= all;   // else fewer than k are in the choice: the filter keeps all of them
+            if (enough && run < target && target <= run + sum) {
+#pragma unroll 1
+                for (uint32_t q = 0;; ++q) {
+                    const uint64_t c = sh.mass[tid * PER + q];
+                    if (target <= run + c) {
+                        sh.found = tid * PER + q;
+                        sh.above = run;
+                        sh.inside = c;
+                        break;
+                    }
+                    run += c;
+                }
+            }
+            __syncthreads();
+            const uint32_t slot = sh.found;
+            const uint64_t above = sh.above, inside = sh.inside;
+            __syncthreads();
+            bool done = !enough;   // with this search
+            if (step == FLOOR) {
+                if (enough) {
+                    bin_range<T>((int)slot, lo, hi);
+                    lo = lo < LOWEST ? LOWEST : lo;
+                }
+                hi = K::INF;
+                step = BIN;
+                continue;
+            }
+            int key = 0;
+            if (enough) {
+                target -= above;
+                if (step == BIN) {
+                    int l, h;
+                    bin_range<T>((int)slot, l, h);
+                    key = l;
+                    done = bin_exact<T>((int)slot);
+                    if (!done) {
+                        const int bits = 32 - __builtin_clz((uint32_t)(h - l));
+                        shift = (bits + DIGIT - 1) / DIGIT * DIGIT;
+                        prefix = 0;
+                        lo = l > lo ? l : lo;
+                        hi = h;
+                        step = DIGITS;
+                    }
+                } else {
+                    prefix = prefix << DIGIT | slot;
+                    key = hi - (int)prefix;
+                    done = shift == 0;
+                }
+            }
+            if (!done) {
+                above_shift = shift;
+                shift -= DIGIT;
+                continue;
+            }
+            if (enough) {
+                if (!by_mass) {
+                    ties = target;
+                    count_f = inside;
+                    key_k = key;
+                    if (need_p) excess = (count_f - ties) * weight(key);
+                } else {
+                    const uint64_t w = weight(key), need = (target + w - 1) / w;
+                    if (key == key_k) {
+                        ties = need < ties ? need : ties;
+                    } else {
+                        ties = need;
+                        count_f = inside / w;
+                    }
+                }
+                key_f = key;
+            }
+            hi = K::INF;
+            lo = key_f;
+            step = need_p && !by_mass ? BIN : ties < count_f ? NTH : DRAW;
+            by_mass = true;
+            if (step == NTH) hi = key_f;
+        } else {
+            if (level == 0) {
+                total = all;
+                target = ties - 1;
+                if (step == DRAW) {
+                    const double u = u_in > 0.f ? (double)fminf(u_in, 0x1.fffffep-1f) : 0.0;
+                    target = (uint64_t)(u * (double)all);
+                }
+                // (the wavefront's sum, not the thread's: its elements alternate between the lanes)
+                run -= incl - sum;
+                sum = sh.wave[wave];
+            }
+            run += base;
+            if ((level || lane == 0) && run <= target && target < run + sum) {
+                sh.above = run;
+                sh.found = level ? from : wave * (nv * 64 * VEC);
+                sh.key = key_in;
+            }
+            __syncthreads();
+            const uint32_t start = sh.found;
+            base = sh.above;
+            key_in = sh.key;
+            __syncthreads();
+            const uint32_t per = (nv + WAVES - 1) / WAVES;   // vectors per thread of a segment
+            if (level == 0) {
+                const uint32_t end = start + nv * 64 * VEC;
+                from = start + tid * per * VEC;
+                until = from + per * VEC < end ? from + per * VEC : end;
+                until = until < n_vocab ? until : n_vocab;
+                begin = from;
+                stride_v = VEC;
+                count_v = from < until ? per : 0;
+            } else if (level == 1) {
+                from = start + tid;
+                until = from + 1;
+                begin = from & ~(uint32_t)(VEC - 1);
+                count_v = tid < per * VEC && from < n_vocab ? 1 : 0;
+            } else {
+                if (step == NTH && !first_alone) {   // now the draw
+                    cut = start;
+                    hi = K::INF;
+                    step = DRAW;
+                    level = 0;
+                    begin = first;
+                    stride_v = 64 * VEC;
+                    count_v = nv;
+                    from = 0;
+                    until = n_vocab;
+                    base = 0;
+                    continue;
+                }
+                if (tid == 0) {
+                    *out_id = start;
+                    if (out_logprob) *out_logprob = first_alone ? 0.f : (float)log((double)weight(key_in) / (double)total);
+                }
+                return;
+            }
+            ++level;
+        }
+    }
+}
+
+
+template <class T>
+__device__ __forceinline__ Row<T> row_of(const T *logits, uint32_t n_vocab, uint64_t stride, const uint32_t *mask, uint64_t mask_stride,
+                                         const float *temperature, const uint32_t *top_k, const float *top_p, const float *min_p,
+                                         const float *uniform, uint64_t r)
+{
+    return Row<T>{logits + r * stride, mask ? mask + r * mask_stride : nullptr, n_vocab, temperature ? temperature[r] : 1.f,
+                  top_p ? top_p[r] : 1.f, min_p ? min_p[r] : 0.f, uniform[r], top_k ? top_k[r] : 0};
+}
+
+// One workgroup, all phases.
+template <class T, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void k_sample(const T *__restrict__ logits, uint32_t n_vocab, uint64_t stride,
                                                        const uint32_t *__restrict__ mask, uint64_t mask_stride,
                                                        const float *__restrict__ temperature,
@@ -445,289 +1079,79 @@ __global__ __launch_bounds__(WAVES * 64) void k_sample(const T *__restrict__ log
                                                        double magic)
 {
     using K = Keys<T>;
-    using V = Vec8<T>;
-    constexpr int THREADS = WAVES * 64;
-    constexpr bool TABLE = __is_same(T, __bf16);   // a weight per bin
-    __shared__ Shared<WAVES> sh;
+    constexpr uint32_t THREADS = WAVES * 64, CELL = THREADS * VEC;
+    constexpr bool TABLE = __is_same(T, __bf16);
+    __shared__ Lds<WAVES> sh;
     const uint64_t r = blockIdx.x;
-    Row<T, WAVES, NV> row;
-    row.x = logits + r * stride;
-    row.mask = mask ? mask + r * mask_stride : nullptr;
-    row.n = n_vocab;
-    row.nv = (n_vocab + THREADS * VEC - 1) / (THREADS * VEC);
-    row.first = (threadIdx.x >> 6) * (row.nv * 64 * VEC) + (threadIdx.x & 63) * VEC;
-    row.nan = false;
-    row.load();
-    const float temp = temperature ? temperature[r] : 1.f;
-    const uint32_t k = top_k ? top_k[r] : 0;
-    const float p = top_p ? top_p[r] : 1.f, mp = min_p ? min_p[r] : 0.f, u_in = uniform[r];
+    const uint32_t tid = threadIdx.x, cells = (n_vocab + CELL - 1) / CELL;
+    const Row<T> row = row_of(logits, n_vocab, stride, mask, mask_stride, temperature, top_k, top_p, min_p, uniform, r);
+    float *out_logprob = out_logprobs ? out_logprobs + r : nullptr;
+    const bool first_alone = row.k == 1 || !(row.temp > 0.f);
+    const bool filtered = !first_alone && ((row.k != 0 && row.k < n_vocab) || row.p < 1.f);
 
-    // 1. the largest key, of each thread and of all
-    int mine, top;
-    for (;;) {
-        mine = (int)0x80000000;
-        row.each([&](uint32_t, const V &v) INLINE {
-            const int m = v.max();
-            mine = m > mine ? m : mine;
-        });
-        int m = mine;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) {
-            const int o = __shfl_xor(m, d);
-            m = o > m ? o : m;
-        }
-        if ((threadIdx.x & 63) == 0) sh.wave[threadIdx.x >> 6] = (uint32_t)m;
-        __syncthreads();
-        top = (int)(uint32_t)sh.wave[0];
-#pragma unroll 4
-        for (int w = 0; w < WAVES; ++w) top = (int)(uint32_t)sh.wave[w] > top ? (int)(uint32_t)sh.wave[w] : top;
-        __syncthreads();
-        if (sizeof(T) == 4 || top <= K::INF) break;
-        row.nan = true;   // NaN of 16 bits: take them out and look again
-        if constexpr (NV > 0) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i < (int)row.nv) row.drop_nan(row.held[i]);
-        }
+    for (int b = tid; b < BINS; b += THREADS) sh.count[b] = 0;
+    if (tid < MAX_CELLS) {
+        sh.cell[tid] = 0;
+        sh.border[tid] = 0;
     }
-    constexpr int LOWEST = -K::INF + 1;   // the smallest key in the choice
-    if (top < LOWEST) {                   // nothing to choose from
-        if (threadIdx.x == 0) {
-            out_ids[r] = NO_ID;
-            if (out_logprobs) out_logprobs[r] = -__builtin_inff();
+    if (tid == 0) sh.n_list = sh.n_odd = 0;
+    __syncthreads();
+    int mine;
+    uint32_t mine_j;
+    scan_keys<T, WAVES>(row, sh, 0, cells, filtered, mine, mine_j);
+    const uint64_t best = block_best<T, WAVES>(row, sh, mine, mine_j);
+    const int top = (int)((uint32_t)(best >> 32) ^ 0x80000000u);
+    if (top <= -K::INF || first_alone) {   // nothing to choose from, or the first alone
+        if (tid == 0) {
+            out_ids[r] = top <= -K::INF ? NO_ID : ~(uint32_t)best;
+            if (out_logprob) *out_logprob = top <= -K::INF ? -__builtin_inff() : 0.f;
         }
         return;
     }
-    const bool first_alone = k == 1 || !(temp > 0.f);
-    const Weights wt{1.4426950408889634 / (double)temp, (double)K::value(top), magic, top};
-    auto weight = [&](int key) INLINE { return wt.of(key, K::value(key)); };
-
-    // 2. kept so far: keys above key_f, and of those equal to it (count_f of them) the first `ties`
-    int key_f = first_alone ? top : LOWEST;
-    uint64_t ties = 1, count_f = first_alone ? 2 : 0;   // count_f 0: no filter so far, all are kept
-    const bool need_k = !first_alone && k != 0 && k < n_vocab, need_p = !first_alone && p < 1.f;
-    if (need_k || need_p) {
-        int floor = LOWEST;
-        bool found;
-        uint32_t bin_k = BINS;
-        uint64_t above, inside, target;
-        auto count_of = [&](int i) INLINE { return (uint64_t)sh.count[i]; };
-        auto target_k = [&](uint64_t) INLINE { return (uint64_t)k; };
-        auto clear_counts = [&]() INLINE {
-            for (int b = threadIdx.x; b < BINS; b += THREADS) sh.count[b] = 0;
-            __syncthreads();
-        };
-        // Two rounds for a small k: k threads with a key >= f hold at least k such keys, so nothing below the
-        // k-th largest of the threads' own largest keys (or its bin's lowest key) can be kept.
-        for (int round = need_k && k <= THREADS / 2 ? 0 : 1;; ++round) {
-            if (need_p && round)
-                for (int b = threadIdx.x; b < BINS; b += THREADS) sh.mass[b] = 0;
-            clear_counts();
-            if (round == 0) {
-                if (mine >= LOWEST) atomicAdd(&sh.count[bin_of<T>(mine)], 1u);
-            } else {
-                row.each([&](uint32_t, const V &v) INLINE {
-                    if (!__any(v.max() >= floor)) return;
-                    int b[VEC];
-                    v.bins(b);
-                    bool more = false;
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        if (v.at(e) >= floor) {
-                            atomicAdd(&sh.count[b[e]], 1u);
-                            more |= !bin_exact<T>(b[e]);
-                        }
-                    if (need_p && __any(more)) {
-#pragma unroll 1
-                        for (int e = 0; e < VEC; ++e) {
-                            const int key = v.pick(e), bin = bin_of<T>(key);
-                            if (key >= floor && !bin_exact<T>(bin))
-                                atomicAdd((unsigned long long *)&sh.mass[bin], (unsigned long long)weight(key));
-                        }
-                    }
-                });
-            }
-            __syncthreads();
-            found = need_k && find_bin<BINS>(sh, count_of, target_k, bin_k, above, inside, target);
-            if (round) break;
-            if (found) {
-                int hi;
-                bin_range<T>((int)bin_k, floor, hi);
-                floor = floor < LOWEST ? LOWEST : floor;
-            }
-        }
-        if (need_p && TABLE) {
-#pragma unroll 1
-            for (int b = threadIdx.x; b < BINS - 1; b += THREADS)
-                if (bin_exact<T>(b) && sh.count[b]) {
-                    int lo, hi;
-                    bin_range<T>(b, lo, hi);
-                    sh.mass[b] = sh.count[b] * weight(lo);
-                }
-            __syncthreads();
-        }
-        // Stage 0 by counts, stage 1 by masses: the bin where the filter ends, then the exact key in it, by the
-        // running sum over the digits of hi - key, highest digit first (overwrites the counts).
-        const bool cut_k = found;
-        uint64_t excess = 0, mass_k = 0;   // mass of what lies beyond the ties of key_f; of the kept part of bin_k
-        int from = LOWEST;
-        for (int stage = cut_k ? 0 : 1; stage < (need_p ? 2 : 1); ++stage) {
-            uint32_t bin = bin_k;
-            if (stage) {
-                find_bin<BINS>(sh, [&](int i) INLINE {
-                    return !cut_k || i < (int)bin_k ? sh.mass[i] : i == (int)bin_k ? mass_k : 0ull;
-                }, [&](uint64_t all) INLINE {
-                    const double t = __builtin_ceil((double)p * (double)all);
-                    const uint64_t q = t > 1.0 ? (uint64_t)t : 1ull;
-                    return q < all ? q : all;
-                }, bin, above, inside, target);
-            }
-            int lo, hi;
-            bin_range<T>((int)bin, lo, hi);
-            uint64_t left = target - above;   // to be reached inside the bin
-            const int key_k = key_f;
-            const bool last = stage && cut_k && bin == bin_k;
-            if (last && from < key_k) from = key_k;
-            key_f = lo;
-            if (!bin_exact<T>((int)bin)) {
-                const int bits = 32 - __builtin_clz((uint32_t)(hi - lo));
-                int shift = (bits + DIGIT - 1) / DIGIT * DIGIT;
-                uint32_t prefix = 0;
-                while (shift > 0) {
-                    const int up = shift;
-                    shift -= DIGIT;
-                    for (int b = threadIdx.x; b < DIGITS; b += THREADS) sh.digit[b] = 0;
-                    __syncthreads();
-                    auto add = [&](int key, uint64_t amount) INLINE {
-                        const uint32_t d = (uint32_t)(hi - key);
-                        if ((up < 32 ? d >> up : 0u) == prefix)
-                            atomicAdd((unsigned long long *)&sh.digit[(d >> shift) & (DIGITS - 1)], (unsigned long long)amount);
-                    };
-                    row.each([&](uint32_t, const V &v) INLINE {
-                        if (!__any(v.max() >= lo)) return;
-#pragma unroll 1
-                        for (int e = 0; e < VEC; ++e) {
-                            const int key = v.pick(e);
-                            if (key >= lo && key <= hi && key >= from) add(key, stage ? weight(key) : 1ull);
-                        }
-                    });
-                    if (threadIdx.x == 0 && last && excess) add(key_k, 0ull - excess);
-                    __syncthreads();
-                    uint32_t digit;
-                    uint64_t a, t;
-                    find_bin<DIGITS>(sh, [&](int i) INLINE { return sh.digit[i]; }, [&](uint64_t) INLINE { return left; }, digit, a,
-                                     inside, t);
-                    left -= a;
-                    prefix = prefix << DIGIT | digit;
-                }
-                key_f = hi - (int)prefix;
-            }
-            if (stage == 0) {
-                ties = left;
-                count_f = inside;
-                if (need_p) {   // what its bin holds below key_f, and of its equals beyond the ties, is no longer kept
-                    const uint64_t w = weight(key_f);
-                    excess = (count_f - ties) * w;
-                    mass_k = ties * w;
-                    if (!bin_exact<T>((int)bin)) {
-                        uint64_t part = 0;
-                        row.each([&](uint32_t, const V &v) INLINE {
-                            if (!__any(v.max() >= key_f)) return;
-#pragma unroll 1
-                            for (int e = 0; e < VEC; ++e) {
-                                const int key = v.pick(e);
-                                if (key >= key_f && key <= hi) part += weight(key);
-                            }
-                        });
-                        block_before(part, sh, mass_k);
-                        mass_k -= excess;
-                    }
-                }
-            } else {
-                const uint64_t w = weight(key_f), need = (left + w - 1) / w;
-                if (last && key_f == key_k) {
-                    ties = need < ties ? need : ties;
-                } else {
-                    count_f = inside / w;
-                    ties = need;
-                }
-            }
-        }
-    }
-    uint32_t id = NO_ID;   // the last index whose key may equal key_f
-    uint64_t total;
-    int key_at;
-    if (ties < count_f)
-        id = locate<WAVES>(row, sh, [&](const V &v, uint32_t) INLINE {
-            uint64_t n = 0;
-            if (__any(v.max() >= key_f)) {
-                uint32_t c = 0;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) c += v.at(e) == key_f;
-                n = c;
-            }
-            return n;
-        }, [&](const V &v, uint32_t, int e) INLINE { return (uint64_t)(v.pick(e) == key_f); },
-        [&](uint64_t) INLINE { return ties - 1; }, total, key_at);
-    if (first_alone) {
-        if (threadIdx.x == 0) {
-            out_ids[r] = id;
-            if (out_logprobs) out_logprobs[r] = 0.f;
-        }
-        return;
-    }
-
-    // 3. the draw
-    const uint32_t cut = id;
+    const Weights wt{1.4426950408889634 / (double)row.temp, (double)K::value(top), magic, top};
+    auto weight = [&](int key) INLINE { return weight_of<T>(wt.c, wt.max, wt.magic, wt.max_key, key); };
     const uint64_t one = wt.one();
-    const uint64_t w_min = mp >= 1.f ? one : mp > 0.f ? (uint64_t)__builtin_ceil((double)mp * (double)one) : 0;
-    const double u = u_in > 0.f ? (double)fminf(u_in, 0x1.fffffep-1f) : 0.0;
-    if (TABLE) {   // the weights of the kept bins, so that no element needs its own exponential
-        __syncthreads();
-#pragma unroll 1
-        for (int b = threadIdx.x; b < BINS - 1; b += THREADS) {
-            int lo, hi;
-            bin_range<T>(b, lo, hi);
-            if (bin_exact<T>(b) && lo <= top) {
-                const uint64_t w = lo >= key_f ? weight(lo) : 0;
-                sh.mass[b] = w >= w_min ? w : 0;
+    const uint64_t w_min = row.min_p >= 1.f ? one : row.min_p > 0.f ? (uint64_t)__builtin_ceil((double)row.min_p * (double)one) : 0;
+    Border b{};
+    b.lo = b.hi = BINS;
+    if (filtered)
+        b = find_border<T, WAVES>(row, sh, weight, [&](uint32_t bin_k) INLINE {
+            for (int i = tid; i < BINS; i += THREADS) {
+                uint64_t m = 0;
+                if (TABLE && i <= (int)bin_k && bin_exact<T>(i) && sh.count[i]) {
+                    int lo, hi;
+                    bin_range<T>(i, lo, hi);
+                    m = sh.count[i] * weight(lo);
+                }
+                sh.mass[i] = m;
             }
-        }
-        __syncthreads();
-    }
-    auto kept = [&](int key, uint32_t j) INLINE { return key > key_f || (key == key_f && j <= cut); };
-    auto element = [&](const V &v, uint32_t j, int e) INLINE {
-        const int key = v.pick(e);
-        const uint64_t w = weight(key);
-        return kept(key, j + e) && w >= w_min ? w : 0ull;
-    };
-    id = locate<WAVES>(row, sh, [&](const V &v, uint32_t j) INLINE {
-        uint64_t sum = 0;
-        if (!__any(v.max() >= key_f)) return sum;
-        bool each = !TABLE;
-        if (TABLE) {
-            int b[VEC];
-            v.bins(b);
-            bool odd = false;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const bool in = kept(v.at(e), j + e);
-                odd |= in && !bin_exact<T>(b[e]);
-                if (in) sum += sh.mass[b[e]];
-            }
-            each = __any(odd);
-            if (each) sum = 0;
-        }
-        if (each) {
+            __syncthreads();
+            const uint32_t n = sh.n_odd;
+            if (TABLE && n <= ODD) {
+                for (uint32_t i = tid; i < n; i += THREADS) {
+                    const int key = (int)sh.odd[i];
+                    atomicAdd((unsigned long long *)&sh.mass[bin_of<T>(key)], (unsigned long long)weight(key));
+                }
+            } else {   // every element by itself
 #pragma unroll 1
-            for (int e = 0; e < VEC; ++e) sum += element(v, j, e);
-        }
-        return sum;
-    }, element, [&](uint64_t all) INLINE { return (uint64_t)(u * (double)all); }, total, key_at);
-    if (threadIdx.x == 0) {
-        out_ids[r] = id;
-        if (out_logprobs) out_logprobs[r] = (float)log((double)weight(key_at) / (double)total);
-    }
+                for (uint32_t c = 0; c < cells; ++c) {
+                    const uint32_t j = c * CELL + tid * VEC;
+                    Vec8<T> v = row.raw(j);
+                    row.finish(v, j);
+#pragma unroll 1
+                    for (int e = 0; e < VEC; ++e) {
+                        const int key = v.pick(e), bin = bin_of<T>(key);
+                        if ((key > -K::INF) & !bin_exact<T>(bin))
+                            atomicAdd((unsigned long long *)&sh.mass[bin], (unsigned long long)wt.of(key, K::value(key)));
+                    }
+                }
+            }
+            __syncthreads();
+        });
+    if (b.hard) return general_row<T, WAVES>(row, sh, magic, out_ids + r, out_logprob);
+    scan_cells<T, WAVES>(row, sh, wt, b, w_min, 0, cells, weight);
+    __syncthreads();
+    draw<T, WAVES>(row, sh, b, w_min, weight, out_ids + r, out_logprob);
 }
 
 // S = 45 fraction bits keep the sum of up to 2^18 weights of at most one below 2^63; one bit less for every doubling.
@@ -772,16 +1196,13 @@ extern "C" int toktier_sample(const void *logits, int type, uint32_t n_rows, uin
     const double magic = weight_magic(n_vocab);
     with_type(type, [&](auto t) {
         using T = decltype(t);
-        auto launch = [&](auto waves, auto nv) {
-            k_sample<T, decltype(waves)::value, decltype(nv)::value><<<n_rows, decltype(waves)::value * 64, 0, (hipStream_t)stream>>>(
-                (const T *)logits, n_vocab, stride, mask, mask_stride, temperature, top_k, top_p, min_p, uniform, out_ids, out_logprobs,
-                magic);
+        auto launch = [&](auto waves) {
+            constexpr int W = decltype(waves)::value;
+            k_sample<T, W><<<n_rows, W * 64, 0, (hipStream_t)stream>>>((const T *)logits, n_vocab, stride, mask, mask_stride, temperature,
+                                                                       top_k, top_p, min_p, uniform, out_ids, out_logprobs, magic);
         };
-        constexpr bool F32 = sizeof(T) == 4;
-        const uint32_t nv = (n_vocab + 1024 * VEC - 1) / (1024 * VEC);
-        if (n_vocab <= 256 * VEC * 4) launch(std::integral_constant<int, 4>{}, std::integral_constant<int, F32 ? 0 : 4>{});
-        else if (!F32 && nv <= 5) launch(std::integral_constant<int, 16>{}, std::integral_constant<int, F32 ? 0 : 5>{});
-        else launch(std::integral_constant<int, 16>{}, std::integral_constant<int, 0>{});
+        if (n_vocab <= 8192) launch(std::integral_constant<int, 4>{});
+        else launch(std::integral_constant<int, 16>{});
     });
     return hip_status(hipGetLastError());
 }
