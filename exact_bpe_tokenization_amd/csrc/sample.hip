@@ -84,6 +84,7 @@ template <class T> __device__ __forceinline__ bool bin_exact(int b)
 }
 
 typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 // Eight keys: packed in pairs for the 16-bit types.
 template <class T> struct Vec8 {
@@ -113,6 +114,35 @@ template <class T> struct Vec8 {
         for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, pair(i));
         return m.x > m.y ? m.x : m.y;
     }
+    // the bins of the keys; true where one of these holds several keys (the middle or the outermost ones)
+    __device__ __forceinline__ bool bins(int (&b)[VEC]) const
+    {
+        using K = Keys<T>;
+        u16x2 far = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const s16x2 k = pair(i), sign = k >> 15;
+            const u16x2 mag = __builtin_bit_cast(u16x2, __builtin_elementwise_max(k, (s16x2)-k));
+            u16x2 m = __builtin_elementwise_sub_sat(mag, (u16x2)(unsigned short)(K::LOW - (1 << K::SHIFT)));
+            m = __builtin_elementwise_min((u16x2)(m >> K::SHIFT), (u16x2)(unsigned short)HALF);
+            far = __builtin_elementwise_max(far, (u16x2)(m - (u16x2)(unsigned short)1));   // 0 becomes the largest
+            const s16x2 t = (s16x2)(short)HALF - ((__builtin_bit_cast(s16x2, m) ^ sign) - sign);
+            b[2 * i] = t.x;
+            b[2 * i + 1] = t.y;
+        }
+        return (far.x >= HALF - 1) | (far.y >= HALF - 1);
+    }
+    // how many of the keys are `key`
+    __device__ __forceinline__ uint32_t equals(int key) const
+    {
+        u16x2 other = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const s16x2 d = pair(i) - (s16x2)(short)key;
+            other += __builtin_elementwise_min(__builtin_bit_cast(u16x2, d), (u16x2)(unsigned short)1);
+        }
+        return VEC - other.x - other.y;
+    }
     // logits to keys, in place
     __device__ __forceinline__ void order()
     {
@@ -139,6 +169,19 @@ template <> struct Vec8<float> {
         else b[e - 4] = (uint32_t)v;
     }
     __device__ __forceinline__ void hide(int e) { set(e, (int)0x80000000); }
+    __device__ __forceinline__ bool bins(int (&b)[VEC]) const
+    {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) b[e] = bin_of<float>(at(e));
+        return true;
+    }
+    __device__ __forceinline__ uint32_t equals(int key) const
+    {
+        uint32_t n = 0;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) n += at(e) == key;
+        return n;
+    }
     __device__ __forceinline__ int max() const
     {
         int m = at(0);
@@ -156,36 +199,48 @@ template <> struct Vec8<float> {
     }
 };
 
-// Weights of one row.  2^y = 2^n 2^f with n the nearest integer: 2^f on [-1/2, 1/2] by the polynomial of degree
-// 10 that interpolates it at the Chebyshev nodes (relative error below 2^-51), the multiple of 2^-S by
-// adding 2^(52 - S) and reading the low bits.
+// p * f + c in one instruction: the compiler copies a constant addend to registers first, which doubles the work.
+__device__ __forceinline__ double fma_const(double p, double f, double c)
+{
+    double r;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(p), "v"(f), "s"(c));
+    return r;
+}
+
+// Weights of one row.  2^y = 2^n 2^f with n the nearest integer (y + 1.5 * 2^52 holds it in its low bits): 2^f on
+// [-1/2, 1/2] by the polynomial of degree 10 that interpolates it at the Chebyshev nodes (relative error below
+// 2^-51), the multiple of 2^-S by adding 2^(52 - S) and reading the low bits.
 struct Weights {
     double c, max, magic;
     int max_key;
 
-    __device__ __forceinline__ uint64_t one() const
+    static constexpr double HUGE_LOGIT = 1e300;   // in place of +inf, whose weight is one and all others' zero
+
+    // the weight as the low bits of a number whose high bits are those of `magic`; y below -80 gives zero
+    __device__ __forceinline__ uint64_t raw(float x, bool in = true) const
     {
-        return __builtin_bit_cast(uint64_t, 1.0 + magic) - __builtin_bit_cast(uint64_t, magic);
-    }
-    __device__ __forceinline__ uint64_t of(int key, float x) const
-    {
-        const double y = ((double)x - max) * c;
-        const double n = __builtin_rint(y), f = y - n;
+        const double d = __builtin_fmin((double)x, HUGE_LOGIT) - max;
+        double y = __builtin_fmax(d * c, -80.0);
+        y = in ? y : -80.0;
+        const double t = y + 0x1.8p52, f = y - (t - 0x1.8p52);
         double p = 7.072585949269224e-09;
-        p = __builtin_fma(p, f, 1.0208690299958306e-07);
-        p = __builtin_fma(p, f, 1.321544258792169e-06);
-        p = __builtin_fma(p, f, 1.5252657260200837e-05);
-        p = __builtin_fma(p, f, 0.0001540353044173605);
-        p = __builtin_fma(p, f, 0.0013333558230164974);
-        p = __builtin_fma(p, f, 0.009618129107606888);
-        p = __builtin_fma(p, f, 0.05550410866444772);
-        p = __builtin_fma(p, f, 0.24022650695910097);
-        p = __builtin_fma(p, f, 0.69314718055995);
-        p = __builtin_fma(p, f, 1.0);
-        const double w = __builtin_amdgcn_ldexp(p, (int)n);
-        const uint64_t q = __builtin_bit_cast(uint64_t, w + magic) - __builtin_bit_cast(uint64_t, magic);
-        return key == max_key ? one() : y > -64.0 ? q : 0ull;   // the largest may be +inf; y may be -inf or NaN
+        p = fma_const(p, f, 1.0208690299958306e-07);
+        p = fma_const(p, f, 1.321544258792169e-06);
+        p = fma_const(p, f, 1.5252657260200837e-05);
+        p = fma_const(p, f, 0.0001540353044173605);
+        p = fma_const(p, f, 0.0013333558230164974);
+        p = fma_const(p, f, 0.009618129107606888);
+        p = fma_const(p, f, 0.05550410866444772);
+        p = fma_const(p, f, 0.24022650695910097);
+        p = fma_const(p, f, 0.69314718055995);
+        p = fma_const(p, f, 1.0);
+        const uint32_t n = (uint32_t)__builtin_bit_cast(uint64_t, t);
+        const uint64_t q = __builtin_bit_cast(uint64_t, p) + ((uint64_t)(n << 20) << 32);
+        return __builtin_bit_cast(uint64_t, __builtin_bit_cast(double, q) + magic);
     }
+    __device__ __forceinline__ uint64_t zero() const { return __builtin_bit_cast(uint64_t, magic); }
+    __device__ __forceinline__ uint64_t of(int, float x) const { return raw(x) - zero(); }
+    __device__ __forceinline__ uint64_t one() const { return __builtin_bit_cast(uint64_t, 1.0 + magic) - zero(); }
 };
 
 // A kernel runs most of its code once per row, so fetching instructions costs more than issuing them: what is
@@ -195,14 +250,27 @@ template <class T> __device__ __attribute__((noinline)) uint64_t weight_of(doubl
     return Weights{c, max, magic, max_key}.of(key, Keys<T>::value(key));
 }
 
-template <class V> __device__ __forceinline__ V wave_scan(V v)
+// Inclusive sum over the wavefront's lanes, by DPP: no LDS round trips, which a shuffle would take.
+template <int CTRL, int ROWS> __device__ __forceinline__ uint64_t dpp_add(uint64_t v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const V o = __shfl_up(v, d);
-        if ((int)(threadIdx.x & 63) >= d) v += o;
-    }
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xF, ROWS == 0xF);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xF, ROWS == 0xF);
+    return v + ((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ uint64_t wave_scan(uint64_t v)
+{
+    v = dpp_add<0x111, 0xF>(v);   // row_shr:1
+    v = dpp_add<0x112, 0xF>(v);   // row_shr:2
+    v = dpp_add<0x114, 0xF>(v);   // row_shr:4
+    v = dpp_add<0x118, 0xF>(v);   // row_shr:8
+    v = dpp_add<0x142, 0xA>(v);   // row_bcast:15
+    v = dpp_add<0x143, 0xC>(v);   // row_bcast:31
     return v;
+}
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, uint32_t lane)
+{
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), (int)lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, (int)lane);
 }
 
 template <int WAVES> struct Lds {
@@ -225,19 +293,14 @@ typedef __attribute__((address_space(3))) uint64_t lds_u64;
 
 template <int WAVES> __device__ __attribute__((noinline)) ulonglong2 block_sums(uint64_t v, lds_u64 *wave_sums)
 {
-    const uint32_t wave = threadIdx.x >> 6;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const uint64_t incl = wave_scan(v);
-    if ((threadIdx.x & 63) == 63) wave_sums[wave] = incl;
+    if (lane == 63) wave_sums[wave] = incl;
     __syncthreads();
-    uint64_t base = 0, all = 0;
-#pragma unroll 4
-    for (uint32_t w = 0; w < WAVES; ++w) {
-        const uint64_t s = wave_sums[w];
-        if (w < wave) base += s;
-        all += s;
-    }
+    const uint64_t sums = wave_scan(lane < WAVES ? wave_sums[lane] : 0);
     __syncthreads();
-    return ulonglong2{base + incl - v, all};
+    const uint64_t base = wave ? lane_value(sums, wave - 1) : 0;
+    return ulonglong2{base + incl - v, lane_value(sums, WAVES - 1)};
 }
 
 template <int WAVES> __device__ __forceinline__ uint64_t block_before(uint64_t v, uint64_t *wave_sums, uint64_t &total)
@@ -304,14 +367,14 @@ struct Border {
     uint64_t ties, count;
 };
 
-// ---- keys: over cells [c0, c1), this thread's largest key and the vector where it first met it
-template <class T, int WAVES>
-__device__ __forceinline__ void scan_keys(const Row<T> &row, Lds<WAVES> &sh, uint32_t c0, uint32_t c1, bool hist, int &mine,
-                                          uint32_t &mine_j)
+// ---- keys: over cells [c0, c1), this thread's largest key and the vector where it first met it; HIST: with the
+// counts of all keys per bin
+template <class T, int WAVES, bool HIST>
+__device__ __forceinline__ void scan_keys(const Row<T> &row, Lds<WAVES> &sh, uint32_t c0, uint32_t c1, int &mine, uint32_t &mine_j)
 {
     using V = Vec8<T>;
     using K = Keys<T>;
-    constexpr uint32_t AHEAD = 4, CELL = WAVES * 64 * VEC;
+    constexpr uint32_t AHEAD = HIST || sizeof(T) == 4 ? 4 : 8, CELL = WAVES * 64 * VEC;
     mine = (int)0x80000000;
     mine_j = 0;
 #pragma unroll 1
@@ -326,19 +389,14 @@ __device__ __forceinline__ void scan_keys(const Row<T> &row, Lds<WAVES> &sh, uin
                 const uint32_t j = (c + q) * CELL + threadIdx.x * VEC;
                 row.finish(v[q], j);
                 const int m = v[q].max();
-                if (m > mine) {
-                    mine = m;
-                    mine_j = j;
-                }
-                if (hist) {
-                    bool odd = false;
+                mine_j = m > mine ? j : mine_j;
+                mine = m > mine ? m : mine;
+                if constexpr (HIST) {
+                    int b[VEC];
+                    const bool odd = v[q].bins(b);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const int key = v[q].at(e), b = bin_of<T>(key);
-                        const bool in = key > -K::INF;
-                        if (in) atomicAdd(&sh.count[b], 1u);
-                        if (__is_same(T, __bf16)) odd |= in & !bin_exact<T>(b);
-                    }
+                    for (int e = 0; e < VEC; ++e)
+                        if (v[q].at(e) > -K::INF) atomicAdd(&sh.count[b[e]], 1u);
                     if (__is_same(T, __bf16) && __any(odd)) {
 #pragma unroll 1
                         for (int e = 0; e < VEC; ++e) {
@@ -354,33 +412,31 @@ __device__ __forceinline__ void scan_keys(const Row<T> &row, Lds<WAVES> &sh, uin
     }
 }
 
-// The largest key of the workgroup with its lowest index, as one number: the order of keys, then of inverted indexes.
-template <class T, int WAVES>
-__device__ __forceinline__ uint64_t block_best(const Row<T> &row, Lds<WAVES> &sh, int mine, uint32_t mine_j)
+// Largest of the workgroup's values.
+template <int WAVES> __device__ __forceinline__ uint32_t block_max(Lds<WAVES> &sh, uint32_t v)
 {
-    uint32_t e0 = 0;
-    if (mine > -Keys<T>::INF) {
+    v = wave_max(v);
+    if ((threadIdx.x & 63) == 0) sh.wave[threadIdx.x >> 6] = v;
+    __syncthreads();
+    const uint32_t lane = threadIdx.x & 63;
+    v = wave_max(lane < WAVES ? (uint32_t)sh.wave[lane] : 0u);
+    __syncthreads();
+    return v;
+}
+
+// The lowest index among the workgroup's largest keys.
+template <class T, int WAVES>
+__device__ __forceinline__ uint32_t first_of(const Row<T> &row, Lds<WAVES> &sh, int top, int mine, uint32_t mine_j)
+{
+    uint32_t at = 0;   // inverted index
+    if (mine == top) {
         Vec8<T> v = row.raw(mine_j);
         row.finish(v, mine_j);
 #pragma unroll
         for (int e = VEC - 1; e >= 0; --e)
-            if (v.at(e) == mine) e0 = e;
+            if (v.at(e) == top) at = ~(mine_j + e);
     }
-    uint64_t best = (uint64_t)((uint32_t)mine ^ 0x80000000u) << 32 | ~(mine_j + e0);
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        const uint64_t o = __shfl_xor(best, d);
-        best = o > best ? o : best;
-    }
-    if ((threadIdx.x & 63) == 0) sh.wave[threadIdx.x >> 6] = best;
-    __syncthreads();
-#pragma unroll 4
-    for (int w = 0; w < WAVES; ++w) {
-        const uint64_t o = sh.wave[w];
-        best = o > best ? o : best;
-    }
-    __syncthreads();
-    return best;
+    return ~block_max(sh, at);
 }
 
 // The first bin at which the running sum of value(bin) reaches target(total), the sum before it and its own;
@@ -415,6 +471,58 @@ __device__ __forceinline__ bool find_bin(Lds<WAVES> &sh, F value, G target_of, u
     before = sh.above;
     inside = sh.inside;
     __syncthreads();
+    return true;
+}
+
+// ---- keys, for a small k: nothing below the k-th largest of the threads' own largest keys can be among the first
+// k, since k threads hold one each.  So the list is filled from the threads that have a key that large (or as
+// large as the lowest key of its bin, which is quicker to find), whose vectors are read again, by all.  False
+// where they are too many.
+template <class T, int WAVES>
+__device__ __forceinline__ bool list_first(const Row<T> &row, Lds<WAVES> &sh, uint32_t cells, int mine, Border &b)
+{
+    using V = Vec8<T>;
+    using K = Keys<T>;
+    constexpr uint32_t THREADS = WAVES * 64, CELL = THREADS * VEC;
+    const uint32_t tid = threadIdx.x;
+    if (mine > -K::INF) atomicAdd(&sh.count[bin_of<T>(mine)], 1u);
+    __syncthreads();
+    uint32_t bin;
+    uint64_t before, inside, target;
+    int floor = -K::INF + 1, hi;
+    b.lo = 0;
+    b.hi = BINS - 1;
+    if (find_bin<WAVES>(sh, [&](int i) INLINE { return (uint64_t)sh.count[i]; }, [&](uint64_t) INLINE { return (uint64_t)row.k; }, bin,
+                        before, inside, target)) {
+        bin_range<T>((int)bin, floor, hi);
+        floor = floor > -K::INF ? floor : -K::INF + 1;
+        b.hi = (int)bin;
+    }
+    uint32_t *holders = (uint32_t *)sh.mass;
+    if (mine >= floor) holders[atomicAdd(&sh.n_odd, 1u)] = tid;
+    __syncthreads();
+    const uint32_t work = sh.n_odd * cells;
+#pragma unroll 1
+    for (uint32_t i = tid; i < work; i += THREADS) {
+        const uint32_t j = i % cells * CELL + holders[i / cells] * VEC;
+        V v = row.raw(j);
+        row.finish(v, j);
+        if (v.max() >= floor) {
+#pragma unroll 1
+            for (int e = 0; e < VEC; ++e) {
+                const int key = v.pick(e);
+                if (key >= floor) {
+                    const uint32_t at = atomicAdd(&sh.n_list, 1u);
+                    if (at < LIST) sh.list[at] = (uint64_t)((uint32_t)key ^ 0x80000000u) << 32 | ~(j + e);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (sh.n_list > LIST) return false;
+    b.listed = b.by_k = true;
+    b.by_p = row.p < 1.f;
+    b.left_k = row.k;
     return true;
 }
 
@@ -494,12 +602,17 @@ __device__ __forceinline__ void scan_cells(const Row<T> &row, Lds<WAVES> &sh, co
     using V = Vec8<T>;
     using K = Keys<T>;
     constexpr bool TABLE = __is_same(T, __bf16);
-    constexpr uint32_t AHEAD = 4, CELL = WAVES * 64 * VEC;
-    int lowest = -K::INF + 1;
+    constexpr uint32_t AHEAD = sizeof(T) == 4 ? 2 : 4, CELL = WAVES * 64 * VEC;
+    const uint32_t lane = threadIdx.x & 63;
+    int lowest = -K::INF + 1, sure = -K::INF + 1;   // the lowest keys of the border, and above it
+    const uint64_t raw_min = wt.zero() + w_min;
+    const bool bordered = b.hi < BINS;
     if (b.hi < BINS) {
         int h;
         bin_range<T>(b.hi, lowest, h);
         lowest = lowest > -K::INF ? lowest : -K::INF + 1;
+        bin_range<T>(b.lo, h, sure);
+        ++sure;
     }
     if (TABLE) {   // the weights of the bins above the border, so that no element needs its own exponential
 #pragma unroll 1
@@ -507,7 +620,7 @@ __device__ __forceinline__ void scan_cells(const Row<T> &row, Lds<WAVES> &sh, co
             int l, h;
             bin_range<T>(i, l, h);
             uint64_t w = 0;
-            if ((i < b.lo) & (l <= wt.max_key) & bin_exact<T>(i)) w = weight(l);
+            if ((l >= sure) & (l <= wt.max_key) & bin_exact<T>(i)) w = weight(l);
             sh.mass[i] = w >= w_min ? w : 0;
         }
         __syncthreads();
@@ -523,59 +636,93 @@ __device__ __forceinline__ void scan_cells(const Row<T> &row, Lds<WAVES> &sh, co
             if (c + q < c1) {
                 const uint32_t j = (c + q) * CELL + threadIdx.x * VEC;
                 row.finish(v[q], j);
-                if (!__any(v[q].max() >= lowest)) continue;
+                const int most = v[q].max();
+                if (!__any(most >= lowest)) continue;
                 uint64_t sum = 0;
-                uint32_t in_border = 0;
-                bool slow = !TABLE;
-                if (TABLE) {
-                    uint64_t w[VEC];
-                    bool odd = false;
+                if (__any(most >= sure)) {
+                    if constexpr (TABLE) {
+                        int bin[VEC];
+                        uint64_t w[VEC];
+                        const bool odd = v[q].bins(bin);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const int key = v[q].at(e), bin = bin_of<T>(key);
-                        w[e] = sh.mass[bin];
-                        in_border += (bin >= b.lo) & (key >= lowest);
-                        odd |= (key >= lowest) & !bin_exact<T>(bin);
-                    }
+                        for (int e = 0; e < VEC; ++e) w[e] = sh.mass[bin[e]];
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) sum += w[e];
-                    slow = __any(odd | (b.listed & (in_border != 0)));
-                    if (slow) in_border = 0;
-                }
-                if (slow) {
+                        for (int e = 0; e < VEC; ++e) sum += w[e];
+                        if (__any(odd)) {
 #pragma unroll 1
-                    for (int e = 0; e < VEC; ++e) {
-                        const int key = v[q].pick(e), bin = bin_of<T>(key);
-                        const bool in = key >= lowest;
-                        if (in & (bin >= b.lo)) {
-                            ++in_border;
-                            if (b.listed) {
-                                const uint32_t at = atomicAdd(&sh.n_list, 1u);
-                                if (at < LIST) sh.list[at] = (uint64_t)((uint32_t)key ^ 0x80000000u) << 32 | ~(j + e);
+                            for (int e = 0; e < VEC; ++e) {
+                                const int key = v[q].pick(e);
+                                const bool own = (key >= sure) & !bin_exact<T>(bin_of<T>(key));
+                                if (!__any(own)) continue;
+                                const uint64_t w1 = wt.of(key, K::value(key));
+                                sum += own && w1 >= w_min ? w1 : 0;
                             }
                         }
-                        const bool own = in & (bin < b.lo) & !bin_exact<T>(bin);
-                        if (__any(own)) {
-                            const uint64_t w = wt.of(key, K::value(key));
-                            sum += own && w >= w_min ? w : 0;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            const int key = v[q].at(e);
+                            const uint64_t w = wt.raw(K::value(key), key >= sure);
+                            sum += w < raw_min ? 0ull : w - wt.zero();
                         }
                     }
+                    const uint64_t all = wave_scan(sum);
+                    if (lane == 63 && all) atomicAdd((unsigned long long *)&sh.cell[c + q], (unsigned long long)all);
+                }
+                // the border: elements from `lowest` up to `sure`, or equal to its one key
+                if (!bordered) continue;
+                uint32_t in_border = 0;
+                if (b.listed) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) in_border += (v[q].at(e) >= lowest) & (v[q].at(e) < sure);
+                } else {
+                    in_border = v[q].equals(lowest);
                 }
                 if (__any(in_border != 0)) {
-                    const uint32_t all = wave_incl_sum(in_border);
-                    if ((threadIdx.x & 63) == 63) atomicAdd(&sh.border[c + q], all);
-                }
-                if (__any(sum != 0)) {
-                    const uint64_t all = wave_scan(sum);
-                    if ((threadIdx.x & 63) == 63) atomicAdd((unsigned long long *)&sh.cell[c + q], (unsigned long long)all);
+                    const uint32_t incl = wave_incl_sum(in_border);
+                    if (!b.listed) {
+                        if (lane == 63) atomicAdd(&sh.border[c + q], incl);
+                    } else {
+                        uint32_t at = 0;
+                        if (lane == 63) at = atomicAdd(&sh.n_list, incl);
+                        at = (uint32_t)__builtin_amdgcn_readlane((int)at, 63) + incl - in_border;
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) {
+                            const int key = v[q].at(e);
+                            if ((key >= lowest) & (key < sure)) {
+                                if (at < LIST) sh.list[at] = (uint64_t)((uint32_t)key ^ 0x80000000u) << 32 | ~(j + e);
+                                ++at;
+                            }
+                        }
+                    }
                 }
             }
     }
 }
 
-// Sorts the first n (at most LIST) of sh.list, descending; a power of two from n on is padded with zeros.
+// Sorts the first n (at most LIST) of sh.list, descending; they are all different.  Few by their ranks: each
+// against all others, which takes fewer steps in a row; more by a bitonic network, a power of two of them padded with
+// zeros.
 template <int WAVES> __device__ __forceinline__ void sort_list(Lds<WAVES> &sh, uint32_t n)
 {
+    constexpr uint32_t FEW = WAVES * 16;   // four threads for each
+    if (n <= FEW) {
+        uint32_t *rank = (uint32_t *)sh.mass;
+        const uint32_t i = threadIdx.x % FEW, part = threadIdx.x / FEW;
+        if (part == 0) rank[i] = 0;
+        __syncthreads();
+        const uint64_t v = i < n ? sh.list[i] : 0;
+        if (i < n) {
+            uint32_t above = 0;
+#pragma unroll 4
+            for (uint32_t o = part; o < n; o += 4) above += sh.list[o] > v;
+            atomicAdd(&rank[i], above);
+        }
+        __syncthreads();
+        if (i < n && part == 0) sh.list[rank[i]] = v;
+        __syncthreads();
+        return;
+    }
     uint32_t size = 2;
     while (size < n) size *= 2;
     for (uint32_t i = n + threadIdx.x; i < size; i += WAVES * 64) sh.list[i] = 0;
@@ -674,10 +821,7 @@ __device__ __forceinline__ void draw(const Row<T> &row, Lds<WAVES> &sh, const Bo
             const uint32_t j = c * CELL + tid * VEC;
             V v = row.raw(j);
             row.finish(v, j);
-            uint32_t equal = 0;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) equal += v.at(e) == key_f;
-            const uint32_t t = find_part(sh, (uint64_t)equal, b.ties - 1 - before, before_thread);
+            const uint32_t t = find_part(sh, (uint64_t)v.equals(key_f), b.ties - 1 - before, before_thread);
             if (tid == t) {
                 uint64_t at = before + before_thread;
 #pragma unroll 1
@@ -787,7 +931,7 @@ __device__ __attribute__((noinline)) void general_row(const Row<T> &in, Lds<WAVE
         }
         return;
     }
-    const Weights wt{1.4426950408889634 / (double)temp, (double)K::value(top), magic, top};
+    const Weights wt{1.4426950408889634 / (double)temp, __builtin_fmin((double)K::value(top), Weights::HUGE_LOGIT), magic, top};
     auto weight = [&](int key) { return weight_of<T>(wt.c, wt.max, wt.magic, wt.max_key, key); };
     const bool first_alone = k == 1 || !(temp > 0.f);
     const bool need_k = !first_alone && k != 0 && k < n_vocab, need_p = !first_alone && p < 1.f;
@@ -1098,23 +1242,30 @@ __global__ __launch_bounds__(WAVES * 64) void k_sample(const T *__restrict__ log
     __syncthreads();
     int mine;
     uint32_t mine_j;
-    scan_keys<T, WAVES>(row, sh, 0, cells, filtered, mine, mine_j);
-    const uint64_t best = block_best<T, WAVES>(row, sh, mine, mine_j);
-    const int top = (int)((uint32_t)(best >> 32) ^ 0x80000000u);
+    const bool small_k = filtered && row.k != 0 && row.k <= THREADS / 4;
+    if (filtered && !small_k) scan_keys<T, WAVES, true>(row, sh, 0, cells, mine, mine_j);
+    else scan_keys<T, WAVES, false>(row, sh, 0, cells, mine, mine_j);
+    const int top = (int)(block_max(sh, (uint32_t)mine ^ 0x80000000u) ^ 0x80000000u);
     if (top <= -K::INF || first_alone) {   // nothing to choose from, or the first alone
+        uint32_t id = NO_ID;
+        if (top > -K::INF) id = first_of(row, sh, top, mine, mine_j);
         if (tid == 0) {
-            out_ids[r] = top <= -K::INF ? NO_ID : ~(uint32_t)best;
+            out_ids[r] = id;
             if (out_logprob) *out_logprob = top <= -K::INF ? -__builtin_inff() : 0.f;
         }
         return;
     }
-    const Weights wt{1.4426950408889634 / (double)row.temp, (double)K::value(top), magic, top};
+    const Weights wt{1.4426950408889634 / (double)row.temp, __builtin_fmin((double)K::value(top), Weights::HUGE_LOGIT), magic, top};
     auto weight = [&](int key) INLINE { return weight_of<T>(wt.c, wt.max, wt.magic, wt.max_key, key); };
     const uint64_t one = wt.one();
     const uint64_t w_min = row.min_p >= 1.f ? one : row.min_p > 0.f ? (uint64_t)__builtin_ceil((double)row.min_p * (double)one) : 0;
     Border b{};
     b.lo = b.hi = BINS;
-    if (filtered)
+    bool listed = false;
+    if (small_k) {
+        listed = list_first<T, WAVES>(row, sh, cells, mine, b);
+        if (!listed) return general_row<T, WAVES>(row, sh, magic, out_ids + r, out_logprob);
+    } else if (filtered) {
         b = find_border<T, WAVES>(row, sh, weight, [&](uint32_t bin_k) INLINE {
             for (int i = tid; i < BINS; i += THREADS) {
                 uint64_t m = 0;
@@ -1148,8 +1299,9 @@ __global__ __launch_bounds__(WAVES * 64) void k_sample(const T *__restrict__ log
             }
             __syncthreads();
         });
-    if (b.hard) return general_row<T, WAVES>(row, sh, magic, out_ids + r, out_logprob);
-    scan_cells<T, WAVES>(row, sh, wt, b, w_min, 0, cells, weight);
+        if (b.hard) return general_row<T, WAVES>(row, sh, magic, out_ids + r, out_logprob);
+    }
+    if (!listed) scan_cells<T, WAVES>(row, sh, wt, b, w_min, 0, cells, weight);
     __syncthreads();
     draw<T, WAVES>(row, sh, b, w_min, weight, out_ids + r, out_logprob);
 }
