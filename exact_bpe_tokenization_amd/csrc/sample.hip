@@ -86,6 +86,14 @@ template <class T> __device__ __forceinline__ bool bin_exact(int b)
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
+// All ones in the halves that are negative (in one instruction: the compiler makes compares and selects of it).
+__device__ __forceinline__ uint32_t sign_pairs(uint32_t v)
+{
+    uint32_t r;
+    asm("v_pk_ashrrev_i16 %0, 15, %1 op_sel_hi:[0,1]" : "=v"(r) : "v"(v));
+    return r;
+}
+
 // Eight keys: packed in pairs for the 16-bit types.
 template <class T> struct Vec8 {
     u32x4 a;
@@ -102,10 +110,6 @@ template <class T> struct Vec8 {
     __device__ __forceinline__ int at(int e) const
     {
         return (e & 1) ? (int)a[e >> 1] >> 16 : (int)(int16_t)(a[e >> 1] & 0xFFFFu);
-    }
-    __device__ __forceinline__ void hide(int e)
-    {
-        a[e >> 1] = (e & 1) ? (a[e >> 1] & 0xFFFFu) | 0x80000000u : (a[e >> 1] & 0xFFFF0000u) | 0x8000u;
     }
     __device__ __forceinline__ int max() const
     {
@@ -143,14 +147,25 @@ template <class T> struct Vec8 {
         }
         return VEC - other.x - other.y;
     }
-    // logits to keys, in place
+    // logits to keys, in place; NaN out of the choice
     __device__ __forceinline__ void order()
     {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const s16x2 b = pair(i), sign = b >> 15;
             const s16x2 m = __builtin_bit_cast(s16x2, a[i] & 0x7FFF7FFFu);
-            a[i] = __builtin_bit_cast(uint32_t, (m ^ sign) - sign);
+            const uint32_t key = __builtin_bit_cast(uint32_t, (m ^ sign) - sign);
+            const uint32_t out = sign_pairs(__builtin_bit_cast(uint32_t, (s16x2)(short)Keys<T>::INF - m));
+            a[i] = (key & ~out) | (0x80008000u & out);
+        }
+    }
+    // elements whose bit is 0 out of the choice
+    __device__ __forceinline__ void allow(uint32_t bits)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t in = ((bits >> (2 * i) & 1u) ? 0xFFFFu : 0u) | ((bits >> (2 * i + 1) & 1u) ? 0xFFFF0000u : 0u);
+            a[i] = (a[i] & in) | (0x80008000u & ~in);
         }
     }
 };
@@ -168,7 +183,11 @@ template <> struct Vec8<float> {
         if (e < 4) a[e] = (uint32_t)v;
         else b[e - 4] = (uint32_t)v;
     }
-    __device__ __forceinline__ void hide(int e) { set(e, (int)0x80000000); }
+    __device__ __forceinline__ void allow(uint32_t bits)
+    {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) set(e, (bits >> e) & 1u ? at(e) : (int)0x80000000);
+    }
     __device__ __forceinline__ bool bins(int (&b)[VEC]) const
     {
 #pragma unroll
@@ -193,8 +212,8 @@ template <> struct Vec8<float> {
     {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            const int x = at(e), sign = x >> 31;
-            set(e, ((x & 0x7FFFFFFF) ^ sign) - sign);
+            const int x = at(e), sign = x >> 31, m = x & 0x7FFFFFFF;
+            set(e, m > Keys<float>::INF ? (int)0x80000000 : (m ^ sign) - sign);
         }
     }
 };
@@ -319,21 +338,24 @@ template <class T> struct Row {
     float temp, p, min_p, u;
     uint32_t k;
 
-    __device__ __forceinline__ V raw(uint32_t j) const
+    __device__ __forceinline__ V raw(uint32_t j) const   // eight elements, all the row's
     {
         V v;
-        if (j + VEC <= n) {
-            v.a = *(const u32x4_row *)(x + j);
-            if constexpr (sizeof(T) == 4) v.b = *(const u32x4_row *)(x + j + 4);
-        } else {
+        v.a = *(const u32x4_row *)(x + j);
+        if constexpr (sizeof(T) == 4) v.b = *(const u32x4_row *)(x + j + 4);
+        return v;
+    }
+    __device__ __forceinline__ V part(uint32_t j) const   // what lies past the row's end is out of the choice
+    {
+        if (j + VEC <= n) return raw(j);
+        V v;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                if constexpr (sizeof(T) == 4) {
-                    v.set(e, j + e < n ? __builtin_bit_cast(int, x[j + e]) : (int)0xFF800000u);
-                } else {
-                    const uint32_t h = j + e < n ? (uint32_t)__builtin_bit_cast(uint16_t, x[j + e]) : 0x8000u | (uint32_t)Keys<T>::INF;
-                    v.a[e >> 1] = (e & 1) ? v.a[e >> 1] | h << 16 : h;
-                }
+        for (int e = 0; e < VEC; ++e) {
+            if constexpr (sizeof(T) == 4) {
+                v.set(e, j + e < n ? __builtin_bit_cast(int, x[j + e]) : (int)0xFF800000u);
+            } else {
+                const uint32_t h = j + e < n ? (uint32_t)__builtin_bit_cast(uint16_t, x[j + e]) : 0x8000u | (uint32_t)Keys<T>::INF;
+                v.a[e >> 1] = (e & 1) ? v.a[e >> 1] | h << 16 : h;
             }
         }
         return v;
@@ -341,20 +363,54 @@ template <class T> struct Row {
     __device__ __forceinline__ void finish(V &v, uint32_t j) const
     {
         v.order();
-        if (__any(v.max() > Keys<T>::INF)) {   // NaN
+        if (mask && j < n) v.allow(mask[j >> 5] >> (j & 31u));
+    }
+    __device__ __forceinline__ V fetch(uint32_t j) const;   // one vector, anywhere
+    // f(index of the first element, keys) over the vectors of this thread, ascending: one of every `step` elements,
+    // AHEAD loads in flight.  (A load under a condition would wait for those before it, so where fewer than AHEAD are
+    // left the last is loaded again.)  Only the last step may pass the row's end.
+    template <uint32_t AHEAD, class F> __device__ __forceinline__ void each(uint32_t step, F f) const
+    {
+        const uint32_t full = n / step, j0 = threadIdx.x * VEC;
+#pragma unroll 1
+        for (uint32_t i = 0; i < full; i += AHEAD) {
+            V v[AHEAD];
+            uint32_t word[AHEAD];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (v.at(e) > Keys<T>::INF) v.hide(e);
+            for (uint32_t q = 0; q < AHEAD; ++q) v[q] = raw((i + q < full ? i + q : full - 1) * step + j0);
+            if (mask) {
+#pragma unroll
+                for (uint32_t q = 0; q < AHEAD; ++q) word[q] = mask[((i + q < full ? i + q : full - 1) * step + j0) >> 5];
+            }
+#pragma unroll
+            for (uint32_t q = 0; q < AHEAD; ++q)
+                if (i + q < full) {
+                    const uint32_t j = (i + q) * step + j0;
+                    v[q].order();
+                    if (mask) v[q].allow(word[q] >> (j & 31u));
+                    f(j, v[q]);
+                }
         }
-        if (mask && j < n) {
-            const uint32_t bits = mask[j >> 5] >> (j & 31u);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (!((bits >> e) & 1u)) v.hide(e);
+        if (full * step < n) {
+            V v = part(full * step + j0);
+            finish(v, full * step + j0);
+            f(full * step + j0, v);
         }
     }
 };
 
+
+template <class T> __device__ __attribute__((noinline)) Vec8<T> fetch_of(const T *x, const uint32_t *mask, uint32_t n, uint32_t j)
+{
+    Row<T> row;
+    row.x = x;
+    row.mask = mask;
+    row.n = n;
+    Vec8<T> v = row.part(j);
+    row.finish(v, j);
+    return v;
+}
+template <class T> __device__ __forceinline__ Vec8<T> Row<T>::fetch(uint32_t j) const { return fetch_of(x, mask, n, j); }
 
 // Where the filters end.  Bins before lo are kept, bins after hi are not; those from lo to hi are the border.
 struct Border {
@@ -367,49 +423,37 @@ struct Border {
     uint64_t ties, count;
 };
 
-// ---- keys: over cells [c0, c1), this thread's largest key and the vector where it first met it; HIST: with the
+// ---- keys: this thread's largest key and the vector where it first met it; HIST: with the
 // counts of all keys per bin
 template <class T, int WAVES, bool HIST>
-__device__ __forceinline__ void scan_keys(const Row<T> &row, Lds<WAVES> &sh, uint32_t c0, uint32_t c1, int &mine, uint32_t &mine_j)
+__device__ __forceinline__ void scan_keys(const Row<T> &row, Lds<WAVES> &sh, int &mine, uint32_t &mine_j)
 {
     using V = Vec8<T>;
     using K = Keys<T>;
-    constexpr uint32_t AHEAD = HIST || sizeof(T) == 4 ? 4 : 8, CELL = WAVES * 64 * VEC;
     mine = (int)0x80000000;
     mine_j = 0;
+    row.template each<HIST || sizeof(T) == 4 ? 4 : 8>(WAVES * 64 * VEC, [&](uint32_t j, const V &v) INLINE {
+        const int m = v.max();
+        mine_j = m > mine ? j : mine_j;
+        mine = m > mine ? m : mine;
+        if constexpr (HIST) {
+            int b[VEC];
+            const bool odd = v.bins(b);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (v.at(e) > -K::INF) atomicAdd(&sh.count[b[e]], 1u);
+            if (__is_same(T, __bf16) && __any(odd)) {
 #pragma unroll 1
-    for (uint32_t c = c0; c < c1; c += AHEAD) {
-        V v[AHEAD];
-#pragma unroll
-        for (uint32_t q = 0; q < AHEAD; ++q)
-            if (c + q < c1) v[q] = row.raw((c + q) * CELL + threadIdx.x * VEC);
-#pragma unroll
-        for (uint32_t q = 0; q < AHEAD; ++q)
-            if (c + q < c1) {
-                const uint32_t j = (c + q) * CELL + threadIdx.x * VEC;
-                row.finish(v[q], j);
-                const int m = v[q].max();
-                mine_j = m > mine ? j : mine_j;
-                mine = m > mine ? m : mine;
-                if constexpr (HIST) {
-                    int b[VEC];
-                    const bool odd = v[q].bins(b);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        if (v[q].at(e) > -K::INF) atomicAdd(&sh.count[b[e]], 1u);
-                    if (__is_same(T, __bf16) && __any(odd)) {
-#pragma unroll 1
-                        for (int e = 0; e < VEC; ++e) {
-                            const int key = v[q].pick(e);
-                            if ((key > -K::INF) & !bin_exact<T>(bin_of<T>(key))) {
-                                const uint32_t at = atomicAdd(&sh.n_odd, 1u);
-                                if (at < ODD) sh.odd[at] = (uint32_t)key;
-                            }
-                        }
+                for (int e = 0; e < VEC; ++e) {
+                    const int key = v.pick(e);
+                    if ((key > -K::INF) & !bin_exact<T>(bin_of<T>(key))) {
+                        const uint32_t at = atomicAdd(&sh.n_odd, 1u);
+                        if (at < ODD) sh.odd[at] = (uint32_t)key;
                     }
                 }
             }
-    }
+        }
+    });
 }
 
 // Largest of the workgroup's values.
@@ -430,8 +474,7 @@ __device__ __forceinline__ uint32_t first_of(const Row<T> &row, Lds<WAVES> &sh, 
 {
     uint32_t at = 0;   // inverted index
     if (mine == top) {
-        Vec8<T> v = row.raw(mine_j);
-        row.finish(v, mine_j);
+        const Vec8<T> v = row.fetch(mine_j);
 #pragma unroll
         for (int e = VEC - 1; e >= 0; --e)
             if (v.at(e) == top) at = ~(mine_j + e);
@@ -505,8 +548,7 @@ __device__ __forceinline__ bool list_first(const Row<T> &row, Lds<WAVES> &sh, ui
 #pragma unroll 1
     for (uint32_t i = tid; i < work; i += THREADS) {
         const uint32_t j = i % cells * CELL + holders[i / cells] * VEC;
-        V v = row.raw(j);
-        row.finish(v, j);
+        const Vec8<T> v = row.fetch(j);
         if (v.max() >= floor) {
 #pragma unroll 1
             for (int e = 0; e < VEC; ++e) {
@@ -531,6 +573,16 @@ __device__ __forceinline__ uint64_t share_of(float p, uint64_t all)   // the mas
     const double t = __builtin_ceil((double)p * (double)all);
     const uint64_t q = t > 1.0 ? (uint64_t)t : 1ull;
     return q < all ? q : all;
+}
+
+__device__ __forceinline__ uint64_t least_weight(const Weights &wt, float min_p)   // that min-p keeps
+{
+    const uint64_t one = wt.one();
+    return min_p >= 1.f ? one : min_p > 0.f ? (uint64_t)__builtin_ceil((double)min_p * (double)one) : 0;
+}
+__device__ __forceinline__ uint64_t aim_of(float u, uint64_t total)   // the running mass that the ID has to exceed
+{
+    return (uint64_t)((u > 0.f ? (double)fminf(u, 0x1.fffffep-1f) : 0.0) * (double)total);
 }
 
 // ---- border, from sh.count; fill_masses() brings the masses into sh.mass where they are needed
@@ -594,10 +646,10 @@ __device__ __forceinline__ Border find_border(const Row<T> &row, Lds<WAVES> &sh,
     return r;
 }
 
-// ---- cells [c0, c1): adds to sh.cell, sh.border and sh.list
+// ---- cells: sh.cell, sh.border and sh.list
 template <class T, int WAVES, class W>
 __device__ __forceinline__ void scan_cells(const Row<T> &row, Lds<WAVES> &sh, const Weights &wt, const Border &b, uint64_t w_min,
-                                           uint32_t c0, uint32_t c1, W weight)
+                                           W weight)
 {
     using V = Vec8<T>;
     using K = Keys<T>;
@@ -625,79 +677,68 @@ __device__ __forceinline__ void scan_cells(const Row<T> &row, Lds<WAVES> &sh, co
         }
         __syncthreads();
     }
+    row.template each<AHEAD>(CELL, [&](uint32_t j, const V &v) INLINE {
+        const int most = v.max();
+        if (!__any(most >= lowest)) return;
+        uint64_t sum = 0;
+        if (__any(most >= sure)) {
+            if constexpr (TABLE) {
+                int bin[VEC];
+                uint64_t w[VEC];
+                const bool odd = v.bins(bin);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) w[e] = sh.mass[bin[e]];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) sum += w[e];
+                if (__any(odd)) {
 #pragma unroll 1
-    for (uint32_t c = c0; c < c1; c += AHEAD) {
-        V v[AHEAD];
-#pragma unroll
-        for (uint32_t q = 0; q < AHEAD; ++q)
-            if (c + q < c1) v[q] = row.raw((c + q) * CELL + threadIdx.x * VEC);
-#pragma unroll
-        for (uint32_t q = 0; q < AHEAD; ++q)
-            if (c + q < c1) {
-                const uint32_t j = (c + q) * CELL + threadIdx.x * VEC;
-                row.finish(v[q], j);
-                const int most = v[q].max();
-                if (!__any(most >= lowest)) continue;
-                uint64_t sum = 0;
-                if (__any(most >= sure)) {
-                    if constexpr (TABLE) {
-                        int bin[VEC];
-                        uint64_t w[VEC];
-                        const bool odd = v[q].bins(bin);
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) w[e] = sh.mass[bin[e]];
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) sum += w[e];
-                        if (__any(odd)) {
-#pragma unroll 1
-                            for (int e = 0; e < VEC; ++e) {
-                                const int key = v[q].pick(e);
-                                const bool own = (key >= sure) & !bin_exact<T>(bin_of<T>(key));
-                                if (!__any(own)) continue;
-                                const uint64_t w1 = wt.of(key, K::value(key));
-                                sum += own && w1 >= w_min ? w1 : 0;
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const int key = v[q].at(e);
-                            const uint64_t w = wt.raw(K::value(key), key >= sure);
-                            sum += w < raw_min ? 0ull : w - wt.zero();
-                        }
+                    for (int e = 0; e < VEC; ++e) {
+                        const int key = v.pick(e);
+                        const bool own = (key >= sure) & !bin_exact<T>(bin_of<T>(key));
+                        if (!__any(own)) continue;
+                        const uint64_t w1 = wt.of(key, K::value(key));
+                        sum += own && w1 >= w_min ? w1 : 0;
                     }
-                    const uint64_t all = wave_scan(sum);
-                    if (lane == 63 && all) atomicAdd((unsigned long long *)&sh.cell[c + q], (unsigned long long)all);
                 }
-                // the border: elements from `lowest` up to `sure`, or equal to its one key
-                if (!bordered) continue;
-                uint32_t in_border = 0;
-                if (b.listed) {
+            } else {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) in_border += (v[q].at(e) >= lowest) & (v[q].at(e) < sure);
-                } else {
-                    in_border = v[q].equals(lowest);
+                for (int e = 0; e < VEC; ++e) {
+                    const int key = v.at(e);
+                    const uint64_t w = wt.raw(K::value(key), key >= sure);
+                    sum += w < raw_min ? 0ull : w - wt.zero();
                 }
-                if (__any(in_border != 0)) {
-                    const uint32_t incl = wave_incl_sum(in_border);
-                    if (!b.listed) {
-                        if (lane == 63) atomicAdd(&sh.border[c + q], incl);
-                    } else {
-                        uint32_t at = 0;
-                        if (lane == 63) at = atomicAdd(&sh.n_list, incl);
-                        at = (uint32_t)__builtin_amdgcn_readlane((int)at, 63) + incl - in_border;
+            }
+            const uint64_t all = wave_scan(sum);
+            if (lane == 63 && all) atomicAdd((unsigned long long *)&sh.cell[j / CELL], (unsigned long long)all);
+        }
+        // the border: elements from `lowest` up to `sure`, or equal to its one key
+        if (!bordered) return;
+        uint32_t in_border = 0;
+        if (b.listed) {
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const int key = v[q].at(e);
-                            if ((key >= lowest) & (key < sure)) {
-                                if (at < LIST) sh.list[at] = (uint64_t)((uint32_t)key ^ 0x80000000u) << 32 | ~(j + e);
-                                ++at;
-                            }
-                        }
+            for (int e = 0; e < VEC; ++e) in_border += (v.at(e) >= lowest) & (v.at(e) < sure);
+        } else {
+            in_border = v.equals(lowest);
+        }
+        if (__any(in_border != 0)) {
+            const uint32_t incl = wave_incl_sum(in_border);
+            if (!b.listed) {
+                if (lane == 63) atomicAdd(&sh.border[j / CELL], incl);
+            } else {
+                uint32_t at = 0;
+                if (lane == 63) at = atomicAdd(&sh.n_list, incl);
+                at = (uint32_t)__builtin_amdgcn_readlane((int)at, 63) + incl - in_border;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const int key = v.at(e);
+                    if ((key >= lowest) & (key < sure)) {
+                        if (at < LIST) sh.list[at] = (uint64_t)((uint32_t)key ^ 0x80000000u) << 32 | ~(j + e);
+                        ++at;
                     }
                 }
             }
-    }
+        }
+    });
 }
 
 // Sorts the first n (at most LIST) of sh.list, descending; they are all different.  Few by their ranks: each
@@ -767,7 +808,7 @@ __device__ __forceinline__ uint32_t find_part(Lds<WAVES> &sh, uint64_t part, uin
 
 // ---- draw
 template <class T, int WAVES, class W>
-__device__ __forceinline__ void draw(const Row<T> &row, Lds<WAVES> &sh, const Border &b, uint64_t w_min, W weight, uint32_t *out_id,
+__device__ __forceinline__ void draw(const Row<T> &row, Lds<WAVES> &sh, const Weights &wt, const Border &b, uint64_t w_min, W weight, uint32_t *out_id,
                                      float *out_logprob)
 {
     using K = Keys<T>;
@@ -819,8 +860,7 @@ __device__ __forceinline__ void draw(const Row<T> &row, Lds<WAVES> &sh, const Bo
             uint64_t before, before_thread;
             const uint32_t c = find_part(sh, full, b.ties - 1, before);
             const uint32_t j = c * CELL + tid * VEC;
-            V v = row.raw(j);
-            row.finish(v, j);
+            const Vec8<T> v = row.fetch(j);
             const uint32_t t = find_part(sh, (uint64_t)v.equals(key_f), b.ties - 1 - before, before_thread);
             if (tid == t) {
                 uint64_t at = before + before_thread;
@@ -840,35 +880,34 @@ __device__ __forceinline__ void draw(const Row<T> &row, Lds<WAVES> &sh, const Bo
     uint64_t total, before, before_thread;
     const uint64_t mass = tid < cells ? sh.cell[tid] : 0;
     block_before<WAVES>(mass, sh.wave, total);
-    const double u = row.u > 0.f ? (double)fminf(row.u, 0x1.fffffep-1f) : 0.0;
-    uint64_t target = (uint64_t)(u * (double)total);
+    uint64_t target = aim_of(row.u, total);
     const uint32_t c = find_part(sh, mass, target, before), j = c * CELL + tid * VEC;
     target -= before;
-    V v = row.raw(j);
-    row.finish(v, j);
-    uint64_t sum = 0;
-    auto amount = [&](int e) INLINE {
-        const int key = v.pick(e);
-        const bool in = (key > key_f) | ((key == key_f) & (j + e <= cut));
-        return __any(in) ? (in ? kept_weight(key) : 0ull) : 0ull;
-    };
+    const Vec8<T> v = row.fetch(j);
+    uint64_t sum = 0, w[VEC] = {};
     if (__any(v.max() >= key_f)) {
-#pragma unroll 1
-        for (int e = 0; e < VEC; ++e) sum += amount(e);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int key = v.at(e);
+            const uint64_t x = wt.of(key, K::value(key));
+            w[e] = ((key > key_f) | ((key == key_f) & (j + e <= cut))) & (x >= w_min) ? x : 0;
+            sum += w[e];
+        }
     }
     const uint32_t t = find_part(sh, sum, target, before_thread);
     if (tid == t) {
-        uint64_t run = before_thread;
-#pragma unroll 1
+        uint64_t run = before_thread, own = 0;
+        uint32_t id = NO_ID;
+#pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            const uint64_t w = amount(e);
-            run += w;
-            if (run > target) {
-                *out_id = j + e;
-                if (out_logprob) *out_logprob = (float)log((double)w / (double)total);
-                break;
+            run += w[e];
+            if (id == NO_ID && run > target) {
+                id = j + e;
+                own = w[e];
             }
         }
+        *out_id = id;
+        if (out_logprob) *out_logprob = (float)log((double)own / (double)total);
     }
 }
 
@@ -900,7 +939,7 @@ __device__ __attribute__((noinline)) void general_row(const Row<T> &in, Lds<WAVE
             V v[AHEAD];
 #pragma unroll
             for (uint32_t q = 0; q < AHEAD; ++q)
-                if (i + q < nv) v[q] = row.raw(first + (i + q) * (64 * VEC));
+                if (i + q < nv) v[q] = row.part(first + (i + q) * (64 * VEC));
 #pragma unroll
             for (uint32_t q = 0; q < AHEAD; ++q)
                 if (i + q < nv) {
@@ -981,12 +1020,12 @@ __device__ __attribute__((noinline)) void general_row(const Row<T> &in, Lds<WAVE
             // threads' own largest keys (or its bin's lowest key) can be among the first k
             if (mine >= LOWEST) atomicAdd((unsigned long long *)&sh.mass[bin_of<T>(mine)], 1ull);
         } else {
-            V next = row.raw(begin);
+            V next = row.part(begin);
 #pragma unroll 1
             for (uint32_t i = 0; i < count_v; ++i) {
                 const uint32_t j = begin + i * stride_v;
                 V v = next;
-                if (i + 1 < count_v) next = row.raw(j + stride_v);
+                if (i + 1 < count_v) next = row.part(j + stride_v);
                 row.finish(v, j);
                 if (!__any(v.max() >= lo)) continue;
 #pragma unroll 1
@@ -1243,8 +1282,8 @@ __global__ __launch_bounds__(WAVES * 64) void k_sample(const T *__restrict__ log
     int mine;
     uint32_t mine_j;
     const bool small_k = filtered && row.k != 0 && row.k <= THREADS / 4;
-    if (filtered && !small_k) scan_keys<T, WAVES, true>(row, sh, 0, cells, mine, mine_j);
-    else scan_keys<T, WAVES, false>(row, sh, 0, cells, mine, mine_j);
+    if (filtered && !small_k) scan_keys<T, WAVES, true>(row, sh, mine, mine_j);
+    else scan_keys<T, WAVES, false>(row, sh, mine, mine_j);
     const int top = (int)(block_max(sh, (uint32_t)mine ^ 0x80000000u) ^ 0x80000000u);
     if (top <= -K::INF || first_alone) {   // nothing to choose from, or the first alone
         uint32_t id = NO_ID;
@@ -1257,8 +1296,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_sample(const T *__restrict__ log
     }
     const Weights wt{1.4426950408889634 / (double)row.temp, __builtin_fmin((double)K::value(top), Weights::HUGE_LOGIT), magic, top};
     auto weight = [&](int key) INLINE { return weight_of<T>(wt.c, wt.max, wt.magic, wt.max_key, key); };
-    const uint64_t one = wt.one();
-    const uint64_t w_min = row.min_p >= 1.f ? one : row.min_p > 0.f ? (uint64_t)__builtin_ceil((double)row.min_p * (double)one) : 0;
+    const uint64_t w_min = least_weight(wt, row.min_p);
     Border b{};
     b.lo = b.hi = BINS;
     bool listed = false;
@@ -1287,8 +1325,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_sample(const T *__restrict__ log
 #pragma unroll 1
                 for (uint32_t c = 0; c < cells; ++c) {
                     const uint32_t j = c * CELL + tid * VEC;
-                    Vec8<T> v = row.raw(j);
-                    row.finish(v, j);
+                    const Vec8<T> v = row.fetch(j);
 #pragma unroll 1
                     for (int e = 0; e < VEC; ++e) {
                         const int key = v.pick(e), bin = bin_of<T>(key);
@@ -1301,9 +1338,9 @@ __global__ __launch_bounds__(WAVES * 64) void k_sample(const T *__restrict__ log
         });
         if (b.hard) return general_row<T, WAVES>(row, sh, magic, out_ids + r, out_logprob);
     }
-    if (!listed) scan_cells<T, WAVES>(row, sh, wt, b, w_min, 0, cells, weight);
+    if (!listed) scan_cells<T, WAVES>(row, sh, wt, b, w_min, weight);
     __syncthreads();
-    draw<T, WAVES>(row, sh, b, w_min, weight, out_ids + r, out_logprob);
+    draw<T, WAVES>(row, sh, wt, b, w_min, weight, out_ids + r, out_logprob);
 }
 
 // S = 45 fraction bits keep the sum of up to 2^18 weights of at most one below 2^63; one bit less for every doubling.
