@@ -6,7 +6,7 @@
 // point: exact in any order, so neither atomics nor the split of a row over threads can change an ID.
 //
 // A row goes through four phases:
-//   keys    the largest key, and a histogram of the keys over 4,095 bins (sign, exponent, 7 mantissa bits);
+//   keys    the largest key, and a histogram of the keys over 6,143 bins (sign, exponent, 7 mantissa bits);
 //   border  the bins in which top-k (by counts) and top-p (by masses) end;
 //   cells   per cell of consecutive IDs, the mass of what lies above the border, and a list of what lies in it;
 //   draw    the list sorted gives the exact border; the running mass over the cells, then inside one, gives the ID.
@@ -21,18 +21,18 @@ namespace {
 #define INLINE __attribute__((always_inline))   // of a lambda
 
 constexpr uint32_t NO_ID = 0xFFFFFFFFu;
-constexpr int BINS = 4096, HALF = BINS / 2 - 1;   // bins of a sign; bin 0 holds the largest keys
-constexpr int DIGIT = 12;
+constexpr int BINS = 6144, HALF = BINS / 2 - 1;   // bins of a sign; bin 0 holds the largest keys
+constexpr int DIGIT = 12, DIGIT_VALUES = 1 << DIGIT;
 constexpr uint32_t LIST = 2048;                   // elements that a border may have to be sorted
 constexpr uint32_t ODD = 512;                     // bfloat16: listed elements of bins with several keys
 constexpr uint32_t MAX_CELLS = 256;               // of 8,192 elements
 
 // A key is the logit's sign and magnitude bits as an integer: the order of the logits, -0 equal to +0.
-// Bins: magnitudes below 2^-9 share the middle one, those from 2^7 on the outermost, and between them a bin
-// has 128 per octave.
+// Bins: magnitudes below LOW (2^-13) share the middle one, those from 2^11 on (nearly) the outermost, and between
+// them there are 128 per octave.
 template <class T> struct Keys;
 template <> struct Keys<__bf16> {
-    static constexpr int INF = 0x7F80, LOW = 0x3B00, SHIFT = 0;
+    static constexpr int INF = 0x7F80, LOW = (127 - 13) << 7, SHIFT = 0;
     static __device__ __forceinline__ float value(int k)
     {
         const uint32_t m = (uint32_t)(k < 0 ? -k : k);
@@ -40,7 +40,7 @@ template <> struct Keys<__bf16> {
     }
 };
 template <> struct Keys<_Float16> {
-    static constexpr int INF = 0x7C00, LOW = 0x1800, SHIFT = 3;
+    static constexpr int INF = 0x7C00, LOW = (15 - 13) << 10, SHIFT = 3;
     static __device__ __forceinline__ float value(int k)
     {
         const uint32_t m = (uint32_t)(k < 0 ? -k : k);
@@ -49,7 +49,7 @@ template <> struct Keys<_Float16> {
     }
 };
 template <> struct Keys<float> {
-    static constexpr int INF = 0x7F800000, LOW = 118 << 23, SHIFT = 16;
+    static constexpr int INF = 0x7F800000, LOW = (127 - 13) << 23, SHIFT = 16;
     static __device__ __forceinline__ float value(int k)
     {
         const uint32_t m = (uint32_t)(k < 0 ? -k : k);
@@ -118,23 +118,25 @@ template <class T> struct Vec8 {
         for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, pair(i));
         return m.x > m.y ? m.x : m.y;
     }
-    // the bins of the keys; true where one of these holds several keys (the middle or the outermost ones)
-    __device__ __forceinline__ bool bins(int (&b)[VEC]) const
+    // the bins of the logits (before order()); least: the first of them; odd: whether one is the first or the middle bin
+    __device__ __forceinline__ void bins(int (&b)[VEC], int &least, bool &odd) const
     {
         using K = Keys<T>;
-        u16x2 far = 0;
+        u16x2 first = (u16x2)(unsigned short)BINS, zero = first;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const s16x2 k = pair(i), sign = k >> 15;
-            const u16x2 mag = __builtin_bit_cast(u16x2, __builtin_elementwise_max(k, (s16x2)-k));
+            const u16x2 mag = __builtin_bit_cast(u16x2, a[i] & 0x7FFF7FFFu);
             u16x2 m = __builtin_elementwise_sub_sat(mag, (u16x2)(unsigned short)(K::LOW - (1 << K::SHIFT)));
             m = __builtin_elementwise_min((u16x2)(m >> K::SHIFT), (u16x2)(unsigned short)HALF);
-            far = __builtin_elementwise_max(far, (u16x2)(m - (u16x2)(unsigned short)1));   // 0 becomes the largest
+            zero = __builtin_elementwise_min(zero, m);
             const s16x2 t = (s16x2)(short)HALF - ((__builtin_bit_cast(s16x2, m) ^ sign) - sign);
+            first = __builtin_elementwise_min(first, __builtin_bit_cast(u16x2, t));
             b[2 * i] = t.x;
             b[2 * i + 1] = t.y;
         }
-        return (far.x >= HALF - 1) | (far.y >= HALF - 1);
+        least = first.x < first.y ? first.x : first.y;
+        odd = (zero.x == 0) | (zero.y == 0) | (least == 0);
     }
     // how many of the keys are `key`
     __device__ __forceinline__ uint32_t equals(int key) const
@@ -147,25 +149,31 @@ template <class T> struct Vec8 {
         }
         return VEC - other.x - other.y;
     }
-    // logits to keys, in place; NaN out of the choice
+    // logits to keys, in place; NaN becomes larger than +inf or smaller than -inf
     __device__ __forceinline__ void order()
     {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const s16x2 b = pair(i), sign = b >> 15;
             const s16x2 m = __builtin_bit_cast(s16x2, a[i] & 0x7FFF7FFFu);
-            const uint32_t key = __builtin_bit_cast(uint32_t, (m ^ sign) - sign);
-            const uint32_t out = sign_pairs(__builtin_bit_cast(uint32_t, (s16x2)(short)Keys<T>::INF - m));
-            a[i] = (key & ~out) | (0x80008000u & out);
+            a[i] = __builtin_bit_cast(uint32_t, (m ^ sign) - sign);
         }
     }
-    // elements whose bit is 0 out of the choice
-    __device__ __forceinline__ void allow(uint32_t bits)
+    __device__ __forceinline__ void drop_nan()   // of keys
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t out = sign_pairs(__builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat((s16x2)(short)Keys<T>::INF, pair(i))));
+            a[i] = (a[i] & ~out) | (0x80008000u & out);
+        }
+    }
+    // elements whose bit is 0 out of the choice: the smallest key, or -inf as a logit
+    template <bool RAW = false> __device__ __forceinline__ void allow(uint32_t bits)
     {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t in = ((bits >> (2 * i) & 1u) ? 0xFFFFu : 0u) | ((bits >> (2 * i + 1) & 1u) ? 0xFFFF0000u : 0u);
-            a[i] = (a[i] & in) | (0x80008000u & ~in);
+            a[i] = (a[i] & in) | ((RAW ? 0x80008000u | (uint32_t)Keys<T>::INF * 0x10001u : 0x80008000u) & ~in);
         }
     }
 };
@@ -183,16 +191,11 @@ template <> struct Vec8<float> {
         if (e < 4) a[e] = (uint32_t)v;
         else b[e - 4] = (uint32_t)v;
     }
-    __device__ __forceinline__ void allow(uint32_t bits)
+    template <bool RAW = false> __device__ __forceinline__ void allow(uint32_t bits)
     {
+        static_assert(!RAW, "keys");
 #pragma unroll
         for (int e = 0; e < VEC; ++e) set(e, (bits >> e) & 1u ? at(e) : (int)0x80000000);
-    }
-    __device__ __forceinline__ bool bins(int (&b)[VEC]) const
-    {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) b[e] = bin_of<float>(at(e));
-        return true;
     }
     __device__ __forceinline__ uint32_t equals(int key) const
     {
@@ -212,9 +215,14 @@ template <> struct Vec8<float> {
     {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            const int x = at(e), sign = x >> 31, m = x & 0x7FFFFFFF;
-            set(e, m > Keys<float>::INF ? (int)0x80000000 : (m ^ sign) - sign);
+            const int x = at(e), sign = x >> 31;
+            set(e, ((x & 0x7FFFFFFF) ^ sign) - sign);
         }
+    }
+    __device__ __forceinline__ void drop_nan()
+    {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) set(e, at(e) > Keys<float>::INF ? (int)0x80000000 : at(e));
     }
 };
 
@@ -363,13 +371,15 @@ template <class T> struct Row {
     __device__ __forceinline__ void finish(V &v, uint32_t j) const
     {
         v.order();
+        v.drop_nan();
         if (mask && j < n) v.allow(mask[j >> 5] >> (j & 31u));
     }
     __device__ __forceinline__ V fetch(uint32_t j) const;   // one vector, anywhere
     // f(index of the first element, keys) over the vectors of this thread, ascending: one of every `step` elements,
     // AHEAD loads in flight.  (A load under a condition would wait for those before it, so where fewer than AHEAD are
-    // left the last is loaded again.)  Only the last step may pass the row's end.
-    template <uint32_t AHEAD, class F> __device__ __forceinline__ void each(uint32_t step, F f) const
+    // left the last is loaded again.)  Only the last step may pass the row's end.  Positive NaN are not taken out, and
+    // with RAW the logits are not made keys.
+    template <uint32_t AHEAD, bool RAW, class F> __device__ __forceinline__ void each(uint32_t step, F f) const
     {
         const uint32_t full = n / step, j0 = threadIdx.x * VEC;
 #pragma unroll 1
@@ -386,15 +396,17 @@ template <class T> struct Row {
             for (uint32_t q = 0; q < AHEAD; ++q)
                 if (i + q < full) {
                     const uint32_t j = (i + q) * step + j0;
-                    v[q].order();
-                    if (mask) v[q].allow(word[q] >> (j & 31u));
+                    if (!RAW) v[q].order();
+                    if (mask) v[q].template allow<RAW>(word[q] >> (j & 31u));
                     f(j, v[q]);
                 }
         }
         if (full * step < n) {
-            V v = part(full * step + j0);
-            finish(v, full * step + j0);
-            f(full * step + j0, v);
+            const uint32_t j = full * step + j0;
+            V v = part(j);
+            if (!RAW) v.order();
+            if (mask && j < n) v.template allow<RAW>(mask[j >> 5] >> (j & 31u));
+            f(j, v);
         }
     }
 };
@@ -432,16 +444,27 @@ __device__ __forceinline__ void scan_keys(const Row<T> &row, Lds<WAVES> &sh, int
     using K = Keys<T>;
     mine = (int)0x80000000;
     mine_j = 0;
-    row.template each<HIST || sizeof(T) == 4 ? 4 : 8>(WAVES * 64 * VEC, [&](uint32_t j, const V &v) INLINE {
+    constexpr bool RAW = HIST && sizeof(T) == 2;
+    row.template each<HIST || sizeof(T) == 4 ? 4 : 8, RAW>(WAVES * 64 * VEC, [&](uint32_t j, const V &logits) INLINE {
+        V v = logits;
+        int b[VEC];
+        bool odd = false;
+        if constexpr (RAW) {
+            int least;
+            v.bins(b, least, odd);
+            v.order();
+        }
         const int m = v.max();
         mine_j = m > mine ? j : mine_j;
         mine = m > mine ? m : mine;
         if constexpr (HIST) {
-            int b[VEC];
-            const bool odd = v.bins(b);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (v.at(e) > -K::INF) atomicAdd(&sh.count[b[e]], 1u);
+            for (int e = 0; e < VEC; ++e) {
+                const int key = v.at(e);
+                if constexpr (!RAW) b[e] = bin_of<T>(key);
+                if (key > -K::INF) atomicAdd(&sh.count[b[e]], 1u);
+                if (__is_same(T, __bf16)) odd |= (key > -K::INF) & (b[e] == 2 * HALF);
+            }
             if (__is_same(T, __bf16) && __any(odd)) {
 #pragma unroll 1
                 for (int e = 0; e < VEC; ++e) {
@@ -677,30 +700,36 @@ __device__ __forceinline__ void scan_cells(const Row<T> &row, Lds<WAVES> &sh, co
         }
         __syncthreads();
     }
-    row.template each<AHEAD>(CELL, [&](uint32_t j, const V &v) INLINE {
-        const int most = v.max();
-        if (!__any(most >= lowest)) return;
+    row.template each<AHEAD, TABLE>(CELL, [&](uint32_t j, const V &logits) INLINE {
+        V v = logits;   // made keys where they are needed
         uint64_t sum = 0;
-        if (__any(most >= sure)) {
-            if constexpr (TABLE) {
-                int bin[VEC];
+        if constexpr (TABLE) {
+            int bin[VEC], least;
+            bool odd;
+            v.bins(bin, least, odd);
+            if (!__any(least <= b.hi)) return;
+            if (__any(least < b.lo)) {
                 uint64_t w[VEC];
-                const bool odd = v.bins(bin);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) w[e] = sh.mass[bin[e]];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) sum += w[e];
-                if (__any(odd)) {
+            }
+            v.order();
+            if (__any(odd)) {
 #pragma unroll 1
-                    for (int e = 0; e < VEC; ++e) {
-                        const int key = v.pick(e);
-                        const bool own = (key >= sure) & !bin_exact<T>(bin_of<T>(key));
-                        if (!__any(own)) continue;
-                        const uint64_t w1 = wt.of(key, K::value(key));
-                        sum += own && w1 >= w_min ? w1 : 0;
-                    }
+                for (int e = 0; e < VEC; ++e) {
+                    const int key = v.pick(e);
+                    const bool own = (key >= sure) & !bin_exact<T>(bin_of<T>(key));
+                    if (!__any(own)) continue;
+                    const uint64_t w1 = wt.of(key, K::value(key));
+                    sum += own && w1 >= w_min ? w1 : 0;
                 }
-            } else {
+            }
+        } else {
+            const int most = v.max();
+            if (!__any(most >= lowest)) return;
+            if (__any(most >= sure)) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const int key = v.at(e);
@@ -708,8 +737,10 @@ __device__ __forceinline__ void scan_cells(const Row<T> &row, Lds<WAVES> &sh, co
                     sum += w < raw_min ? 0ull : w - wt.zero();
                 }
             }
+        }
+        if (__any(sum != 0)) {
             const uint64_t all = wave_scan(sum);
-            if (lane == 63 && all) atomicAdd((unsigned long long *)&sh.cell[j / CELL], (unsigned long long)all);
+            if (lane == 63) atomicAdd((unsigned long long *)&sh.cell[j / CELL], (unsigned long long)all);
         }
         // the border: elements from `lowest` up to `sure`, or equal to its one key
         if (!bordered) return;
@@ -1050,7 +1081,7 @@ __device__ __attribute__((noinline)) void general_row(const Row<T> &in, Lds<WAVE
                     if (hist) {
                         const uint32_t d = (uint32_t)(hi - key);
                         if (in & (step == BIN || (above_shift < 32 ? d >> above_shift : 0u) == prefix))
-                            atomicAdd((unsigned long long *)&sh.mass[step == BIN ? (uint32_t)b : (d >> shift) & (BINS - 1)],
+                            atomicAdd((unsigned long long *)&sh.mass[step == BIN ? (uint32_t)b : (d >> shift) & (DIGIT_VALUES - 1)],
                                       (unsigned long long)amount);
                     } else if (in) {
                         sum += amount;
@@ -1067,7 +1098,7 @@ __device__ __attribute__((noinline)) void general_row(const Row<T> &in, Lds<WAVE
                 const uint32_t d = (uint32_t)(hi - key_k);
                 if (step == BIN) sh.mass[bin_of<T>(key_k)] -= TABLE && bin_exact<T>(bin_of<T>(key_k)) ? count_f - ties : excess;
                 else if ((key_k >= lo) & (key_k <= hi) & ((above_shift < 32 ? d >> above_shift : 0u) == prefix))
-                    sh.mass[(d >> shift) & (BINS - 1)] -= excess;
+                    sh.mass[(d >> shift) & (DIGIT_VALUES - 1)] -= excess;
             }
             __syncthreads();
 #pragma unroll 1
@@ -1285,6 +1316,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_sample(const T *__restrict__ log
     if (filtered && !small_k) scan_keys<T, WAVES, true>(row, sh, mine, mine_j);
     else scan_keys<T, WAVES, false>(row, sh, mine, mine_j);
     const int top = (int)(block_max(sh, (uint32_t)mine ^ 0x80000000u) ^ 0x80000000u);
+    if (top > K::INF) return general_row<T, WAVES>(row, sh, magic, out_ids + r, out_logprob);   // NaN
     if (top <= -K::INF || first_alone) {   // nothing to choose from, or the first alone
         uint32_t id = NO_ID;
         if (top > -K::INF) id = first_of(row, sh, top, mine, mine_j);
@@ -1299,6 +1331,11 @@ __global__ __launch_bounds__(WAVES * 64) void k_sample(const T *__restrict__ log
     const uint64_t w_min = least_weight(wt, row.min_p);
     Border b{};
     b.lo = b.hi = BINS;
+    if (TABLE) {   // the last bin's keys (from -2,047 down) have no weight in the table: it has to be zero
+        int lo, hi;
+        bin_range<T>(2 * HALF, lo, hi);
+        if (top <= hi || weight(hi) != 0) return general_row<T, WAVES>(row, sh, magic, out_ids + r, out_logprob);
+    }
     bool listed = false;
     if (small_k) {
         listed = list_first<T, WAVES>(row, sh, cells, mine, b);
