@@ -582,3 +582,83 @@ def test_graph_replays(tt):
         torch.cuda.synchronize()
         for name in RESULTS:
             assert torch.equal(b[name], other[name]), (seed, name)
+
+
+# ---------------------------------------------------------------------------------------------
+# borders between one way of working and another
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", [300, 9000, 131328])
+def test_sample_crowded_borders(tt, vocab, dtype):
+    """Many logits, equal or nearly so, where top-k and top-p end: more than are sorted at once."""
+    _say("sample crowded", vocab, dtype)
+    rng = np.random.default_rng(vocab + 7)
+    rows = 10
+    near = 1.0 + rng.random((rows, vocab)) * 2.0 ** -7
+    same = np.where(rng.random((rows, vocab)) < 0.01, 2.5, 1.0)
+    last = rng.permuted(np.arange(rows * vocab).reshape(rows, vocab) % vocab < 40, axis=1) * 1.0   # 40 of one, the rest of another
+    k = np.array([0, 1, 2, 41, 63, 255, 700, vocab // 2, vocab - 1, vocab])
+    for x in (near, same, last):
+        for p in (1.0, 0.37):
+            _sample(tt, x, dtype, 0.01 if x is near else 0.7, k, p, rng.choice([0.0, 0.5], rows), rng.random(rows))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", [2000, 40000])
+@pytest.mark.parametrize("scale,temperature", [(1e-6, 1e-6), (1e-3, 3e-4), (4000.0, 3000.0), (200.0, 40.0), (1e4, 1e30)])
+def test_sample_scales(tt, vocab, dtype, scale, temperature):
+    """Logits far smaller or larger than usual, whose weights do differ, and a temperature that makes them equal."""
+    _say("sample scale", vocab, dtype, scale, temperature)
+    rng = np.random.default_rng(vocab + 11)
+    rows = 8
+    x = scale * rng.standard_normal((rows, vocab))
+    x[0] = -np.abs(x[0])
+    x[1] = np.abs(x[1])
+    k = np.array([0, 0, 50, 1500, 0, 20, vocab, 700])
+    for p in (1.0, 0.9):
+        _sample(tt, x, dtype, temperature, k, p, 0.0, rng.random(rows))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", [500, 131328])
+def test_sample_nan_beside_logits(tt, vocab, dtype):
+    """NaN of either sign is never chosen, and changes nothing else."""
+    import torch
+    _say("sample nan", vocab, dtype)
+    rng = np.random.default_rng(vocab + 13)
+    rows = 12
+    x = _logits(rng, rows, vocab)
+    for r in range(rows):
+        x[r, rng.integers(0, vocab, 1 + r)] = math.nan if r % 2 else -math.nan
+    x[3, 0] = x[4, vocab - 1] = math.nan
+    assert torch.isnan(torch.from_numpy(x)).any(dim=1).all()
+    s = np.array([SETTINGS[r % 6] for r in range(rows)])
+    allowed = rng.random((rows, vocab)) < 0.7
+    allowed[:, 1] = True
+    for mask in (None, allowed):
+        _sample(tt, x, dtype, s[:, 0], s[:, 1].astype(np.int64), s[:, 2], s[:, 3], rng.random(rows), allowed=mask)
+        _sample(tt, x, dtype, 0.9, 0, 1.0, 0.0, rng.random(rows), allowed=mask)
+
+
+@pytest.mark.parametrize("rows,vocab", [(1, 65528), (1, 65536), (5, 65537), (159, 65536), (160, 65536)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_cross_entropy_few_long_rows(tt, rows, vocab, dtype):
+    _say("cross_entropy few long rows", rows, vocab, dtype)
+    _loss(tt, rows, vocab, dtype, "plain")
+
+
+@pytest.mark.parametrize("tokens", [4095, 4096, 4097, 8191, 8192, 8193, 16385, 1200001])
+@pytest.mark.parametrize("vocab", [5, 2048, 2049, 50000])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_backward_lengths_are_exact_on_integers(tt, tokens, vocab, accumulate):
+    import torch
+    _say("embed_backward lengths", tokens, vocab, accumulate)
+    rng = np.random.default_rng(tokens + vocab)
+    ids = _ids(rng, tokens, vocab, 0.05)
+    vals = rng.integers(-3, 4, size=(tokens, 2))
+    table = torch.full((vocab, 2), 5.0, device="cuda")
+    ws = _ws(tt.toktier_embed_backward_workspace_bytes(tokens, vocab, 2))
+    tt.toktier_embed_backward(_dev(vals, "float32"), _dev(ids), table, ws, accumulate=accumulate)
+    ok = (ids >= 0) & (ids < vocab)
+    ref = np.stack([np.bincount(ids[ok], weights=vals[ok, k], minlength=vocab) for k in range(2)], axis=1)
+    assert np.array_equal(plain.f64(table), ref + 5.0 if accumulate else ref)
