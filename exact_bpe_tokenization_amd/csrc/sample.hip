@@ -623,10 +623,11 @@ __device__ __forceinline__ Border find_border(const Row<T> &row, Lds<WAVES> &sh,
         need_k = find_bin<WAVES>(sh, [&](int b) INLINE { return (uint64_t)sh.count[b]; }, [&](uint64_t) INLINE { return k; }, bin_k,
                                  above_k, count_k, target);
     if (!need_k && !need_p) return r;
-    if (need_k && (above_k + count_k <= LIST || !need_p)) {
+    const bool list_k = above_k + count_k <= LIST && !bin_exact<T>((int)bin_k);
+    if (need_k && (list_k || !need_p)) {
         r.hi = (int)bin_k;
         r.by_k = true;
-        if (above_k + count_k <= LIST) {   // all that top-k may keep goes to the list
+        if (list_k) {   // all that top-k may keep goes to the list
             r.lo = 0;
             r.listed = true;
             r.by_p = need_p;
