@@ -94,6 +94,23 @@ __device__ __forceinline__ uint32_t sign_pairs(uint32_t v)
     return r;
 }
 
+// The bins of eight elements.
+struct Bins {
+    u16x2 t[4];
+    int least;   // the first of them
+    bool odd;    // whether one is the first or the middle bin
+    __device__ __forceinline__ int at(int e) const { return e & 1 ? t[e / 2].y : t[e / 2].x; }
+    // how many are `bin`
+    __device__ __forceinline__ uint32_t equals(int bin) const
+    {
+        u16x2 other = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            other += __builtin_elementwise_min((u16x2)(t[i] ^ (u16x2)(unsigned short)bin), (u16x2)(unsigned short)1);
+        return VEC - other.x - other.y;
+    }
+};
+
 // Eight keys: packed in pairs for the 16-bit types.
 template <class T> struct Vec8 {
     u32x4 a;
@@ -118,10 +135,11 @@ template <class T> struct Vec8 {
         for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, pair(i));
         return m.x > m.y ? m.x : m.y;
     }
-    // the bins of the logits (before order()); least: the first of them; odd: whether one is the first or the middle bin
-    __device__ __forceinline__ void bins(int (&b)[VEC], int &least, bool &odd) const
+    // the bins of the logits (before order())
+    __device__ __forceinline__ Bins bins() const
     {
         using K = Keys<T>;
+        Bins r;
         u16x2 first = (u16x2)(unsigned short)BINS, zero = first;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -130,13 +148,12 @@ template <class T> struct Vec8 {
             u16x2 m = __builtin_elementwise_sub_sat(mag, (u16x2)(unsigned short)(K::LOW - (1 << K::SHIFT)));
             m = __builtin_elementwise_min((u16x2)(m >> K::SHIFT), (u16x2)(unsigned short)HALF);
             zero = __builtin_elementwise_min(zero, m);
-            const s16x2 t = (s16x2)(short)HALF - ((__builtin_bit_cast(s16x2, m) ^ sign) - sign);
-            first = __builtin_elementwise_min(first, __builtin_bit_cast(u16x2, t));
-            b[2 * i] = t.x;
-            b[2 * i + 1] = t.y;
+            r.t[i] = __builtin_bit_cast(u16x2, (s16x2)((s16x2)(short)HALF - ((__builtin_bit_cast(s16x2, m) ^ sign) - sign)));
+            first = __builtin_elementwise_min(first, r.t[i]);
         }
-        least = first.x < first.y ? first.x : first.y;
-        odd = (zero.x == 0) | (zero.y == 0) | (least == 0);
+        r.least = first.x < first.y ? first.x : first.y;
+        r.odd = (zero.x == 0) | (zero.y == 0) | (r.least == 0);
+        return r;
     }
     // how many of the keys are `key`
     __device__ __forceinline__ uint32_t equals(int key) const
@@ -294,6 +311,29 @@ __device__ __forceinline__ uint64_t wave_scan(uint64_t v)
     v = dpp_add<0x143, 0xC>(v);   // row_bcast:31
     return v;
 }
+// Sums over the lanes of two or four values at once: halves, then rows of 16 lanes, change places between the
+// registers, so that every addition is of two values' parts.  The last lane of each half or row has a sum.
+__device__ __forceinline__ uint64_t halves(uint64_t a, uint64_t b)   // a in lanes 0..31, b in 32..63
+{
+    const auto l = __builtin_amdgcn_permlane32_swap((uint32_t)a, (uint32_t)b, false, false);
+    const auto h = __builtin_amdgcn_permlane32_swap((uint32_t)(a >> 32), (uint32_t)(b >> 32), false, false);
+    return ((uint64_t)h[0] << 32 | l[0]) + ((uint64_t)h[1] << 32 | l[1]);
+}
+__device__ __forceinline__ uint64_t rows_of(uint64_t a, uint64_t b)   // a in the even rows, b in the odd ones
+{
+    const auto l = __builtin_amdgcn_permlane16_swap((uint32_t)a, (uint32_t)b, false, false);
+    const auto h = __builtin_amdgcn_permlane16_swap((uint32_t)(a >> 32), (uint32_t)(b >> 32), false, false);
+    return ((uint64_t)h[0] << 32 | l[0]) + ((uint64_t)h[1] << 32 | l[1]);
+}
+__device__ __forceinline__ uint64_t row_scan(uint64_t v)
+{
+    v = dpp_add<0x111, 0xF>(v);
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    return dpp_add<0x118, 0xF>(v);
+}
+__device__ __forceinline__ uint64_t wave_sums(const uint64_t (&v)[4]) { return row_scan(rows_of(halves(v[0], v[2]), halves(v[1], v[3]))); }
+__device__ __forceinline__ uint64_t wave_sums(const uint64_t (&v)[2]) { return dpp_add<0x142, 0xA>(row_scan(halves(v[0], v[1]))); }
 __device__ __forceinline__ uint64_t lane_value(uint64_t v, uint32_t lane)
 {
     return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), (int)lane) << 32 |
@@ -375,11 +415,11 @@ template <class T> struct Row {
         if (mask && j < n) v.allow(mask[j >> 5] >> (j & 31u));
     }
     __device__ __forceinline__ V fetch(uint32_t j) const;   // one vector, anywhere
-    // f(index of the first element, keys) over the vectors of this thread, ascending: one of every `step` elements,
-    // AHEAD loads in flight.  (A load under a condition would wait for those before it, so where fewer than AHEAD are
+    // f(index of the first element, keys, q) over the vectors of this thread, ascending: one of every `step` elements,
+    // AHEAD loads in flight; q counts these, and after them g(index of their first element, how many they were).  (A load under a condition would wait for those before it, so where fewer than AHEAD are
     // left the last is loaded again.)  Only the last step may pass the row's end.  Positive NaN are not taken out, and
     // with RAW the logits are not made keys.
-    template <uint32_t AHEAD, bool RAW, class F> __device__ __forceinline__ void each(uint32_t step, F f) const
+    template <uint32_t AHEAD, bool RAW, class F, class G> __device__ __forceinline__ void each(uint32_t step, F f, G g) const
     {
         const uint32_t full = n / step, j0 = threadIdx.x * VEC;
 #pragma unroll 1
@@ -398,15 +438,17 @@ template <class T> struct Row {
                     const uint32_t j = (i + q) * step + j0;
                     if (!RAW) v[q].order();
                     if (mask) v[q].template allow<RAW>(word[q] >> (j & 31u));
-                    f(j, v[q]);
+                    f(j, v[q], q);
                 }
+            g(i * step + j0, full - i < AHEAD ? full - i : AHEAD);
         }
         if (full * step < n) {
             const uint32_t j = full * step + j0;
             V v = part(j);
             if (!RAW) v.order();
             if (mask && j < n) v.template allow<RAW>(mask[j >> 5] >> (j & 31u));
-            f(j, v);
+            f(j, v, 0);
+            g(j, 1);
         }
     }
 };
@@ -445,13 +487,13 @@ __device__ __forceinline__ void scan_keys(const Row<T> &row, Lds<WAVES> &sh, int
     mine = (int)0x80000000;
     mine_j = 0;
     constexpr bool RAW = HIST && sizeof(T) == 2;
-    row.template each<HIST || sizeof(T) == 4 ? 4 : 8, RAW>(WAVES * 64 * VEC, [&](uint32_t j, const V &logits) INLINE {
+    row.template each<HIST || sizeof(T) == 4 ? 4 : 8, RAW>(WAVES * 64 * VEC, [&](uint32_t j, const V &logits, uint32_t) INLINE {
         V v = logits;
-        int b[VEC];
+        Bins bins;
         bool odd = false;
         if constexpr (RAW) {
-            int least;
-            v.bins(b, least, odd);
+            bins = v.bins();
+            odd = bins.odd;
             v.order();
         }
         const int m = v.max();
@@ -461,9 +503,11 @@ __device__ __forceinline__ void scan_keys(const Row<T> &row, Lds<WAVES> &sh, int
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const int key = v.at(e);
-                if constexpr (!RAW) b[e] = bin_of<T>(key);
-                if (key > -K::INF) atomicAdd(&sh.count[b[e]], 1u);
-                if (__is_same(T, __bf16)) odd |= (key > -K::INF) & (b[e] == 2 * HALF);
+                int bin;
+                if constexpr (RAW) bin = bins.at(e);
+                else bin = bin_of<T>(key);
+                if (key > -K::INF) atomicAdd(&sh.count[bin], 1u);
+                if (__is_same(T, __bf16)) odd |= (key > -K::INF) & (bin == 2 * HALF);
             }
             if (__is_same(T, __bf16) && __any(odd)) {
 #pragma unroll 1
@@ -476,7 +520,7 @@ __device__ __forceinline__ void scan_keys(const Row<T> &row, Lds<WAVES> &sh, int
                 }
             }
         }
-    });
+    }, [](uint32_t, uint32_t) INLINE {});
 }
 
 // Largest of the workgroup's values.
@@ -701,23 +745,25 @@ __device__ __forceinline__ void scan_cells(const Row<T> &row, Lds<WAVES> &sh, co
         }
         __syncthreads();
     }
-    row.template each<AHEAD, TABLE>(CELL, [&](uint32_t j, const V &logits) INLINE {
-        V v = logits;   // made keys where they are needed
+    uint64_t sums[AHEAD];   // a thread's, of the cells in flight
+    row.template each<AHEAD, TABLE>(CELL, [&](uint32_t j, const V &logits, uint32_t q) INLINE {
+        uint64_t &out = sums[q];
+        out = 0;
+        V v = logits;
+        Bins bins;
         uint64_t sum = 0;
         if constexpr (TABLE) {
-            int bin[VEC], least;
-            bool odd;
-            v.bins(bin, least, odd);
-            if (!__any(least <= b.hi)) return;
-            if (__any(least < b.lo)) {
+            bins = v.bins();
+            if (!__any(bins.least <= b.hi)) return;
+            if (__any(bins.least < b.lo)) {
                 uint64_t w[VEC];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) w[e] = sh.mass[bin[e]];
+                for (int e = 0; e < VEC; ++e) w[e] = sh.mass[bins.at(e)];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) sum += w[e];
             }
-            v.order();
-            if (__any(odd)) {
+            if (__any(bins.odd) | b.listed) v.order();
+            if (__any(bins.odd)) {
 #pragma unroll 1
                 for (int e = 0; e < VEC; ++e) {
                     const int key = v.pick(e);
@@ -739,10 +785,7 @@ __device__ __forceinline__ void scan_cells(const Row<T> &row, Lds<WAVES> &sh, co
                 }
             }
         }
-        if (__any(sum != 0)) {
-            const uint64_t all = wave_scan(sum);
-            if (lane == 63) atomicAdd((unsigned long long *)&sh.cell[j / CELL], (unsigned long long)all);
-        }
+        out = sum;
         // the border: elements from `lowest` up to `sure`, or equal to its one key
         if (!bordered) return;
         uint32_t in_border = 0;
@@ -750,7 +793,7 @@ __device__ __forceinline__ void scan_cells(const Row<T> &row, Lds<WAVES> &sh, co
 #pragma unroll
             for (int e = 0; e < VEC; ++e) in_border += (v.at(e) >= lowest) & (v.at(e) < sure);
         } else {
-            in_border = v.equals(lowest);
+            in_border = TABLE ? bins.equals(b.hi) : v.equals(lowest);
         }
         if (__any(in_border != 0)) {
             const uint32_t incl = wave_incl_sum(in_border);
@@ -770,6 +813,17 @@ __device__ __forceinline__ void scan_cells(const Row<T> &row, Lds<WAVES> &sh, co
                 }
             }
         }
+    }, [&](uint32_t j, uint32_t some) INLINE {
+#pragma unroll
+        for (uint32_t q = 0; q < AHEAD; ++q)
+            if (q >= some) sums[q] = 0;
+        uint64_t any = sums[0];
+#pragma unroll
+        for (uint32_t q = 1; q < AHEAD; ++q) any |= sums[q];
+        if (!__any(any != 0)) return;
+        const uint64_t all = wave_sums(sums);
+        constexpr uint32_t LANES = 64 / AHEAD;
+        if (lane % LANES == LANES - 1 && all) atomicAdd((unsigned long long *)&sh.cell[j / CELL + lane / LANES], (unsigned long long)all);
     });
 }
 
