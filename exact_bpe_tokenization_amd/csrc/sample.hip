@@ -875,12 +875,11 @@ template <int WAVES> __device__ __forceinline__ void sort_list(Lds<WAVES> &sh, u
     __syncthreads();
 }
 
-// The cell, or the thread, at which the running sum exceeds the target: every thread brings its part.
+// The cell, or the thread, at which the running sum exceeds the target: every thread brings its part and the sum
+// of those before it.
 template <int WAVES>
-__device__ __forceinline__ uint32_t find_part(Lds<WAVES> &sh, uint64_t part, uint64_t target, uint64_t &before)
+__device__ __forceinline__ uint32_t find_part(Lds<WAVES> &sh, uint64_t run, uint64_t part, uint64_t target, uint64_t &before)
 {
-    uint64_t total;
-    const uint64_t run = block_before<WAVES>(part, sh.wave, total);
     if (run <= target && target < run + part) {
         sh.found = threadIdx.x;
         sh.above = run;
@@ -890,6 +889,13 @@ __device__ __forceinline__ uint32_t find_part(Lds<WAVES> &sh, uint64_t part, uin
     before = sh.above;
     __syncthreads();
     return at;
+}
+template <int WAVES>
+__device__ __forceinline__ uint32_t find_part(Lds<WAVES> &sh, uint64_t part, uint64_t target, uint64_t &before)
+{
+    uint64_t total;
+    const uint64_t run = block_before<WAVES>(part, sh.wave, total);
+    return find_part(sh, run, part, target, before);
 }
 
 // ---- draw
@@ -965,9 +971,9 @@ __device__ __forceinline__ void draw(const Row<T> &row, Lds<WAVES> &sh, const We
     // the cell, the thread's vector in it, the element
     uint64_t total, before, before_thread;
     const uint64_t mass = tid < cells ? sh.cell[tid] : 0;
-    block_before<WAVES>(mass, sh.wave, total);
+    const uint64_t before_cell = block_before<WAVES>(mass, sh.wave, total);
     uint64_t target = aim_of(row.u, total);
-    const uint32_t c = find_part(sh, mass, target, before), j = c * CELL + tid * VEC;
+    const uint32_t c = find_part(sh, before_cell, mass, target, before), j = c * CELL + tid * VEC;
     target -= before;
     const Vec8<T> v = row.fetch(j);
     uint64_t sum = 0, w[VEC] = {};
