@@ -410,8 +410,8 @@ int toktier_embed(const void *table, int table_type, uint32_t n_vocab, uint32_t 
 
 /*
  * Gradient of the lookup: grad_table[r, :] = scale * (sum of grad_out[t, :] over the tokens with ids[t] = r),
- * summed in 32 bits in an order fixed by the token order (tokens are sorted by ID; no floating-point
- * atomics), rounded once.
+ * summed in 32 bits in an order fixed by the tokens' positions and the sizes (no floating-point atomics),
+ * rounded once.
  *   accumulate  0: all n_vocab rows are written, those of absent IDs with zeros.  1: the sums are added to
  *               grad_table's values; rows of absent IDs are left alone.
  *   workspace   device, toktier_embed_backward_workspace_bytes(n_tokens, n_vocab, dim) bytes.

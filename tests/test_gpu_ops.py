@@ -662,3 +662,23 @@ def test_embed_backward_lengths_are_exact_on_integers(tt, tokens, vocab, accumul
     ok = (ids >= 0) & (ids < vocab)
     ref = np.stack([np.bincount(ids[ok], weights=vals[ok, k], minlength=vocab) for k in range(2)], axis=1)
     assert np.array_equal(plain.f64(table), ref + 5.0 if accumulate else ref)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n", [17, 700, 2048, 2049, 4096])
+@pytest.mark.parametrize("kind", ["one row", "two rows in turn", "no row", "all different", "runs of 64", "first and last", "mixed"])
+def test_embed_backward_few_tokens(tt, kind, n, accumulate):
+    """Rows of several blocks of columns, of one token and of many."""
+    vocab, dim = 5000, 1100
+    _say("embed_backward few", kind, n, accumulate)
+    ids = {"one row": np.full(n, 77), "two rows in turn": np.arange(n) % 2 * (vocab - 1), "no row": np.full(n, -1),
+           "all different": np.arange(n)[::-1].copy(), "runs of 64": np.arange(n) // 64 * 3,
+           "first and last": np.where(np.arange(n) == n - 1, vocab - 1, 0),
+           "mixed": np.where(np.arange(n) % 3 == 0, 5, np.where(np.arange(n) % 5 == 0, vocab, np.arange(n) // 2))}[kind]
+    _embed_backward(tt, n, vocab, dim, "bfloat16", "float32", accumulate, ids=ids.astype(np.int64))
+
+
+def test_embed_backward_few_tokens_of_a_large_table(tt):
+    """A table that is zeroed by a launch of its own."""
+    _embed_backward(tt, 900, 40000, 500, "float16", "float16", False)
+    _embed_backward(tt, 900, 40000, 500, "float16", "float16", False, pad=3, lead=1)
