@@ -360,43 +360,102 @@ __global__ __launch_bounds__(256) void k_embed_sum(const TG *__restrict__ grad, 
     }
 }
 
-template <class TT>
-__global__ __launch_bounds__(256) void k_embed_join(const uint32_t *__restrict__ keys, uint32_t n, uint32_t n_vocab,
-                                                    uint32_t dim, uint32_t chunk, uint32_t n_chunks, uint32_t ncb,
-                                                    float scale, int accumulate, TT *__restrict__ table,
-                                                    uint64_t tstride, const float *__restrict__ part, uint32_t dpad)
+// Adds up `count` partial sums, `step` elements apart, PARTS in flight.
+__device__ __forceinline__ void add_parts(const float *__restrict__ p, uint64_t step, uint32_t count, float (&acc)[VEC])
 {
-    const uint32_t lane = threadIdx.x & 63u;
-    const uint32_t unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4u + (threadIdx.x >> 6));
-    if (unit >= n_chunks * ncb) return;
-    const uint32_t ch = unit / ncb, c = unit % ncb * COLS + lane * VEC;
-    const uint32_t i0 = ch * chunk, end = i0 + chunk;
-    if (end >= n) return;
-    const uint32_t prev = i0 > 0 ? keys[i0 - 1] : 0xFFFFFFFFu, head = keys[i0], key = keys[end - 1], next = keys[end];
-    if (key >= n_vocab || next != key) return;       // no run leaves this chunk
-    if (head == key && prev == key) return;          // it started in an earlier chunk
-    float acc[VEC] = {};
-    if (c < dim) load_part(part + ((uint64_t)ch * 2 + 1) * dpad + c, VEC, 0.f, acc);
-    // the chunks that the run enters: 64 heads are compared at once, and their partial sums loaded together
-    for (uint32_t h0 = ch + 1; h0 < n_chunks; h0 += 64) {
+    for (uint32_t q = 0; q < count; q += PARTS) {
+        Vec<float> x[PARTS];
+#pragma unroll
+        for (int u = 0; u < PARTS; ++u)
+            if (q + u < count) x[u] = load_vec(p + (q + u) * step);
+#pragma unroll
+        for (int u = 0; u < PARTS; ++u)
+            if (q + u < count)
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) acc[k] += vec_at(x[u], k);
+    }
+}
+
+// Runs that leave their chunk.  A wavefront looks after one chunk and 512 columns and joins a run that starts there
+// and enters fewer than 64 chunks; a longer one is shared out between the workgroup's wavefronts, whose sums
+// meet in LDS (40,000 tokens of text, 1,256 IDs, 320 columns: 38 us by one wavefront a run).
+constexpr uint32_t JOIN_WAVES = 8, JOIN_THREADS = JOIN_WAVES * 64;
+
+template <class TT>
+__global__ __launch_bounds__(JOIN_THREADS) void k_embed_join(const uint32_t *__restrict__ keys, uint32_t n, uint32_t n_vocab,
+                                                             uint32_t dim, uint32_t chunk, uint32_t n_chunks, uint32_t ncb,
+                                                             float scale, int accumulate, TT *__restrict__ table,
+                                                             uint64_t tstride, const float *__restrict__ part, uint32_t dpad)
+{
+    __shared__ float sums[JOIN_WAVES][COLS];
+    __shared__ uint32_t entered[JOIN_WAVES], any_long[JOIN_WAVES];
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t units = n_chunks * ncb;
+    // the columns of one run go to several workgroups
+    auto unit = [&](uint32_t w) { return w * gridDim.x + blockIdx.x; };
+    // the chunks after ch whose first token is `key`, of 64 from h0 on
+    auto heads = [&](uint32_t h0, uint32_t key) {
         const uint32_t h = h0 + lane;
         const uint64_t same = __ballot(h < n_chunks && keys[(uint64_t)min(h, n_chunks - 1) * chunk] == key);
-        const uint32_t count = ~same ? (uint32_t)__builtin_ctzll(~same) : 64u;
-        if (c < dim)
-            for (uint32_t q = 0; q < count; q += PARTS) {
-                Vec<float> x[PARTS];
-#pragma unroll
-                for (int u = 0; u < PARTS; ++u)
-                    if (q + u < count) x[u] = load_vec(part + (uint64_t)(h0 + q + u) * 2 * dpad + c);
-#pragma unroll
-                for (int u = 0; u < PARTS; ++u)
-                    if (q + u < count)
-#pragma unroll
-                        for (int k = 0; k < VEC; ++k) acc[k] += vec_at(x[u], k);
+        return ~same ? (uint32_t)__builtin_ctzll(~same) : 64u;
+    };
+    auto starts = [&](uint32_t ch, uint32_t &key) {   // whether a run starts in this chunk and leaves it
+        const uint32_t i0 = ch * chunk, end = i0 + chunk;
+        if (end >= n) return false;
+        const uint32_t prev = i0 > 0 ? keys[i0 - 1] : 0xFFFFFFFFu, head = keys[i0], next = keys[end];
+        key = keys[end - 1];
+        return key < n_vocab && next == key && !(head == key && prev == key);
+    };
+    uint32_t key;
+    bool is_long = false;
+    if (unit(wave) < units) {
+        const uint32_t ch = unit(wave) / ncb, c = unit(wave) % ncb * COLS + lane * VEC;
+        if (starts(ch, key)) {
+            const uint32_t count = heads(ch + 1, key);
+            is_long = count == 64;
+            if (!is_long && c < dim) {
+                float acc[VEC] = {};
+                load_part(part + ((uint64_t)ch * 2 + 1) * dpad + c, VEC, 0.f, acc);
+                add_parts(part + (uint64_t)(ch + 1) * 2 * dpad + c, 2ull * dpad, count, acc);
+                put_row(table + key * tstride + c, dim - c, scale, accumulate, acc);
             }
-        if (count < 64) break;
+        }
     }
-    if (c < dim) put_row(table + key * tstride + c, dim - c, scale, accumulate, acc);
+    if (lane == 0) any_long[wave] = is_long;
+    __syncthreads();
+    for (uint32_t w = 0; w < JOIN_WAVES; ++w) {
+        if (!any_long[w]) continue;
+        const uint32_t ch = unit(w) / ncb, c = unit(w) % ncb * COLS + lane * VEC;
+        starts(ch, key);
+        uint32_t count = 0;
+        for (uint32_t h0 = ch + 1;; h0 += JOIN_THREADS) {   // 64 chunks a wavefront
+            const uint32_t mine = heads(h0 + wave * 64, key);
+            if (lane == 0) entered[wave] = mine;
+            __syncthreads();
+            uint32_t all = 0;
+            for (uint32_t o = 0; o < JOIN_WAVES && all == o * 64; ++o) all += entered[o];
+            __syncthreads();
+            count += all;
+            if (all < JOIN_THREADS) break;
+        }
+        const uint32_t share = (count + JOIN_WAVES - 1) / JOIN_WAVES, from = min(wave * share, count), to = min(from + share, count);
+        float acc[VEC] = {};
+        if (c < dim) {
+            if (wave == 0) load_part(part + ((uint64_t)ch * 2 + 1) * dpad + c, VEC, 0.f, acc);
+            add_parts(part + (uint64_t)(ch + 1 + from) * 2 * dpad + c, 2ull * dpad, to - from, acc);
+        }
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) sums[wave][k * 64 + lane] = acc[k];
+        __syncthreads();
+        if (wave == 0 && c < dim) {
+#pragma unroll
+            for (uint32_t o = 1; o < JOIN_WAVES; ++o)
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) acc[k] += sums[o][k * 64 + lane];
+            put_row(table + key * tstride + c, dim - c, scale, accumulate, acc);
+        }
+        __syncthreads();
+    }
 }
 
 __global__ __launch_bounds__(SORT_THREADS) void k_zero_rows(Zeros z) { zero_block(z, blockIdx.x); }
@@ -700,7 +759,7 @@ extern "C" int toktier_embed_backward(const void *grad_out, int grad_type, uint6
     }
     float *part = (float *)(ws + L.part);
     const uint64_t absent = accumulate || early ? 0 : (n_vocab + ZROWS - 1) / ZROWS;
-    const uint32_t blocks = (uint32_t)((sums + absent + 3) / 4), jblocks = (uint32_t)((sums + 3) / 4);
+    const uint32_t blocks = (uint32_t)((sums + absent + 3) / 4), jblocks = (uint32_t)((sums + JOIN_WAVES - 1) / JOIN_WAVES);
     with_type(grad_type, [&](auto tg) {
         with_type(table_type, [&](auto tt_) {
             using TG = decltype(tg);
@@ -712,7 +771,7 @@ extern "C" int toktier_embed_backward(const void *grad_out, int grad_type, uint6
     });
     with_type(table_type, [&](auto tt_) {
         using TT = decltype(tt_);
-        k_embed_join<TT><<<jblocks, 256, 0, s>>>(keys[last], n, n_vocab, dim, L.chunk, L.n_chunks, L.ncb, scale, accumulate,
+        k_embed_join<TT><<<jblocks, JOIN_THREADS, 0, s>>>(keys[last], n, n_vocab, dim, L.chunk, L.n_chunks, L.ncb, scale, accumulate,
                                                  (TT *)grad_table, table_stride, part, L.dpad);
     });
     return hip_status(hipGetLastError());
