@@ -50,18 +50,18 @@ __global__ __launch_bounds__(256) void k_embed(const TI *__restrict__ table, uin
 // Sort: least-significant-digit radix sort in one or two passes of up to 11 bits.  A wavefront owns a
 // contiguous part of its block, so the rank of an element is (places of lower digits and earlier blocks +
 // counts of the block's earlier wavefronts + the wavefront's own count so far + equal digits in lower lanes,
-// from one ballot per digit bit).  Up to SORT_ONE tokens one block does every pass in one launch; more take a
-// histogram launch and a scatter launch per pass.
+// from one ballot per digit bit).  A pass is a histogram launch and a scatter launch.
 //
 // The launches of the sort leave most of the chip idle, so where rows of absent IDs have to become zeros and
 // most of the rows are absent, the zeros are written by further blocks of these launches.
 constexpr int SORT_WAVES = 8, SORT_THREADS = SORT_WAVES * 64;
-constexpr int R_MANY = 8, R_ONE = 16;   // elements per thread
-constexpr uint32_t SORT_ONE = SORT_THREADS * R_ONE;
+// Elements per thread.  Two spread few tokens over more blocks (65,536 tokens, 33,024 IDs, 256 columns: the call takes 46 us,
+// 48 with four, 56 with eight; 20,000: 35, 38, 48); for 600,000 it makes no difference.
+constexpr int SORT_R = 2;
 constexpr uint32_t MAX_BINS = 2048;
 
 struct SortPlan {
-    uint32_t bits, passes, dbits, bins, groups, blocks;   // a block sorts `groups` groups of 512 x R_MANY elements
+    uint32_t bits, passes, dbits, bins, groups, blocks;   // a block sorts `groups` groups of 512 x SORT_R elements
 };
 
 SortPlan sort_plan(uint64_t n_tokens, uint32_t n_vocab)
@@ -69,10 +69,10 @@ SortPlan sort_plan(uint64_t n_tokens, uint32_t n_vocab)
     SortPlan p;
     p.bits = 32 - __builtin_clz(n_vocab);   // keys 0 .. n_vocab (n_vocab itself: no row)
     p.passes = p.bits <= 11 ? 1 : 2;
-    p.dbits = (p.bits + p.passes - 1) / p.passes;
+    p.dbits = std::max(2u, (p.bits + p.passes - 1) / p.passes);   // bins are taken four at a time
     p.bins = 1u << p.dbits;
     // every block reads all blocks' histograms, so there are at most 256 of them
-    const uint64_t group = SORT_THREADS * R_MANY;
+    const uint64_t group = SORT_THREADS * SORT_R;
     p.groups = (uint32_t)((n_tokens + group * 256 - 1) / (group * 256));
     if (p.groups < 1) p.groups = 1;
     p.blocks = (uint32_t)((n_tokens + group * p.groups - 1) / (group * p.groups));
@@ -108,21 +108,27 @@ struct SortLds {
     uint32_t wsum[SORT_WAVES];
 };
 
-// One pass over this block's elements, `groups` groups of `rounds` (at most R) per thread.  hist: the counts of every block
-// ([blocks][bins]), or NULL where this block is the only one.
-template <int R>
-__device__ __forceinline__ void sort_pass(SortLds &sh, const uint32_t *keys, const uint32_t *pos, bool first, uint32_t n,
-                                          uint32_t n_vocab, uint32_t shift, uint32_t dbits, uint32_t rounds, uint32_t groups,
-                                          uint32_t block, uint32_t blocks, const uint32_t *hist, uint32_t *keys_out, uint32_t *pos_out)
+// One pass over this block's elements, `groups` groups of R per thread.  hist: the counts of every block ([blocks][bins]).
+__global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(const uint32_t *__restrict__ keys,
+                                                               const uint32_t *__restrict__ pos, int first, uint32_t n,
+                                                               uint32_t n_vocab, uint32_t shift, uint32_t dbits,
+                                                               uint32_t groups, uint32_t blocks,
+                                                               const uint32_t *__restrict__ hist,
+                                                               uint32_t *__restrict__ keys_out,
+                                                               uint32_t *__restrict__ pos_out, Zeros z)
 {
+    __shared__ __align__(16) SortLds sh;
+    if (blockIdx.x >= blocks) return zero_block(z, blockIdx.x - blocks);
+    constexpr int R = SORT_R;
+    const uint32_t block = blockIdx.x;
     const uint32_t bins = 1u << dbits, tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
-    const uint64_t base = ((uint64_t)block * SORT_WAVES + wave) * (64 * rounds) * groups + lane;
+    const uint64_t base = ((uint64_t)block * SORT_WAVES + wave) * (64 * R) * groups + lane;
     uint32_t key[R];
     auto load = [&](uint32_t g) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const uint64_t i = base + ((uint64_t)g * rounds + r) * 64;
-            key[r] = r < (int)rounds && i < n ? keys[i] : 0xFFFFFFFFu;
+            const uint64_t i = base + ((uint64_t)g * R + r) * 64;
+            key[r] = i < n ? keys[i] : 0xFFFFFFFFu;
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) key[r] = min(key[r], n_vocab);   // an ID without a row; also what lies past the end
@@ -133,7 +139,7 @@ __device__ __forceinline__ void sort_pass(SortLds &sh, const uint32_t *keys, con
     for (uint32_t g = 0;;) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            if (r < (int)rounds && base + ((uint64_t)g * rounds + r) * 64 < n)
+            if (base + ((uint64_t)g * R + r) * 64 < n)
                 atomicAdd(&sh.cnt[wave][(key[r] >> shift) & (bins - 1)], 1u);
         if (++g == groups) break;
         load(g);
@@ -144,16 +150,11 @@ __device__ __forceinline__ void sort_pass(SortLds &sh, const uint32_t *keys, con
     const uint32_t b0 = tid * 4;
     u32x4 all = 0, before = 0, sum;
     if (b0 < bins) {
-        if (hist) {
 #pragma unroll 8
-            for (uint32_t k = 0; k < blocks; ++k) {
-                const u32x4 v = *(const u32x4 *)&hist[(uint64_t)k * bins + b0];
-                all += v;
-                if (k < block) before += v;
-            }
-        } else {
-#pragma unroll
-            for (int w = 0; w < SORT_WAVES; ++w) all += *(u32x4 *)&sh.cnt[w][b0];
+        for (uint32_t k = 0; k < blocks; ++k) {
+            const u32x4 v = *(const u32x4 *)&hist[(uint64_t)k * bins + b0];
+            all += v;
+            if (k < block) before += v;
         }
     }
     sum[0] = all[0];
@@ -184,13 +185,12 @@ __device__ __forceinline__ void sort_pass(SortLds &sh, const uint32_t *keys, con
         uint32_t from[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const uint64_t i = base + ((uint64_t)g * rounds + r) * 64;
-            from[r] = first || r >= (int)rounds || i >= n ? (uint32_t)i : pos[i];
+            const uint64_t i = base + ((uint64_t)g * R + r) * 64;
+            from[r] = first || i >= n ? (uint32_t)i : pos[i];
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (r >= (int)rounds) break;
-            const bool in = base + ((uint64_t)g * rounds + r) * 64 < n;
+            const bool in = base + ((uint64_t)g * R + r) * 64 < n;
             const uint32_t d = (key[r] >> shift) & (bins - 1);
             uint64_t same = __ballot(in);
             for (uint32_t b = 0; b < dbits; ++b) {
@@ -210,19 +210,6 @@ __device__ __forceinline__ void sort_pass(SortLds &sh, const uint32_t *keys, con
     }
 }
 
-__global__ __launch_bounds__(SORT_THREADS) void k_sort_one(const uint32_t *__restrict__ ids, uint32_t n, uint32_t n_vocab,
-                                                           uint32_t passes, uint32_t dbits, uint32_t rounds, uint32_t *keys0, uint32_t *pos0,
-                                                           uint32_t *keys1, uint32_t *pos1, Zeros z)
-{
-    __shared__ __align__(16) SortLds sh;
-    if (blockIdx.x > 0) return zero_block(z, blockIdx.x - 1);
-    sort_pass<R_ONE>(sh, ids, nullptr, true, n, n_vocab, 0, dbits, rounds, 1, 0, 1, nullptr, keys0, pos0);
-    if (passes == 1) return;
-    __threadfence_block();
-    __syncthreads();
-    sort_pass<R_ONE>(sh, keys0, pos0, false, n, n_vocab, dbits, dbits, rounds, 1, 0, 1, nullptr, keys1, pos1);
-}
-
 __global__ __launch_bounds__(SORT_THREADS) void k_sort_hist(const uint32_t *__restrict__ keys, uint32_t n, uint32_t n_vocab,
                                                             uint32_t shift, uint32_t bins, uint32_t groups, uint32_t blocks,
                                                             uint32_t *__restrict__ hist, Zeros z)
@@ -231,34 +218,21 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_hist(const uint32_t *__re
     if (blockIdx.x >= blocks) return zero_block(z, blockIdx.x - blocks);
     for (uint32_t b = threadIdx.x; b < bins; b += SORT_THREADS) h[b] = 0;
     __syncthreads();
-    const uint64_t base = (uint64_t)blockIdx.x * (SORT_THREADS * R_MANY) * groups + threadIdx.x;
+    const uint64_t base = (uint64_t)blockIdx.x * (SORT_THREADS * SORT_R) * groups + threadIdx.x;
     for (uint32_t g = 0; g < groups; ++g) {
-        uint32_t key[R_MANY];
+        uint32_t key[SORT_R];
 #pragma unroll
-        for (int r = 0; r < R_MANY; ++r) {
-            const uint64_t i = base + ((uint64_t)g * R_MANY + r) * SORT_THREADS;
+        for (int r = 0; r < SORT_R; ++r) {
+            const uint64_t i = base + ((uint64_t)g * SORT_R + r) * SORT_THREADS;
             key[r] = i < n ? keys[i] : 0;
         }
 #pragma unroll
-        for (int r = 0; r < R_MANY; ++r)
-            if (base + ((uint64_t)g * R_MANY + r) * SORT_THREADS < n)
+        for (int r = 0; r < SORT_R; ++r)
+            if (base + ((uint64_t)g * SORT_R + r) * SORT_THREADS < n)
                 atomicAdd(&h[(min(key[r], n_vocab) >> shift) & (bins - 1)], 1u);
     }
     __syncthreads();
     for (uint32_t b = threadIdx.x; b < bins; b += SORT_THREADS) hist[(uint64_t)blockIdx.x * bins + b] = h[b];
-}
-
-__global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(const uint32_t *__restrict__ keys,
-                                                               const uint32_t *__restrict__ pos, int first, uint32_t n,
-                                                               uint32_t n_vocab, uint32_t shift, uint32_t dbits,
-                                                               uint32_t groups, uint32_t blocks,
-                                                               const uint32_t *__restrict__ hist,
-                                                               uint32_t *__restrict__ keys_out,
-                                                               uint32_t *__restrict__ pos_out, Zeros z)
-{
-    __shared__ __align__(16) SortLds sh;
-    if (blockIdx.x >= blocks) return zero_block(z, blockIdx.x - blocks);
-    sort_pass<R_MANY>(sh, keys, pos, first, n, n_vocab, shift, dbits, R_MANY, groups, blockIdx.x, blocks, hist, keys_out, pos_out);
 }
 
 // Sums.  The sorted tokens are cut into chunks; a wavefront takes one chunk and 512 columns and adds up
@@ -742,20 +716,14 @@ extern "C" int toktier_embed_backward(const void *grad_out, int grad_type, uint6
         return (z.rows - z.from + z.per_block - 1) / z.per_block;
     };
     const uint32_t last = L.sort.passes - 1;
-    if (n <= SORT_ONE) {
-        const uint32_t zb = zero_blocks(0, 1);
-        k_sort_one<<<1 + zb, SORT_THREADS, 0, s>>>(ids, n, n_vocab, L.sort.passes, L.sort.dbits,
-                                                      (n + SORT_THREADS - 1) / SORT_THREADS, keys[0], pos[0], keys[1], pos[1], z);
-    } else {
-        for (uint32_t p = 0; p <= last; ++p) {
-            const uint32_t *ki = p ? keys[0] : ids, *pi = p ? pos[0] : nullptr, shift = p * L.sort.dbits, launches = 2 * L.sort.passes;
-            const uint32_t zh = zero_blocks(2 * p, launches);
-            k_sort_hist<<<L.sort.blocks + zh, SORT_THREADS, 0, s>>>(ki, n, n_vocab, shift, L.sort.bins, L.sort.groups, L.sort.blocks,
-                                                                    hist, z);
-            const uint32_t zs = zero_blocks(2 * p + 1, launches);
-            k_sort_scatter<<<L.sort.blocks + zs, SORT_THREADS, 0, s>>>(ki, pi, p == 0, n, n_vocab, shift, L.sort.dbits, L.sort.groups,
-                                                                       L.sort.blocks, hist, keys[p], pos[p], z);
-        }
+    for (uint32_t p = 0; p <= last; ++p) {
+        const uint32_t *ki = p ? keys[0] : ids, *pi = p ? pos[0] : nullptr, shift = p * L.sort.dbits, launches = 2 * L.sort.passes;
+        const uint32_t zh = zero_blocks(2 * p, launches);
+        k_sort_hist<<<L.sort.blocks + zh, SORT_THREADS, 0, s>>>(ki, n, n_vocab, shift, L.sort.bins, L.sort.groups, L.sort.blocks,
+                                                                hist, z);
+        const uint32_t zs = zero_blocks(2 * p + 1, launches);
+        k_sort_scatter<<<L.sort.blocks + zs, SORT_THREADS, 0, s>>>(ki, pi, p == 0, n, n_vocab, shift, L.sort.dbits, L.sort.groups,
+                                                                   L.sort.blocks, hist, keys[p], pos[p], z);
     }
     float *part = (float *)(ws + L.part);
     const uint64_t absent = accumulate || early ? 0 : (n_vocab + ZROWS - 1) / ZROWS;

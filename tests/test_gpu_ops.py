@@ -682,3 +682,10 @@ def test_embed_backward_few_tokens_of_a_large_table(tt):
     """A table that is zeroed by a launch of its own."""
     _embed_backward(tt, 900, 40000, 500, "float16", "float16", False)
     _embed_backward(tt, 900, 40000, 500, "float16", "float16", False, pad=3, lead=1)
+
+
+@pytest.mark.parametrize("vocab", [1, 2, 3])
+@pytest.mark.parametrize("tokens", [4097, 9000])
+def test_embed_backward_many_tokens_of_few_ids(tt, tokens, vocab):
+    _embed_backward(tt, tokens, vocab, 40, "bfloat16", "float32", False)
+    _embed_backward(tt, tokens, vocab, 600, "float32", "bfloat16", True)
