@@ -439,9 +439,10 @@ __global__ __launch_bounds__(SORT_THREADS) void k_zero_rows(Zeros z) { zero_bloc
 // brings the workgroups that its many rows need.  Up to 2 * ROWS rows a wavefront adds up by itself, in every
 // eighth of the workgroup's blocks; more are shared out between the wavefronts, and their sums joined in LDS.  Further
 // workgroups write the zeros of a small table, each for the rows that no ID names.
-// The work grows with the square of the tokens, the sort's four to six launches hardly: with the IDs of text, bfloat16
-// rows of 2,048 into float32 sums take 7.0 us here and 16.9 us sorted at 777 tokens (7 of them the call's
-// own), 17.5 and 35.4 at 4,096; where all tokens have one ID 18 and 25, 79 and 78.
+// The work grows with the square of the tokens, the sort's four to six launches hardly.  With the IDs of text (one in ten
+// the most frequent), gradients of bfloat16 added to a float32 table of 33,024 x 2,048: 777 tokens 6.9 us (the call's own cost),
+// 2,048 9.0 us, 26 us sorted, 4,096 17.6 and 31 us.  Tokens of one ID alone, which one workgroup per 512 columns then adds
+// up, take longer: 777 18 us, 2,048 40 and 30 us, 4,096 80 and 40 us.
 constexpr uint32_t FEW = 4096, FEW_WAVES = 8, FEW_THREADS = FEW_WAVES * 64;
 constexpr uint64_t ZEROS_BESIDE = 32u << 20;       // larger tables are zeroed by a launch of their own (10 MB: 7.1 and 9.8 us)
 constexpr uint32_t ZBYTES = 16384, ZMOST = 1024;   // of a workgroup that writes zeros: bytes (of at least a row), rows
