@@ -23,11 +23,12 @@ __global__ __launch_bounds__(256) void k_embed(const TI *__restrict__ table, uin
     if (c >= dim) return;
     const uint64_t t0 = (uint64_t)blockIdx.x * (U * step) + sub;
     const uint32_t n = dim - c;
-    float x[U][VEC];
+    float x[U][VEC], by[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const uint64_t t = t0 + (uint64_t)u * step;
         const uint32_t id = t < n_tokens ? ids[t] : 0xFFFFFFFFu;
+        by[u] = id < n_vocab ? scale : 0.f;   // zeros stay zeros, whatever the scale
         if (id < n_vocab) load_part(table + id * tstride + c, n, 0.f, x[u]);
         else
 #pragma unroll
@@ -38,7 +39,7 @@ __global__ __launch_bounds__(256) void k_embed(const TI *__restrict__ table, uin
         const uint64_t t = t0 + (uint64_t)u * step;
         if (t >= n_tokens) break;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) x[u][k] *= scale;
+        for (int k = 0; k < VEC; ++k) x[u][k] *= by[u];
         store_part(out + t * ostride + c, n, x[u]);
     }
 }
