@@ -12,11 +12,16 @@ namespace {
 //
 // A copy with a gather in front: bound by the bytes read and written.  A workgroup takes L lanes per
 // token (the row's vectors, a power of two up to 256) and 256 / L tokens per step, U steps whose loads
-// are all in flight together.
+// are all in flight together (16,384 rows of 4,096 bfloat16: 45 us with four steps, as with two, 54 with eight).  An output larger
+// than the caches of the chip's parts is stored past them, so that it does not drive out table rows: 33.5 us,
+// 5.7 TB/s.
+constexpr uint64_t STREAM_BYTES = 32u << 20;
+
 template <class TI, class TO, int U>
 __global__ __launch_bounds__(256) void k_embed(const TI *__restrict__ table, uint64_t tstride, uint32_t n_vocab,
                                                uint32_t dim, const uint32_t *__restrict__ ids, uint32_t n_tokens,
-                                               float scale, TO *__restrict__ out, uint64_t ostride, uint32_t lshift)
+                                               float scale, TO *__restrict__ out, uint64_t ostride, uint32_t lshift,
+                                               bool stream)
 {
     const uint32_t lane = threadIdx.x & ((1u << lshift) - 1u), sub = threadIdx.x >> lshift, step = 256u >> lshift;
     const uint32_t c = (blockIdx.y << lshift) * VEC + lane * VEC;
@@ -40,7 +45,8 @@ __global__ __launch_bounds__(256) void k_embed(const TI *__restrict__ table, uin
         if (t >= n_tokens) break;
 #pragma unroll
         for (int k = 0; k < VEC; ++k) x[u][k] *= by[u];
-        store_part(out + t * ostride + c, n, x[u]);
+        if (stream) stream_part(out + t * ostride + c, n, x[u]);
+        else store_part(out + t * ostride + c, n, x[u]);
     }
 }
 
@@ -87,7 +93,7 @@ struct Zeros {
     uint32_t rows, per_block, from;   // from: the launch's first row
 };
 
-__device__ __forceinline__ void zero_block(const Zeros &z, uint32_t block)
+template <bool STREAM> __device__ __forceinline__ void zero_rows(const Zeros &z, uint32_t block)
 {
     const uint64_t r0 = z.from + (uint64_t)block * z.per_block;
     for (uint32_t q = 0; q < z.per_block && r0 + q < z.rows; ++q) {
@@ -96,12 +102,19 @@ __device__ __forceinline__ void zero_block(const Zeros &z, uint32_t block)
         uint8_t *row = z.p + at;
         for (uint64_t c = threadIdx.x * 16ull; c < n; c += blockDim.x * 16ull) {
             if (c + 16 <= n) {
-                *(u32x4_row *)(row + c) = u32x4{0, 0, 0, 0};
+                if constexpr (STREAM) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, (u32x4_row *)(row + c));
+                else *(u32x4_row *)(row + c) = u32x4{0, 0, 0, 0};
             } else {
                 for (uint64_t d = c; d < n; d += 2) *(uint16_t *)(row + d) = 0;
             }
         }
     }
+}
+__device__ __forceinline__ void zero_block(const Zeros &z, uint32_t block)
+{
+    // past the caches where they are more than these hold: 538 MB in 22 us in each of four launches, 24 us through them
+    if (z.end > STREAM_BYTES) zero_rows<true>(z, block);
+    else zero_rows<false>(z, block);
 }
 
 struct SortLds {
@@ -241,7 +254,7 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_hist(const uint32_t *__re
 // that crosses a chunk's border leaves a partial sum (slot 0: the run entered from the chunk before, slot 1:
 // it starts here and goes on), joined in chunk order by k_embed_join.
 constexpr uint32_t COLS = 64 * VEC;
-constexpr int ROWS = 8, PARTS = 16;   // rows, and partial sums, of a wavefront in flight
+constexpr int ROWS = 8, PARTS = 8;   // rows, and partial sums, of a wavefront in flight
 
 template <class TT>
 __device__ __forceinline__ void put_row(TT *__restrict__ row, uint32_t n, float scale, bool accumulate,
@@ -261,7 +274,11 @@ __device__ __forceinline__ void put_row(TT *__restrict__ row, uint32_t n, float 
 
 constexpr int ZROWS = 16;   // table rows that a wavefront looks after when absent IDs get zeros here
 
-template <class TG, class TT>
+// ONCE: gradients too large for any cache are loaded past them (537 MB added to a table of 131,328 x 4,096: 258 -> 242 us; 82 MB
+// that the kernels before have left in the caches would take 156 instead of 121 us).
+constexpr uint64_t ONCE_BYTES = 256u << 20;
+
+template <class TG, class TT, bool ONCE>
 __global__ __launch_bounds__(256) void k_embed_sum(const TG *__restrict__ grad, uint64_t gstride,
                                                    const uint32_t *__restrict__ keys, const uint32_t *__restrict__ pos,
                                                    uint32_t n, uint32_t n_vocab, uint32_t dim, uint32_t chunk,
@@ -289,7 +306,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(const TG *__restrict__ grad, 
 #pragma unroll
             for (int u = 0; u < ROWS; ++u) {
                 const uint32_t p = (uint32_t)__builtin_amdgcn_readlane((int)pos_l, (int)min(i + u, live - 1));
-                if (i + u < live && m) x[u] = load_some(grad + p * gstride + c, m);
+                if (i + u < live && m) x[u] = ONCE ? load_once(grad + p * gstride + c, m) : load_some(grad + p * gstride + c, m);
             }
 #pragma unroll
             for (int u = 0; u < ROWS; ++u) {
@@ -637,7 +654,8 @@ extern "C" int toktier_embed(const void *table, int table_type, uint32_t n_vocab
             using TI = decltype(ti);
             using TO = decltype(to);
             k_embed<TI, TO, U><<<dim3((uint32_t)gx, gy), 256, 0, (hipStream_t)stream>>>(
-                (const TI *)table, table_stride, n_vocab, dim, ids, (uint32_t)n_tokens, scale, (TO *)out, out_stride, lshift);
+                (const TI *)table, table_stride, n_vocab, dim, ids, (uint32_t)n_tokens, scale, (TO *)out, out_stride, lshift,
+                n_tokens * dim * sizeof(TO) > STREAM_BYTES);
         });
     });
     return hip_status(hipGetLastError());
@@ -734,9 +752,13 @@ extern "C" int toktier_embed_backward(const void *grad_out, int grad_type, uint6
         with_type(table_type, [&](auto tt_) {
             using TG = decltype(tg);
             using TT = decltype(tt_);
-            k_embed_sum<TG, TT><<<blocks, 256, 0, s>>>((const TG *)grad_out, grad_stride, keys[last], pos[last], n, n_vocab, dim, L.chunk,
-                                                       L.n_chunks, L.ncb, scale, accumulate, (TT *)grad_table, table_stride, part, L.dpad,
-                                                       (uint32_t)absent);
+            auto launch = [&](auto once) {
+                k_embed_sum<TG, TT, decltype(once)::value><<<blocks, 256, 0, s>>>(
+                    (const TG *)grad_out, grad_stride, keys[last], pos[last], n, n_vocab, dim, L.chunk, L.n_chunks, L.ncb, scale, accumulate,
+                    (TT *)grad_table, table_stride, part, L.dpad, (uint32_t)absent);
+            };
+            if ((uint64_t)n * dim * sizeof(TG) > ONCE_BYTES) launch(std::true_type{});
+            else launch(std::false_type{});
         });
     });
     with_type(table_type, [&](auto tt_) {

@@ -86,6 +86,16 @@ template <class T> __device__ __forceinline__ Vec<T> load_some(const T *p, uint3
     return to_vec<T>(x);
 }
 
+// load_some past the caches, for what is read once
+template <class T> __device__ __forceinline__ Vec<T> load_once(const T *p, uint32_t n)
+{
+    if (n < VEC) return load_some(p, n);
+    Vec<T> v;
+    v.a = __builtin_nontemporal_load((const u32x4_row *)p);
+    if constexpr (sizeof(T) == 4) v.b = __builtin_nontemporal_load((const u32x4_row *)(p + 4));
+    return v;
+}
+
 template <class T> __device__ __forceinline__ void store_part(T *p, uint32_t n, const float (&x)[VEC])
 {
     if (n >= VEC) {
