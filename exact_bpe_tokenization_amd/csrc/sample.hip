@@ -11,6 +11,18 @@
 //   cells   per cell of consecutive IDs, the mass of what lies above the border, and a list of what lies in it;
 //   draw    the list sorted gives the exact border; the running mass over the cells, then inside one, gives the ID.
 // A bin of bfloat16 holds one key, so that its mass is its count times one weight and its list is not needed.
+// The least temperature, or k = 1, ends after the first phase; without top-k and top-p there is no border; a small k
+// needs no histogram (list_first); rows that the phases do not fit (NaN, a border of thousands of equals) take
+// general_row.
+//
+// A workgroup of 1,024 threads takes a row (256 threads up to 8,192 elements), so a row's time is the time of its chain of
+// phases, and the rows of a batch of up to 256 run side by side.  131,328 bfloat16, one row and 256 of them (67 MB): first
+// alone 8.5 and 16.3 us (4.1 TB/s), temperature with top-k 50 and top-p 0.95 18.3 and 28.5, top-k 1,000 with top-p 0.9 40 and
+// 50, top-p 0.95 50 and 55, full distribution 29 and 39.  What bounds them: the loads of one CU in the keys phase without
+// a histogram (5.8 us of a row); the LDS atomics of the histogram (16 us); in the cells phase VALU issue, some 100
+// instructions for a vector of eight (18 us); for float32 and float16 the exponentials in 64 bits, 30
+// instructions each; else the latency of some ten barriers.  Not split over workgroups: a second launch costs 3 us, and a
+// phase needs the one before from the whole row.
 #include <type_traits>
 
 #include "ops.h"
