@@ -310,7 +310,9 @@ extern "C" int toktier_cross_entropy(const void *logits, int type, uint32_t n_ro
     if (workspace_bytes < L.total) return TOKTIER_E_CAPACITY;
     const uint64_t lb = extent(type, n_rows, n_vocab, stride), nb = 4ull * n_rows;
     if (!apart(workspace, L.total, logits, lb) || !apart(workspace, L.total, loss, nb) || !apart(workspace, L.total, lse, nb) ||
-        !apart(loss, nb, lse, nb) || !apart(loss, nb, logits, lb) || !apart(lse, nb, logits, lb) ||
+        !apart(workspace, L.total, targets, nb) || (grad_loss && !apart(workspace, L.total, grad_loss, nb)) ||
+        !apart(loss, nb, lse, nb) || !apart(loss, nb, logits, lb) || !apart(lse, nb, logits, lb) || !apart(loss, nb, targets, nb) ||
+        !apart(lse, nb, targets, nb) || (grad_loss && (!apart(loss, nb, grad_loss, nb) || !apart(lse, nb, grad_loss, nb))) ||
         (grad_logits && (!apart(grad_logits, extent(type, n_rows, n_vocab, grad_stride), loss, nb) ||
                          !apart(workspace, L.total, grad_logits, extent(type, n_rows, n_vocab, grad_stride)))))
         return TOKTIER_E_INVALID_ARG;

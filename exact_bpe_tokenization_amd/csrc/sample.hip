@@ -1502,8 +1502,13 @@ extern "C" int toktier_sample(const void *logits, int type, uint32_t n_rows, uin
     if (!workspace || ((uintptr_t)workspace & 255u)) return TOKTIER_E_INVALID_ARG;
     if (workspace_bytes < 256) return TOKTIER_E_CAPACITY;
     const uint64_t lb = extent(type, n_rows, n_vocab, stride), ob = 4ull * n_rows;
-    if (!apart(out_ids, ob, logits, lb) || (out_logprobs && (!apart(out_logprobs, ob, logits, lb) || !apart(out_logprobs, ob, out_ids, ob))))
-        return TOKTIER_E_INVALID_ARG;
+    const uint64_t mb = 4 * (words + (mask_stride ? (n_rows - 1) * mask_stride : 0));
+    auto alone = [&](const void *out) {   // an output beside all inputs
+        return apart(out, ob, logits, lb) && apart(out, ob, uniform, ob) && (!mask || apart(out, ob, mask, mb)) &&
+               (!temperature || apart(out, ob, temperature, ob)) && (!top_k || apart(out, ob, top_k, ob)) &&
+               (!top_p || apart(out, ob, top_p, ob)) && (!min_p || apart(out, ob, min_p, ob));
+    };
+    if (!alone(out_ids) || (out_logprobs && (!alone(out_logprobs) || !apart(out_logprobs, ob, out_ids, ob)))) return TOKTIER_E_INVALID_ARG;
     const double magic = weight_magic(n_vocab);
     with_type(type, [&](auto t) {
         using T = decltype(t);

@@ -689,3 +689,21 @@ def test_embed_backward_few_tokens_of_a_large_table(tt):
 def test_embed_backward_many_tokens_of_few_ids(tt, tokens, vocab):
     _embed_backward(tt, tokens, vocab, 40, "bfloat16", "float32", False)
     _embed_backward(tt, tokens, vocab, 600, "float32", "bfloat16", True)
+
+
+@pytest.mark.parametrize("tokens", [4096, 5000])
+def test_embed_backward_offsets_past_32_bits(tt, tokens):
+    """Gradient rows and table rows 2^20 elements apart, against the same rows side by side."""
+    import torch
+    dim, stride = 24, (1 << 20) + 8
+    _say("embed_backward far rows", tokens)
+    far = torch.empty(tokens * stride, dtype=torch.bfloat16, device="cuda").view(tokens, stride)[:, :dim]
+    near = torch.randn(tokens, dim, device="cuda").to(torch.bfloat16)
+    far.copy_(near)
+    ids = torch.randint(tokens, (tokens,), device="cuda", dtype=torch.int32)
+    ws = _ws(tt.toktier_embed_backward_workspace_bytes(tokens, tokens, dim))
+    out = torch.empty(tokens, dim, device="cuda")
+    far_out = torch.empty(tokens * stride, dtype=torch.float32, device="cuda").view(tokens, stride)[:, :dim]
+    tt.toktier_embed_backward(near, ids, out, ws)
+    tt.toktier_embed_backward(far, ids, far_out, ws)
+    assert torch.equal(out, far_out)

@@ -120,3 +120,15 @@ def test_binding_refuses_host_tensors():
         with pytest.raises(tt.ToktierError) as e:
             f()
         assert e.value.status == INVALID
+
+
+@pytest.mark.parametrize("name,base,change", [
+    ("toktier_sample", SAMPLE, dict(out_ids=at(9216))), ("toktier_sample", SAMPLE, dict(out_ids=at(8192))),
+    ("toktier_sample", SAMPLE, dict(out_logprobs=at(8448))), ("toktier_sample", SAMPLE, dict(out_logprobs=at(8712))),
+    ("toktier_sample", SAMPLE, dict(out_ids=at(8964))), ("toktier_sample", SAMPLE, dict(out_logprobs=at(4096 + 24))),
+    ("toktier_cross_entropy", LOSS, dict(loss=at(4096))), ("toktier_cross_entropy", LOSS, dict(lse=at(4104))),
+    ("toktier_cross_entropy", LOSS, dict(loss=at(16384))), ("toktier_cross_entropy", LOSS, dict(lse=at(16380))),
+    ("toktier_cross_entropy", LOSS, dict(workspace=at(4096))), ("toktier_cross_entropy", LOSS, dict(workspace=at(16384)))])
+def test_outputs_on_inputs_are_refused(name, base, change):
+    args = {**base, **change}
+    assert getattr(tt.lib(), name)(*args.values()) == INVALID
