@@ -7,6 +7,12 @@
 namespace tt {
 namespace {
 
+// The first column of a vector: a row's last one is moved back so that it is whole (elements one by one take several times
+// as long) where it may share columns with the vector before, whose lane then loads and stores the same values.
+// A row that is added to needs both in one wavefront: its loads precede its stores.  (Gradient of 65,536 tokens, 33,024 x 2,047:
+// 224 us with a last vector of seven, 156 us so.)
+__device__ __forceinline__ uint32_t whole(uint32_t c, uint32_t dim, bool may) { return may & (c < dim) & (dim - c < VEC) ? dim - VEC : c; }
+
 // ---------------------------------------------------------------------------------------------
 // lookup: out[t, :] = scale * table[ids[t], :]
 //
@@ -24,8 +30,9 @@ __global__ __launch_bounds__(256) void k_embed(const TI *__restrict__ table, uin
                                                bool stream)
 {
     const uint32_t lane = threadIdx.x & ((1u << lshift) - 1u), sub = threadIdx.x >> lshift, step = 256u >> lshift;
-    const uint32_t c = (blockIdx.y << lshift) * VEC + lane * VEC;
+    uint32_t c = (blockIdx.y << lshift) * VEC + lane * VEC;
     if (c >= dim) return;
+    c = whole(c, dim, c > 0);
     const uint64_t t0 = (uint64_t)blockIdx.x * (U * step) + sub;
     const uint32_t n = dim - c;
     float x[U][VEC], by[U];
@@ -289,7 +296,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(const TG *__restrict__ grad, 
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4u + (threadIdx.x >> 6)), sums = n_chunks * ncb;
     if (unit < sums) {
-        const uint32_t ch = unit / ncb, c = unit % ncb * COLS + lane * VEC;
+        const uint32_t ch = unit / ncb, c = whole(unit % ncb * COLS + lane * VEC, dim, lane > 0);
         const uint32_t i0 = ch * chunk, len = min(chunk, n - i0);
         const uint32_t my = min(lane, len - 1);
         const uint32_t key_l = keys[i0 + my], pos_l = pos[i0 + my];
@@ -348,7 +355,10 @@ __global__ __launch_bounds__(256) void k_embed_sum(const TG *__restrict__ grad, 
     while (todo) {
         const uint32_t r = (uint32_t)r0 + (uint32_t)__builtin_ctzll(todo);
         todo &= todo - 1;
-        for (uint32_t c = lane * VEC; c < dim; c += COLS) store_part(table + r * tstride + c, dim - c, zero);
+        for (uint32_t c0 = lane * VEC; c0 < dim; c0 += COLS) {
+            const uint32_t c = whole(c0, dim, c0 > 0);
+            store_part(table + r * tstride + c, dim - c, zero);
+        }
     }
 }
 
@@ -401,7 +411,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_embed_join(const uint32_t *__r
     uint32_t key;
     bool is_long = false;
     if (unit(wave) < units) {
-        const uint32_t ch = unit(wave) / ncb, c = unit(wave) % ncb * COLS + lane * VEC;
+        const uint32_t ch = unit(wave) / ncb, c = whole(unit(wave) % ncb * COLS + lane * VEC, dim, lane > 0);
         if (starts(ch, key)) {
             const uint32_t count = heads(ch + 1, key);
             is_long = count == 64;
@@ -417,7 +427,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_embed_join(const uint32_t *__r
     __syncthreads();
     for (uint32_t w = 0; w < JOIN_WAVES; ++w) {
         if (!any_long[w]) continue;
-        const uint32_t ch = unit(w) / ncb, c = unit(w) % ncb * COLS + lane * VEC;
+        const uint32_t ch = unit(w) / ncb, c = whole(unit(w) % ncb * COLS + lane * VEC, dim, lane > 0);
         starts(ch, key);
         uint32_t count = 0;
         for (uint32_t h0 = ch + 1;; h0 += JOIN_THREADS) {   // 64 chunks a wavefront
@@ -518,7 +528,7 @@ __global__ __launch_bounds__(FEW_THREADS) void k_embed_few(const TG *__restrict_
         const uint32_t share = shared ? (total + FEW_WAVES - 1) / FEW_WAVES : total;
         const uint32_t from = shared ? min(wave * share, total) : 0, to = min(from + share, total);
         for (uint32_t cb = rank + (shared ? 0 : total * wave); cb < ncb; cb += shared ? total : total * FEW_WAVES) {
-            const uint32_t c = cb * COLS + lane * VEC, m = c < dim ? dim - c : 0;
+            const uint32_t c = whole(cb * COLS + lane * VEC, dim, lane > 0), m = c < dim ? dim - c : 0;
             float acc[VEC] = {};
             for (uint32_t i = from; i < to; i += ROWS) {
                 Vec<TG> x[ROWS];
@@ -560,7 +570,7 @@ __global__ __launch_bounds__(FEW_THREADS) void k_embed_few(const TG *__restrict_
     const uint32_t vectors = (dim + VEC - 1) / VEC;
     const float zero[VEC] = {};
     for (uint32_t i = tid; i < rows * vectors; i += FEW_THREADS) {
-        const uint32_t r = i / vectors, c = (i - r * vectors) * VEC;
+        const uint32_t r = i / vectors, c0 = (i - r * vectors) * VEC, c = whole(c0, dim, c0 > 0);
         if (!sh.present[r]) store_part(table + (uint64_t)(r0 + r) * tstride + c, dim - c, zero);
     }
 }
