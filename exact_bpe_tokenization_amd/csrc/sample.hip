@@ -196,7 +196,8 @@ template <class T> struct Vec8 {
     {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t out = sign_pairs(__builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat((s16x2)(short)Keys<T>::INF, pair(i))));
+            const s16x2 left = __builtin_elementwise_sub_sat((s16x2)(short)Keys<T>::INF, pair(i));
+            const uint32_t out = sign_pairs(__builtin_bit_cast(uint32_t, left));
             a[i] = (a[i] & ~out) | (0x80008000u & out);
         }
     }
@@ -348,8 +349,14 @@ __device__ __forceinline__ uint64_t row_scan(uint64_t v)
     v = dpp_add<0x114, 0xF>(v);
     return dpp_add<0x118, 0xF>(v);
 }
-__device__ __forceinline__ uint64_t wave_sums(const uint64_t (&v)[4]) { return row_scan(rows_of(halves(v[0], v[2]), halves(v[1], v[3]))); }
-__device__ __forceinline__ uint64_t wave_sums(const uint64_t (&v)[2]) { return dpp_add<0x142, 0xA>(row_scan(halves(v[0], v[1]))); }
+__device__ __forceinline__ uint64_t wave_sums(const uint64_t (&v)[4])
+{
+    return row_scan(rows_of(halves(v[0], v[2]), halves(v[1], v[3])));
+}
+__device__ __forceinline__ uint64_t wave_sums(const uint64_t (&v)[2])
+{
+    return dpp_add<0x142, 0xA>(row_scan(halves(v[0], v[1])));
+}
 __device__ __forceinline__ uint64_t lane_value(uint64_t v, uint32_t lane)
 {
     return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), (int)lane) << 32 |
@@ -432,9 +439,10 @@ template <class T> struct Row {
     }
     __device__ __forceinline__ V fetch(uint32_t j) const;   // one vector, anywhere
     // f(index of the first element, keys, q) over the vectors of this thread, ascending: one of every `step` elements,
-    // AHEAD loads in flight; q counts these, and after them g(index of their first element, how many they were).  (A load under a condition would wait for those before it, so where fewer than AHEAD are
-    // left the last is loaded again.)  Only the last step may pass the row's end.  Positive NaN are not taken out, and
-    // with RAW the logits are not made keys.
+    // AHEAD loads in flight; q counts these, and after them g(index of their first element, how many they were).  (A
+    // load under a condition would wait for those before it, so where fewer than AHEAD are left the last is loaded
+    // again.)  Only the last step may pass the row's end.  Positive NaN are not taken out, and with RAW the logits are
+    // not made keys.
     template <uint32_t AHEAD, bool RAW, class F, class G> __device__ __forceinline__ void each(uint32_t step, F f, G g) const
     {
         const uint32_t full = n / step, j0 = threadIdx.x * VEC;
@@ -916,8 +924,8 @@ __device__ __forceinline__ uint32_t find_part(Lds<WAVES> &sh, uint64_t part, uin
 
 // ---- draw
 template <class T, int WAVES, class W>
-__device__ __forceinline__ void draw(const Row<T> &row, Lds<WAVES> &sh, const Weights &wt, const Border &b, uint64_t w_min, W weight, uint32_t *out_id,
-                                     float *out_logprob)
+__device__ __forceinline__ void draw(const Row<T> &row, Lds<WAVES> &sh, const Weights &wt, const Border &b, uint64_t w_min, W weight,
+                                     uint32_t *out_id, float *out_logprob)
 {
     using K = Keys<T>;
     using V = Vec8<T>;
