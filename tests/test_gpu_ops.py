@@ -707,3 +707,46 @@ def test_embed_backward_offsets_past_32_bits(tt, tokens):
     tt.toktier_embed_backward(near, ids, out, ws)
     tt.toktier_embed_backward(far, ids, far_out, ws)
     assert torch.equal(out, far_out)
+
+
+def test_graph_replays_of_the_longer_paths(tt):
+    """The sorted gradient with zeros beside the sort and with sums added, and the loss of few long rows."""
+    import torch
+    n, vocab, dim, rows, wide = 5000, 9000, 72, 3, 70000
+    dev, bf = "cuda", torch.bfloat16
+
+    def buffers(seed):
+        g = torch.Generator(device=dev).manual_seed(seed)
+        return dict(grad=torch.randn(n, dim, generator=g, device=dev).to(bf),
+                    ids=torch.randint(-1, vocab, (n,), generator=g, device=dev, dtype=torch.int32),
+                    logits=(3 * torch.randn(rows, wide, generator=g, device=dev)).to(bf),
+                    targets=torch.randint(wide, (rows,), generator=g, device=dev, dtype=torch.int32),
+                    dense=torch.empty(vocab, dim, device=dev), added=torch.randn(vocab, dim, generator=g, device=dev),
+                    loss=torch.empty(rows, device=dev), lse=torch.empty(rows, device=dev),
+                    dlogits=torch.empty(rows, wide, device=dev, dtype=bf),
+                    ws=_ws(max(tt.toktier_embed_backward_workspace_bytes(n, vocab, dim),
+                               tt.toktier_cross_entropy_workspace_bytes(rows, wide))))
+
+    def step(b):
+        tt.toktier_embed_backward(b["grad"], b["ids"], b["dense"], b["ws"])
+        tt.toktier_embed_backward(b["grad"], b["ids"], b["added"], b["ws"], accumulate=True)
+        tt.toktier_cross_entropy(b["logits"], b["targets"], b["loss"], b["lse"], b["ws"], grad_logits=b["dlogits"])
+
+    b = buffers(1)
+    step(b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        step(b)
+    for seed in (2, 3, 4, 2):
+        other = buffers(seed)
+        for name in ("grad", "ids", "logits", "targets", "added"):
+            b[name].copy_(other[name])
+        b["ws"].fill_(seed)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        step(other)
+        torch.cuda.synchronize()
+        for name in ("dense", "added", "loss", "lse", "dlogits"):
+            assert torch.equal(b[name], other[name]), (seed, name)
