@@ -9,7 +9,7 @@ namespace {
 
 // The first column of a vector: a row's last one is moved back so that it is whole (elements one by one take several times
 // as long) where it may share columns with the vector before, whose lane then loads and stores the same values.
-// A row that is added to needs both in one wavefront: its loads precede its stores.  (Gradient of 65,536 tokens, 33,024 x 2,047:
+// A row that is added to needs both in one wavefront, its loads before its stores: see put_row.  (Gradient of 65,536 tokens, 33,024 x 2,047:
 // 224 us with a last vector of seven, 156 us so.)
 __device__ __forceinline__ uint32_t whole(uint32_t c, uint32_t dim, bool may)
 {
@@ -276,6 +276,7 @@ __device__ __forceinline__ void put_row(TT *__restrict__ row, uint32_t n, float 
     float x[VEC];
     if (accumulate) {
         load_part(row, n, 0.f, x);
+        wave_order();   // a neighbour may load, and store, some of the same columns
 #pragma unroll
         for (int k = 0; k < VEC; ++k) x[k] += scale * acc[k];
     } else {

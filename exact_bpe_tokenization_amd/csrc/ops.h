@@ -116,6 +116,16 @@ template <class T> __device__ __forceinline__ void stream_part(T *p, uint32_t n,
     if constexpr (sizeof(T) == 4) __builtin_nontemporal_store(v.b, (u32x4_row *)(p + 4));
 }
 
+// Every lane's accesses before this point come before every lane's after it.  A wavefront's lanes run in step, so this
+// is no instruction; it keeps the compiler from moving an access of one lane past another lane's of the same place, which
+// within a lane would change nothing.
+__device__ __forceinline__ void wave_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---------------------------------------------------------------------------------------------
 // host side
 
