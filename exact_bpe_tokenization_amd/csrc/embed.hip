@@ -223,13 +223,13 @@ __global__ __launch_bounds__(SORT_THREADS) void k_sort_scatter(const uint32_t *_
             }
             const uint32_t rank = __popcll(same & ((1ull << lane) - 1ull));
             const uint32_t place = sh.cnt[wave][d];
-            __builtin_amdgcn_wave_barrier();
+            wave_order();   // the bin's place is read by all its lanes before one moves it on
             if (in) {
                 if (rank == 0) sh.cnt[wave][d] = place + __popcll(same);
                 keys_out[place + rank] = key[r];
                 pos_out[place + rank] = from[r];
             }
-            __builtin_amdgcn_wave_barrier();
+            wave_order();
         }
     }
 }

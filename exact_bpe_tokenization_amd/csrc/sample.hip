@@ -894,7 +894,7 @@ template <int WAVES> __device__ __forceinline__ void sort_list(Lds<WAVES> &sh, u
             // pairs less than 64 apart stay inside the 128 elements of one wavefront
             const uint32_t next = stride > 1 ? stride / 2 : run;
             if (stride >= 64 || next >= 64) __syncthreads();
-            else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            else wave_order();
         }
     __syncthreads();
 }

@@ -1,0 +1,24 @@
+"""Token operators on the GPU over the parts of their range between the ordinary sizes."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_ops import _dev, _say, _ws, tt  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("distinct", [1, 2, 3, 63, 64, 65])
+@pytest.mark.parametrize("apart", [1, 64, 2048])
+def test_sort_keeps_every_token(tt, distinct, apart):  # noqa: F811
+    """Neighbouring tokens with equal digits of the sort, low or high: a column per bit of the token's position, so that the
+    sums of an ID count the bits of all of its tokens."""
+    tokens, vocab = 20000, 70 * 2048
+    _say("sort", distinct, apart)
+    ids = np.arange(tokens) % distinct * apart
+    bits = (np.arange(tokens)[:, None] >> np.arange(16)) & 1
+    bits = np.concatenate([bits, 1 - bits], axis=1)
+    table = torch.full((vocab, 32), 5.0, device="cuda")
+    tt.toktier_embed_backward(_dev(bits, "bfloat16"), _dev(ids), table, _ws(tt.toktier_embed_backward_workspace_bytes(tokens, vocab, 32)))
+    ref = torch.zeros(vocab, 32, dtype=torch.int64).index_add_(0, torch.from_numpy(ids), torch.from_numpy(bits))
+    assert torch.equal(table.cpu().long(), ref)
