@@ -4,6 +4,8 @@
 //   dx_j = c (exp(x_j - m) / s - [j == y])
 //
 // Bound by memory: the logits are read and the gradient written, with one exponential per element.
+#include <algorithm>
+
 #include "ops.h"
 
 namespace tt {
@@ -271,7 +273,8 @@ namespace {
 // Few long rows are split: a second launch (3 us) buys the other CUs.  131,328 bfloat16 with gradient, split /
 // whole: 1 row 10.4 / 22.3 us, 128 rows 20.0 / 24.9, 192 rows 30.0 / 27.9; of 33,024 elements 10.3 / 9.1 us and
 // never better.
-bool split_rows(uint32_t n_rows, uint32_t n_vocab) { return n_vocab >= 8 * PIECE && n_rows < 160; }
+constexpr uint32_t MOST_SPLIT = 159;
+bool split_rows(uint32_t n_rows, uint32_t n_vocab) { return n_vocab >= 8 * PIECE && n_rows <= MOST_SPLIT; }
 
 struct LossLayout {
     uint32_t pieces;   // 0: rows are not split
@@ -293,8 +296,8 @@ LossLayout loss_layout(uint32_t n_rows, uint32_t n_vocab)
 extern "C" int toktier_cross_entropy_workspace_bytes(uint32_t n_rows, uint32_t n_vocab, uint64_t *out_bytes)
 {
     if (!out_bytes || n_vocab == 0 || n_vocab > TOKTIER_MAX_VOCAB || n_rows > 0x7FFFFFFFu) return TOKTIER_E_INVALID_ARG;
-    const uint64_t n = loss_layout(n_rows, n_vocab).total;
-    *out_bytes = n < 256 ? 256 : n;
+    // what any call of up to n_rows rows needs: the most of those whose rows are split
+    *out_bytes = loss_layout(std::clamp(n_rows, 1u, MOST_SPLIT), n_vocab).total;
     return TOKTIER_OK;
 }
 

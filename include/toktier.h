@@ -437,7 +437,8 @@ int toktier_embed_backward(const void *grad_out, int grad_type, uint64_t grad_st
  *   grad_loss    device, float[n_rows], or NULL.
  *   grad_logits  device, n_rows rows of n_vocab elements of `type`, or NULL for the loss alone; may be
  *                `logits` itself with the same stride (in place), else must not overlap it.
- *   workspace    device, toktier_cross_entropy_workspace_bytes(n_rows, n_vocab) bytes.
+ *   workspace    device, toktier_cross_entropy_workspace_bytes(n_rows, n_vocab) bytes, which are enough for
+ *                every call of no more rows and IDs.
  */
 int toktier_cross_entropy_workspace_bytes(uint32_t n_rows, uint32_t n_vocab, uint64_t *out_bytes);
 int toktier_cross_entropy(const void *logits, int type, uint32_t n_rows, uint32_t n_vocab, uint64_t stride,

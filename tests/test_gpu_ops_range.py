@@ -22,3 +22,22 @@ def test_sort_keeps_every_token(tt, distinct, apart):  # noqa: F811
     tt.toktier_embed_backward(_dev(bits, "bfloat16"), _dev(ids), table, _ws(tt.toktier_embed_backward_workspace_bytes(tokens, vocab, 32)))
     ref = torch.zeros(vocab, 32, dtype=torch.int64).index_add_(0, torch.from_numpy(ids), torch.from_numpy(bits))
     assert torch.equal(table.cpu().long(), ref)
+
+
+def test_loss_of_a_last_batch_in_the_workspace_of_the_others(tt):  # noqa: F811
+    """One workspace for a batch and for the few rows left after it."""
+    vocab, most = 70001, 300
+    torch.manual_seed(1)
+    ws = _ws(tt.toktier_cross_entropy_workspace_bytes(most, vocab))
+    x = (3 * torch.randn(most, vocab, device="cuda")).bfloat16()
+    y = torch.randint(vocab, (most,), device="cuda", dtype=torch.int32)
+    outs = []
+    for rows in (most, 159, 3):
+        _say("loss workspace", rows)
+        loss, lse, grad = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), torch.empty_like(x[:rows])
+        tt.toktier_cross_entropy(x[:rows], y[:rows], loss, lse, ws, grad_logits=grad)
+        outs.append((loss, grad))
+    for loss, grad in outs[1:]:   # split or whole: sums in another order, 32 roundings at most along a longest chain
+        n = len(loss)
+        assert torch.allclose(loss, outs[0][0][:n], rtol=0, atol=20 * 64 * 2.0 ** -24)
+        assert torch.allclose(grad.float(), outs[0][1][:n].float(), rtol=2.0 ** -7, atol=1e-30)
