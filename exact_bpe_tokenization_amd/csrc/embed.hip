@@ -590,6 +590,10 @@ struct BackwardLayout {
     uint64_t keys[2], pos[2], hist, part, total;
 };
 
+constexpr uint32_t LONG_CHUNK = 64, SHORT_CHUNK = 8, FULL_CHIP = 4096;   // tokens, tokens, wavefronts
+
+uint64_t padded(uint64_t bytes) { return (bytes + 255) & ~255ull; }
+
 BackwardLayout backward_layout(uint64_t n_tokens, uint32_t n_vocab, uint32_t dim)
 {
     BackwardLayout L;
@@ -598,13 +602,13 @@ BackwardLayout backward_layout(uint64_t n_tokens, uint32_t n_vocab, uint32_t dim
     L.dpad = (dim + VEC - 1) / VEC * VEC;
     // tokens per chunk: 64 (fewest partial sums), fewer where that would leave the chip with under 4,096
     // wavefronts, eight per CU and SIMD pair
-    L.chunk = 64;
-    while (L.chunk > 8 && n_tokens * L.ncb < 4096ull * L.chunk) L.chunk /= 2;
+    L.chunk = LONG_CHUNK;
+    while (L.chunk > SHORT_CHUNK && n_tokens * L.ncb < (uint64_t)FULL_CHIP * L.chunk) L.chunk /= 2;
     L.n_chunks = (uint32_t)((n_tokens + L.chunk - 1) / L.chunk);
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t o = at;
-        at += (bytes + 255) & ~255ull;
+        at += padded(bytes);
         return o;
     };
     for (int k = 0; k < 2; ++k) {
@@ -615,6 +619,20 @@ BackwardLayout backward_layout(uint64_t n_tokens, uint32_t n_vocab, uint32_t dim
     L.part = take(8ull * L.n_chunks * L.dpad);
     L.total = n_tokens <= FEW ? 256 : at;   // few tokens need none
     return L;
+}
+
+// Bytes for every call of no more tokens, IDs and columns; single parts of the layout shrink as these grow.
+// Histograms: of at most 256 blocks, and one digit of 11 bits from 1,024 IDs on.  Partial sums: chunks shorter than 64 are fewer
+// than 2 FULL_CHIP / ncb, one more for the last, of at most ncb * COLS columns.
+uint64_t backward_bytes(uint64_t n_tokens, uint32_t n_vocab, uint32_t dim)
+{
+    if (n_tokens <= FEW) return 256;
+    const uint64_t blocks = std::min<uint64_t>(256, (n_tokens + SORT_THREADS * SORT_R - 1) / (SORT_THREADS * SORT_R));
+    const uint64_t bins = n_vocab >= MAX_BINS / 2 ? MAX_BINS : sort_plan(n_tokens, n_vocab).bins;
+    const uint64_t dpad = (dim + VEC - 1) / VEC * VEC;
+    const uint64_t brief = std::min<uint64_t>(n_tokens / SHORT_CHUNK * dpad, 2ull * FULL_CHIP * COLS);
+    const uint64_t sums = std::max(n_tokens / LONG_CHUNK * dpad, brief) + dpad;
+    return 4 * padded(4 * n_tokens) + padded(4 * blocks * bins) + padded(8 * sums);
 }
 
 // The rows of a table as zeros to write; contiguous rows are cut into pieces of 16 KiB, one per block
@@ -684,7 +702,7 @@ extern "C" int toktier_embed_backward_workspace_bytes(uint64_t n_tokens, uint32_
                                                       uint64_t *out_bytes)
 {
     if (!out_bytes || !sizes_ok(n_tokens, n_vocab, dim)) return TOKTIER_E_INVALID_ARG;
-    *out_bytes = backward_layout(n_tokens, n_vocab, dim).total;
+    *out_bytes = backward_bytes(n_tokens, n_vocab, dim);
     return TOKTIER_OK;
 }
 

@@ -382,7 +382,8 @@ int toktier_plan_free(toktier_plan *p);
  *   - Work is enqueued on `stream` (hipStream_t as void*, NULL = default) of the current device; nothing
  *     is allocated or waited for, so every call can be captured into a HIP graph.  A workspace is
  *     caller-owned scratch, 256-byte aligned, its contents on entry do not matter, and it must not be
- *     shared by two calls in flight.
+ *     shared by two calls in flight.  The sizes never fall as rows, tokens, IDs or columns grow: what is
+ *     enough for a program's largest call is enough for all of them.
  *   - Results depend on the arguments alone: repeated calls give the same bits.
  * Errors of every call: E_INVALID_ARG (null pointer, unknown type, bad size, stride or alignment,
  * overlapping output), E_CAPACITY (workspace too small), E_HIP; arguments are checked before any device
@@ -437,8 +438,7 @@ int toktier_embed_backward(const void *grad_out, int grad_type, uint64_t grad_st
  *   grad_loss    device, float[n_rows], or NULL.
  *   grad_logits  device, n_rows rows of n_vocab elements of `type`, or NULL for the loss alone; may be
  *                `logits` itself with the same stride (in place), else must not overlap it.
- *   workspace    device, toktier_cross_entropy_workspace_bytes(n_rows, n_vocab) bytes, which are enough for
- *                every call of no more rows and IDs.
+ *   workspace    device, toktier_cross_entropy_workspace_bytes(n_rows, n_vocab) bytes.
  */
 int toktier_cross_entropy_workspace_bytes(uint32_t n_rows, uint32_t n_vocab, uint64_t *out_bytes);
 int toktier_cross_entropy(const void *logits, int type, uint32_t n_rows, uint32_t n_vocab, uint64_t stride,

@@ -41,3 +41,20 @@ def test_loss_of_a_last_batch_in_the_workspace_of_the_others(tt):  # noqa: F811
         n = len(loss)
         assert torch.allclose(loss, outs[0][0][:n], rtol=0, atol=20 * 64 * 2.0 ** -24)
         assert torch.allclose(grad.float(), outs[0][1][:n].float(), rtol=2.0 ** -7, atol=1e-30)
+
+
+def test_gradients_of_fewer_tokens_in_the_workspace_of_the_most(tt):  # noqa: F811
+    """One workspace through lengths at which the chunks and the sort's blocks change; integers, so sums are exact."""
+    vocab, dim, most = 3000, 64, 262145
+    rng = np.random.default_rng(5)
+    ids, vals = rng.integers(-1, vocab, most), rng.integers(-3, 4, (most, dim))
+    ws = _ws(tt.toktier_embed_backward_workspace_bytes(most, vocab, dim))
+    grad, dev = _dev(vals, "bfloat16"), _dev(ids)
+    for n in (most, 262144, 65536, 65535, 32767, 16384, 16383, 4097, 100):
+        _say("gradient workspace", n)
+        table = torch.full((vocab, dim), 5.0, device="cuda")
+        tt.toktier_embed_backward(grad[:n], dev[:n], table, ws)
+        ok = torch.from_numpy(ids[:n] >= 0)
+        ref = torch.zeros(vocab, dim, dtype=torch.int64)
+        ref.index_add_(0, torch.from_numpy(ids[:n])[ok], torch.from_numpy(vals[:n])[ok])
+        assert torch.equal(table.cpu().long(), ref)

@@ -49,3 +49,41 @@ def test_cross_entropy_takes_the_workspace_of_a_larger_call(most, vocab):
             if rows <= most and v <= vocab:
                 assert tt.lib().toktier_cross_entropy(_area(0), 3, rows, v, v, _area(1), _area(2), _area(3), None, 1.0, None, 0,
                                                       _area(4), given, None) == HIP, (rows, v)
+
+
+TOKENS = [1, 4096, 4097, 5000, 8191, 8192, 16383, 16384, 32767, 32768, 65535, 65536, 131071, 131072, 262143, 262144, 262145,
+          524288, 524289, 1 << 20, (1 << 20) + 1, 1 << 26]
+VOCABS = [1, 3, 1023, 1024, V1, 2047, 2048, V2, V3, MOST]
+DIMS = [1, 7, 8, 64, 512, 513, 1024, 1025, 2048, 4096, 4097]
+
+
+def test_gradient_sizes_never_fall():
+    f = tt.toktier_embed_backward_workspace_bytes
+    for dim in DIMS:
+        for vocab in VOCABS:
+            assert _never_falls([f(n, vocab, dim) for n in TOKENS]), (vocab, dim)
+        for n in TOKENS:
+            assert _never_falls([f(n, vocab, dim) for vocab in VOCABS]), (n, dim)
+    for n in TOKENS:
+        assert _never_falls([f(n, V3, dim) for dim in DIMS]), n
+
+
+def test_gradient_sizes_stay_near_the_tokens():
+    """IDs and positions twice, the histograms, partial sums of a chunk of 64 tokens or of 4,096 wavefronts."""
+    f = tt.toktier_embed_backward_workspace_bytes
+    for n in TOKENS:
+        for dim in DIMS:
+            assert f(n, V3, dim) <= 16 * n + n * (dim + 8) // 8 + 40_000_000
+
+
+@pytest.mark.parametrize("most,vocab,dim", [(65536, V3, 64), (32768, V3, 4096), (262145, V3, 512), (1 << 20, MOST, 1025),
+                                            (65536, 2048, 513), (4097, V3, 4097)])
+def test_gradient_takes_the_workspace_of_a_larger_call(most, vocab, dim):
+    _no_gpu()
+    given = tt.toktier_embed_backward_workspace_bytes(most, vocab, dim)
+    for n in TOKENS + [most - 1, most]:
+        for v in VOCABS:
+            for d in DIMS:
+                if n <= most and v <= vocab and d <= dim:
+                    assert tt.lib().toktier_embed_backward(_area(0), 3, d, _area(1), n, 1.0, _area(2), 1, v, d, d, 1, _area(3),
+                                                           given, None) == HIP, (n, v, d)
