@@ -5,6 +5,7 @@
 //
 // Bound by memory: the logits are read and the gradient written, with one exponential per element.
 #include <algorithm>
+#include <type_traits>
 
 #include "ops.h"
 
@@ -332,12 +333,21 @@ extern "C" int toktier_cross_entropy(const void *logits, int type, uint32_t n_ro
             k_loss_pieces<T><<<dim3(L.pieces, n_rows), PIECE_THREADS, 0, s>>>(x, n_vocab, stride, targets, sums, at_target);
             k_loss_join<T><<<dim3(g ? L.pieces : 1, n_rows), PIECE_THREADS, 0, s>>>(x, n_vocab, stride, L.pieces, targets, sums, at_target,
                                                                                     loss, lse, grad_loss, grad_scale, g, grad_stride);
-        } else if (n_vocab <= 256 * VEC * 4) {   // short rows: more workgroups per CU
-            k_loss<T, 256, 4><<<n_rows, 256, 0, s>>>(x, n_vocab, stride, targets, loss, lse, grad_loss, grad_scale, g, grad_stride);
-        } else if (n_vocab <= 512 * VEC * 8) {
-            k_loss<T, 512, HELD><<<n_rows, 512, 0, s>>>(x, n_vocab, stride, targets, loss, lse, grad_loss, grad_scale, g, grad_stride);
         } else {
-            k_loss<T, 1024, HELD><<<n_rows, 1024, 0, s>>>(x, n_vocab, stride, targets, loss, lse, grad_loss, grad_scale, g, grad_stride);
+            auto launch = [&](auto threads, auto held) {
+                constexpr int N = decltype(threads)::value, H = decltype(held)::value;
+                in_launches(n_rows, N, [&](uint64_t r, uint32_t rows) {
+                    k_loss<T, N, H><<<rows, N, 0, s>>>(x + r * stride, n_vocab, stride, targets + r, loss + r, lse + r,
+                                                       grad_loss ? grad_loss + r : nullptr, grad_scale,
+                                                       g ? g + r * grad_stride : nullptr, grad_stride);
+                });
+            };
+            if (n_vocab <= 256 * VEC * 4)   // short rows: more workgroups per CU
+                launch(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+            else if (n_vocab <= 512 * VEC * 8)
+                launch(std::integral_constant<int, 512>{}, std::integral_constant<int, HELD>{});
+            else
+                launch(std::integral_constant<int, 1024>{}, std::integral_constant<int, HELD>{});
         }
     });
     return hip_status(hipGetLastError());

@@ -158,6 +158,14 @@ inline bool apart(const void *a, uint64_t na, const void *b, uint64_t nb)
 
 inline bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
+// A dimension of a grid holds fewer than 2^32 threads; a launch of more reports success and runs what is left of the
+// number modulo 2^32.  Calls f(first block, blocks) for launches of at most 2^31 threads that make up `blocks`.
+template <class F> inline void in_launches(uint64_t blocks, uint32_t threads, F f)
+{
+    const uint64_t most = (1ull << 31) / threads;
+    for (uint64_t first = 0; first < blocks; first += most) f(first, (uint32_t)(blocks - first < most ? blocks - first : most));
+}
+
 // Calls f with a value of the element type as its argument.
 template <class F> inline void with_type(int type, F f)
 {

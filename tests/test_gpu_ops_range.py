@@ -58,3 +58,26 @@ def test_gradients_of_fewer_tokens_in_the_workspace_of_the_most(tt):  # noqa: F8
         ref = torch.zeros(vocab, dim, dtype=torch.int64)
         ref.index_add_(0, torch.from_numpy(ids[:n])[ok], torch.from_numpy(vals[:n])[ok])
         assert torch.equal(table.cpu().long(), ref)
+
+
+ROWS = (1 << 24) + 3   # 256 threads each: 2^32 and more
+
+
+def test_loss_of_more_rows_than_a_launch_takes(tt):  # noqa: F811
+    _say("loss rows", ROWS)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(ROWS, 3, generator=g, device="cuda")
+    y = torch.randint(-1, 3, (ROWS,), generator=g, device="cuda", dtype=torch.int32)
+    c = torch.rand(ROWS, generator=g, device="cuda")
+    loss, lse, grad = torch.full_like(c, 7.0), torch.full_like(c, 7.0), torch.full_like(x, 7.0)
+    tt.toktier_cross_entropy(x, y, loss, lse, _ws(tt.toktier_cross_entropy_workspace_bytes(ROWS, 3)), grad_logits=grad, grad_loss=c)
+    z = torch.logsumexp(x.double(), 1)
+    kept, at = y >= 0, y.clamp(min=0).long().unsqueeze(1)
+    ref = torch.where(kept, z - x.double().gather(1, at).squeeze(1), torch.zeros_like(z))
+    # three exponentials and a logarithm of numbers below 16: 16 roundings of 16 at most
+    assert float((lse.double() - z).abs().max()) <= 16 * 16 * 2.0 ** -24
+    assert float((loss.double() - ref).abs().max()) <= 16 * 16 * 2.0 ** -24
+    p = torch.exp(x.double() - z.unsqueeze(1))
+    p.scatter_add_(1, at, -torch.ones_like(z).unsqueeze(1))
+    p *= (c.double() * kept).unsqueeze(1)
+    assert float((grad.double() - p).abs().max()) <= 64 * 2.0 ** -24
