@@ -1522,8 +1522,12 @@ extern "C" int toktier_sample(const void *logits, int type, uint32_t n_rows, uin
         using T = decltype(t);
         auto launch = [&](auto waves) {
             constexpr int W = decltype(waves)::value;
-            k_sample<T, W><<<n_rows, W * 64, 0, (hipStream_t)stream>>>((const T *)logits, n_vocab, stride, mask, mask_stride, temperature,
-                                                                       top_k, top_p, min_p, uniform, out_ids, out_logprobs, magic);
+            auto from = [](auto *p, uint64_t r) { return p ? p + r : p; };
+            in_launches(n_rows, W * 64, [&](uint64_t r, uint32_t rows) {
+                k_sample<T, W><<<rows, W * 64, 0, (hipStream_t)stream>>>(
+                    (const T *)logits + r * stride, n_vocab, stride, from(mask, r * mask_stride), mask_stride, from(temperature, r),
+                    from(top_k, r), from(top_p, r), from(min_p, r), uniform + r, out_ids + r, from(out_logprobs, r), magic);
+            });
         };
         if (n_vocab <= 8192) launch(std::integral_constant<int, 4>{});
         else launch(std::integral_constant<int, 16>{});

@@ -81,3 +81,27 @@ def test_loss_of_more_rows_than_a_launch_takes(tt):  # noqa: F811
     p.scatter_add_(1, at, -torch.ones_like(z).unsqueeze(1))
     p *= (c.double() * kept).unsqueeze(1)
     assert float((grad.double() - p).abs().max()) <= 64 * 2.0 ** -24
+
+
+def test_sampling_of_more_rows_than_a_launch_takes(tt):  # noqa: F811
+    _say("sample rows", ROWS)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(ROWS, 3, generator=g, device="cuda")
+    ids, lp = torch.full((ROWS,), 7, dtype=torch.int32, device="cuda"), torch.full((ROWS,), 7.0, device="cuda")
+    t = torch.zeros(ROWS, device="cuda")
+    t[-5:] = 1.0
+    u, k = torch.rand(ROWS, generator=g, device="cuda"), torch.zeros(ROWS, dtype=torch.int32, device="cuda")
+    k[-2:] = 1
+    p = torch.ones_like(u)
+    p[-3] = 0.0
+    mask = torch.full((ROWS, 1), 7, dtype=torch.int32, device="cuda")
+    mask[-1] = 0
+    tt.toktier_sample(x, u, ids, lp, _ws(tt.toktier_sample_workspace_bytes(ROWS, 3)), temperature=t, top_k=k, top_p=p,
+                      min_p=torch.zeros_like(u), mask=mask)
+    assert torch.equal(ids[:-5].long(), x[:-5].argmax(1)) and not lp[:-5].any()
+    assert ids[-1] == -1 and lp[-1] == float("-inf")
+    for r in (-5, -4):
+        w = torch.exp(x[r].double() - x[r].max().double())
+        run = w.cumsum(0)
+        assert int(ids[r]) == int((run <= u[r].double() * run[-1]).sum())
+    assert torch.equal(ids[-3:-1].long(), x[-3:-1].argmax(1))
