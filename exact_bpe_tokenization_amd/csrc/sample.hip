@@ -1506,7 +1506,7 @@ extern "C" int toktier_sample(const void *logits, int type, uint32_t n_rows, uin
         !aligned4(uniform) || !aligned4(out_ids) || !aligned4(out_logprobs))
         return TOKTIER_E_INVALID_ARG;
     const uint64_t words = (n_vocab + 31) / 32;
-    if (mask && mask_stride != 0 && (mask_stride < words || mask_stride > (1ull << 40))) return TOKTIER_E_INVALID_ARG;
+    if (mask && mask_stride != 0 && (mask_stride < words || mask_stride > (1ull << 46) / n_rows)) return TOKTIER_E_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace & 255u)) return TOKTIER_E_INVALID_ARG;
     if (workspace_bytes < 256) return TOKTIER_E_CAPACITY;
     const uint64_t lb = extent(type, n_rows, n_vocab, stride), ob = 4ull * n_rows;
