@@ -684,15 +684,17 @@ extern "C" int toktier_embed(const void *table, int table_type, uint32_t n_vocab
     while (lshift < 8 && (1u << lshift) < nv) ++lshift;
     const uint32_t step = 256u >> lshift, gy = (nv + (1u << lshift) - 1) >> lshift;
     constexpr int U = 4;
-    const uint64_t gx = (n_tokens + U * step - 1) / (U * step);
-    if (gx > 0x7FFFFFFFull || gy > 65535) return TOKTIER_E_INVALID_ARG;
+    const uint64_t gx = (n_tokens + U * step - 1) / (U * step);   // gy is 8,192 at most
     with_type(table_type, [&](auto ti) {
         with_type(out_type, [&](auto to) {
             using TI = decltype(ti);
             using TO = decltype(to);
-            k_embed<TI, TO, U><<<dim3((uint32_t)gx, gy), 256, 0, (hipStream_t)stream>>>(
-                (const TI *)table, table_stride, n_vocab, dim, ids, (uint32_t)n_tokens, scale, (TO *)out, out_stride, lshift,
-                n_tokens * dim * sizeof(TO) > STREAM_BYTES);
+            in_launches(gx, 256, [&](uint64_t first, uint32_t blocks) {
+                const uint64_t t = first * (U * step);
+                k_embed<TI, TO, U><<<dim3(blocks, gy), 256, 0, (hipStream_t)stream>>>(
+                    (const TI *)table, table_stride, n_vocab, dim, ids + t, (uint32_t)(n_tokens - t), scale, (TO *)out + t * out_stride,
+                    out_stride, lshift, n_tokens * dim * sizeof(TO) > STREAM_BYTES);
+            });
         });
     });
     return hip_status(hipGetLastError());

@@ -105,3 +105,24 @@ def test_sampling_of_more_rows_than_a_launch_takes(tt):  # noqa: F811
         run = w.cumsum(0)
         assert int(ids[r]) == int((run <= u[r].double() * run[-1]).sum())
     assert torch.equal(ids[-3:-1].long(), x[-3:-1].argmax(1))
+
+
+def test_lookup_of_more_tokens_than_a_launch_takes(tt):  # noqa: F811
+    """Four tokens to a workgroup of 256 threads: 2^26 tokens are 2^32 threads."""
+    tokens, dim, vocab = (1 << 26) + 9, 1025, 50
+    need = 2 * tokens * dim + (4 << 30)
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip(f"needs {need >> 30} GiB of device memory")
+    _say("lookup tokens", tokens)
+    table = torch.randn(vocab, dim, device="cuda").bfloat16()
+    ids = torch.randint(vocab, (tokens,), device="cuda", dtype=torch.int32)
+    out = torch.empty(tokens, dim, device="cuda", dtype=torch.bfloat16)
+    rows = [slice(a, a + 20) for a in (0, 4090, (1 << 25) - 10, (1 << 26) - 15, tokens - 20)]
+    for r in rows:
+        out[r] = 7.0
+    tt.toktier_embed(table, ids, out)
+    for r in rows:
+        assert torch.equal(out[r], table[ids[r].long()]), r
+    del out
+    torch.cuda.empty_cache()
