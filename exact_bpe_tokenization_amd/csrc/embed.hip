@@ -638,6 +638,8 @@ uint64_t backward_bytes(uint64_t n_tokens, uint32_t n_vocab, uint32_t dim)
 // The rows of a table as zeros to write; contiguous rows are cut into pieces of 16 KiB, one per block
 // (538 MB in one launch, through the caches: 88 us; in pieces of 64 KiB 96 us).
 constexpr uint64_t PIECE = 16384;
+// Blocks of a launch, beside those of a sort: 2^31 threads (tables over 68 GB take larger pieces).
+constexpr uint32_t MOST_PIECES = (1u << 31) / SORT_THREADS;
 
 Zeros zeros_of(void *table, uint32_t size, uint32_t n_vocab, uint32_t dim, uint64_t stride)
 {
@@ -652,6 +654,7 @@ Zeros zeros_of(void *table, uint32_t size, uint32_t n_vocab, uint32_t dim, uint6
         z.rows = (uint32_t)((z.end + PIECE - 1) / PIECE);
     }
     z.per_block = z.row_bytes >= PIECE ? 1 : (uint32_t)(PIECE / z.row_bytes);
+    while (z.rows / z.per_block >= MOST_PIECES) z.per_block *= 2;
     z.from = 0;
     return z;
 }

@@ -126,3 +126,22 @@ def test_lookup_of_more_tokens_than_a_launch_takes(tt):  # noqa: F811
         assert torch.equal(out[r], table[ids[r].long()]), r
     del out
     torch.cuda.empty_cache()
+
+
+def test_zeros_of_a_table_that_a_launch_does_not_hold(tt):  # noqa: F811
+    """No tokens: all of a table of 138 GB becomes zeros, 512 threads for every 16 KiB."""
+    vocab, dim = 1 << 21, 33000
+    need = 2 * vocab * dim + (1 << 30)
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip(f"needs {need >> 30} GiB of device memory")
+    _say("zeros", vocab, dim)
+    table = torch.empty(vocab, dim, device="cuda", dtype=torch.bfloat16)
+    rows = [slice(a, a + 3) for a in (0, 1000, vocab // 2, vocab - 3)]
+    for r in rows:
+        table[r] = 7.0
+    tt.toktier_embed_backward(torch.empty(0, dim, device="cuda", dtype=torch.bfloat16), _dev(np.zeros(0, np.int64)), table, _ws(256))
+    for r in rows:
+        assert not table[r].any(), r
+    del table
+    torch.cuda.empty_cache()
