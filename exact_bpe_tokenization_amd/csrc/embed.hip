@@ -298,10 +298,10 @@ __global__ __launch_bounds__(256) void k_embed_sum(const TG *__restrict__ grad, 
                                                    uint32_t n, uint32_t n_vocab, uint32_t dim, uint32_t chunk,
                                                    uint32_t n_chunks, uint32_t ncb, float scale, int accumulate,
                                                    TT *__restrict__ table, uint64_t tstride, float *__restrict__ part,
-                                                   uint32_t dpad, uint32_t absent_units)
+                                                   uint32_t dpad, uint32_t absent_units, uint32_t first)
 {
     const uint32_t lane = threadIdx.x & 63u;
-    const uint32_t unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4u + (threadIdx.x >> 6)), sums = n_chunks * ncb;
+    const uint32_t unit = __builtin_amdgcn_readfirstlane((first + blockIdx.x) * 4u + (threadIdx.x >> 6)), sums = n_chunks * ncb;
     if (unit < sums) {
         const uint32_t ch = unit / ncb, c = whole(unit % ncb * COLS + lane * VEC, dim, lane > 0);
         const uint32_t i0 = ch * chunk, len = min(chunk, n - i0);
@@ -394,14 +394,15 @@ template <class TT>
 __global__ __launch_bounds__(JOIN_THREADS) void k_embed_join(const uint32_t *__restrict__ keys, uint32_t n, uint32_t n_vocab,
                                                              uint32_t dim, uint32_t chunk, uint32_t n_chunks, uint32_t ncb,
                                                              float scale, int accumulate, TT *__restrict__ table,
-                                                             uint64_t tstride, const float *__restrict__ part, uint32_t dpad)
+                                                             uint64_t tstride, const float *__restrict__ part, uint32_t dpad,
+                                                             uint32_t first, uint32_t blocks)
 {
     __shared__ float sums[JOIN_WAVES][COLS];
     __shared__ uint32_t entered[JOIN_WAVES], any_long[JOIN_WAVES];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t units = n_chunks * ncb;
     // the columns of one run go to several workgroups
-    auto unit = [&](uint32_t w) { return w * gridDim.x + blockIdx.x; };
+    auto unit = [&](uint32_t w) { return w * blocks + first + blockIdx.x; };
     // the chunks after ch whose first token is `key`, of 64 from h0 on
     auto heads = [&](uint32_t h0, uint32_t key) {
         const uint32_t h = h0 + lane;
@@ -409,8 +410,9 @@ __global__ __launch_bounds__(JOIN_THREADS) void k_embed_join(const uint32_t *__r
         return ~same ? (uint32_t)__builtin_ctzll(~same) : 64u;
     };
     auto starts = [&](uint32_t ch, uint32_t &key) {   // whether a run starts in this chunk and leaves it
-        const uint32_t i0 = ch * chunk, end = i0 + chunk;
-        if (end >= n) return false;
+        const uint32_t i0 = ch * chunk;
+        if (n - i0 <= chunk) return false;   // (i0 + chunk may be 2^32)
+        const uint32_t end = i0 + chunk;
         const uint32_t prev = i0 > 0 ? keys[i0 - 1] : 0xFFFFFFFFu, head = keys[i0], next = keys[end];
         key = keys[end - 1];
         return key < n_vocab && next == key && !(head == key && prev == key);
@@ -797,9 +799,11 @@ extern "C" int toktier_embed_backward(const void *grad_out, int grad_type, uint6
             using TG = decltype(tg);
             using TT = decltype(tt_);
             auto launch = [&](auto once) {
-                k_embed_sum<TG, TT, decltype(once)::value><<<blocks, 256, 0, s>>>(
-                    (const TG *)grad_out, grad_stride, keys[last], pos[last], n, n_vocab, dim, L.chunk, L.n_chunks, L.ncb,
-                    scale, accumulate, (TT *)grad_table, table_stride, part, L.dpad, (uint32_t)absent);
+                in_launches(blocks, 256, [&](uint64_t first, uint32_t some) {
+                    k_embed_sum<TG, TT, decltype(once)::value><<<some, 256, 0, s>>>(
+                        (const TG *)grad_out, grad_stride, keys[last], pos[last], n, n_vocab, dim, L.chunk, L.n_chunks, L.ncb,
+                        scale, accumulate, (TT *)grad_table, table_stride, part, L.dpad, (uint32_t)absent, (uint32_t)first);
+                });
             };
             if ((uint64_t)n * dim * sizeof(TG) > ONCE_BYTES) launch(std::true_type{});
             else launch(std::false_type{});
@@ -807,8 +811,10 @@ extern "C" int toktier_embed_backward(const void *grad_out, int grad_type, uint6
     });
     with_type(table_type, [&](auto tt_) {
         using TT = decltype(tt_);
-        k_embed_join<TT><<<jblocks, JOIN_THREADS, 0, s>>>(keys[last], n, n_vocab, dim, L.chunk, L.n_chunks, L.ncb, scale, accumulate,
-                                                 (TT *)grad_table, table_stride, part, L.dpad);
+        in_launches(jblocks, JOIN_THREADS, [&](uint64_t first, uint32_t some) {
+            k_embed_join<TT><<<some, JOIN_THREADS, 0, s>>>(keys[last], n, n_vocab, dim, L.chunk, L.n_chunks, L.ncb, scale, accumulate,
+                                                           (TT *)grad_table, table_stride, part, L.dpad, (uint32_t)first, jblocks);
+        });
     });
     return hip_status(hipGetLastError());
 }

@@ -145,3 +145,31 @@ def test_zeros_of_a_table_that_a_launch_does_not_hold(tt):  # noqa: F811
         assert not table[r].any(), r
     del table
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gradient_of_the_most_tokens(tt, accumulate):  # noqa: F811
+    """2^32 - 2 tokens of one column, each ID 2,048 times (two of them once less): the chunks' wavefronts and the joins' workgroups
+    are 2^32 threads, and the last chunk ends where 32 bits do."""
+    tokens, vocab = (1 << 32) - 2, 1 << 21
+    size = tt.toktier_embed_backward_workspace_bytes(tokens, vocab, 1)
+    need = size + 6 * tokens + (4 << 30)
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip(f"needs {need >> 30} GiB of device memory")
+    _say("gradient of the most tokens", accumulate)
+    ids = torch.empty(tokens, dtype=torch.int32, device="cuda")
+    part = torch.arange(vocab, device="cuda", dtype=torch.int64) * 1048573 % vocab   # odd: every ID once
+    part = part.to(torch.int32).repeat(64)
+    for a in range(0, tokens, len(part)):
+        n = min(len(part), tokens - a)
+        ids[a:a + n] = part[:n]
+    grad = torch.ones(tokens, 1, device="cuda", dtype=torch.bfloat16)
+    table = torch.full((vocab, 1), 5.0, device="cuda")
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    tt.toktier_embed_backward(grad, ids, table, ws, accumulate=accumulate)
+    ref = torch.full((vocab, 1), 2048.0 + (5.0 if accumulate else 0.0), device="cuda")
+    ref[part[vocab - 2:vocab].long()] -= 1.0
+    assert torch.equal(table, ref)
+    del ids, grad, ws
+    torch.cuda.empty_cache()
