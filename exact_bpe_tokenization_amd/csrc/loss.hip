@@ -1,6 +1,6 @@
 // loss.hip -- next-token cross entropy over the vocabulary and its gradient.
 //
-//   lse = m + log(s),  m = max_j x_j,  s = sum_j exp(x_j - m);  loss = lse - x_y
+//   lse = m + log(s),  m = max_j x_j,  s = sum_j exp(x_j - m);  loss = (m - x_y) + log(s)
 //   dx_j = c (exp(x_j - m) / s - [j == y])
 //
 // Bound by memory: the logits are read and the gradient written, with one exponential per element.
@@ -131,11 +131,17 @@ __device__ __forceinline__ void put_grad(RowPart<T, THREADS, HELD> &part, T *g, 
     });
 }
 
-// -inf where the row has nothing but -inf, then `none`
-__device__ __forceinline__ float log_sum(MaxSum a, bool &none)
+__device__ __forceinline__ bool empty(MaxSum a) { return a.m == NEG_INF && a.s == 0.f; }   // nothing but -inf
+__device__ __forceinline__ float log_of(float s) { return LN2 * __builtin_amdgcn_logf(s); }
+
+// The loss comes from m - x_y, not from the rounded lse: at logits of 10,000 that is off by half a thousandth, in a row of
+// the type's lowest value by all of the loss.
+__device__ __forceinline__ void put_loss(MaxSum a, bool ignored, float target, float &loss, float &lse)
 {
-    none = a.m == NEG_INF && a.s == 0.f;
-    return none ? NEG_INF : a.m + LN2 * __builtin_amdgcn_logf(a.s);
+    const bool none = empty(a);
+    const float log_s = log_of(a.s);
+    lse = none ? NEG_INF : a.m + log_s;
+    loss = ignored ? 0.f : none ? -NEG_INF : (a.m - target) + log_s;
 }
 
 template <class T, int THREADS, int HELD>
@@ -154,14 +160,9 @@ __global__ __launch_bounds__(THREADS, 8) void k_loss(const T *logits, uint32_t n
     MaxSum a{NEG_INF, 0.f};
     part.template each<true>(NEG_INF, [&](uint32_t, uint32_t, float (&v)[VEC]) { add_vec(a, v); });
     a = block_join<THREADS>(a, lds);
-    bool none;
-    const float lse = log_sum(a, none);
-    if (threadIdx.x == 0) {
-        lse_out[row] = lse;
-        loss[row] = y >= n_vocab ? 0.f : none ? -NEG_INF : lse - target;
-    }
+    if (threadIdx.x == 0) put_loss(a, y >= n_vocab, target, loss[row], lse_out[row]);
     if (grad)
-        put_grad(part, grad + row * gstride, none || y >= n_vocab, a, grad_scale * (grad_loss ? grad_loss[row] : 1.f), y);
+        put_grad(part, grad + row * gstride, empty(a) || y >= n_vocab, a, grad_scale * (grad_loss ? grad_loss[row] : 1.f), y);
 }
 
 // Few rows: each is split into pieces of one workgroup.  The first launch leaves the pieces' maxima and sums,
@@ -201,16 +202,12 @@ __global__ __launch_bounds__(PIECE_THREADS) void k_loss_join(const T *logits, ui
     MaxSum a{NEG_INF, 0.f};
     if (threadIdx.x < pieces) a = sums[row * pieces + threadIdx.x];
     a = block_join<PIECE_THREADS>(a, lds);
-    bool none;
-    const float lse = log_sum(a, none);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        lse_out[row] = lse;
-        loss[row] = y >= n_vocab ? 0.f : none ? -NEG_INF : lse - at_target[row];
-    }
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        put_loss(a, y >= n_vocab, y >= n_vocab ? 0.f : at_target[row], loss[row], lse_out[row]);
     if (!grad) return;
     RowPart<T, PIECE_THREADS, 1> part{logits + row * stride, begin, end};
     const float c = grad_scale * (grad_loss ? grad_loss[row] : 1.f), r = 1.f / a.s;
-    const bool zero = none || y >= n_vocab;
+    const bool zero = empty(a) || y >= n_vocab;
     T *g = grad + row * gstride;
     part.template each<true>(0.f, [&](uint32_t j, uint32_t n, float (&v)[VEC]) {
         if (zero) {

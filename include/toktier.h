@@ -427,7 +427,8 @@ int toktier_embed_backward(const void *grad_out, int grad_type, uint64_t grad_st
 /*
  * Next-token cross entropy, and in the same pass its gradient.  For row i with target y = targets[i]:
  *   lse[i]  = log(sum_j exp(logits[i, j]))
- *   loss[i] = lse[i] - logits[i, y]                            (0 where y >= n_vocab)
+ *   loss[i] = lse[i] - logits[i, y]                            (0 where y >= n_vocab; taken from the row's
+ *             maximum, not from the rounded lse, so that it keeps its digits wherever the logits lie)
  *   grad_logits[i, j] = c_i * (exp(logits[i, j] - lse[i]) - [j == y])   (zeros where y >= n_vocab)
  *   c_i = grad_scale * (grad_loss ? grad_loss[i] : 1)          (the mean over N positions: c_i = 1 / N)
  * Logits of -inf have probability 0.  A row of nothing else has lse -inf, loss +inf and a gradient of
