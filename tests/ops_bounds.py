@@ -44,3 +44,37 @@ def loss(x, y):
     ref = (m - at) + np.log(s)
     err = rel + 4 * U * (np.log(s) + 1) + U * np.abs(m - at) + U * np.abs(ref)
     return ref[:, 0], err[:, 0]
+
+
+FAR = 128.0   # the gradient from lse forms the sums of a row again from this |lse| on
+
+
+def gradient(x, y, c, dtype, from_lse):
+    """(gradient, its error bound) of rows x, targets y (none ignored) and factors c; no row is -inf alone.
+
+    Fused, p_j = exp(x_j - m) / s: the power, the sum, the reciprocal and the product.  From lse: exp(x_j - lse) with
+    the lse's own error (that of log s, and a rounding relative to lse), by rows of 256 threads where |lse| is FAR or more.
+    c rounds once as a product, and the difference from one at the target, the product with c and the
+    result in the output's type round once each.  The hardware's power of two has no subnormal results."""
+    from ops_plain import rounding
+    m, s, p, rel = parts(x, threads_vectors(x.shape[1]))
+    with np.errstate(all="ignore"):
+        d = np.where(np.isfinite(x), np.minimum(m - x, 104), 0.0)
+        own = rel + U * (2 * d + 4 + 2)
+        if from_lse:
+            z = m + np.log(s)
+            below = np.where(np.isfinite(x), np.minimum(np.abs(z - x), 104), 0.0)
+            near = rel + 4 * U * (np.log(s) + 1) + U * np.abs(z) + U * (2 * below + 4)
+            wide = parts(x, -(-x.shape[1] // 2048))[3] + U * (2 * d + 4 + 2)
+            own = np.where(np.abs(z) < FAR, near, np.where(np.abs(z) > FAR + 1, wide, np.maximum(near, wide)))
+    c = np.asarray(c)[:, None]
+    hit = np.zeros_like(x)
+    hit[np.arange(len(x)), y] = 1.0
+    ref = c * (p - hit)
+    err = np.abs(c) * (p * own + hit * U * np.abs(p - hit) + 2.0 ** -126) + 2 * U * np.abs(ref)
+    return ref, err + rounding(np.abs(ref) + err, dtype)
+
+
+def rounding_floor(dtype):
+    from ops_plain import SMALLEST, type_name
+    return max(SMALLEST[type_name(dtype)], 2.0 ** -126)

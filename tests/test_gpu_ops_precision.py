@@ -41,3 +41,43 @@ def test_loss_of_logits_far_from_zero(tt, rows, vocab, dtype, kind):  # noqa: F8
     tt.toktier_cross_entropy(logits, _dev(y), loss, lse, _ws(tt.toktier_cross_entropy_workspace_bytes(rows, vocab)))
     ref, err = bounds.loss(plain.f64(logits), y)
     _close(plain.f64(loss), ref, err, "loss")
+
+
+def _gradient(tt, x, dtype, from_lse, in_place=False, pad=0, lead=0):  # noqa: F811
+    rows, vocab = x.shape
+    rng = np.random.default_rng(rows + vocab)
+    logits, _ = _view(x, _dtype(dtype), pad, lead)
+    x = plain.f64(logits)
+    y = rng.integers(0, vocab, rows)
+    y[0] = vocab // 2
+    c = _dev(rng.random(rows) + 0.5, "float32")
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    grad = logits if in_place else _view(np.full((rows, vocab), 5.0), _dtype(dtype), pad, lead)[0]
+    ws = _ws(tt.toktier_cross_entropy_workspace_bytes(rows, vocab))
+    if from_lse:
+        tt.toktier_cross_entropy(logits, _dev(y), loss, lse, ws)
+        tt.toktier_cross_entropy_backward(logits, _dev(y), lse, grad, grad_loss=c, grad_scale=0.5)
+    else:
+        tt.toktier_cross_entropy(logits, _dev(y), loss, lse, ws, grad_logits=grad, grad_loss=c, grad_scale=0.5)
+    ref, err = bounds.gradient(x, y, 0.5 * plain.f64(c), _dtype(dtype), from_lse)
+    _close(plain.f64(grad), ref, err, "gradient")
+
+
+@pytest.mark.parametrize("rows,vocab,pad,lead", [
+    (1, 1, 0, 0), (3, 7, 1, 1), (9, 1256, 0, 0), (5, 8191, 0, 0), (4, 8193, 3, 1), (3, 33024, 0, 0), (2, 65535, 0, 0), (2, 65536, 0, 0),
+    (2, 131328, 0, 0), (170, 70001, 0, 0), (300, 515, 0, 0)])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("from_lse", [False, True])
+@pytest.mark.parametrize("kind", [0.0, "peaked", "equal", "masked"])
+def test_gradient_element_by_element(tt, rows, vocab, pad, lead, dtype, from_lse, kind):  # noqa: F811
+    _say("gradient", rows, vocab, dtype, from_lse, kind)
+    rng = np.random.default_rng(vocab)
+    x = 3.0 * rng.standard_normal((rows, vocab))
+    if kind == "peaked":
+        x[:, vocab // 2] = 40.0
+    elif kind == "equal":
+        x[:] = 2.5
+    elif kind == "masked":
+        x[:, 1::3] = -np.inf
+        x[:, 2::5] = LOWEST[dtype]
+    _gradient(tt, x, dtype, from_lse, pad=pad, lead=lead)
