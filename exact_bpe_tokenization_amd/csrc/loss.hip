@@ -220,18 +220,34 @@ __global__ __launch_bounds__(PIECE_THREADS) void k_loss_join(const T *logits, ui
     });
 }
 
+// The gradient from lse.  A rounding of lse is relative to it, so far from zero exp(x - lse) loses the digits that tell the
+// probabilities (in a row of the type's lowest value each would be 1, not 1 / n).  From FAR on, where that would be as
+// much as the power itself can be off (its exponent is rounded too, and reaches 104 before the power is zero), a row's
+// maximum and sum are formed again.  One workgroup takes such a row whole, since in place the others would read
+// what it has written.
+constexpr float FAR = 128.f;
+
 template <class T, int THREADS>
 __global__ __launch_bounds__(THREADS, 8) void k_loss_backward(const T *logits, uint32_t n_vocab, uint64_t stride,
                                                               const uint32_t *__restrict__ targets,
                                                               const float *__restrict__ lse, const float *__restrict__ grad_loss,
                                                               float grad_scale, T *grad, uint64_t gstride)
 {
+    __shared__ MaxSum lds[THREADS / 64];
     const uint64_t row = blockIdx.y;
     const uint32_t y = targets[row], begin = blockIdx.x * PIECE, end = n_vocab - begin < PIECE ? n_vocab : begin + PIECE;
     const float z = lse[row], c = grad_scale * (grad_loss ? grad_loss[row] : 1.f);
     RowPart<T, THREADS, PIECE / (THREADS * VEC)> part{logits + row * stride, begin, end};
     T *g = grad + row * gstride;
     if (z == NEG_INF || y >= n_vocab) return put_grad(part, g, true, MaxSum{z, 1.f}, c, y);
+    if (!(__builtin_fabsf(z) < FAR)) {   // NaN too
+        if (blockIdx.x) return;
+        part.end = n_vocab;
+        MaxSum a{NEG_INF, 0.f};
+        part.template each<true>(NEG_INF, [&](uint32_t, uint32_t, float (&v)[VEC]) { add_vec(a, v); });
+        a = block_join<THREADS>(a, lds);
+        return put_grad(part, g, empty(a), a, c, y);
+    }
     part.template each<true>(0.f, [&](uint32_t j, uint32_t n, float (&v)[VEC]) {
         grad_vec(v, z, 1.f, c, j, y);
         stream_part(g + j, n, v);

@@ -447,7 +447,8 @@ int toktier_cross_entropy(const void *logits, int type, uint32_t n_rows, uint32_
                           float grad_scale, void *grad_logits, uint64_t grad_stride, void *workspace,
                           uint64_t workspace_bytes, void *stream);
 
-/* The gradient alone, later, from the lse that toktier_cross_entropy wrote for the same logits. */
+/* The gradient alone, later, from the lse that toktier_cross_entropy wrote for the same logits.  A row whose |lse| is 128
+ * or more is summed again, since a 32-bit lse no longer holds its probabilities' digits. */
 int toktier_cross_entropy_backward(const void *logits, int type, uint32_t n_rows, uint32_t n_vocab, uint64_t stride,
                                    const uint32_t *targets, const float *lse, const float *grad_loss,
                                    float grad_scale, void *grad_logits, uint64_t grad_stride, void *stream);

@@ -81,3 +81,17 @@ def test_gradient_element_by_element(tt, rows, vocab, pad, lead, dtype, from_lse
         x[:, 1::3] = -np.inf
         x[:, 2::5] = LOWEST[dtype]
     _gradient(tt, x, dtype, from_lse, pad=pad, lead=lead)
+
+
+@pytest.mark.parametrize("kind", KINDS + [-110.0, 100.0])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("from_lse", [False, True])
+@pytest.mark.parametrize("rows,vocab", [(5, 40), (4, 9001), (3, 70001)])
+def test_gradient_of_logits_far_from_zero(tt, rows, vocab, dtype, from_lse, kind):  # noqa: F811
+    _say("gradient far", rows, vocab, dtype, from_lse, kind)
+    rng = np.random.default_rng(vocab)
+    x = _far(rng, rows, vocab, dtype, kind)
+    if rows > 3:
+        x[1] = 3.0 * rng.standard_normal(vocab)    # an ordinary row among them
+    _gradient(tt, x, dtype, from_lse)
+    _gradient(tt, x, dtype, from_lse, in_place=True, pad=1)
