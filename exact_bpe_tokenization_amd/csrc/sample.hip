@@ -276,6 +276,8 @@ struct Weights {
     int max_key;
 
     static constexpr double HUGE_LOGIT = 1e300;   // in place of +inf, whose weight is one and all others' zero
+    // At a temperature of +inf finite logits weigh the same, but nothing beside +inf: a scale too small for the former.
+    static __device__ __forceinline__ double scale_of(float temp) { return __builtin_fmax(1.4426950408889634 / (double)temp, 1e-290); }
 
     // the weight as the low bits of a number whose high bits are those of `magic`; y below -80 gives zero
     __device__ __forceinline__ uint64_t raw(float x, bool in = true) const
@@ -1086,7 +1088,7 @@ __device__ __attribute__((noinline)) void general_row(const Row<T> &in, Lds<WAVE
         }
         return;
     }
-    const Weights wt{1.4426950408889634 / (double)temp, __builtin_fmin((double)K::value(top), Weights::HUGE_LOGIT), magic, top};
+    const Weights wt{Weights::scale_of(temp), __builtin_fmin((double)K::value(top), Weights::HUGE_LOGIT), magic, top};
     auto weight = [&](int key) { return weight_of<T>(wt.c, wt.max, wt.magic, wt.max_key, key); };
     const bool first_alone = k == 1 || !(temp > 0.f);
     const bool need_k = !first_alone && k != 0 && k < n_vocab, need_p = !first_alone && p < 1.f;
@@ -1411,7 +1413,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_sample(const T *__restrict__ log
         }
         return;
     }
-    const Weights wt{1.4426950408889634 / (double)row.temp, __builtin_fmin((double)K::value(top), Weights::HUGE_LOGIT), magic, top};
+    const Weights wt{Weights::scale_of(row.temp), __builtin_fmin((double)K::value(top), Weights::HUGE_LOGIT), magic, top};
     auto weight = [&](int key) INLINE { return weight_of<T>(wt.c, wt.max, wt.magic, wt.max_key, key); };
     const uint64_t w_min = least_weight(wt, row.min_p);
     Border b{};

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_ops import _dev, _say, _ws, tt  # noqa: F401
+from test_gpu_ops import _dev, _sample, _say, _ws, tt  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -173,3 +173,21 @@ def test_gradient_of_the_most_tokens(tt, accumulate):  # noqa: F811
     assert torch.equal(table, ref)
     del ids, grad, ws
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("vocab", [40, 9000])
+def test_sampling_at_an_endless_temperature(tt, vocab, dtype):  # noqa: F811
+    """All finite logits weigh the same, and one of +inf still more than all of them."""
+    _say("sample endless", vocab, dtype)
+    rng = np.random.default_rng(vocab)
+    rows = 8
+    x = rng.standard_normal((rows, vocab))
+    x[1, 7] = x[2, [3, vocab - 1]] = x[3, 0] = x[4, 5] = np.inf
+    x[5, ::2] = -np.inf
+    k = np.array([0, 0, 0, 3, 0, 0, 30, 0])
+    p = np.array([1.0, 1.0, 1.0, 1.0, 0.5, 1.0, 0.7, 0.3])
+    for u in (0.0, 0.5, 0.999):
+        _sample(tt, x, dtype, np.inf, k, p, 0.0, u)
+        _sample(tt, x, dtype, np.inf, k, p, 0.5, u)
+        _sample(tt, x, dtype, 3.0e38, k, p, 0.0, u)
