@@ -95,3 +95,31 @@ def test_gradient_of_logits_far_from_zero(tt, rows, vocab, dtype, from_lse, kind
         x[1] = 3.0 * rng.standard_normal(vocab)    # an ordinary row among them
     _gradient(tt, x, dtype, from_lse)
     _gradient(tt, x, dtype, from_lse, in_place=True, pad=1)
+
+
+@pytest.mark.parametrize("vocab", [50, 9001, 70001])
+@pytest.mark.parametrize("from_lse", [False, True])
+def test_gradient_matches_differences_of_the_64_bit_loss(tt, vocab, from_lse):  # noqa: F811
+    """Central differences of a loss that shares nothing with the kernels."""
+    rows, h = 3, 2.0 ** -10
+    _say("differences", vocab, from_lse)
+    rng = np.random.default_rng(vocab)
+    x = torch.from_numpy(2.0 * rng.standard_normal((rows, vocab))).float().cuda()
+    y = np.array([vocab // 2, 0, vocab - 1])
+    loss, lse, grad = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), torch.empty_like(x)
+    ws = _ws(tt.toktier_cross_entropy_workspace_bytes(rows, vocab))
+    tt.toktier_cross_entropy(x, _dev(y), loss, lse, ws, grad_logits=None if from_lse else grad)
+    if from_lse:
+        tt.toktier_cross_entropy_backward(x, _dev(y), lse, grad)
+    x64, got = plain.f64(x), plain.f64(grad)
+    bound = bounds.gradient(x64, y, np.ones(rows), torch.float32, from_lse)[1]
+    ones = np.ones(rows)
+    for j in [0, 1, vocab // 2, vocab - 1] + [int(v) for v in rng.integers(0, vocab, 6)]:
+        up, down = x64.copy(), x64.copy()
+        up[:, j] += h
+        down[:, j] -= h
+        slope = (plain.cross_entropy(up, y, ones)[0] - plain.cross_entropy(down, y, ones)[0]) / (2 * h)
+        # the third derivative of the loss is p (1 - p) (1 - 2 p), at most p in size (p moves by less than h of itself);
+        # two 64-bit losses below 32, each some 32 roundings off, over 2 h
+        p = np.exp(x64[:, j] - plain.f64(lse)) * 1.01
+        assert np.all(np.abs(slope - got[:, j]) <= bound[:, j] + p * h * h / 6 + 2 * 32 * 32 * 2.0 ** -53 / (2 * h))
