@@ -18,11 +18,12 @@
 // A workgroup of 1,024 threads takes a row (256 threads up to 8,192 elements), so a row's time is the time of its chain of
 // phases, and the rows of a batch of up to 256 run side by side.  131,328 bfloat16, one row and 256 of them (67 MB): first
 // alone 8.5 and 16.3 us (4.1 TB/s), temperature with top-k 50 and top-p 0.95 18.3 and 28.5, top-k 1,000 with top-p 0.9 40 and
-// 50, top-p 0.95 50 and 55, full distribution 29 and 39.  What bounds them: the loads of one CU in the keys phase without
-// a histogram (5.8 us of a row); the LDS atomics of the histogram (16 us); in the cells phase VALU issue, some 100
-// instructions for a vector of eight (18 us); for float32 and float16 the exponentials in 64 bits, 30
-// instructions each; else the latency of some ten barriers.  Not split over workgroups: a second launch costs 3 us, and a
-// phase needs the one before from the whole row.
+// 50, top-p 0.95 50 and 56, full distribution 29 and 40.  What bounds them: the loads of one CU in the keys phase without
+// a histogram (5.8 us of a row); the LDS atomics of the histogram (the keys phase takes 16 us of a row alone, 20 in a
+// batch of 256); in the cells phase VALU issue, some 100 instructions for a vector of eight (19 and 21 us); for float32
+// and float16 the exponentials in 64 bits, 30 instructions each; else the latency of some ten barriers.  Every variant
+// uses scratch: 128 VGPRs and 7 to 21 spilled ones (96 to 128 bytes a lane) at 16 wavefronts, 184 to 200 VGPRs and 64 bytes
+// at four.  Not split over workgroups: a second launch costs 3 us, and a phase needs the one before from the whole row.
 #include <type_traits>
 
 #include "ops.h"
@@ -1030,7 +1031,12 @@ __device__ __forceinline__ void draw(const Row<T> &row, Lds<WAVES> &sh, const We
 }
 
 // Any row, by one search: histograms over bins and then over digits of the key, for counts and for masses, and
-// the ID by running masses.  For borders with more elements than the list holds.
+// the ID by running masses.  For borders with more elements than the list holds (float32 and float16 also where top-k ends past
+// it and top-p follows), rows with a NaN of positive sign, and bfloat16 rows whose weights do not end at -2,047 (temperatures from about 64 on, or logits all below it).  An element at
+// a time, in several passes.  131,328 elements, one row and 256: with a NaN, full distribution 91 and 105 us in bfloat16, 101
+// and 115 in float16, 103 and 130 in float32, top-p 209 to 266 and 219 to 287; top-k 5,000 with top-p, float16 275 and 321,
+// float32 330 and 379; top-p where all logits lie in a few bins (near -20), float16 567 and 578, float32 622 and 645; bfloat16
+// at a temperature of 100, top-p 215 and 225.
 template <class T, int WAVES>
 __device__ __attribute__((noinline)) void general_row(const Row<T> &in, Lds<WAVES> &sh, double magic, uint32_t *out_id, float *out_logprob)
 {
