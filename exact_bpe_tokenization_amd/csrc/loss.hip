@@ -227,7 +227,7 @@ __global__ __launch_bounds__(PIECE_THREADS) void k_loss_join(const T *logits, ui
 // probabilities (in a row of the type's lowest value each would be 1, not 1 / n).  From FAR on, where that would be as
 // much as the power itself can be off (its exponent is rounded too, and reaches 104 before the power is zero), a row's
 // maximum and sum are formed again.  One workgroup takes such a row whole, since in place the others would read
-// what it has written.  (1,500 x 33,001 float16: 32 us, 51 with all rows far; 8,192 x 131,328 bfloat16: 767 and 1,216 us.)
+// what it has written.  (Two inputs in turn, 1,500 x 33,001 float16: 32 us, 51 with all rows far; 8,192 x 131,328 bfloat16: 767 and 1,216 us.)
 constexpr float FAR = 128.f;
 
 template <class T, int THREADS>

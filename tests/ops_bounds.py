@@ -10,6 +10,8 @@ u = 2^-24 is half a step of a 32-bit number, relative to it.
   log(s): a step of the hardware's logarithm to base 2, its product with log 2, the addition."""
 import numpy as np
 
+from ops_plain import SMALLEST, rounding, type_name
+
 U = 2.0 ** -24
 
 
@@ -56,7 +58,6 @@ def gradient(x, y, c, dtype, from_lse):
     the lse's own error (that of log s, and a rounding relative to lse), by rows of 256 threads where |lse| is FAR or more.
     c rounds once as a product, and the difference from one at the target, the product with c and the
     result in the output's type round once each.  The hardware's power of two has no subnormal results."""
-    from ops_plain import rounding
     m, s, p, rel = parts(x, threads_vectors(x.shape[1]))
     with np.errstate(all="ignore"):
         d = np.where(np.isfinite(x), np.minimum(m - x, 104), 0.0)
@@ -76,5 +77,4 @@ def gradient(x, y, c, dtype, from_lse):
 
 
 def rounding_floor(dtype):
-    from ops_plain import SMALLEST, type_name
     return max(SMALLEST[type_name(dtype)], 2.0 ** -126)

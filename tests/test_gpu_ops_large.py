@@ -5,7 +5,7 @@ import torch
 
 import ops_bounds as bounds
 import ops_plain as plain
-from test_gpu_ops import TYPES, _close, _dev, _dtype, _say, _ws, tt  # noqa: F401
+from test_gpu_ops import TYPES, _close, _dev, _dtype, _say, _ws
 
 pytestmark = pytest.mark.gpu
 MOST = 1 << 21
@@ -26,7 +26,7 @@ def _kept(x, temperature, k, p, min_p):
 
 @pytest.mark.parametrize("vocab", [1 << 18, (1 << 18) + 1, 1 << 19, (1 << 20) + 3, MOST])
 @pytest.mark.parametrize("dtype", TYPES)
-def test_sample_of_the_largest_vocabularies(tt, vocab, dtype):  # noqa: F811
+def test_sample_of_the_largest_vocabularies(tt, vocab, dtype):
     """IDs are aimed at: u is the middle of an ID's share of the kept mass, which is far wider than the sums' errors."""
     _say("sample large", vocab, dtype)
     rng = np.random.default_rng(vocab)
@@ -61,7 +61,7 @@ def test_sample_of_the_largest_vocabularies(tt, vocab, dtype):  # noqa: F811
 @pytest.mark.parametrize("vocab", [MOST, MOST - 5, 1 << 20])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("rows", [2, 160])
-def test_cross_entropy_of_the_largest_vocabularies(tt, rows, vocab, dtype):  # noqa: F811
+def test_cross_entropy_of_the_largest_vocabularies(tt, rows, vocab, dtype):
     _say("cross_entropy large", rows, vocab, dtype)
     g = torch.Generator(device="cuda").manual_seed(vocab)
     x = (3 * torch.randn(rows, vocab, generator=g, device="cuda")).to(_dtype(dtype))
@@ -83,7 +83,7 @@ def test_cross_entropy_of_the_largest_vocabularies(tt, rows, vocab, dtype):  # n
 
 @pytest.mark.parametrize("table_type,out_type", [("bfloat16", "bfloat16"), ("float32", "float16"), ("float16", "float32")])
 @pytest.mark.parametrize("dim", [4096, 4099])
-def test_lookup_larger_than_the_caches(tt, dim, table_type, out_type):  # noqa: F811
+def test_lookup_larger_than_the_caches(tt, dim, table_type, out_type):
     tokens, vocab = 4500, 900
     _say("lookup large", dim, table_type, out_type)
     g = torch.Generator(device="cuda").manual_seed(dim)
@@ -97,7 +97,7 @@ def test_lookup_larger_than_the_caches(tt, dim, table_type, out_type):  # noqa: 
 
 @pytest.mark.parametrize("dim", [2048, 2051])
 @pytest.mark.parametrize("accumulate", [False, True])
-def test_gradient_larger_than_the_caches(tt, dim, accumulate):  # noqa: F811
+def test_gradient_larger_than_the_caches(tt, dim, accumulate):
     tokens, vocab = 70000, 5000
     _say("gradient large", dim, accumulate)
     g = torch.Generator(device="cuda").manual_seed(dim)

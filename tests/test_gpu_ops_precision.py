@@ -5,7 +5,7 @@ import torch
 
 import ops_bounds as bounds
 import ops_plain as plain
-from test_gpu_ops import TYPES, _close, _dev, _dtype, _say, _view, _ws, tt  # noqa: F401
+from test_gpu_ops import TYPES, _close, _dev, _dtype, _say, _view, _ws
 
 pytestmark = pytest.mark.gpu
 LOWEST = {"float32": -3.4028234663852886e38, "float16": -65504.0, "bfloat16": -3.3895313892515355e38}
@@ -31,7 +31,7 @@ KINDS = ["lowest", "lowest but one", "largest", 0.0, 200.0, 10000.0, -10000.0]
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,vocab", [(5, 40), (4, 9001), (3, 70001), (161, 66000)])
-def test_loss_of_logits_far_from_zero(tt, rows, vocab, dtype, kind):  # noqa: F811
+def test_loss_of_logits_far_from_zero(tt, rows, vocab, dtype, kind):
     _say("loss far", rows, vocab, dtype, kind)
     rng = np.random.default_rng(vocab)
     logits, _ = _view(_far(rng, rows, vocab, dtype, kind), _dtype(dtype))
@@ -43,7 +43,7 @@ def test_loss_of_logits_far_from_zero(tt, rows, vocab, dtype, kind):  # noqa: F8
     _close(plain.f64(loss), ref, err, "loss")
 
 
-def _gradient(tt, x, dtype, from_lse, in_place=False, pad=0, lead=0):  # noqa: F811
+def _gradient(tt, x, dtype, from_lse, in_place=False, pad=0, lead=0):
     rows, vocab = x.shape
     rng = np.random.default_rng(rows + vocab)
     logits, _ = _view(x, _dtype(dtype), pad, lead)
@@ -69,7 +69,7 @@ def _gradient(tt, x, dtype, from_lse, in_place=False, pad=0, lead=0):  # noqa: F
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("from_lse", [False, True])
 @pytest.mark.parametrize("kind", [0.0, "peaked", "equal", "masked"])
-def test_gradient_element_by_element(tt, rows, vocab, pad, lead, dtype, from_lse, kind):  # noqa: F811
+def test_gradient_element_by_element(tt, rows, vocab, pad, lead, dtype, from_lse, kind):
     _say("gradient", rows, vocab, dtype, from_lse, kind)
     rng = np.random.default_rng(vocab)
     x = 3.0 * rng.standard_normal((rows, vocab))
@@ -87,7 +87,7 @@ def test_gradient_element_by_element(tt, rows, vocab, pad, lead, dtype, from_lse
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("from_lse", [False, True])
 @pytest.mark.parametrize("rows,vocab", [(5, 40), (4, 9001), (3, 70001)])
-def test_gradient_of_logits_far_from_zero(tt, rows, vocab, dtype, from_lse, kind):  # noqa: F811
+def test_gradient_of_logits_far_from_zero(tt, rows, vocab, dtype, from_lse, kind):
     _say("gradient far", rows, vocab, dtype, from_lse, kind)
     rng = np.random.default_rng(vocab)
     x = _far(rng, rows, vocab, dtype, kind)
@@ -99,7 +99,7 @@ def test_gradient_of_logits_far_from_zero(tt, rows, vocab, dtype, from_lse, kind
 
 @pytest.mark.parametrize("vocab", [50, 9001, 70001])
 @pytest.mark.parametrize("from_lse", [False, True])
-def test_gradient_matches_differences_of_the_64_bit_loss(tt, vocab, from_lse):  # noqa: F811
+def test_gradient_matches_differences_of_the_64_bit_loss(tt, vocab, from_lse):
     """Central differences of a loss that shares nothing with the kernels."""
     rows, h = 3, 2.0 ** -10
     _say("differences", vocab, from_lse)

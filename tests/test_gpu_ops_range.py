@@ -3,14 +3,14 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_ops import _dev, _sample, _say, _ws, tt  # noqa: F401
+from test_gpu_ops import _dev, _sample, _say, _ws
 
 pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("distinct", [1, 2, 3, 63, 64, 65])
 @pytest.mark.parametrize("apart", [1, 64, 2048])
-def test_sort_keeps_every_token(tt, distinct, apart):  # noqa: F811
+def test_sort_keeps_every_token(tt, distinct, apart):
     """Neighbouring tokens with equal digits of the sort, low or high: a column per bit of the token's position, so that the
     sums of an ID count the bits of all of its tokens."""
     tokens, vocab = 20000, 70 * 2048
@@ -24,7 +24,7 @@ def test_sort_keeps_every_token(tt, distinct, apart):  # noqa: F811
     assert torch.equal(table.cpu().long(), ref)
 
 
-def test_loss_of_a_last_batch_in_the_workspace_of_the_others(tt):  # noqa: F811
+def test_loss_of_a_last_batch_in_the_workspace_of_the_others(tt):
     """One workspace for a batch and for the few rows left after it."""
     vocab, most = 70001, 300
     torch.manual_seed(1)
@@ -43,7 +43,7 @@ def test_loss_of_a_last_batch_in_the_workspace_of_the_others(tt):  # noqa: F811
         assert torch.allclose(grad.float(), outs[0][1][:n].float(), rtol=2.0 ** -7, atol=1e-30)
 
 
-def test_gradients_of_fewer_tokens_in_the_workspace_of_the_most(tt):  # noqa: F811
+def test_gradients_of_fewer_tokens_in_the_workspace_of_the_most(tt):
     """One workspace through lengths at which the chunks and the sort's blocks change; integers, so sums are exact."""
     vocab, dim, most = 3000, 64, 262145
     rng = np.random.default_rng(5)
@@ -63,7 +63,7 @@ def test_gradients_of_fewer_tokens_in_the_workspace_of_the_most(tt):  # noqa: F8
 ROWS = (1 << 24) + 3   # 256 threads each: 2^32 and more
 
 
-def test_loss_of_more_rows_than_a_launch_takes(tt):  # noqa: F811
+def test_loss_of_more_rows_than_a_launch_takes(tt):
     _say("loss rows", ROWS)
     g = torch.Generator(device="cuda").manual_seed(1)
     x = torch.randn(ROWS, 3, generator=g, device="cuda")
@@ -83,7 +83,7 @@ def test_loss_of_more_rows_than_a_launch_takes(tt):  # noqa: F811
     assert float((grad.double() - p).abs().max()) <= 64 * 2.0 ** -24
 
 
-def test_sampling_of_more_rows_than_a_launch_takes(tt):  # noqa: F811
+def test_sampling_of_more_rows_than_a_launch_takes(tt):
     _say("sample rows", ROWS)
     g = torch.Generator(device="cuda").manual_seed(2)
     x = torch.randn(ROWS, 3, generator=g, device="cuda")
@@ -107,7 +107,7 @@ def test_sampling_of_more_rows_than_a_launch_takes(tt):  # noqa: F811
     assert torch.equal(ids[-3:-1].long(), x[-3:-1].argmax(1))
 
 
-def test_lookup_of_more_tokens_than_a_launch_takes(tt):  # noqa: F811
+def test_lookup_of_more_tokens_than_a_launch_takes(tt):
     """Four tokens to a workgroup of 256 threads: 2^26 tokens are 2^32 threads."""
     tokens, dim, vocab = (1 << 26) + 9, 1025, 50
     need = 2 * tokens * dim + (4 << 30)
@@ -128,7 +128,7 @@ def test_lookup_of_more_tokens_than_a_launch_takes(tt):  # noqa: F811
     torch.cuda.empty_cache()
 
 
-def test_zeros_of_a_table_that_a_launch_does_not_hold(tt):  # noqa: F811
+def test_zeros_of_a_table_that_a_launch_does_not_hold(tt):
     """No tokens: all of a table of 138 GB becomes zeros, 512 threads for every 16 KiB."""
     vocab, dim = 1 << 21, 33000
     need = 2 * vocab * dim + (1 << 30)
@@ -148,7 +148,7 @@ def test_zeros_of_a_table_that_a_launch_does_not_hold(tt):  # noqa: F811
 
 
 @pytest.mark.parametrize("accumulate", [False, True])
-def test_gradient_of_the_most_tokens(tt, accumulate):  # noqa: F811
+def test_gradient_of_the_most_tokens(tt, accumulate):
     """2^32 - 2 tokens of one column, each ID 2,048 times (two of them once less): the chunks' wavefronts and the joins' workgroups
     are 2^32 threads, and the last chunk ends where 32 bits do."""
     tokens, vocab = (1 << 32) - 2, 1 << 21
@@ -177,7 +177,7 @@ def test_gradient_of_the_most_tokens(tt, accumulate):  # noqa: F811
 
 @pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
 @pytest.mark.parametrize("vocab", [40, 9000])
-def test_sampling_at_an_endless_temperature(tt, vocab, dtype):  # noqa: F811
+def test_sampling_at_an_endless_temperature(tt, vocab, dtype):
     """All finite logits weigh the same, and one of +inf still more than all of them."""
     _say("sample endless", vocab, dtype)
     rng = np.random.default_rng(vocab)

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_ops import _dev, _dtype, _gaps_kept, _ids, _say, _view, _ws, tt  # noqa: F401
+from test_gpu_ops import _dev, _dtype, _gaps_kept, _ids, _say, _view, _ws
 
 pytestmark = pytest.mark.gpu
 
@@ -16,7 +16,7 @@ def _sums(vals, ids, vocab):
     return out.index_add_(0, torch.from_numpy(ids[ok]), torch.from_numpy(vals[ok])).numpy()
 
 
-def _exact(tt, ids, vocab, dim, grad_type, table_type, accumulate, pad=0, lead=0):  # noqa: F811
+def _exact(tt, ids, vocab, dim, grad_type, table_type, accumulate, pad=0, lead=0):
     """Small integers sum exactly in 32 bits, whatever the order, so that only the rounding to the table's type is
     left, to nearest even as torch rounds."""
     tokens = len(ids)
@@ -37,7 +37,7 @@ def _exact(tt, ids, vocab, dim, grad_type, table_type, accumulate, pad=0, lead=0
 @pytest.mark.parametrize("grad_type,table_type", [("bfloat16", "float32"), ("float32", "bfloat16"), ("float16", "float16")])
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("kind", ["text", "one row of many chunks", "runs across chunks"])
-def test_sorted_gradient_of_odd_widths(tt, dim, grad_type, table_type, accumulate, kind):  # noqa: F811
+def test_sorted_gradient_of_odd_widths(tt, dim, grad_type, table_type, accumulate, kind):
     tokens, vocab = 6000, 900
     _say("sorted gradient", kind, dim, grad_type, table_type, accumulate)
     rng = np.random.default_rng(dim)
@@ -53,7 +53,7 @@ def test_sorted_gradient_of_odd_widths(tt, dim, grad_type, table_type, accumulat
 
 @pytest.mark.parametrize("dim", [9, 15, 513, 1001])
 @pytest.mark.parametrize("accumulate", [False, True])
-def test_few_tokens_of_odd_widths(tt, dim, accumulate):  # noqa: F811
+def test_few_tokens_of_odd_widths(tt, dim, accumulate):
     _say("few tokens", dim, accumulate)
     rng = np.random.default_rng(dim + 1)
     ids = _ids(rng, 1500, 600, 0.05)
