@@ -12,7 +12,8 @@ from .binding import (EXPORTS, FAMILIES, KERNELS, TOKTIER_CL100K, TOKTIER_DEEPSE
                       toktier_vocab_info, toktier_workspace_bytes, toktier_workspace_bytes_ex)
 from .binding import (TOKTIER_BF16, TOKTIER_F16, TOKTIER_F32, TOKTIER_MAX_VOCAB, toktier_cross_entropy,
                       toktier_cross_entropy_backward, toktier_cross_entropy_workspace_bytes, toktier_embed,
-                      toktier_embed_backward, toktier_embed_backward_workspace_bytes, toktier_sample,
+                      toktier_embed_backward, toktier_embed_backward_workspace_bytes, toktier_linear_cross_entropy,
+                      toktier_linear_cross_entropy_backward, toktier_linear_cross_entropy_workspace_bytes, toktier_sample,
                       toktier_sample_workspace_bytes)
 
 __all__ = ["EXPORTS", "FAMILIES", "KERNELS", "TOKTIER_CL100K", "TOKTIER_DEEPSEEK", "TOKTIER_GPT2", "TOKTIER_IGNORE_MERGES",
@@ -24,5 +25,6 @@ __all__ = ["EXPORTS", "FAMILIES", "KERNELS", "TOKTIER_CL100K", "TOKTIER_DEEPSEEK
            "toktier_vocab_info", "toktier_workspace_bytes", "toktier_workspace_bytes_ex",
            "TOKTIER_BF16", "TOKTIER_F16", "TOKTIER_F32", "TOKTIER_MAX_VOCAB", "toktier_cross_entropy",
            "toktier_cross_entropy_backward", "toktier_cross_entropy_workspace_bytes", "toktier_embed",
-           "toktier_embed_backward", "toktier_embed_backward_workspace_bytes", "toktier_sample",
+           "toktier_embed_backward", "toktier_embed_backward_workspace_bytes", "toktier_linear_cross_entropy",
+           "toktier_linear_cross_entropy_backward", "toktier_linear_cross_entropy_workspace_bytes", "toktier_sample",
            "toktier_sample_workspace_bytes"]

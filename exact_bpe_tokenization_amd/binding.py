@@ -35,7 +35,9 @@ EXPORTS = ("toktier_load_vocab", "toktier_load_vocab_ex", "toktier_free_vocab", 
            "toktier_unicode_table_sha256",
            "toktier_embed", "toktier_embed_backward_workspace_bytes", "toktier_embed_backward",
            "toktier_cross_entropy_workspace_bytes", "toktier_cross_entropy", "toktier_cross_entropy_backward",
-           "toktier_sample_workspace_bytes", "toktier_sample")
+           "toktier_sample_workspace_bytes", "toktier_sample",
+           "toktier_linear_cross_entropy_workspace_bytes", "toktier_linear_cross_entropy",
+           "toktier_linear_cross_entropy_backward")
 
 # kernel launches of one encode call, in stream order (TOKTIER_K_* in toktier.h)
 KERNELS = ("summary", "pieces", "tiles", "giant_seams", "bpe", "bpe_giant", "emit")
@@ -101,6 +103,11 @@ def lib():
     L.toktier_cross_entropy_backward.argtypes = [vp, i32, u32, u32, u64, vp, vp, vp, f32, vp, u64, vp]
     L.toktier_sample_workspace_bytes.argtypes = [u32, u32, u64p]
     L.toktier_sample.argtypes = [vp, i32, u32, u32, u64, vp, u64, vp, vp, vp, vp, vp, vp, vp, vp, u64, vp]
+    L.toktier_linear_cross_entropy_workspace_bytes.argtypes = [u32, u32, u32, i32, i32, u64p]
+    L.toktier_linear_cross_entropy.argtypes = [vp, i32, u32, u32, u64, vp, u32, u64, vp, vp, vp, vp, f32, vp, u64, vp, i32,
+                                               u64, i32, vp, u64, vp]
+    L.toktier_linear_cross_entropy_backward.argtypes = [vp, i32, u32, u32, u64, vp, u32, u64, vp, vp, vp, f32, vp, u64, vp,
+                                                        i32, u64, i32, vp, u64, vp]
     for f in ("toktier_status_string",):
         getattr(L, f).argtypes = [i32]
         getattr(L, f).restype = ctypes.c_char_p
@@ -583,6 +590,64 @@ def toktier_cross_entropy_backward(logits, targets, lse, grad_logits, grad_loss=
                                                 _vector(lse, dev, what, "lse", n, _FLOAT),
                                                 _optional(grad_loss, dev, what, "grad_loss", n, _FLOAT),
                                                 float(grad_scale), gp, gs, st), what)
+
+
+def toktier_linear_cross_entropy_workspace_bytes(n_rows, n_vocab, dim, dtype, grads=True):
+    out = ctypes.c_uint64()
+    _check(lib().toktier_linear_cross_entropy_workspace_bytes(int(n_rows), int(n_vocab), int(dim), TYPES.get(dtype, 0),
+                                                              int(bool(grads)), ctypes.byref(out)),
+           "toktier_linear_cross_entropy_workspace_bytes")
+    return out.value
+
+
+def _linear(hidden, weight, grad_hidden, grad_weight, dev, what):
+    """(arguments of hidden and weight, those of the gradients)"""
+    hp, ht, n, dim, hs = _matrix(hidden, dev, what, "hidden")
+    wp, wt, n_vocab, wdim, ws = _matrix(weight, dev, what, "weight")
+    if wt != ht or wdim != dim:
+        _refuse(what, "weight differs from hidden in columns or type")
+    gp, gs, qp, qt, qs = None, 0, None, ht, 0
+    if grad_hidden is not None:
+        gp, _, _, _, gs = _matrix(grad_hidden, dev, what, "grad_hidden")
+        if grad_hidden.shape != hidden.shape or grad_hidden.dtype != hidden.dtype:
+            _refuse(what, "grad_hidden differs from hidden in shape or type")
+    if grad_weight is not None:
+        qp, qt, _, _, qs = _matrix(grad_weight, dev, what, "grad_weight")
+        if grad_weight.shape != weight.shape or qt not in (wt, TOKTIER_F32):
+            _refuse(what, "grad_weight differs from weight in shape, or is neither of its type nor float32")
+    return (hp, ht, n, dim, hs, wp, n_vocab, ws), (gp, gs, qp, qt, qs)
+
+
+def toktier_linear_cross_entropy(hidden, weight, targets, loss, lse, workspace, grad_hidden=None, grad_weight=None,
+                                 grad_loss=None, grad_scale=1.0, accumulate=False, stream=None):
+    """Cross entropy of the logits hidden @ weight.T, which are not kept: loss[i] = lse[i] - logit of targets[i] (both 0
+    where targets[i] is no ID, a row that takes no part), and, where they are given, the gradients of
+    grad_scale * grad_loss[i] * loss[i].  hidden, grad_hidden: [n, dim]; weight, grad_weight: [n_vocab, dim] (grad_weight of
+    weight's type or float32, added to when accumulate is True); targets: int32 [n]; loss, lse, grad_loss: float32 [n];
+    workspace: uint8 of toktier_linear_cross_entropy_workspace_bytes(n, n_vocab, dim, dtype, grads)."""
+    what = "toktier_linear_cross_entropy"
+    dev, st = _here(stream)
+    (hp, ht, n, dim, hs, wp, n_vocab, ws), grads = _linear(hidden, weight, grad_hidden, grad_weight, dev, what)
+    sp, sn = _scratch(workspace, dev, what)
+    _check(lib().toktier_linear_cross_entropy(hp, ht, n, dim, hs, wp, n_vocab, ws, _vector(targets, dev, what, "targets", n, _IDS),
+                                              _vector(loss, dev, what, "loss", n, _FLOAT),
+                                              _vector(lse, dev, what, "lse", n, _FLOAT),
+                                              _optional(grad_loss, dev, what, "grad_loss", n, _FLOAT), float(grad_scale),
+                                              *grads, int(bool(accumulate)), sp, sn, st), what)
+
+
+def toktier_linear_cross_entropy_backward(hidden, weight, targets, lse, workspace, grad_hidden=None, grad_weight=None,
+                                          grad_loss=None, grad_scale=1.0, accumulate=False, stream=None):
+    """The gradients alone, from the lse that toktier_linear_cross_entropy wrote for the same arguments."""
+    what = "toktier_linear_cross_entropy_backward"
+    dev, st = _here(stream)
+    (hp, ht, n, dim, hs, wp, n_vocab, ws), grads = _linear(hidden, weight, grad_hidden, grad_weight, dev, what)
+    sp, sn = _scratch(workspace, dev, what)
+    _check(lib().toktier_linear_cross_entropy_backward(hp, ht, n, dim, hs, wp, n_vocab, ws,
+                                                       _vector(targets, dev, what, "targets", n, _IDS),
+                                                       _vector(lse, dev, what, "lse", n, _FLOAT),
+                                                       _optional(grad_loss, dev, what, "grad_loss", n, _FLOAT),
+                                                       float(grad_scale), *grads, int(bool(accumulate)), sp, sn, st), what)
 
 
 def toktier_sample_workspace_bytes(n_rows, n_vocab):

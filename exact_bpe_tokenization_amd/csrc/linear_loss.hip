@@ -1,0 +1,640 @@
+// linear_loss.hip -- next-token cross entropy straight from hidden states and the table of the logits, and its gradients,
+// without keeping the logits.
+//
+//   x = h W^T,  lse = log sum_v exp(x_v),  loss = lse - x_y
+//   G = c (exp(x - lse) - [v == y]),  dh = G W,  dW = G^T h
+//
+// One product gives every tile's running maximum and sum per row; then, a piece of the vocabulary at a time, the
+// product is formed again for G (in the operands' type), which goes into dh (32-bit sums over the pieces) and into
+// the piece's rows of dW.  Positions whose target is no ID are left out of all products: the hidden states of the others
+// are copied together first, into rows that the products need not check for their ends.
+#include <algorithm>
+#include <type_traits>
+
+#include "product.h"
+
+namespace tt {
+namespace {
+
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
+constexpr float NEG_INF = -__builtin_inff();
+constexpr uint32_t NONE = 0xFFFFFFFFu;
+constexpr uint32_t PAD = 256;            // rows of the packed matrices come in this many
+constexpr uint32_t MAX_ROWS = TOKTIER_MAX_LINEAR_ROWS, MAX_DIM = TOKTIER_MAX_LINEAR_DIM;
+
+__device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * LOG2E); }
+
+struct MaxSum {
+    float m, s;
+};
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b)
+{
+    const float m = fmaxf(a.m, b.m);
+    if (m == NEG_INF) return MaxSum{m, a.s + b.s};
+    return MaxSum{m, a.s * exp_f(a.m - m) + b.s * exp_f(b.m - m)};
+}
+
+// What the calls leave for each other in the workspace.
+struct Head {
+    uint32_t count;       // rows that take part
+    float scale, unscale; // G is kept times `scale`
+    uint32_t pad[61];
+};
+
+struct Rows {             // of the packed rows
+    Head *head;
+    uint32_t *list;       // row of the caller's matrices, NONE for padding
+    uint32_t *target;
+    float *factor;        // c
+    float *shift, *recip; // G = c (exp(x - shift) recip - [v == y])
+    float *at_target;     // x_y
+};
+
+// ---------------------------------------------------------------------------------------------
+// rows
+
+// Numbers the rows that take part, in order, and clears what the others get.  float16's range does not hold c times a
+// small probability: G is kept times the power of two that brings the largest |c| to 2^14..2^15, so that probabilities
+// down to 2^-28 (2^-39 with fewer digits) keep their digits.
+__global__ __launch_bounds__(1024) void k_rows(const uint32_t *__restrict__ targets, uint32_t n_rows, uint32_t n_pad, uint32_t n_vocab,
+                                               const float *__restrict__ lse_in, const float *__restrict__ grad_loss, float grad_scale,
+                                               int scaled, float *loss, float *lse_out, Rows rows)
+{
+    __shared__ uint32_t part[16];
+    __shared__ uint32_t largest;
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (threadIdx.x == 0) largest = 0;
+    uint32_t most = 0, count = 0;
+    for (uint32_t r0 = 0; r0 < n_rows; r0 += 1024) {
+        const uint32_t r = r0 + threadIdx.x;
+        const uint32_t y = r < n_rows ? targets[r] : NONE;
+        const bool in = r < n_rows && y < n_vocab;
+        const uint64_t mask = __ballot(in);
+        __syncthreads();
+        if (lane == 0) part[wave] = __popcll(mask);
+        __syncthreads();
+        uint32_t at = count;
+        for (uint32_t w = 0; w < 16; ++w) {
+            at += w < wave ? part[w] : 0;
+            count += part[w];
+        }
+        at += __popcll(mask & ((1ull << lane) - 1));
+        if (in) {
+            float c = grad_scale * (grad_loss ? grad_loss[r] : 1.f), shift = 0.f, recip = 1.f;
+            if (lse_in) {
+                shift = lse_in[r];
+                if (shift == NEG_INF) c = shift = 0.f;   // nothing but -inf: no gradient
+            }
+            rows.list[at] = r;
+            rows.target[at] = y;
+            rows.factor[at] = c;
+            rows.shift[at] = shift;
+            rows.recip[at] = recip;
+            const uint32_t size = __builtin_bit_cast(uint32_t, c) & 0x7FFFFFFFu;
+            if (size < 0x7F800000u && size > most) most = size;
+        } else if (r < n_rows && loss) {
+            loss[r] = 0.f;
+            lse_out[r] = 0.f;
+        }
+    }
+    for (uint32_t i = count + threadIdx.x; i < n_pad; i += 1024) {
+        rows.list[i] = NONE;
+        rows.target[i] = NONE;
+        rows.factor[i] = rows.shift[i] = rows.recip[i] = 0.f;
+    }
+    __syncthreads();
+    atomicMax(&largest, most);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float scale = 1.f;
+        const int e = (int)(largest >> 23) - 127;   // the largest |c| is 2^e .. 2^(e + 1); subnormal ones count as 2^-127
+        if (scaled && largest) scale = __builtin_amdgcn_ldexpf(1.f, 14 - e > 126 ? 126 : 14 - e);
+        rows.head->count = count;
+        rows.head->scale = scale;
+        rows.head->unscale = 1.f / scale;
+    }
+}
+
+// Copies a row of n elements to one of n_pad, zeros behind it (or throughout).
+template <class T> __device__ __forceinline__ void copy_row(T *to, const T *from, uint32_t n, uint32_t n_pad)
+{
+    for (uint32_t j = threadIdx.x * VEC; j < n_pad; j += blockDim.x * VEC) {
+        float x[VEC] = {};
+        if (from && j < n) load_part(from + j, n - j, 0.f, x);
+        store_vec(to + j, x);
+    }
+}
+
+// The packed hidden states, and zeros as the gradient of the rows that take no part.
+template <class T>
+__global__ __launch_bounds__(256) void k_pack_hidden(const T *__restrict__ hidden, uint64_t stride, uint32_t dim, uint32_t dim_pad,
+                                                     uint32_t n_rows, uint32_t n_vocab, const uint32_t *__restrict__ targets, Rows rows,
+                                                     T *__restrict__ packed, T *__restrict__ grad, uint64_t grad_stride)
+{
+    const uint32_t i = blockIdx.x, r = rows.list[i];
+    copy_row(packed + (uint64_t)i * dim_pad, r == NONE ? (const T *)nullptr : hidden + r * stride, dim, dim_pad);
+    if (grad && i < n_rows && targets[i] >= n_vocab) {
+        const float zero[VEC] = {};
+        for (uint32_t j = threadIdx.x * VEC; j < dim; j += 256 * VEC) store_part(grad + i * grad_stride + j, dim - j, zero);
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void k_pack_weight(const T *__restrict__ weight, uint64_t stride, uint32_t dim, uint32_t dim_pad, T *__restrict__ packed)
+{
+    copy_row(packed + (uint64_t)blockIdx.x * dim_pad, weight + blockIdx.x * stride, dim, dim_pad);
+}
+
+// ---------------------------------------------------------------------------------------------
+// logits
+
+// A tile of logits, vocabulary along m, rows along n; what becomes of it: each row's maximum and sum of exponentials
+// over the tile's IDs (KEEP = false), or G (KEEP = true).
+template <class T, class TILE, bool KEEP>
+__global__ __launch_bounds__(TILE::THREADS, 2) void k_logits(Operand w, Operand h, uint32_t steps, uint32_t m_tiles, uint32_t first_id,
+                                                             uint32_t n_vocab, uint32_t n_pad, Rows rows, MaxSum *__restrict__ sums,
+                                                             T *__restrict__ g, uint32_t g_cols)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t shared[2 * TILE::STAGE];
+    lds_u8 *lds = (lds_u8 *)shared;
+    const uint32_t count = rows.head->count;
+    uint32_t tm, tn;
+    if (!tile_of(blockIdx.x, m_tiles, (count + TILE::N - 1) / TILE::N, tm, tn)) return;
+    const uint32_t m0 = tm * TILE::M, n0 = tn * TILE::N;
+    f32x4 acc[TILE::TM][TILE::TN];
+    product<T, TILE, false, false>(acc, lds, w, h, m0, n0, 0, steps, 0);
+
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / TILE::WN, wn = wave % TILE::WN;
+    const uint32_t m_lane = m0 + wm * TILE::TM * 16 + (lane >> 4) * 4;   // of the tile's first value in this lane
+    const bool edge = first_id + m0 + TILE::M > n_vocab;
+    MaxSum *meet = (MaxSum *)shared;   // [WM][N]
+#pragma unroll
+    for (int j = 0; j < TILE::TN; ++j) {
+        const uint32_t n = n0 + (wn * TILE::TN + j) * 16 + (lane & 15);   // the packed rows reach that far
+        const uint32_t y = rows.target[n] - (first_id + m_lane);          // target, from this lane's first ID
+        if constexpr (!KEEP) {
+            float m = NEG_INF;
+#pragma unroll
+            for (int i = 0; i < TILE::TM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (edge && first_id + m_lane + i * 16 + e >= n_vocab) acc[i][j][e] = NEG_INF;
+                    const float x = acc[i][j][e];
+                    m = fmaxf(m, x);
+                    if (y == (uint32_t)(i * 16 + e)) rows.at_target[n] = x;
+                }
+            const float from = m == NEG_INF ? 0.f : m;
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < TILE::TM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s += exp_f(acc[i][j][e] - from);
+            MaxSum v{m, s};
+            v = join(v, MaxSum{__shfl_xor(v.m, 16), __shfl_xor(v.s, 16)});
+            v = join(v, MaxSum{__shfl_xor(v.m, 32), __shfl_xor(v.s, 32)});
+            if (lane < 16) meet[wm * TILE::N + (n - n0)] = v;
+        } else {
+            const float c = rows.factor[n] * rows.head->scale, shift = rows.shift[n], recip = rows.recip[n];
+            const bool row = n < count;
+            T *to = g + (uint64_t)n * g_cols + m_lane;
+#pragma unroll
+            for (int i = 0; i < TILE::TM; ++i) {
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = c * (exp_f(acc[i][j][e] - shift) * recip - (y == (uint32_t)(i * 16 + e) ? 1.f : 0.f));
+                    if (!row || (edge && first_id + m_lane + i * 16 + e >= n_vocab)) x[e] = 0.f;
+                }
+                if constexpr (sizeof(T) == 4) {
+                    *(f32x4 *)(to + i * 16) = f32x4{x[0], x[1], x[2], x[3]};
+                } else {
+                    u32x2 v;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        v[k] = (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k]) | (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k + 1]) << 16;
+                    *(u32x2 *)(to + i * 16) = v;
+                }
+            }
+        }
+    }
+    if constexpr (!KEEP) {
+        __syncthreads();
+        for (uint32_t n = threadIdx.x; n < TILE::N; n += TILE::THREADS) {
+            MaxSum v = meet[n];
+#pragma unroll
+            for (int k = 1; k < TILE::WM; ++k) v = join(v, meet[k * TILE::N + n]);
+            sums[(uint64_t)tm * n_pad + n0 + n] = v;
+        }
+    }
+}
+
+// Joins the tiles' maxima and sums of 64 rows, 16 threads a row.
+__global__ __launch_bounds__(1024) void k_join(const MaxSum *__restrict__ sums, uint32_t tiles, uint32_t n_pad, Rows rows,
+                                               float *__restrict__ loss, float *__restrict__ lse)
+{
+    __shared__ MaxSum part[16][64];
+    const uint32_t n = blockIdx.x * 64 + (threadIdx.x & 63), k = threadIdx.x >> 6;
+    if (blockIdx.x * 64 >= rows.head->count) return;
+    MaxSum v{NEG_INF, 0.f};
+    for (uint32_t t = k; t < tiles; t += 16) v = join(v, sums[(uint64_t)t * n_pad + n]);
+    part[k][threadIdx.x & 63] = v;
+    __syncthreads();
+    if (k || n >= rows.head->count) return;
+    for (uint32_t i = 1; i < 16; ++i) v = join(v, part[i][threadIdx.x]);
+    const bool none = v.m == NEG_INF && v.s == 0.f;
+    const float log_s = LN2 * __builtin_amdgcn_logf(v.s);
+    const uint32_t r = rows.list[n];
+    lse[r] = none ? NEG_INF : v.m + log_s;
+    loss[r] = none ? -NEG_INF : (v.m - rows.at_target[n]) + log_s;
+    rows.shift[n] = none ? 0.f : v.m;
+    rows.recip[n] = none ? 0.f : 1.f / v.s;
+    if (none) rows.factor[n] = 0.f;
+}
+
+// ---------------------------------------------------------------------------------------------
+// gradients
+
+// Four neighbouring elements of an output row.
+template <class T> __device__ __forceinline__ void put4(T *to, const float (&x)[4], bool whole, uint32_t n)
+{
+    if (whole) {
+        if constexpr (sizeof(T) == 4) {
+            *(f32x4 *)to = f32x4{x[0], x[1], x[2], x[3]};
+        } else {
+            u32x2 v;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                v[k] = (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k]) | (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k + 1]) << 16;
+            *(u32x2 *)to = v;
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (k < (int)n) to[k] = (T)x[k];
+}
+
+// dh: columns along m, rows along n, k over the piece's IDs, of which blockIdx.y takes a share.  The sums go to `sums`
+// ([share][n_pad][dim_pad], added to where the piece is not the first), or rounded to the caller's rows if one share of one
+// piece is all.
+template <class T, class TILE>
+__global__ __launch_bounds__(TILE::THREADS, 2) void k_grad_hidden(Operand w, Operand g, uint32_t steps, uint32_t ids, uint32_t m_tiles,
+                                                                  uint32_t dim, uint32_t dim_pad, uint32_t n_pad, int add, Rows rows,
+                                                                  float *__restrict__ sums, T *__restrict__ out, uint64_t stride, int whole)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t shared[2 * TILE::STAGE];
+    const uint32_t count = rows.head->count;
+    uint32_t tm, tn;
+    if (!tile_of(blockIdx.x, m_tiles, (count + TILE::N - 1) / TILE::N, tm, tn)) return;
+    const uint32_t m0 = tm * TILE::M, n0 = tn * TILE::N, share = (steps + gridDim.y - 1) / gridDim.y;
+    const uint32_t begin = blockIdx.y * share < steps ? blockIdx.y * share : steps, end = begin + share < steps ? begin + share : steps;
+    f32x4 acc[TILE::TM][TILE::TN];
+    product<T, TILE, true, false>(acc, (lds_u8 *)shared, w, g, m0, n0, begin, end, ids);
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / TILE::WN, wn = wave % TILE::WN;
+    const uint32_t m_lane = m0 + wm * TILE::TM * 16 + (lane >> 4) * 4;
+    if (!out) sums += (uint64_t)blockIdx.y * n_pad * dim_pad;
+    const float unscale = rows.head->unscale;
+#pragma unroll
+    for (int j = 0; j < TILE::TN; ++j) {
+        const uint32_t n = n0 + (wn * TILE::TN + j) * 16 + (lane & 15);
+        if (n >= count) continue;
+        if (!out) {
+            float *to = sums + (uint64_t)n * dim_pad + m_lane;
+#pragma unroll
+            for (int i = 0; i < TILE::TM; ++i) {
+                if (m_lane + i * 16 >= dim_pad) continue;
+                f32x4 v = acc[i][j];
+                if (add) v += *(const f32x4 *)(to + i * 16);
+                *(f32x4 *)(to + i * 16) = v;
+            }
+        } else {
+            T *to = out + rows.list[n] * stride + m_lane;
+#pragma unroll
+            for (int i = 0; i < TILE::TM; ++i) {
+                const uint32_t m = m_lane + i * 16;
+                if (m >= dim) continue;
+                const float x[4] = {acc[i][j][0] * unscale, acc[i][j][1] * unscale, acc[i][j][2] * unscale, acc[i][j][3] * unscale};
+                put4(to + i * 16, x, whole && m + 4 <= dim, dim - m);
+            }
+        }
+    }
+}
+
+// The shares of dh summed, in order, and rounded.
+template <class T>
+__global__ __launch_bounds__(256) void k_finish_hidden(const float *__restrict__ sums, uint32_t shares, uint32_t n_pad, uint32_t dim,
+                                                       uint32_t dim_pad, Rows rows, T *__restrict__ out, uint64_t stride)
+{
+    const uint32_t i = blockIdx.x, r = rows.list[i];
+    if (r == NONE) return;
+    const float unscale = rows.head->unscale;
+    for (uint32_t j = threadIdx.x * VEC; j < dim; j += 256 * VEC) {
+        float x[VEC] = {};
+        for (uint32_t k = 0; k < shares; ++k) {
+            const Vec<float> v = load_vec(sums + ((uint64_t)k * n_pad + i) * dim_pad + j);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[e] += vec_at(v, e);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] *= unscale;
+        store_part(out + r * stride + j, dim - j, x);
+    }
+}
+
+// dW of a piece: columns along m, IDs along n, k over the rows that take part.
+template <class T, class TILE, class OUT>
+__global__ __launch_bounds__(TILE::THREADS, 2) void k_grad_weight(Operand h, Operand g, uint32_t m_tiles, uint32_t n_tiles, uint32_t ids,
+                                                                  uint32_t dim, int accumulate, Rows rows, OUT *__restrict__ out,
+                                                                  uint64_t stride, int whole)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t shared[2 * TILE::STAGE];
+    uint32_t tm, tn;
+    if (!tile_of(blockIdx.x, m_tiles, n_tiles, tm, tn)) return;
+    const uint32_t m0 = tm * TILE::M, n0 = tn * TILE::N;
+    f32x4 acc[TILE::TM][TILE::TN];
+    product<T, TILE, true, true>(acc, (lds_u8 *)shared, h, g, m0, n0, 0, (rows.head->count + STEP_K<T> - 1) / STEP_K<T>, 0);
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / TILE::WN, wn = wave % TILE::WN;
+    const uint32_t m_lane = m0 + wm * TILE::TM * 16 + (lane >> 4) * 4;
+    const float unscale = rows.head->unscale;
+#pragma unroll
+    for (int j = 0; j < TILE::TN; ++j) {
+        const uint32_t n = n0 + (wn * TILE::TN + j) * 16 + (lane & 15);
+        if (n >= ids) continue;
+        OUT *to = out + n * stride + m_lane;
+#pragma unroll
+        for (int i = 0; i < TILE::TM; ++i) {
+            const uint32_t m = m_lane + i * 16;
+            if (m >= dim) continue;
+            const bool all = whole && m + 4 <= dim;
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = acc[i][j][e] * unscale;
+            if (accumulate) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (m + e < dim) x[e] += (float)to[i * 16 + e];
+            }
+            put4(to + i * 16, x, all, dim - m);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// host side
+
+uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
+
+// What a workspace holds.  Every part grows with rows, IDs and columns.
+//   G is kept for a piece of the vocabulary of up to PIECE_BYTES (which the last-level cache holds), of at least
+//   LEAST_IDS IDs; a table whose rows are not whole steps of aligned 16-byte pieces is copied, PIECE_BYTES at a time.
+constexpr uint64_t PIECE_BYTES = 128ull << 20;
+constexpr uint32_t LEAST_IDS = 4096;
+constexpr uint32_t MOST_SHARES = 32;
+constexpr uint64_t SHARE_FLOATS = 1ull << 23;
+constexpr uint32_t MANY_TILES = 192;   // of 256 x 256, or of 128 x 128: enough for the CUs
+
+struct Sizes {
+    uint32_t n_pad, dim_pad, v_pad, elem;
+    uint64_t rows, hidden, weight, sums, g, shares;   // bytes of the parts
+    uint64_t total;
+};
+
+Sizes sizes_of(uint32_t n_rows, uint32_t n_vocab, uint32_t dim, int type, bool grads)
+{
+    Sizes z{};
+    z.elem = elem_size(type);
+    z.n_pad = (uint32_t)up(std::max(n_rows, 1u), PAD);
+    z.dim_pad = (uint32_t)up(dim, STEP_BYTES / z.elem);
+    z.v_pad = (uint32_t)up(n_vocab, PAD);
+    z.rows = sizeof(Head) + 6ull * 4 * z.n_pad;
+    z.hidden = (uint64_t)z.n_pad * z.dim_pad * z.elem;
+    const uint64_t row = (uint64_t)z.dim_pad * z.elem;
+    z.weight = std::min(z.v_pad * row, std::max(PIECE_BYTES, PAD * row));
+    // per tile of 256 IDs; tiles of 64 are for fewer than MANY_TILES of those
+    z.sums = 8 * std::max((uint64_t)z.v_pad / 256 * z.n_pad, std::min((uint64_t)z.v_pad / 64 * z.n_pad, (uint64_t)4 * 256 * MANY_TILES));
+    if (grads) {
+        z.g = z.elem * std::min((uint64_t)z.n_pad * z.v_pad, std::max(PIECE_BYTES / z.elem, (uint64_t)z.n_pad * LEAST_IDS));
+        const uint64_t one = (uint64_t)z.n_pad * z.dim_pad;
+        z.shares = 4 * (one + std::min((MOST_SHARES - 1) * one, SHARE_FLOATS));
+    }
+    for (uint64_t *p : {&z.rows, &z.hidden, &z.weight, &z.sums, &z.g, &z.shares}) z.total += *p = up(*p, 256);
+    return z;
+}
+
+typedef Tile<2, 4, 8, 4> Big;      // 256 x 256
+typedef Tile<2, 2, 4, 4> Middle;   // 128 x 128
+typedef Tile<2, 2, 2, 2> Small;    // 64 x 64
+
+uint32_t tiles(uint64_t n, uint32_t of) { return (uint32_t)((n + of - 1) / of); }
+
+// The largest tiles of which there are enough for the CUs.
+template <class F> void with_tile(uint64_t m, uint64_t n, F f)
+{
+    if ((uint64_t)tiles(m, 256) * tiles(n, 256) >= MANY_TILES) f(Big{});
+    else if ((uint64_t)tiles(m, 128) * tiles(n, 128) >= MANY_TILES) f(Middle{});
+    else f(Small{});
+}
+
+struct Call {
+    const void *hidden, *weight;
+    int type;
+    uint32_t n_rows, n_vocab, dim;
+    uint64_t hidden_stride, weight_stride;
+    const uint32_t *targets;
+    float *loss, *lse;
+    const float *lse_in, *grad_loss;
+    float grad_scale;
+    void *grad_hidden;
+    uint64_t grad_hidden_stride;
+    void *grad_weight;
+    int grad_weight_type;
+    uint64_t grad_weight_stride;
+    int accumulate;
+};
+
+template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipStream_t s)
+{
+    Rows rows;
+    rows.head = (Head *)ws;
+    rows.list = (uint32_t *)(ws + sizeof(Head));
+    rows.target = rows.list + z.n_pad;
+    rows.factor = (float *)(rows.target + z.n_pad);
+    rows.shift = rows.factor + z.n_pad;
+    rows.recip = rows.shift + z.n_pad;
+    rows.at_target = rows.recip + z.n_pad;
+    T *hidden = (T *)(ws + z.rows), *packed = (T *)(ws + z.rows + z.hidden);
+    MaxSum *sums = (MaxSum *)(ws + z.rows + z.hidden + z.weight);
+    T *g = (T *)((uint8_t *)sums + z.sums);
+    float *shares = (float *)((uint8_t *)g + z.g);
+    const T *weight = (const T *)c.weight;
+    const bool grads = c.grad_hidden || c.grad_weight, forward = c.loss != nullptr;
+
+    k_rows<<<1, 1024, 0, s>>>(c.targets, c.n_rows, z.n_pad, c.n_vocab, c.lse_in, c.grad_loss, c.grad_scale, std::is_same_v<T, _Float16>, c.loss,
+                              c.lse, rows);
+    k_pack_hidden<T><<<z.n_pad, 256, 0, s>>>((const T *)c.hidden, c.hidden_stride, c.dim, z.dim_pad, c.n_rows, c.n_vocab, c.targets, rows, hidden,
+                                             (T *)c.grad_hidden, c.grad_hidden_stride);
+
+    // The table as it lies: whole steps, aligned, a tile within 32-bit offsets.  Otherwise pieces of it are copied.
+    const uint64_t w_bytes = c.weight_stride * z.elem;
+    const bool as_is = c.dim == z.dim_pad && (uintptr_t)c.weight % 16 == 0 && w_bytes % 16 == 0 && w_bytes <= (1u << 22);
+    const uint64_t row = (uint64_t)z.dim_pad * z.elem;
+    const uint32_t most_packed = (uint32_t)std::min<uint64_t>(z.v_pad, z.weight / row / PAD * PAD);
+    const uint32_t steps = z.dim_pad / STEP_K<T>;
+    const Operand h{hidden, row, z.n_pad};
+    auto table = [&](uint32_t first, uint32_t ids) {
+        const T *from = weight + first * c.weight_stride;
+        if (as_is) return Operand{from, w_bytes, ids};
+        k_pack_weight<T><<<ids, 256, 0, s>>>(from, c.weight_stride, c.dim, z.dim_pad, packed);
+        return Operand{packed, row, ids};
+    };
+
+    if (forward && c.n_rows) {
+        with_tile(z.v_pad, c.n_rows, [&](auto t) {
+            using TILE = decltype(t);
+            const uint32_t most = as_is ? z.v_pad : most_packed;
+            for (uint32_t first = 0; first < c.n_vocab; first += most) {
+                const uint32_t ids = std::min(most, c.n_vocab - first), m_tiles = tiles(ids, TILE::M);
+                const Operand w = table(first, ids);
+                k_logits<T, TILE, false><<<tile_blocks(m_tiles, tiles(c.n_rows, TILE::N)), TILE::THREADS, 0, s>>>(
+                    w, h, steps, m_tiles, first, c.n_vocab, z.n_pad, rows, sums + (uint64_t)first / TILE::M * z.n_pad, nullptr, 0);
+            }
+            k_join<<<z.n_pad / 64, 1024, 0, s>>>(sums, tiles(c.n_vocab, TILE::M), z.n_pad, rows, c.loss, c.lse);
+        });
+    }
+    if (!grads) return;
+
+    // pieces of about the same size, whose G fits
+    uint32_t piece = (uint32_t)std::min<uint64_t>(z.v_pad, z.g / z.elem / z.n_pad / PAD * PAD);
+    if (!as_is) piece = std::min(piece, most_packed);
+    const uint32_t pieces = tiles(z.v_pad, piece);
+    piece = (uint32_t)up(tiles(c.n_vocab, pieces), PAD);
+    uint32_t n_shares = 1;
+    for (uint32_t first = 0; first < c.n_vocab; first += piece) {
+        const uint32_t ids = std::min(piece, c.n_vocab - first);
+        const Operand w = c.n_rows ? table(first, ids) : Operand{};
+        if (c.n_rows) with_tile(ids, c.n_rows, [&](auto t) {
+            using TILE = decltype(t);
+            // every column of G up to the piece's width is written: the products read it in whole steps
+            const uint32_t m_tiles = tiles(up(ids, PAD), TILE::M);
+            k_logits<T, TILE, true><<<tile_blocks(m_tiles, tiles(c.n_rows, TILE::N)), TILE::THREADS, 0, s>>>(
+                w, h, steps, m_tiles, first, c.n_vocab, z.n_pad, rows, nullptr, g, piece);
+        });
+        const Operand go{g, (uint64_t)piece * z.elem, z.n_pad};
+        if (c.grad_hidden && c.n_rows) {
+            with_tile(c.dim, c.n_rows, [&](auto t) {
+                using TILE = decltype(t);
+                const uint32_t m_tiles = tiles(c.dim, TILE::M), n_tiles = tiles(c.n_rows, TILE::N), k_steps = tiles(ids, STEP_K<T>);
+                if (first == 0) {
+                    const uint64_t most = z.shares / 4 / ((uint64_t)z.n_pad * z.dim_pad);
+                    n_shares = std::max(1u, std::min({512 / (m_tiles * n_tiles), k_steps / 8, (uint32_t)std::min<uint64_t>(most, MOST_SHARES)}));
+                }
+                const bool direct = pieces == 1 && n_shares == 1;
+                const int whole = (uintptr_t)c.grad_hidden % (4 * z.elem) == 0 && c.grad_hidden_stride % 4 == 0;
+                k_grad_hidden<T, TILE><<<dim3(tile_blocks(m_tiles, n_tiles), n_shares), TILE::THREADS, 0, s>>>(
+                    Operand{w.p, w.stride, z.dim_pad}, go, k_steps, ids, m_tiles, c.dim, z.dim_pad, z.n_pad, first != 0, rows, shares,
+                    direct ? (T *)c.grad_hidden : nullptr, c.grad_hidden_stride, whole);
+            });
+        }
+        if (c.grad_weight) {
+            auto weights = [&](auto o) {
+                using OUT = decltype(o);
+                with_tile(c.dim, ids, [&](auto t) {
+                    using TILE = decltype(t);
+                    const uint32_t m_tiles = tiles(c.dim, TILE::M), n_tiles = tiles(ids, TILE::N);
+                    const int whole = (uintptr_t)c.grad_weight % (4 * sizeof(OUT)) == 0 && c.grad_weight_stride % 4 == 0;
+                    k_grad_weight<T, TILE, OUT><<<tile_blocks(m_tiles, n_tiles), TILE::THREADS, 0, s>>>(
+                        Operand{hidden, row, z.dim_pad}, Operand{g, (uint64_t)piece * z.elem, piece}, m_tiles, n_tiles, ids, c.dim, c.accumulate,
+                        rows, (OUT *)c.grad_weight + first * c.grad_weight_stride, c.grad_weight_stride, whole);
+                });
+            };
+            if (c.grad_weight_type == c.type) weights(T{});
+            else weights(float{});
+        }
+    }
+    if (c.grad_hidden && c.n_rows && !(pieces == 1 && n_shares == 1))
+        k_finish_hidden<T><<<z.n_pad, 256, 0, s>>>(shares, n_shares, z.n_pad, c.dim, z.dim_pad, rows, (T *)c.grad_hidden, c.grad_hidden_stride);
+}
+
+int run(const Call &c, void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    const bool forward = !c.lse_in, grads = c.grad_hidden || c.grad_weight;
+    if (!elem_size(c.type) || c.n_vocab == 0 || c.n_vocab > TOKTIER_MAX_VOCAB || c.dim == 0 || c.dim > MAX_DIM || c.n_rows > MAX_ROWS)
+        return TOKTIER_E_INVALID_ARG;
+    if (c.grad_weight && c.grad_weight_type != c.type && c.grad_weight_type != TOKTIER_F32) return TOKTIER_E_INVALID_ARG;
+    if (c.n_rows == 0 && (!c.grad_weight || c.accumulate)) return TOKTIER_OK;
+    const Sizes z = sizes_of(c.n_rows, c.n_vocab, c.dim, c.type, grads);
+    struct Area {
+        const void *p;
+        uint64_t n;
+    };
+    Area in[8], out[8];
+    int n_in = 0, n_out = 0;
+    auto matrix = [&](const void *p, int type, uint64_t r, uint64_t cols, uint64_t stride, Area *list, int &k) {
+        if (r == 0) return true;
+        list[k++] = Area{p, extent(type, r, cols, stride)};
+        return matrix_ok(p, type, r, cols, stride);
+    };
+    auto vector = [&](const void *p, bool needed, Area *list, int &k) {
+        if (c.n_rows == 0) return true;
+        if (p) list[k++] = Area{p, 4ull * c.n_rows};
+        return (p || !needed) && aligned4(p);
+    };
+    if (!matrix(c.hidden, c.type, c.n_rows, c.dim, c.hidden_stride, in, n_in) ||
+        !matrix(c.weight, c.type, c.n_vocab, c.dim, c.weight_stride, in, n_in) || !vector(c.targets, true, in, n_in) ||
+        !vector(c.grad_loss, false, in, n_in))
+        return TOKTIER_E_INVALID_ARG;
+    if (forward ? !vector(c.loss, true, out, n_out) || !vector(c.lse, true, out, n_out) : !vector(c.lse_in, true, in, n_in))
+        return TOKTIER_E_INVALID_ARG;
+    if (c.grad_hidden && !matrix(c.grad_hidden, c.type, c.n_rows, c.dim, c.grad_hidden_stride, out, n_out)) return TOKTIER_E_INVALID_ARG;
+    if (c.grad_weight && !matrix(c.grad_weight, c.grad_weight_type, c.n_vocab, c.dim, c.grad_weight_stride, out, n_out)) return TOKTIER_E_INVALID_ARG;
+    if (!workspace || ((uintptr_t)workspace & 255u)) return TOKTIER_E_INVALID_ARG;
+    if (workspace_bytes < z.total) return TOKTIER_E_CAPACITY;
+    out[n_out++] = Area{workspace, z.total};
+    for (int i = 0; i < n_out; ++i) {
+        for (int k = 0; k < n_in; ++k)
+            if (!apart(out[i].p, out[i].n, in[k].p, in[k].n)) return TOKTIER_E_INVALID_ARG;
+        for (int k = 0; k < i; ++k)
+            if (!apart(out[i].p, out[i].n, out[k].p, out[k].n)) return TOKTIER_E_INVALID_ARG;
+    }
+    with_type(c.type, [&](auto t) { enqueue<decltype(t)>(c, z, (uint8_t *)workspace, (hipStream_t)stream); });
+    return hip_status(hipGetLastError());
+}
+
+}  // namespace
+}  // namespace tt
+
+using namespace tt;
+
+extern "C" int toktier_linear_cross_entropy_workspace_bytes(uint32_t n_rows, uint32_t n_vocab, uint32_t dim, int type, int grads,
+                                                            uint64_t *out_bytes)
+{
+    if (!out_bytes || !elem_size(type) || n_vocab == 0 || n_vocab > TOKTIER_MAX_VOCAB || dim == 0 || dim > MAX_DIM || n_rows > MAX_ROWS)
+        return TOKTIER_E_INVALID_ARG;
+    *out_bytes = sizes_of(n_rows, n_vocab, dim, type, grads != 0).total;
+    return TOKTIER_OK;
+}
+
+extern "C" int toktier_linear_cross_entropy(const void *hidden, int type, uint32_t n_rows, uint32_t dim, uint64_t hidden_stride,
+                                            const void *weight, uint32_t n_vocab, uint64_t weight_stride, const uint32_t *targets, float *loss,
+                                            float *lse, const float *grad_loss, float grad_scale, void *grad_hidden,
+                                            uint64_t grad_hidden_stride, void *grad_weight, int grad_weight_type, uint64_t grad_weight_stride,
+                                            int accumulate, void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    return run(Call{hidden, weight, type, n_rows, n_vocab, dim, hidden_stride, weight_stride, targets, loss, lse, nullptr, grad_loss, grad_scale,
+                    grad_hidden, grad_hidden_stride, grad_weight, grad_weight_type, grad_weight_stride, accumulate},
+               workspace, workspace_bytes, stream);
+}
+
+extern "C" int toktier_linear_cross_entropy_backward(const void *hidden, int type, uint32_t n_rows, uint32_t dim, uint64_t hidden_stride,
+                                                     const void *weight, uint32_t n_vocab, uint64_t weight_stride, const uint32_t *targets,
+                                                     const float *lse, const float *grad_loss, float grad_scale, void *grad_hidden,
+                                                     uint64_t grad_hidden_stride, void *grad_weight, int grad_weight_type,
+                                                     uint64_t grad_weight_stride, int accumulate, void *workspace, uint64_t workspace_bytes,
+                                                     void *stream)
+{
+    if (!lse && n_rows) return TOKTIER_E_INVALID_ARG;
+    static const float nothing = 0.f;   // of no rows
+    return run(Call{hidden, weight, type, n_rows, n_vocab, dim, hidden_stride, weight_stride, targets, nullptr, nullptr, lse ? lse : &nothing,
+                    grad_loss, grad_scale, grad_hidden, grad_hidden_stride, grad_weight, grad_weight_type, grad_weight_stride, accumulate},
+               workspace, workspace_bytes, stream);
+}

@@ -1,0 +1,228 @@
+// product.h -- matrix products on the matrix cores (gfx950) with an epilogue of the caller's: the tiles of
+// linear_loss.hip.
+//
+//   out[n][m] = sum_k A(m, k) B(n, k)
+//
+// An operand is stored either along k ([row][k], "plain") or across it ([k][row], "turned").  All of them are aligned
+// to 16 bytes and padded or clamped by the caller, so that the inner loop knows no edges.
+#pragma once
+#include "ops.h"
+
+namespace tt {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+constexpr uint32_t STEP_BYTES = 128;                                        // of k in a step, per row of an operand
+template <class T> constexpr uint32_t STEP_K = STEP_BYTES / sizeof(T);      // 64 elements of 16 bits, 32 floats
+
+// A workgroup's tile: WM x WN wavefronts, each with TM x TN tiles of 16 x 16.
+template <int WM_, int WN_, int TM_, int TN_> struct Tile {
+    static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;
+    static constexpr int M = WM * TM * 16, N = WN * TN * 16, THREADS = WM * WN * 64;
+    static constexpr uint32_t LDS_A = M * STEP_BYTES, LDS_B = N * STEP_BYTES, STAGE = LDS_A + LDS_B;
+};
+
+__device__ __forceinline__ uint32_t lds_address(const lds_u8 *p) { return (uint32_t)(uintptr_t)p; }
+
+// 16 bytes per lane from base + offset to LDS, at `to` + 16 * lane.  No register is written, and the caller waits
+// (wait_loads) before a barrier; the compiler's own builtin would make every read of LDS wait for all of them.
+__device__ __forceinline__ void load_to_lds(uint32_t to, const void *base, uint32_t offset)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// The 16-byte pieces of an operand's rows in LDS change places within the row, so that the lanes of a read meet
+// different banks: plain rows (128 bytes) by their number, turned ones so that the four (16-bit) or one (float) rows that
+// a group of 16 lanes reads, and the groups beside it, lie apart.
+template <class T, bool TURNED, int WIDTH> __device__ __forceinline__ uint32_t swizzle(uint32_t row)
+{
+    if constexpr (!TURNED) return row & 7;
+    else if constexpr (sizeof(T) == 4) return ((row >> 2) & 3) << 2;
+    else if constexpr (WIDTH >= 128) return ((row & 3) | ((row >> 3) & 1) << 2) << 1;
+    else return (((row >> 1) & 1) | ((row >> 3) & 1) << 1) << 1;
+}
+
+// One operand's way into LDS.  Every thread copies 16-byte pieces at fixed offsets from a base that advances with k.
+template <class T, bool TURNED, int WIDTH, int THREADS> struct Loader {
+    static constexpr uint32_t PER_ROW = TURNED ? WIDTH * sizeof(T) / 16 : STEP_BYTES / 16;
+    static constexpr uint32_t PIECES = WIDTH * STEP_BYTES / 16;
+    static constexpr int LOADS = (PIECES + THREADS - 1) / THREADS;
+    const uint8_t *base;
+    uint64_t advance;     // bytes of a step
+    uint32_t offset[LOADS];
+    uint32_t wave;
+
+    // rows of `stride` bytes; the operand's rows (plain) or columns (turned) from `first` on, `count` in all: the last one,
+    // or the last 16 bytes, stand for those behind it, also where the whole tile lies there
+    __device__ __forceinline__ void init(const T *p, uint64_t stride, uint32_t first, uint32_t count, uint32_t k_first)
+    {
+        constexpr uint32_t LEAST = TURNED ? 16 / sizeof(T) : 1;
+        first = first < count - LEAST ? first : count - LEAST;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        if constexpr (TURNED) {
+            base = (const uint8_t *)p + (uint64_t)k_first * stride + (uint64_t)first * sizeof(T);
+            advance = STEP_K<T> * stride;
+        } else {
+            base = (const uint8_t *)p + (uint64_t)first * stride + (uint64_t)k_first * sizeof(T);
+            advance = STEP_BYTES;
+        }
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const uint32_t piece = i * THREADS + threadIdx.x, row = piece / PER_ROW;
+            const uint32_t col = (piece % PER_ROW) ^ swizzle<T, TURNED, WIDTH>(row);
+            if constexpr (TURNED) {
+                const uint32_t last = (count - first) * sizeof(T) / 16 - 1;   // pieces of a row, of a count that fills them
+                offset[i] = row * (uint32_t)stride + (col < last ? col : last) * 16;
+            } else {
+                const uint32_t last = count - first - 1;
+                offset[i] = (row < last ? row : last) * (uint32_t)stride + col * 16;
+            }
+        }
+    }
+    __device__ __forceinline__ void load(uint32_t lds)
+    {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            if (PIECES % THREADS == 0 || i * THREADS + wave * 64 < PIECES)
+                load_to_lds(lds + (i * THREADS + wave * 64) * 16, base, offset[i]);
+        base += advance;
+    }
+    // the step in which only `rows` rows of k are there (turned): the last one stands for those behind it
+    __device__ __forceinline__ void clamp(uint64_t stride, uint32_t rows)
+    {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const uint32_t row = (i * THREADS + threadIdx.x) / PER_ROW;
+            if (row >= rows) offset[i] -= (row - (rows - 1)) * (uint32_t)stride;
+        }
+    }
+};
+
+// A lane's part of a 16-row fragment, half `s` of a step: 16 bytes, of 16-bit types k = 8 (lane / 16) + 0..7 of 32, of
+// floats k = 4 (lane / 16) + 0..3 of 16.
+template <class T, bool TURNED, int WIDTH> __device__ __forceinline__ u32x4 fragment(const lds_u8 *lds, uint32_t tile, uint32_t s)
+{
+    const uint32_t lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+    if constexpr (!TURNED) {
+        const uint32_t row = tile * 16 + l;
+        return *(const __attribute__((address_space(3))) u32x4 *)(lds + row * STEP_BYTES + (((4 * s + g) ^ (l & 7)) << 4));
+    } else if constexpr (sizeof(T) == 4) {
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t k = 4 * (4 * s + g) + i, col = tile * 16 + l;
+            v[i] = *(const __attribute__((address_space(3))) uint32_t *)(lds + k * (WIDTH * 4) + (((col >> 2) ^ swizzle<T, true, WIDTH>(k)) << 4) +
+                                                                       ((col & 3) << 2));
+        }
+        return v;
+    } else {
+        // the transposing read: 16 lanes read four rows of 16 elements and each gets a column of them
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        u32x4 v;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t k = 32 * s + 8 * g + 4 * h + (l >> 2), piece = 2 * tile + ((l & 3) >> 1);
+            const lds_u8 *at = lds + k * (WIDTH * 2) + ((piece ^ swizzle<T, true, WIDTH>(k)) << 4) + ((l & 1) << 3);
+            const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at));
+            v[2 * h] = w[0];
+            v[2 * h + 1] = w[1];
+        }
+        return v;
+    }
+}
+
+template <class T> __device__ __forceinline__ void multiply(u32x4 a, u32x4 b, f32x4 &acc)
+{
+    if constexpr (sizeof(T) == 4) {
+        const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], y[i], acc, 0, 0, 0);
+    } else if constexpr (__is_same(T, __bf16)) {
+        typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), acc, 0, 0, 0);
+    } else {
+        typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), acc, 0, 0, 0);
+    }
+}
+
+// An operand as the host gives it: rows of `stride` bytes (a multiple of 16), of which `count` are there (plain) or
+// `count` columns (turned).
+struct Operand {
+    const void *p;
+    uint64_t stride;
+    uint32_t count;
+};
+
+// The product of one tile, steps [begin, end) of k; `rows` > 0: rows of k that are there (turned A only, in the last step
+// fewer than a step has).  After it all wavefronts are past their reads of LDS.
+template <class T, class TILE, bool TURN_A, bool TURN_B>
+__device__ __forceinline__ void product(f32x4 (&acc)[TILE::TM][TILE::TN], lds_u8 *lds, Operand a, Operand b, uint32_t m0, uint32_t n0,
+                                        uint32_t begin, uint32_t end, uint32_t rows)
+{
+    const uint32_t wave = threadIdx.x >> 6, wm = wave / TILE::WN, wn = wave % TILE::WN;
+#pragma unroll
+    for (int i = 0; i < TILE::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TILE::TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (begin >= end) return;
+    Loader<T, TURN_A, TILE::M, TILE::THREADS> la;
+    Loader<T, TURN_B, TILE::N, TILE::THREADS> lb;
+    la.init((const T *)a.p, a.stride, m0, a.count, begin * STEP_K<T>);
+    lb.init((const T *)b.p, b.stride, n0, b.count, begin * STEP_K<T>);
+    const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(lds));
+    auto load = [&](uint32_t step, uint32_t stage) {
+        if (TURN_A && rows && (step + 1) * STEP_K<T> > rows) la.clamp(a.stride, rows - step * STEP_K<T>);
+        la.load(at + stage * TILE::STAGE);
+        lb.load(at + stage * TILE::STAGE + TILE::LDS_A);
+    };
+    load(begin, 0);
+    for (uint32_t step = begin; step < end; ++step) {
+        const uint32_t stage = (step - begin) & 1;
+        wait_loads();
+        barrier();
+        if (step + 1 < end) load(step + 1, stage ^ 1);
+        const lds_u8 *sa = lds + stage * TILE::STAGE, *sb = sa + TILE::LDS_A;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            u32x4 fb[TILE::TN];
+#pragma unroll
+            for (int j = 0; j < TILE::TN; ++j) fb[j] = fragment<T, TURN_B, TILE::N>(sb, wn * TILE::TN + j, s);
+#pragma unroll
+            for (int i = 0; i < TILE::TM; ++i) {
+                const u32x4 fa = fragment<T, TURN_A, TILE::M>(sa, wm * TILE::TM + i, s);
+#pragma unroll
+                for (int j = 0; j < TILE::TN; ++j) multiply<T>(fa, fb[j], acc[i][j]);
+            }
+        }
+    }
+    barrier();
+}
+
+// Workgroups go round the eight XCDs, each with an L2 of its own; so that neighbours in a block of tiles share one, XCD x
+// takes the tiles from x * (all / 8) on, in bands of GROUP tiles of m that go along n.  False: no tile.
+constexpr uint32_t XCDS = 8, GROUP = 8;
+__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t m_tiles, uint32_t n_tiles, uint32_t &tm, uint32_t &tn)
+{
+    const uint32_t all = m_tiles * n_tiles, per = (all + XCDS - 1) / XCDS, x = id % XCDS, at = id / XCDS;
+    const uint32_t i = x * per + at;
+    if (at >= per || i >= all) return false;
+    const uint32_t band = i / (GROUP * n_tiles), in = i % (GROUP * n_tiles);
+    const uint32_t high = m_tiles - band * GROUP < GROUP ? m_tiles - band * GROUP : GROUP;
+    tm = band * GROUP + in % high;
+    tn = in / high;
+    return true;
+}
+inline uint32_t tile_blocks(uint32_t m_tiles, uint32_t n_tiles) { return (m_tiles * n_tiles + XCDS - 1) / XCDS * XCDS; }
+
+}  // namespace tt

@@ -371,8 +371,8 @@ int toktier_plan_free(toktier_plan *p);
 
 /*
  * Token operators: what a model does with the IDs at either end, on the same device and stream as the
- * encoder -- embedding lookup and its gradient (IDs in), next-token cross entropy and its gradient, and
- * sampling of the next ID (IDs out).
+ * encoder -- embedding lookup and its gradient (IDs in), next-token cross entropy and its gradient, from
+ * logits or straight from hidden states, and sampling of the next ID (IDs out).
  *   - They take no vocabulary handle: n_vocab is the caller's number of IDs (<= TOKTIER_MAX_VOCAB).
  *   - Matrices are row-major device memory with unit stride inside a row; `stride` counts elements from
  *     one row to the next and is at least the row's length.  Any alignment that is a multiple of the
@@ -452,6 +452,53 @@ int toktier_cross_entropy(const void *logits, int type, uint32_t n_rows, uint32_
 int toktier_cross_entropy_backward(const void *logits, int type, uint32_t n_rows, uint32_t n_vocab, uint64_t stride,
                                    const uint32_t *targets, const float *lse, const float *grad_loss,
                                    float grad_scale, void *grad_logits, uint64_t grad_stride, void *stream);
+
+/*
+ * Cross entropy straight from hidden states and the table of the logits, without keeping the logits, and in the same
+ * call its gradients.  For row i with target y = targets[i] < n_vocab, and x_j = sum_d hidden[i, d] weight[j, d]:
+ *   lse[i]  = log(sum_j exp(x_j)),   loss[i] = lse[i] - x_y
+ *   G[i, j] = c_i * (exp(x_j - lse[i]) - [j == y]),   c_i = grad_scale * (grad_loss ? grad_loss[i] : 1)
+ *   grad_hidden[i, :] = sum_j G[i, j] weight[j, :],   grad_weight[j, :] (+)= sum_i G[i, j] hidden[i, :]
+ * A row whose target is no ID takes no part: its hidden state is not used, its loss and lse are 0, its grad_hidden is
+ * zeros, and products are formed for the other rows alone.
+ * Products are summed in 32 bits; G enters the second two as numbers of `type` (for float16 times a power of two that brings
+ * the largest |c_i| to 2^14 .. 2^15; what lies below 2^-39 of it is lost), each gradient is rounded once at the end.  The
+ * order of every sum is fixed by the sizes, the types, the alignment of the table and the targets that are IDs.
+ * Values that are not finite go through the products as products do; a row with a logit that is NaN or +inf has a NaN
+ * loss, one whose logits are all -inf the loss +inf and no part in the gradients' sums beyond 0 * weight.
+ *   hidden, weight  device, n_rows and n_vocab rows of dim elements of `type`; n_rows <= TOKTIER_MAX_LINEAR_ROWS,
+ *                dim <= TOKTIER_MAX_LINEAR_DIM.  Tables whose rows start at multiples of 16 bytes and are whole
+ *                multiples of 128 bytes long (rows at most 4 MiB apart) are read where they lie; others are copied
+ *                through the workspace piece by piece.
+ *   targets      device, uint32[n_rows].
+ *   loss, lse    device, float[n_rows].
+ *   grad_loss    device, float[n_rows], or NULL.
+ *   grad_hidden  device, n_rows rows of dim elements of `type`, or NULL.
+ *   grad_weight  device, n_vocab rows of dim elements of grad_weight_type (`type`, or TOKTIER_F32), or NULL;
+ *                accumulate 0: all rows are written, 1: the sums are added to its values.
+ *   workspace    device, toktier_linear_cross_entropy_workspace_bytes(n_rows, n_vocab, dim, type, grads) bytes, where
+ *                grads is 0 for the loss alone.
+ * No output may overlap an input, another output or the workspace.
+ */
+#define TOKTIER_MAX_LINEAR_ROWS (1u << 20)
+#define TOKTIER_MAX_LINEAR_DIM (1u << 16)
+int toktier_linear_cross_entropy_workspace_bytes(uint32_t n_rows, uint32_t n_vocab, uint32_t dim, int type, int grads,
+                                                 uint64_t *out_bytes);
+int toktier_linear_cross_entropy(const void *hidden, int type, uint32_t n_rows, uint32_t dim, uint64_t hidden_stride,
+                                 const void *weight, uint32_t n_vocab, uint64_t weight_stride, const uint32_t *targets,
+                                 float *loss, float *lse, const float *grad_loss, float grad_scale, void *grad_hidden,
+                                 uint64_t grad_hidden_stride, void *grad_weight, int grad_weight_type,
+                                 uint64_t grad_weight_stride, int accumulate, void *workspace, uint64_t workspace_bytes,
+                                 void *stream);
+
+/* The gradients alone, later, from the lse that toktier_linear_cross_entropy wrote for the same arguments. */
+int toktier_linear_cross_entropy_backward(const void *hidden, int type, uint32_t n_rows, uint32_t dim,
+                                          uint64_t hidden_stride, const void *weight, uint32_t n_vocab,
+                                          uint64_t weight_stride, const uint32_t *targets, const float *lse,
+                                          const float *grad_loss, float grad_scale, void *grad_hidden,
+                                          uint64_t grad_hidden_stride, void *grad_weight, int grad_weight_type,
+                                          uint64_t grad_weight_stride, int accumulate, void *workspace,
+                                          uint64_t workspace_bytes, void *stream);
 
 /*
  * Sampling of one ID per row with temperature, top-k, top-p and min-p from given random numbers.  With
