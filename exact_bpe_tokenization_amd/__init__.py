@@ -15,6 +15,9 @@ from .binding import (TOKTIER_BF16, TOKTIER_F16, TOKTIER_F32, TOKTIER_MAX_VOCAB,
                       toktier_embed_backward, toktier_embed_backward_workspace_bytes, toktier_linear_cross_entropy,
                       toktier_linear_cross_entropy_backward, toktier_linear_cross_entropy_workspace_bytes, toktier_sample,
                       toktier_sample_workspace_bytes)
+from .binding import (TOKTIER_MAX_LINEAR_DIM, TOKTIER_MAX_LINEAR_ROWS, TOKTIER_MAX_TOP, toktier_distill,
+                      toktier_distill_backward, toktier_distill_workspace_bytes, toktier_top_logits,
+                      toktier_top_logits_workspace_bytes)
 
 __all__ = ["EXPORTS", "FAMILIES", "KERNELS", "TOKTIER_CL100K", "TOKTIER_DEEPSEEK", "TOKTIER_GPT2", "TOKTIER_IGNORE_MERGES",
            "TOKTIER_O200K",
@@ -27,4 +30,7 @@ __all__ = ["EXPORTS", "FAMILIES", "KERNELS", "TOKTIER_CL100K", "TOKTIER_DEEPSEEK
            "toktier_cross_entropy_backward", "toktier_cross_entropy_workspace_bytes", "toktier_embed",
            "toktier_embed_backward", "toktier_embed_backward_workspace_bytes", "toktier_linear_cross_entropy",
            "toktier_linear_cross_entropy_backward", "toktier_linear_cross_entropy_workspace_bytes", "toktier_sample",
-           "toktier_sample_workspace_bytes"]
+           "toktier_sample_workspace_bytes",
+           "TOKTIER_MAX_LINEAR_DIM", "TOKTIER_MAX_LINEAR_ROWS", "TOKTIER_MAX_TOP", "toktier_distill",
+           "toktier_distill_backward", "toktier_distill_workspace_bytes", "toktier_top_logits",
+           "toktier_top_logits_workspace_bytes"]

@@ -18,6 +18,7 @@ TOKTIER_GPT2, TOKTIER_CL100K, TOKTIER_O200K, TOKTIER_DEEPSEEK = 1, 2, 3, 4
 TOKTIER_IGNORE_MERGES = 1
 TOKTIER_F32, TOKTIER_F16, TOKTIER_BF16 = 1, 2, 3
 TOKTIER_MAX_VOCAB = 1 << 21
+TOKTIER_MAX_LINEAR_ROWS, TOKTIER_MAX_LINEAR_DIM, TOKTIER_MAX_TOP = 1 << 20, 1 << 16, 1024
 TYPES = {torch.float32: TOKTIER_F32, torch.float16: TOKTIER_F16, torch.bfloat16: TOKTIER_BF16}
 FAMILIES = {"gpt2": TOKTIER_GPT2, "cl100k": TOKTIER_CL100K, "o200k": TOKTIER_O200K,
             "deepseek": TOKTIER_DEEPSEEK}
@@ -37,7 +38,9 @@ EXPORTS = ("toktier_load_vocab", "toktier_load_vocab_ex", "toktier_free_vocab", 
            "toktier_cross_entropy_workspace_bytes", "toktier_cross_entropy", "toktier_cross_entropy_backward",
            "toktier_sample_workspace_bytes", "toktier_sample",
            "toktier_linear_cross_entropy_workspace_bytes", "toktier_linear_cross_entropy",
-           "toktier_linear_cross_entropy_backward")
+           "toktier_linear_cross_entropy_backward",
+           "toktier_distill_workspace_bytes", "toktier_distill", "toktier_distill_backward",
+           "toktier_top_logits_workspace_bytes", "toktier_top_logits")
 
 # kernel launches of one encode call, in stream order (TOKTIER_K_* in toktier.h)
 KERNELS = ("summary", "pieces", "tiles", "giant_seams", "bpe", "bpe_giant", "emit")
@@ -108,6 +111,11 @@ def lib():
                                                u64, i32, vp, u64, vp]
     L.toktier_linear_cross_entropy_backward.argtypes = [vp, i32, u32, u32, u64, vp, u32, u64, vp, vp, vp, f32, vp, u64, vp,
                                                         i32, u64, i32, vp, u64, vp]
+    L.toktier_distill_workspace_bytes.argtypes = [u32, u32, u32, u64p]
+    L.toktier_distill.argtypes = [vp, i32, u32, u32, u64, vp, u64, vp, u64, u32, vp, f32, vp, vp, vp, f32, vp, u64, vp, u64, vp]
+    L.toktier_distill_backward.argtypes = [vp, i32, u32, u32, u64, vp, u64, vp, u64, u32, vp, f32, vp, vp, f32, vp, u64, vp]
+    L.toktier_top_logits_workspace_bytes.argtypes = [u32, u32, u32, u64p]
+    L.toktier_top_logits.argtypes = [vp, i32, u32, u32, u64, u32, f32, vp, u64, vp, u64, vp, vp, u64, vp]
     for f in ("toktier_status_string",):
         getattr(L, f).argtypes = [i32]
         getattr(L, f).restype = ctypes.c_char_p
@@ -648,6 +656,85 @@ def toktier_linear_cross_entropy_backward(hidden, weight, targets, lse, workspac
                                                        _vector(lse, dev, what, "lse", n, _FLOAT),
                                                        _optional(grad_loss, dev, what, "grad_loss", n, _FLOAT),
                                                        float(grad_scale), *grads, int(bool(accumulate)), sp, sn, st), what)
+
+
+def _list(t, dev, what, name, n, dtypes):
+    """(pointer, entries, row stride) of a list per row."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in dtypes or t.dim() != 2 or t.size(0) != n or
+            (t.stride(1) != 1 and t.size(1) > 1)):
+        _refuse(what, f"{name} is not a tensor of {n} rows of {dtypes[0]} on the current device with unit stride in a row")
+    return t.data_ptr(), t.size(1), t.stride(0) if n > 1 else t.size(1)
+
+
+def _teacher(top_ids, top_logits, teacher_lse, temperature, dev, what, n):
+    ip, k, is_ = _list(top_ids, dev, what, "top_ids", n, _IDS)
+    tp, k2, ts = _list(top_logits, dev, what, "top_logits", n, _FLOAT)
+    if k != k2:
+        _refuse(what, f"top_ids has {k} columns, top_logits {k2}")
+    return ip, is_, tp, ts, k, _optional(teacher_lse, dev, what, "teacher_lse", n, _FLOAT), float(temperature)
+
+
+def toktier_distill_workspace_bytes(n_rows, n_vocab, top_k):
+    out = ctypes.c_uint64()
+    _check(lib().toktier_distill_workspace_bytes(int(n_rows), int(n_vocab), int(top_k), ctypes.byref(out)),
+           "toktier_distill_workspace_bytes")
+    return out.value
+
+
+def toktier_distill(logits, top_ids, top_logits, loss, lse, workspace, temperature=1.0, teacher_lse=None, grad_logits=None,
+                    grad_loss=None, grad_scale=1.0, stream=None):
+    """loss[i] = sum_k q_k (log q_k - log p[top_ids[i, k]]) with p = softmax(logits[i] / temperature) and q the teacher's
+    probabilities of the listed IDs: renormalised over the list, or exp(top_logits[i, k] / temperature - teacher_lse[i]);
+    and, where grad_logits is given (logits itself is allowed), the gradient times grad_scale * grad_loss[i] in the same
+    pass.  logits, grad_logits: [n, n_vocab]; top_ids: int32 [n, k] (-1: no entry); top_logits: float32 [n, k]; loss, lse,
+    grad_loss, teacher_lse: float32 [n]; workspace: uint8 of toktier_distill_workspace_bytes(n, n_vocab, k)."""
+    what = "toktier_distill"
+    dev, st = _here(stream)
+    xp, xt, n, n_vocab, xs = _matrix(logits, dev, what, "logits")
+    gp, gs = _grad_logits(grad_logits, logits, dev, what) if grad_logits is not None else (None, 0)
+    teacher = _teacher(top_ids, top_logits, teacher_lse, temperature, dev, what, n)
+    wp, wn = _scratch(workspace, dev, what)
+    _check(lib().toktier_distill(xp, xt, n, n_vocab, xs, *teacher, _vector(loss, dev, what, "loss", n, _FLOAT),
+                                 _vector(lse, dev, what, "lse", n, _FLOAT),
+                                 _optional(grad_loss, dev, what, "grad_loss", n, _FLOAT), float(grad_scale), gp, gs, wp, wn, st),
+           what)
+
+
+def toktier_distill_backward(logits, top_ids, top_logits, lse, grad_logits, temperature=1.0, teacher_lse=None, grad_loss=None,
+                             grad_scale=1.0, stream=None):
+    """The gradient alone, from the lse that toktier_distill wrote for the same arguments."""
+    what = "toktier_distill_backward"
+    dev, st = _here(stream)
+    xp, xt, n, n_vocab, xs = _matrix(logits, dev, what, "logits")
+    gp, gs = _grad_logits(grad_logits, logits, dev, what)
+    teacher = _teacher(top_ids, top_logits, teacher_lse, temperature, dev, what, n)
+    _check(lib().toktier_distill_backward(xp, xt, n, n_vocab, xs, *teacher, _vector(lse, dev, what, "lse", n, _FLOAT),
+                                          _optional(grad_loss, dev, what, "grad_loss", n, _FLOAT), float(grad_scale), gp, gs,
+                                          st), what)
+
+
+def toktier_top_logits_workspace_bytes(n_rows, n_vocab, k):
+    out = ctypes.c_uint64()
+    _check(lib().toktier_top_logits_workspace_bytes(int(n_rows), int(n_vocab), int(k), ctypes.byref(out)),
+           "toktier_top_logits_workspace_bytes")
+    return out.value
+
+
+def toktier_top_logits(logits, out_ids, out_logits, workspace, lse=None, temperature=1.0, stream=None):
+    """The k largest logits of each row of logits [n, n_vocab], largest first, the lower ID of equals first: their IDs into
+    out_ids (int32 [n, k], -1 where there are no more), themselves into out_logits (float32 [n, k]); and logsumexp(logits /
+    temperature) into lse (float32 [n]) where that is given.  workspace: uint8 of
+    toktier_top_logits_workspace_bytes(n, n_vocab, k)."""
+    what = "toktier_top_logits"
+    dev, st = _here(stream)
+    xp, xt, n, n_vocab, xs = _matrix(logits, dev, what, "logits")
+    ip, k, is_ = _list(out_ids, dev, what, "out_ids", n, _IDS)
+    op, k2, os_ = _list(out_logits, dev, what, "out_logits", n, _FLOAT)
+    if k != k2:
+        _refuse(what, f"out_ids has {k} columns, out_logits {k2}")
+    wp, wn = _scratch(workspace, dev, what)
+    _check(lib().toktier_top_logits(xp, xt, n, n_vocab, xs, k, float(temperature), ip, is_, op, os_,
+                                    _optional(lse, dev, what, "lse", n, _FLOAT), wp, wn, st), what)
 
 
 def toktier_sample_workspace_bytes(n_rows, n_vocab):

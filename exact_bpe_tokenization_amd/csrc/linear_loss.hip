@@ -12,27 +12,14 @@
 #include <type_traits>
 
 #include "product.h"
+#include "rows.h"
 
 namespace tt {
 namespace {
 
-constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
-constexpr float NEG_INF = -__builtin_inff();
 constexpr uint32_t NONE = 0xFFFFFFFFu;
 constexpr uint32_t PAD = 256;            // rows of the packed matrices come in this many
 constexpr uint32_t MAX_ROWS = TOKTIER_MAX_LINEAR_ROWS, MAX_DIM = TOKTIER_MAX_LINEAR_DIM;
-
-__device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * LOG2E); }
-
-struct MaxSum {
-    float m, s;
-};
-__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b)
-{
-    const float m = fmaxf(a.m, b.m);
-    if (m == NEG_INF) return MaxSum{m, a.s + b.s};
-    return MaxSum{m, a.s * exp_f(a.m - m) + b.s * exp_f(b.m - m)};
-}
 
 // What the calls leave for each other in the workspace.
 struct Head {
@@ -241,8 +228,8 @@ __global__ __launch_bounds__(1024) void k_join(const MaxSum *__restrict__ sums, 
     __syncthreads();
     if (k || n >= rows.head->count) return;
     for (uint32_t i = 1; i < 16; ++i) v = join(v, part[i][threadIdx.x]);
-    const bool none = v.m == NEG_INF && v.s == 0.f;
-    const float log_s = LN2 * __builtin_amdgcn_logf(v.s);
+    const bool none = empty(v);
+    const float log_s = log_of(v.s);
     const uint32_t r = rows.list[n];
     lse[r] = none ? NEG_INF : v.m + log_s;
     loss[r] = none ? -NEG_INF : (v.m - rows.at_target[n]) + log_s;

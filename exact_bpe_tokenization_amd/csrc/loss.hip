@@ -9,57 +9,10 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "ops.h"
+#include "rows.h"
 
 namespace tt {
 namespace {
-
-constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
-constexpr float NEG_INF = -__builtin_inff();
-
-__device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * LOG2E); }
-
-// Running maximum m and sum s of exp(x - m); an empty sum is (-inf, 0).  m is only ever -inf, finite or
-// +inf; a NaN among the logits goes into s.
-struct MaxSum {
-    float m, s;
-};
-
-__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b)
-{
-    const float m = fmaxf(a.m, b.m);
-    if (m == NEG_INF) return MaxSum{m, a.s + b.s};
-    return MaxSum{m, a.s * exp_f(a.m - m) + b.s * exp_f(b.m - m)};
-}
-
-template <int THREADS> __device__ __forceinline__ MaxSum block_join(MaxSum v, MaxSum *lds)
-{
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v = join(v, MaxSum{__shfl_xor(v.m, d), __shfl_xor(v.s, d)});
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = lds[0];
-#pragma unroll 4
-    for (int w = 1; w < THREADS / 64; ++w) v = join(v, lds[w]);
-    return v;
-}
-
-__device__ __forceinline__ void add_vec(MaxSum &a, const float (&x)[VEC])
-{
-    float m = a.m;
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) m = fmaxf(m, x[k]);
-    if (m == NEG_INF) {   // nothing but -inf so far, or NaN
-#pragma unroll
-        for (int k = 0; k < VEC; ++k)
-            if (x[k] != x[k]) a.s = x[k];
-        return;
-    }
-    float s = a.s * exp_f(a.m - m);
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) s += exp_f(x[k] - m);
-    a = MaxSum{m, s};
-}
 
 // Gradient of one vector: x becomes c (exp(x - m) * r - [j == y]).
 __device__ __forceinline__ void grad_vec(float (&x)[VEC], float m, float r, float c, uint32_t j, uint32_t y)
@@ -67,56 +20,6 @@ __device__ __forceinline__ void grad_vec(float (&x)[VEC], float m, float r, floa
 #pragma unroll
     for (int k = 0; k < VEC; ++k) x[k] = c * (exp_f(x[k] - m) * r - (j + k == y ? 1.f : 0.f));
 }
-
-// Elements [begin, end) of a row as a workgroup's vectors, the first HELD of each thread in registers, so that
-// the second pass over them reads nothing.  The others are read again: from the caches, which hold the rows
-// in work (two workgroups of 1,024 per CU) because the gradient is stored past them.
-//
-// 8,192 rows of 131,328 bfloat16 in 815 us (4.3 GB, 5.28 TB/s; a copy reaches 5.15), 4,096 of float32, of which half as
-// much is held, in 1,011 us (4.26 TB/s); bfloat16 without registers 957 us
-// with ordinary stores, 845 us with four held and streaming stores, 845 us with ten (64 VGPRs are used up at
-// eight), 924 to 944 us with all seventeen (one workgroup per CU).
-template <class T, int THREADS, int HELD> struct RowPart {
-    static constexpr uint32_t STEP = THREADS * VEC;
-    const T *x;
-    uint32_t begin, end;
-    Vec<T> held[HELD];
-
-    template <class F> __device__ __forceinline__ void with(const Vec<T> &v, uint32_t j, F f) const
-    {
-        float x8[VEC];
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) x8[k] = vec_at(v, k);
-        f(j, (uint32_t)VEC, x8);
-    }
-    // f(index, elements, values): values past the row's end are `fill`
-    template <bool FIRST, class F> __device__ __forceinline__ void each(float fill, F f)
-    {
-        const uint32_t j0 = begin + threadIdx.x * VEC;
-        if constexpr (FIRST) {
-#pragma unroll
-            for (int i = 0; i < HELD; ++i)
-                if (j0 + i * STEP + VEC <= end) held[i] = load_vec(x + j0 + i * STEP);
-        }
-#pragma unroll
-        for (int i = 0; i < HELD; ++i)
-            if (j0 + i * STEP + VEC <= end) with(held[i], j0 + i * STEP, f);
-        uint32_t j = j0 + HELD * STEP;
-        for (; j + STEP + VEC <= end; j += 2 * STEP) {
-            const Vec<T> v = load_vec(x + j), w = load_vec(x + j + STEP);
-            with(v, j, f);
-            with(w, j + STEP, f);
-        }
-        if (j + VEC <= end) with(load_vec(x + j), j, f);
-        // the thread in whose vector the row ends
-        const uint32_t tail = begin + (end - begin) / VEC * VEC;
-        if (tail < end && (tail - begin) % STEP == threadIdx.x * VEC) {
-            float x8[VEC];
-            load_part(x + tail, end - tail, fill, x8);
-            f(tail, end - tail, x8);
-        }
-    }
-};
 
 // A row's gradient, once its maximum and sum are known.
 template <class T, int THREADS, int HELD>
@@ -133,9 +36,6 @@ __device__ __forceinline__ void put_grad(RowPart<T, THREADS, HELD> &part, T *g, 
         stream_part(g + j, n, v);
     });
 }
-
-__device__ __forceinline__ bool empty(MaxSum a) { return a.m == NEG_INF && a.s == 0.f; }   // nothing but -inf
-__device__ __forceinline__ float log_of(float s) { return LN2 * __builtin_amdgcn_logf(s); }
 
 // The loss comes from m - x_y, not from the rounded lse: at logits of 10,000 that is off by half a thousandth, in a row of
 // the type's lowest value by all of the loss.
@@ -170,10 +70,6 @@ __global__ __launch_bounds__(THREADS, 8) void k_loss(const T *logits, uint32_t n
 
 // Few rows: each is split into pieces of one workgroup.  The first launch leaves the pieces' maxima and sums,
 // and the target's logit; the second joins them, in the pieces' order, and writes the gradient.
-constexpr int PIECE_THREADS = 256, PIECE_HELD = 4;
-constexpr uint32_t PIECE = PIECE_THREADS * PIECE_HELD * VEC;
-constexpr uint32_t MAX_PIECES = TOKTIER_MAX_VOCAB / PIECE;
-
 template <class T>
 __global__ __launch_bounds__(PIECE_THREADS) void k_loss_pieces(const T *logits, uint32_t n_vocab, uint64_t stride,
                                                                const uint32_t *__restrict__ targets,

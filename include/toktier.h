@@ -372,7 +372,8 @@ int toktier_plan_free(toktier_plan *p);
 /*
  * Token operators: what a model does with the IDs at either end, on the same device and stream as the
  * encoder -- embedding lookup and its gradient (IDs in), next-token cross entropy and its gradient, from
- * logits or straight from hidden states, and sampling of the next ID (IDs out).
+ * logits or straight from hidden states, distillation from a teacher's top logits and those top logits, and
+ * sampling of the next ID (IDs out).
  *   - They take no vocabulary handle: n_vocab is the caller's number of IDs (<= TOKTIER_MAX_VOCAB).
  *   - Matrices are row-major device memory with unit stride inside a row; `stride` counts elements from
  *     one row to the next and is at least the row's length.  Any alignment that is a multiple of the
@@ -499,6 +500,60 @@ int toktier_linear_cross_entropy_backward(const void *hidden, int type, uint32_t
                                           uint64_t grad_hidden_stride, void *grad_weight, int grad_weight_type,
                                           uint64_t grad_weight_stride, int accumulate, void *workspace,
                                           uint64_t workspace_bytes, void *stream);
+
+/*
+ * Distillation from a teacher's top logits, and in the same pass its gradient.  For row i, with z_j = logits[i, j] /
+ * temperature, p = softmax(z), and the entries k of its list whose ID is below n_vocab, t_k = top_logits[i, k] / temperature:
+ *   lse[i]  = log(sum_j exp(z_j))
+ *   q_k     = exp(t_k - L),  L = teacher_lse ? teacher_lse[i] : log(sum_k exp(t_k));   Q = sum_k q_k
+ *   loss[i] = sum_k q_k (log q_k - log p[id_k])
+ *   grad_logits[i, j] = c_i / temperature * (Q p_j - sum of q_k over id_k = j)
+ *   c_i = grad_scale * (grad_loss ? grad_loss[i] : 1)
+ * Without teacher_lse q is renormalised over the list (Q = 1) and the loss is the divergence of p from it; with the teacher's
+ * own log-sum-exp at the same temperature q are its probabilities, and what is not listed has no part.  (The customary factor
+ * temperature squared is the caller's: grad_scale.)  An ID may be listed twice: its entries add up.  A list without an entry,
+ * or whose logits are all -inf, gives loss 0 and a gradient of zeros.  Entries of q 0 have no part in the loss.  A row of
+ * logits of -inf alone has lse -inf, loss +inf and a gradient of zeros; a listed logit of -inf with q > 0 makes the loss +inf;
+ * a NaN or +inf among the logits makes lse, loss and gradient NaN, one among the list's logits loss and gradient.
+ *   top_ids      device, n_rows rows of top_k uint32, top_ids_stride apart; 1 <= top_k <= TOKTIER_MAX_TOP.
+ *   top_logits   device, n_rows rows of top_k float, top_logits_stride apart.
+ *   teacher_lse  device, float[n_rows], or NULL.     temperature  > 0 and finite, as is its reciprocal.
+ *   loss, lse    device, float[n_rows].              grad_loss    device, float[n_rows], or NULL.
+ *   grad_logits  device, n_rows rows of n_vocab elements of `type`, or NULL for the loss alone; may be `logits` itself with
+ *                the same stride (in place), else must not overlap it.
+ *   workspace    device, toktier_distill_workspace_bytes(n_rows, n_vocab, top_k) bytes.
+ */
+#define TOKTIER_MAX_TOP 1024u
+int toktier_distill_workspace_bytes(uint32_t n_rows, uint32_t n_vocab, uint32_t top_k, uint64_t *out_bytes);
+int toktier_distill(const void *logits, int type, uint32_t n_rows, uint32_t n_vocab, uint64_t stride,
+                    const uint32_t *top_ids, uint64_t top_ids_stride, const float *top_logits,
+                    uint64_t top_logits_stride, uint32_t top_k, const float *teacher_lse, float temperature,
+                    float *loss, float *lse, const float *grad_loss, float grad_scale, void *grad_logits,
+                    uint64_t grad_stride, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* The gradient alone, later, from the lse that toktier_distill wrote for the same arguments.  A row whose |lse| is 128 or
+ * more is summed again. */
+int toktier_distill_backward(const void *logits, int type, uint32_t n_rows, uint32_t n_vocab, uint64_t stride,
+                             const uint32_t *top_ids, uint64_t top_ids_stride, const float *top_logits,
+                             uint64_t top_logits_stride, uint32_t top_k, const float *teacher_lse, float temperature,
+                             const float *lse, const float *grad_loss, float grad_scale, void *grad_logits,
+                             uint64_t grad_stride, void *stream);
+
+/*
+ * The k largest logits of each row, by (logit descending, ID ascending), and the row's log-sum-exp: a teacher's list for
+ * toktier_distill, or the top log-probabilities of a step (out_logits / temperature - lse).  Logits of -inf or NaN are not
+ * listed; places that are left get ID 0xFFFFFFFF and -inf.  -0 counts as (and is given as) +0.
+ *   k            1 .. TOKTIER_MAX_TOP; more than n_vocab is valid.
+ *   out_ids      device, n_rows rows of k uint32, out_ids_stride apart.
+ *   out_logits   device, n_rows rows of k float, out_logits_stride apart: the logits themselves.
+ *   lse          device, float[n_rows], or NULL: log(sum_j exp(logits[i, j] / temperature)); -inf in a row of nothing else, NaN
+ *                in one with a NaN or +inf.      temperature  > 0 and finite, as is its reciprocal.
+ *   workspace    device, toktier_top_logits_workspace_bytes(n_rows, n_vocab, k) bytes.
+ */
+int toktier_top_logits_workspace_bytes(uint32_t n_rows, uint32_t n_vocab, uint32_t k, uint64_t *out_bytes);
+int toktier_top_logits(const void *logits, int type, uint32_t n_rows, uint32_t n_vocab, uint64_t stride, uint32_t k,
+                       float temperature, uint32_t *out_ids, uint64_t out_ids_stride, float *out_logits,
+                       uint64_t out_logits_stride, float *lse, void *workspace, uint64_t workspace_bytes, void *stream);
 
 /*
  * Sampling of one ID per row with temperature, top-k, top-p and min-p from given random numbers.  With
