@@ -4,9 +4,10 @@
 //   x = h W^T,  lse = log sum_v exp(x_v),  loss = lse - x_y
 //   G = c (exp(x - lse) - [v == y]),  dh = G W,  dW = G^T h
 //
-// One product gives every tile's running maximum and sum per row; then, a piece of the vocabulary at a time, the
-// product is formed again for G (in the operands' type), which goes into dh (32-bit sums over the pieces) and into
-// the piece's rows of dW.  Positions whose target is no ID are left out of all products: the hidden states of the others
+// One product gives every tile's maximum and sum of exponentials per row, and, for as many IDs as a gibibyte holds, leaves
+// the exponentials (in the operands' type), which become G once the rows' sums are known.  For the others the
+// product is formed again, a piece of the vocabulary at a time.  G goes into dh (32-bit sums over the pieces) and into
+// the pieces' rows of dW.  Positions whose target is no ID are left out of all products: the hidden states of the others
 // are copied together first, into rows that the products need not check for their ends.
 #include <algorithm>
 #include <type_traits>
@@ -135,99 +136,128 @@ __global__ __launch_bounds__(256) void k_pack_weight(const T *__restrict__ weigh
 // ---------------------------------------------------------------------------------------------
 // logits
 
-// A tile of logits, vocabulary along m, rows along n; what becomes of it: each row's maximum and sum of exponentials
-// over the tile's IDs (KEEP = false), or G (KEEP = true).
-template <class T, class TILE, bool KEEP>
+// What becomes of a tile of logits, vocabulary along m, rows along n.
+enum Use {
+    SUMS,    // each row's maximum and sum of exponentials over a wavefront's IDs
+    KEPT,    // those, and the exponentials themselves, which k_scale turns into G
+    G_AGAIN  // G
+};
+// Exponentials of 16 bits are kept rounded; float16's range holds those from 2^-24 on (2^-14 with all digits), so that it
+// keeps them times 2^15.
+template <class T> constexpr float KEPT_SCALE = __is_same(T, _Float16) ? 32768.f : 1.f;
+
+// Four neighbouring elements.
+template <class T> __device__ __forceinline__ void store4(T *to, const float (&x)[4])
+{
+    if constexpr (sizeof(T) == 4) {
+        *(f32x4 *)to = f32x4{x[0], x[1], x[2], x[3]};
+    } else {
+        u32x2 v;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            v[k] = (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k]) | (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k + 1]) << 16;
+        *(u32x2 *)to = v;
+    }
+}
+
+// first_id: the ID that the operand w and the columns of g begin with.
+template <class T, class TILE, Use USE>
 __global__ __launch_bounds__(TILE::THREADS, 2) void k_logits(Operand w, Operand h, uint32_t steps, uint32_t m_tiles, uint32_t first_id,
                                                              uint32_t n_vocab, uint32_t n_pad, Rows rows, MaxSum *__restrict__ sums,
                                                              T *__restrict__ g, uint32_t g_cols)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t shared[2 * TILE::STAGE];
-    lds_u8 *lds = (lds_u8 *)shared;
+    __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::LDS];
     const uint32_t count = rows.head->count;
     uint32_t tm, tn;
     if (!tile_of(blockIdx.x, m_tiles, (count + TILE::N - 1) / TILE::N, tm, tn)) return;
     const uint32_t m0 = tm * TILE::M, n0 = tn * TILE::N;
     f32x4 acc[TILE::TM][TILE::TN];
-    product<T, TILE, false, false>(acc, lds, w, h, m0, n0, 0, steps, 0);
+    product<T, TILE, false, false>(acc, (lds_u8 *)shared, w, h, m0, n0, 0, steps, 0);
 
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / TILE::WN, wn = wave % TILE::WN;
-    const uint32_t m_lane = m0 + wm * TILE::TM * 16 + (lane >> 4) * 4;   // of the tile's first value in this lane
+    const uint32_t m_wave = m0 + wm * TILE::TM * 16, m_lane = m_wave + (lane >> 4) * 4;   // the first in this wavefront, this lane
     const bool edge = first_id + m0 + TILE::M > n_vocab;
-    MaxSum *meet = (MaxSum *)shared;   // [WM][N]
 #pragma unroll
     for (int j = 0; j < TILE::TN; ++j) {
         const uint32_t n = n0 + (wn * TILE::TN + j) * 16 + (lane & 15);   // the packed rows reach that far
         const uint32_t y = rows.target[n] - (first_id + m_lane);          // target, from this lane's first ID
-        if constexpr (!KEEP) {
-            float m = NEG_INF;
+        if constexpr (USE != G_AGAIN) {
+            float m = NEG_INF, at = 0.f;
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < TILE::TM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (first_id + m_lane + i * 16 + e >= n_vocab) acc[i][j][e] = NEG_INF;
+            }
 #pragma unroll
             for (int i = 0; i < TILE::TM; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    if (edge && first_id + m_lane + i * 16 + e >= n_vocab) acc[i][j][e] = NEG_INF;
-                    const float x = acc[i][j][e];
-                    m = fmaxf(m, x);
-                    if (y == (uint32_t)(i * 16 + e)) rows.at_target[n] = x;
+                    m = fmaxf(m, acc[i][j][e]);
+                    at = y == (uint32_t)(i * 16 + e) ? acc[i][j][e] : at;
                 }
-            const float from = m == NEG_INF ? 0.f : m;
+            if (y < TILE::TM * 16 && (y & 15) < 4) rows.at_target[n] = at;
+            m = fmaxf(m, __shfl_xor(m, 16));
+            m = fmaxf(m, __shfl_xor(m, 32));
+            const float from = m == NEG_INF ? 0.f : m * LOG2E;
             float s = 0.f;
 #pragma unroll
-            for (int i = 0; i < TILE::TM; ++i)
+            for (int i = 0; i < TILE::TM; ++i) {
+                float x[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s += exp_f(acc[i][j][e] - from);
-            MaxSum v{m, s};
-            v = join(v, MaxSum{__shfl_xor(v.m, 16), __shfl_xor(v.s, 16)});
-            v = join(v, MaxSum{__shfl_xor(v.m, 32), __shfl_xor(v.s, 32)});
-            if (lane < 16) meet[wm * TILE::N + (n - n0)] = v;
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], LOG2E, -from));
+                    s += x[e];
+                    x[e] *= KEPT_SCALE<T>;
+                }
+                if constexpr (USE == KEPT) store4(g + (uint64_t)n * g_cols + m_lane + i * 16, x);
+            }
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
+            if (lane < 16) sums[(uint64_t)((first_id + m_wave) / (TILE::TM * 16)) * n_pad + n] = MaxSum{m, s};
         } else {
-            const float c = rows.factor[n] * rows.head->scale, shift = rows.shift[n], recip = rows.recip[n];
+            // padding, rows and IDs, is zeros whatever the products are: the other two products run over it
             const bool row = n < count;
+            const float c = rows.factor[n] * rows.head->scale, from = rows.shift[n] * LOG2E, r = rows.recip[n];
             T *to = g + (uint64_t)n * g_cols + m_lane;
 #pragma unroll
             for (int i = 0; i < TILE::TM; ++i) {
                 float x[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[e] = c * (exp_f(acc[i][j][e] - shift) * recip - (y == (uint32_t)(i * 16 + e) ? 1.f : 0.f));
-                    if (!row || (edge && first_id + m_lane + i * 16 + e >= n_vocab)) x[e] = 0.f;
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], LOG2E, -from)) * r;
+                    x[e] = c * (p - (y == (uint32_t)(i * 16 + e) ? 1.f : 0.f));
+                    x[e] = row ? x[e] : 0.f;
                 }
-                if constexpr (sizeof(T) == 4) {
-                    *(f32x4 *)(to + i * 16) = f32x4{x[0], x[1], x[2], x[3]};
-                } else {
-                    u32x2 v;
+                if (edge) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        v[k] = (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k]) | (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k + 1]) << 16;
-                    *(u32x2 *)(to + i * 16) = v;
+                    for (int e = 0; e < 4; ++e) x[e] = first_id + m_lane + i * 16 + e < n_vocab ? x[e] : 0.f;
                 }
+                store4(to + i * 16, x);
             }
-        }
-    }
-    if constexpr (!KEEP) {
-        __syncthreads();
-        for (uint32_t n = threadIdx.x; n < TILE::N; n += TILE::THREADS) {
-            MaxSum v = meet[n];
-#pragma unroll
-            for (int k = 1; k < TILE::WM; ++k) v = join(v, meet[k * TILE::N + n]);
-            sums[(uint64_t)tm * n_pad + n0 + n] = v;
         }
     }
 }
 
-// Joins the tiles' maxima and sums of 64 rows, 16 threads a row.
-__global__ __launch_bounds__(1024) void k_join(const MaxSum *__restrict__ sums, uint32_t tiles, uint32_t n_pad, Rows rows,
+// Joins the maxima and sums over the vocabulary (`parts` of them) of 16 rows, 64 threads a row.
+__global__ __launch_bounds__(1024) void k_join(const MaxSum *__restrict__ sums, uint32_t parts, uint32_t n_pad, Rows rows,
                                                float *__restrict__ loss, float *__restrict__ lse)
 {
-    __shared__ MaxSum part[16][64];
-    const uint32_t n = blockIdx.x * 64 + (threadIdx.x & 63), k = threadIdx.x >> 6;
-    if (blockIdx.x * 64 >= rows.head->count) return;
+    __shared__ MaxSum part[64][16];
+    const uint32_t l = threadIdx.x & 15, n = blockIdx.x * 16 + l, k = threadIdx.x >> 4;
+    if (blockIdx.x * 16 >= rows.head->count) return;
     MaxSum v{NEG_INF, 0.f};
-    for (uint32_t t = k; t < tiles; t += 16) v = join(v, sums[(uint64_t)t * n_pad + n]);
-    part[k][threadIdx.x & 63] = v;
+    for (uint32_t t = k; t < parts; t += 64) v = join(v, sums[(uint64_t)t * n_pad + n]);
+    part[k][l] = v;
+    __syncthreads();
+    if (k >= 8) return;
+    for (uint32_t i = 1; i < 8; ++i) v = join(v, part[k + 8 * i][l]);
+    // threads 0 .. 127: the first two wavefronts
+    part[k][l] = v;
     __syncthreads();
     if (k || n >= rows.head->count) return;
-    for (uint32_t i = 1; i < 16; ++i) v = join(v, part[i][threadIdx.x]);
+    for (uint32_t i = 1; i < 8; ++i) v = join(v, part[i][l]);
     const bool none = empty(v);
     const float log_s = log_of(v.s);
     const uint32_t r = rows.list[n];
@@ -238,24 +268,42 @@ __global__ __launch_bounds__(1024) void k_join(const MaxSum *__restrict__ sums, 
     if (none) rows.factor[n] = 0.f;
 }
 
+// Kept exponentials into G, in place: a row's `cols` columns times c exp(m - shift) recip, m the maximum that each `span`
+// of them was formed from; the target's element from its own logit, since p - 1 would show the rounding of p.  (A product
+// for them again would cost 2 dim operations an element where this moves four bytes.)
+template <class T>
+__global__ __launch_bounds__(256) void k_scale(T *__restrict__ g, uint32_t g_cols, uint32_t cols, uint32_t span, const MaxSum *__restrict__ sums,
+                                               uint32_t n_pad, Rows rows, uint32_t first_row)
+{
+    const uint32_t n = first_row + blockIdx.y, count = rows.head->count;
+    if (n >= ((count + PAD - 1) / PAD) * PAD) return;
+    const uint32_t j = (blockIdx.x * 256 + threadIdx.x) * VEC;
+    if (j >= cols) return;
+    T *at = g + (uint64_t)n * g_cols + j;
+    float x[VEC] = {};
+    if (n < count) {
+        const float c = rows.factor[n] * rows.head->scale, shift = rows.shift[n], r = rows.recip[n];
+        const float f = c * exp_f(sums[(uint64_t)(j / span) * n_pad + n].m - shift) * r * (1.f / KEPT_SCALE<T>);
+        const Vec<T> v = load_vec(at);
+        const uint32_t y = rows.target[n] - j;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] = vec_at(v, e) * f;
+        if (y < VEC) {
+            const float own = c * (exp_f(rows.at_target[n] - shift) * r - 1.f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[e] = y == (uint32_t)e ? own : x[e];
+        }
+    }
+    store_vec(at, x);
+}
+
 // ---------------------------------------------------------------------------------------------
 // gradients
 
-// Four neighbouring elements of an output row.
+// Four neighbouring elements of an output row, or the n that are there.
 template <class T> __device__ __forceinline__ void put4(T *to, const float (&x)[4], bool whole, uint32_t n)
 {
-    if (whole) {
-        if constexpr (sizeof(T) == 4) {
-            *(f32x4 *)to = f32x4{x[0], x[1], x[2], x[3]};
-        } else {
-            u32x2 v;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                v[k] = (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k]) | (uint32_t)__builtin_bit_cast(uint16_t, (T)x[2 * k + 1]) << 16;
-            *(u32x2 *)to = v;
-        }
-        return;
-    }
+    if (whole) return store4(to, x);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (k < (int)n) to[k] = (T)x[k];
@@ -269,7 +317,7 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void k_grad_hidden(Operand w, Ope
                                                                   uint32_t dim, uint32_t dim_pad, uint32_t n_pad, int add, Rows rows,
                                                                   float *__restrict__ sums, T *__restrict__ out, uint64_t stride, int whole)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t shared[2 * TILE::STAGE];
+    __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::LDS];
     const uint32_t count = rows.head->count;
     uint32_t tm, tn;
     if (!tile_of(blockIdx.x, m_tiles, (count + TILE::N - 1) / TILE::N, tm, tn)) return;
@@ -334,7 +382,7 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void k_grad_weight(Operand h, Ope
                                                                   uint32_t dim, int accumulate, Rows rows, OUT *__restrict__ out,
                                                                   uint64_t stride, int whole)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t shared[2 * TILE::STAGE];
+    __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::LDS];
     uint32_t tm, tn;
     if (!tile_of(blockIdx.x, m_tiles, n_tiles, tm, tn)) return;
     const uint32_t m0 = tm * TILE::M, n0 = tn * TILE::N;
@@ -372,9 +420,11 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void k_grad_weight(Operand h, Ope
 uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 
 // What a workspace holds.  Every part grows with rows, IDs and columns.
-//   G is kept for a piece of the vocabulary of up to PIECE_BYTES (which the last-level cache holds), of at least
-//   LEAST_IDS IDs; a table whose rows are not whole steps of aligned 16-byte pieces is copied, PIECE_BYTES at a time.
-constexpr uint64_t PIECE_BYTES = 128ull << 20;
+//   Where gradients follow in the same call, exponentials of the first IDs are kept, up to KEEP_BYTES; G of the others is
+//   formed again from the products, for a piece of the vocabulary of up to PIECE_BYTES (which the last-level cache
+//   holds), of at least LEAST_IDS IDs.  A table whose rows are not whole steps of aligned 16-byte pieces is copied,
+//   PIECE_BYTES at a time.
+constexpr uint64_t KEEP_BYTES = 1ull << 30, PIECE_BYTES = 128ull << 20;
 constexpr uint32_t LEAST_IDS = 4096;
 constexpr uint32_t MOST_SHARES = 32;
 constexpr uint64_t SHARE_FLOATS = 1ull << 23;
@@ -382,7 +432,7 @@ constexpr uint32_t MANY_TILES = 192;   // of 256 x 256, or of 128 x 128: enough 
 
 struct Sizes {
     uint32_t n_pad, dim_pad, v_pad, elem;
-    uint64_t rows, hidden, weight, sums, g, shares;   // bytes of the parts
+    uint64_t rows, hidden, weight, sums, kept, g, shares;   // bytes of the parts
     uint64_t total;
 };
 
@@ -397,14 +447,15 @@ Sizes sizes_of(uint32_t n_rows, uint32_t n_vocab, uint32_t dim, int type, bool g
     z.hidden = (uint64_t)z.n_pad * z.dim_pad * z.elem;
     const uint64_t row = (uint64_t)z.dim_pad * z.elem;
     z.weight = std::min(z.v_pad * row, std::max(PIECE_BYTES, PAD * row));
-    // per tile of 256 IDs; tiles of 64 are for fewer than MANY_TILES of those
-    z.sums = 8 * std::max((uint64_t)z.v_pad / 256 * z.n_pad, std::min((uint64_t)z.v_pad / 64 * z.n_pad, (uint64_t)4 * 256 * MANY_TILES));
+    // per wavefront of 128 IDs; those of 64 and 32 are for fewer than MANY_TILES tiles of 256 x 256
+    z.sums = 8 * std::max((uint64_t)z.v_pad / 128 * z.n_pad, std::min((uint64_t)z.v_pad / 32 * z.n_pad, (uint64_t)8 * 256 * MANY_TILES));
     if (grads) {
+        z.kept = std::min((uint64_t)z.n_pad * z.v_pad * z.elem, KEEP_BYTES);
         z.g = z.elem * std::min((uint64_t)z.n_pad * z.v_pad, std::max(PIECE_BYTES / z.elem, (uint64_t)z.n_pad * LEAST_IDS));
         const uint64_t one = (uint64_t)z.n_pad * z.dim_pad;
         z.shares = 4 * (one + std::min((MOST_SHARES - 1) * one, SHARE_FLOATS));
     }
-    for (uint64_t *p : {&z.rows, &z.hidden, &z.weight, &z.sums, &z.g, &z.shares}) z.total += *p = up(*p, 256);
+    for (uint64_t *p : {&z.rows, &z.hidden, &z.weight, &z.sums, &z.kept, &z.g, &z.shares}) z.total += *p = up(*p, 256);
     return z;
 }
 
@@ -451,7 +502,7 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
     rows.at_target = rows.recip + z.n_pad;
     T *hidden = (T *)(ws + z.rows), *packed = (T *)(ws + z.rows + z.hidden);
     MaxSum *sums = (MaxSum *)(ws + z.rows + z.hidden + z.weight);
-    T *g = (T *)((uint8_t *)sums + z.sums);
+    T *kept = (T *)((uint8_t *)sums + z.sums), *g = (T *)((uint8_t *)kept + z.kept);
     float *shares = (float *)((uint8_t *)g + z.g);
     const T *weight = (const T *)c.weight;
     const bool grads = c.grad_hidden || c.grad_weight, forward = c.loss != nullptr;
@@ -468,58 +519,86 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
     const uint32_t most_packed = (uint32_t)std::min<uint64_t>(z.v_pad, z.weight / row / PAD * PAD);
     const uint32_t steps = z.dim_pad / STEP_K<T>;
     const Operand h{hidden, row, z.n_pad};
+    bool copied = false;   // all of it, where that fits
     auto table = [&](uint32_t first, uint32_t ids) {
         const T *from = weight + first * c.weight_stride;
         if (as_is) return Operand{from, w_bytes, ids};
-        k_pack_weight<T><<<ids, 256, 0, s>>>(from, c.weight_stride, c.dim, z.dim_pad, packed);
-        return Operand{packed, row, ids};
+        if (c.n_vocab > most_packed) {
+            k_pack_weight<T><<<ids, 256, 0, s>>>(from, c.weight_stride, c.dim, z.dim_pad, packed);
+            return Operand{packed, row, ids};
+        }
+        if (!copied) k_pack_weight<T><<<c.n_vocab, 256, 0, s>>>(weight, c.weight_stride, c.dim, z.dim_pad, packed);
+        copied = true;
+        return Operand{packed + (uint64_t)first * z.dim_pad, row, ids};
     };
+
+    // What is kept: the exponentials of the first `keep` IDs (of a table that is copied in pieces, one piece's or none).
+    uint32_t keep = 0;
+    if (forward && grads) keep = (uint32_t)std::min<uint64_t>(z.v_pad, z.kept / z.elem / z.n_pad / PAD * PAD);
+    if (!as_is && c.n_vocab > most_packed) keep = keep < most_packed ? 0 : most_packed;
+    uint32_t span = 0;
 
     if (forward && c.n_rows) {
         with_tile(z.v_pad, c.n_rows, [&](auto t) {
             using TILE = decltype(t);
-            const uint32_t most = as_is ? z.v_pad : most_packed;
-            for (uint32_t first = 0; first < c.n_vocab; first += most) {
+            span = TILE::TM * 16;
+            for (uint32_t first = 0; first < c.n_vocab;) {
+                uint32_t most = as_is ? z.v_pad : most_packed;
+                if (first < keep) most = std::min(most, keep - first);
                 const uint32_t ids = std::min(most, c.n_vocab - first), m_tiles = tiles(ids, TILE::M);
                 const Operand w = table(first, ids);
-                k_logits<T, TILE, false><<<tile_blocks(m_tiles, tiles(c.n_rows, TILE::N)), TILE::THREADS, 0, s>>>(
-                    w, h, steps, m_tiles, first, c.n_vocab, z.n_pad, rows, sums + (uint64_t)first / TILE::M * z.n_pad, nullptr, 0);
+                const uint32_t blocks = tile_blocks(m_tiles, tiles(c.n_rows, TILE::N));
+                if (first < keep)
+                    k_logits<T, TILE, KEPT><<<blocks, TILE::THREADS, 0, s>>>(w, h, steps, m_tiles, first, c.n_vocab, z.n_pad, rows, sums, kept + first,
+                                                                             keep);
+                else
+                    k_logits<T, TILE, SUMS><<<blocks, TILE::THREADS, 0, s>>>(w, h, steps, m_tiles, first, c.n_vocab, z.n_pad, rows, sums, nullptr, 0);
+                first += most;
             }
-            k_join<<<z.n_pad / 64, 1024, 0, s>>>(sums, tiles(c.n_vocab, TILE::M), z.n_pad, rows, c.loss, c.lse);
+            k_join<<<z.n_pad / 16, 1024, 0, s>>>(sums, tiles(c.n_vocab, TILE::TM * 16), z.n_pad, rows, c.loss, c.lse);
         });
+        if (keep) {
+            const uint32_t cols = (uint32_t)std::min<uint64_t>(keep, up(c.n_vocab, PAD));
+            for (uint32_t first = 0; first < z.n_pad; first += 32768)
+                k_scale<T><<<dim3(tiles(cols, 256 * VEC), std::min(32768u, z.n_pad - first)), 256, 0, s>>>(kept, keep, cols, span, sums, z.n_pad, rows,
+                                                                                                          first);
+        }
     }
     if (!grads) return;
 
-    // pieces of about the same size, whose G fits
+    // pieces of about the same size, whose G fits, after what is kept
     uint32_t piece = (uint32_t)std::min<uint64_t>(z.v_pad, z.g / z.elem / z.n_pad / PAD * PAD);
     if (!as_is) piece = std::min(piece, most_packed);
-    const uint32_t pieces = tiles(z.v_pad, piece);
-    piece = (uint32_t)up(tiles(c.n_vocab, pieces), PAD);
+    const uint32_t rest = c.n_vocab > keep ? c.n_vocab - keep : 0, pieces = tiles(rest, piece);
+    if (pieces) piece = (uint32_t)up(tiles(rest, pieces), PAD);
+    const uint32_t all = pieces + (keep ? 1 : 0);
     uint32_t n_shares = 1;
-    for (uint32_t first = 0; first < c.n_vocab; first += piece) {
-        const uint32_t ids = std::min(piece, c.n_vocab - first);
+    for (uint32_t i = 0, first = 0; i < all; ++i) {
+        const bool old = i == 0 && keep;
+        const uint32_t width = old ? keep : piece, ids = std::min(width, c.n_vocab - first);
         const Operand w = c.n_rows ? table(first, ids) : Operand{};
-        if (c.n_rows) with_tile(ids, c.n_rows, [&](auto t) {
-            using TILE = decltype(t);
-            // every column of G up to the piece's width is written: the products read it in whole steps
-            const uint32_t m_tiles = tiles(up(ids, PAD), TILE::M);
-            k_logits<T, TILE, true><<<tile_blocks(m_tiles, tiles(c.n_rows, TILE::N)), TILE::THREADS, 0, s>>>(
-                w, h, steps, m_tiles, first, c.n_vocab, z.n_pad, rows, nullptr, g, piece);
-        });
-        const Operand go{g, (uint64_t)piece * z.elem, z.n_pad};
+        T *const go = old ? kept : g;
+        if (!old && c.n_rows)
+            with_tile(ids, c.n_rows, [&](auto t) {
+                using TILE = decltype(t);
+                // every column of G up to the piece's width is written: the products read it in whole steps
+                const uint32_t m_tiles = tiles(up(ids, PAD), TILE::M);
+                k_logits<T, TILE, G_AGAIN><<<tile_blocks(m_tiles, tiles(c.n_rows, TILE::N)), TILE::THREADS, 0, s>>>(
+                    w, h, steps, m_tiles, first, c.n_vocab, z.n_pad, rows, nullptr, g, piece);
+            });
         if (c.grad_hidden && c.n_rows) {
             with_tile(c.dim, c.n_rows, [&](auto t) {
                 using TILE = decltype(t);
                 const uint32_t m_tiles = tiles(c.dim, TILE::M), n_tiles = tiles(c.n_rows, TILE::N), k_steps = tiles(ids, STEP_K<T>);
-                if (first == 0) {
+                if (i == 0) {
                     const uint64_t most = z.shares / 4 / ((uint64_t)z.n_pad * z.dim_pad);
                     n_shares = std::max(1u, std::min({512 / (m_tiles * n_tiles), k_steps / 8, (uint32_t)std::min<uint64_t>(most, MOST_SHARES)}));
                 }
-                const bool direct = pieces == 1 && n_shares == 1;
+                const bool direct = all == 1 && n_shares == 1;
                 const int whole = (uintptr_t)c.grad_hidden % (4 * z.elem) == 0 && c.grad_hidden_stride % 4 == 0;
                 k_grad_hidden<T, TILE><<<dim3(tile_blocks(m_tiles, n_tiles), n_shares), TILE::THREADS, 0, s>>>(
-                    Operand{w.p, w.stride, z.dim_pad}, go, k_steps, ids, m_tiles, c.dim, z.dim_pad, z.n_pad, first != 0, rows, shares,
-                    direct ? (T *)c.grad_hidden : nullptr, c.grad_hidden_stride, whole);
+                    Operand{w.p, w.stride, z.dim_pad}, Operand{go, (uint64_t)width * z.elem, z.n_pad}, k_steps, ids, m_tiles, c.dim, z.dim_pad,
+                    z.n_pad, i != 0, rows, shares, direct ? (T *)c.grad_hidden : nullptr, c.grad_hidden_stride, whole);
             });
         }
         if (c.grad_weight) {
@@ -530,15 +609,16 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
                     const uint32_t m_tiles = tiles(c.dim, TILE::M), n_tiles = tiles(ids, TILE::N);
                     const int whole = (uintptr_t)c.grad_weight % (4 * sizeof(OUT)) == 0 && c.grad_weight_stride % 4 == 0;
                     k_grad_weight<T, TILE, OUT><<<tile_blocks(m_tiles, n_tiles), TILE::THREADS, 0, s>>>(
-                        Operand{hidden, row, z.dim_pad}, Operand{g, (uint64_t)piece * z.elem, piece}, m_tiles, n_tiles, ids, c.dim, c.accumulate,
+                        Operand{hidden, row, z.dim_pad}, Operand{go, (uint64_t)width * z.elem, width}, m_tiles, n_tiles, ids, c.dim, c.accumulate,
                         rows, (OUT *)c.grad_weight + first * c.grad_weight_stride, c.grad_weight_stride, whole);
                 });
             };
             if (c.grad_weight_type == c.type) weights(T{});
             else weights(float{});
         }
+        first += width;
     }
-    if (c.grad_hidden && c.n_rows && !(pieces == 1 && n_shares == 1))
+    if (c.grad_hidden && c.n_rows && !(all == 1 && n_shares == 1))
         k_finish_hidden<T><<<z.n_pad, 256, 0, s>>>(shares, n_shares, z.n_pad, c.dim, z.dim_pad, rows, (T *)c.grad_hidden, c.grad_hidden_stride);
 }
 

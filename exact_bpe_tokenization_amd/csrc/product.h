@@ -6,6 +6,9 @@
 // An operand is stored either along k ([row][k], "plain") or across it ([k][row], "turned").  All of them are aligned
 // to 16 bytes and padded or clamped by the caller, so that the inner loop knows no edges.
 #pragma once
+#include <type_traits>
+#include <utility>
+
 #include "ops.h"
 
 namespace tt {
@@ -21,7 +24,7 @@ template <class T> constexpr uint32_t STEP_K = STEP_BYTES / sizeof(T);      // 6
 template <int WM_, int WN_, int TM_, int TN_> struct Tile {
     static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;
     static constexpr int M = WM * TM * 16, N = WN * TN * 16, THREADS = WM * WN * 64;
-    static constexpr uint32_t LDS_A = M * STEP_BYTES, LDS_B = N * STEP_BYTES, STAGE = LDS_A + LDS_B;
+    static constexpr uint32_t LDS_A = M * STEP_BYTES, LDS_B = N * STEP_BYTES, STAGE = LDS_A + LDS_B, LDS = 2 * STAGE;
 };
 
 __device__ __forceinline__ uint32_t lds_address(const lds_u8 *p) { return (uint32_t)(uintptr_t)p; }
@@ -32,7 +35,12 @@ __device__ __forceinline__ void load_to_lds(uint32_t to, const void *base, uint3
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
 }
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// until at most N of them are in flight
+template <int N> __device__ __forceinline__ void wait_loads()
+{
+    static_assert(N < 64, "the counter's range");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void barrier()
 {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -55,7 +63,8 @@ template <class T, bool TURNED, int WIDTH> __device__ __forceinline__ uint32_t s
 template <class T, bool TURNED, int WIDTH, int THREADS> struct Loader {
     static constexpr uint32_t PER_ROW = TURNED ? WIDTH * sizeof(T) / 16 : STEP_BYTES / 16;
     static constexpr uint32_t PIECES = WIDTH * STEP_BYTES / 16;
-    static constexpr int LOADS = (PIECES + THREADS - 1) / THREADS;
+    static constexpr int LOADS = PIECES / THREADS;
+    static_assert(PIECES % THREADS == 0, "every wavefront has as many copies in flight");
     const uint8_t *base;
     uint64_t advance;     // bytes of a step
     uint32_t offset[LOADS];
@@ -88,13 +97,10 @@ template <class T, bool TURNED, int WIDTH, int THREADS> struct Loader {
             }
         }
     }
-    __device__ __forceinline__ void load(uint32_t lds)
+    // the i-th of this thread's LOADS copies of a step
+    __device__ __forceinline__ void load(uint32_t lds, int i) const
     {
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i)
-            if (PIECES % THREADS == 0 || i * THREADS + wave * 64 < PIECES)
-                load_to_lds(lds + (i * THREADS + wave * 64) * 16, base, offset[i]);
-        base += advance;
+        load_to_lds(lds + (i * THREADS + wave * 64) * 16, base, offset[i]);
     }
     // the step in which only `rows` rows of k are there (turned): the last one stands for those behind it
     __device__ __forceinline__ void clamp(uint64_t stride, uint32_t rows)
@@ -107,8 +113,8 @@ template <class T, bool TURNED, int WIDTH, int THREADS> struct Loader {
     }
 };
 
-// A lane's part of a 16-row fragment, half `s` of a step: 16 bytes, of 16-bit types k = 8 (lane / 16) + 0..7 of 32, of
-// floats k = 4 (lane / 16) + 0..3 of 16.
+// A lane's part of a 16-row fragment, half `s` of a step, 16 bytes: of 16-bit types k = 8 (lane / 16) + 0..7 of
+// 32, of floats k = 4 (lane / 16) + 0..3 of 16.
 template <class T, bool TURNED, int WIDTH> __device__ __forceinline__ u32x4 fragment(const lds_u8 *lds, uint32_t tile, uint32_t s)
 {
     const uint32_t lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
@@ -156,6 +162,13 @@ template <class T> __device__ __forceinline__ void multiply(u32x4 a, u32x4 b, f3
     }
 }
 
+// f(0), f(1) .. f(N - 1) with constants as arguments: registers can only be told apart when the code is written.
+template <class F, int... I> __device__ __forceinline__ void for_each(F f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F> __device__ __forceinline__ void unrolled(F f) { for_each(f, std::make_integer_sequence<int, N>{}); }
+
 // An operand as the host gives it: rows of `stride` bytes (a multiple of 16), of which `count` are there (plain) or
 // `count` columns (turned).
 struct Operand {
@@ -181,31 +194,74 @@ __device__ __forceinline__ void product(f32x4 (&acc)[TILE::TM][TILE::TN], lds_u8
     la.init((const T *)a.p, a.stride, m0, a.count, begin * STEP_K<T>);
     lb.init((const T *)b.p, b.stride, n0, b.count, begin * STEP_K<T>);
     const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(lds));
-    auto load = [&](uint32_t step, uint32_t stage) {
-        if (TURN_A && rows && (step + 1) * STEP_K<T> > rows) la.clamp(a.stride, rows - step * STEP_K<T>);
-        la.load(at + stage * TILE::STAGE);
-        lb.load(at + stage * TILE::STAGE + TILE::LDS_A);
+    constexpr int LOADS_A = decltype(la)::LOADS, LOADS = LOADS_A + decltype(lb)::LOADS;
+    auto load = [&](int k, uint32_t place) {   // the k-th copy of a step
+        if (k < LOADS_A) la.load(at + place, k);
+        else lb.load(at + place + TILE::LDS_A, k - LOADS_A);
     };
-    load(begin, 0);
-    for (uint32_t step = begin; step < end; ++step) {
-        const uint32_t stage = (step - begin) & 1;
-        wait_loads();
-        barrier();
-        if (step + 1 < end) load(step + 1, stage ^ 1);
-        const lds_u8 *sa = lds + stage * TILE::STAGE, *sb = sa + TILE::LDS_A;
+    auto before = [&](uint32_t step) {
+        if (TURN_A && rows && (step + 1) * STEP_K<T> > rows) la.clamp(a.stride, rows - step * STEP_K<T>);
+    };
+    auto after = [&] {
+        la.base += la.advance;
+        lb.base += lb.advance;
+    };
+    auto whole = [&](uint32_t step, uint32_t place) {
+        before(step);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            u32x4 fb[TILE::TN];
-#pragma unroll
-            for (int j = 0; j < TILE::TN; ++j) fb[j] = fragment<T, TURN_B, TILE::N>(sb, wn * TILE::TN + j, s);
-#pragma unroll
-            for (int i = 0; i < TILE::TM; ++i) {
-                const u32x4 fa = fragment<T, TURN_A, TILE::M>(sa, wm * TILE::TM + i, s);
-#pragma unroll
-                for (int j = 0; j < TILE::TN; ++j) multiply<T>(fa, fb[j], acc[i][j]);
+        for (int k = 0; k < LOADS; ++k) load(k, place);
+        after();
+    };
+    // Half a step's fragments are read while the other half's are multiplied; a step's copies are in flight for the time of
+    // one, from the barrier behind which no wavefront reads their place any more.  The matrix instructions take 16 cycles (of
+    // 16 bits) and issue 4: the others stand between them, one at a time, in the order as it is written.
+    u32x4 fa[2][TILE::TM], fb[2][TILE::TN];
+    constexpr int CELLS = TILE::TM * TILE::TN;
+    auto half = [&](auto cur, const lds_u8 *from, uint32_t s, auto between) {
+        constexpr int C = decltype(cur)::value, X = C ^ 1, READS = TILE::TM + TILE::TN;
+        unrolled<CELLS>([&](auto cell) {
+            constexpr int c = decltype(cell)::value, i = c / TILE::TN, j = c % TILE::TN;
+            multiply<T>(fa[C][i], fb[C][j], acc[i][j]);
+            constexpr int r = (c * READS + CELLS - 1) / CELLS;   // the read that has its place here, B's first
+            if constexpr (r < READS && r * CELLS / READS == c) {
+                if constexpr (r < TILE::TN) fb[X][r] = fragment<T, TURN_B, TILE::N>(from + TILE::LDS_A, wn * TILE::TN + r, s);
+                else fa[X][r - TILE::TN] = fragment<T, TURN_A, TILE::M>(from, wm * TILE::TM + r - TILE::TN, s);
             }
-        }
+            between(cell);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    static_assert(TILE::TM + TILE::TN <= CELLS && LOADS <= CELLS, "one at a time");
+    // (behind the last step the fragments are read from a place that holds another's: they are not used)
+    auto body = [&](uint32_t step, auto loads) {
+        const uint32_t place = ((step - begin) & 1) * TILE::STAGE;
+        half(std::integral_constant<int, 0>{}, lds + place, 1, [](auto) {});
+        wait_loads<0>();
+        barrier();
+        if (decltype(loads)::value) before(step + 2);
+        half(std::integral_constant<int, 1>{}, lds + (place ^ TILE::STAGE), 0, [&](auto cell) {
+            if constexpr (decltype(loads)::value) {
+                constexpr int c = decltype(cell)::value, k = c * LOADS / CELLS;
+                if constexpr (k * CELLS / LOADS + CELLS / LOADS / 2 == c) load(k, place);
+            }
+        });
+        if (decltype(loads)::value) after();
+    };
+    whole(begin, 0);
+    if (begin + 1 < end) {
+        whole(begin + 1, TILE::STAGE);
+        wait_loads<LOADS>();
+    } else {
+        wait_loads<0>();
     }
+    barrier();
+#pragma unroll
+    for (int j = 0; j < TILE::TN; ++j) fb[0][j] = fragment<T, TURN_B, TILE::N>(lds + TILE::LDS_A, wn * TILE::TN + j, 0);
+#pragma unroll
+    for (int i = 0; i < TILE::TM; ++i) fa[0][i] = fragment<T, TURN_A, TILE::M>(lds, wm * TILE::TM + i, 0);
+    uint32_t step = begin;
+    for (; step + 2 < end; ++step) body(step, std::true_type{});
+    for (; step < end; ++step) body(step, std::false_type{});
     barrier();
 }
 

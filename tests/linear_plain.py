@@ -8,7 +8,9 @@ once for float32; a sum of n products in 32 bits, in any order, is off by at mos
         size for the product with log2 e, 4 u for the power and the sum's roundings: log2 of the IDs summed pairwise
         would do, but a lane adds up to 32 of them and wavefronts and tiles join in turn: (32 + 8 + tiles) steps, each of
         which may rescale (2 u a unit of the maximum's growth, which is no more than the logits' range)
-  G     c (p - [j = y]), rounded to the type (half a step, and the type's smallest number over the scale for float16)
+  G     c (p - [j = y]), rounded to the type (half a step, and the type's smallest number over the scale for float16).  Where
+        exponentials are kept, e = exp(x - m') is rounded to the type before it is multiplied by c exp(m' - m) / s: half a
+        step of c p more (and float16's smallest number over 2^15), except at the target, which has its own logit
   dh    sum_j |dG| |w| and the sum's own error over the padded IDs; then one rounding to the type
   dW    the same over the rows, plus one addition and a rounding where it accumulates."""
 import torch
@@ -74,6 +76,9 @@ def bounds(h, weight, x, lse, kept, at, c, g, dtype, from_lse, base=None):
     hit = torch.zeros_like(g).scatter_(1, at, 1.0)
     lost = SMALLEST[dtype] * (float(c.abs().max()) * 2.0 ** -14 if dtype == torch.float16 else 1.0)
     dg = size * (p * torch.expm1(own.clamp(max=50.0)) + 2.0 ** -126) + (3 * U + HALF_STEP[dtype]) * (g.abs() + size * (p + hit) * own) + lost
+    if not from_lse:
+        kept_lost = 2.0 ** -40 if dtype == torch.float16 else SMALLEST[dtype]
+        dg = dg + size * (1 + HALF_STEP[dtype]) * ((1 - hit) * HALF_STEP[dtype] * p * (1 + own) + kept_lost)
     dg = torch.where(kept.unsqueeze(1), dg, torch.zeros_like(dg))
     ag = g.abs() + dg
     e_h = torch.mm(dg, w) + (v + 256 + 34) * 2 * U * torch.mm(ag, w)

@@ -125,7 +125,8 @@ def test_strides_and_alignments(tt, pad, lead, dtype):
     (300, 6000, 1024),        # several tiles of the middle size; dh in shares
     (1100, 9000, 576),
     (2100, 6500, 640),        # the largest tiles
-    (600, 140001, 64),        # several pieces
+    (600, 140001, 64),        # several pieces of the backward pass alone
+    (4200, 140001, 64),       # more than is kept
 ])
 def test_large_tiles_and_pieces(tt, n, v, d, dtype):
     _say("linear large", n, v, d, dtype)

@@ -67,13 +67,15 @@ def make(n, v, dtype, seed=0, size=2.5):
     return (size * torch.randn(n, v, generator=g, device="cuda")).to(dtype)
 
 
+FEW = [(1, 1), (3, 7), (5, 64), (4, 1256), (3, 2048), (3, 2049), (2, 8192), (2, 8193), (2, 33001), (1, 65535), (1, 65536), (1, 131328),
+       (2, 500001)]
+SIZES = ([(n, v, k) for n, v in FEW for k in (1, 3, 20, 64, 65, 200, 700, 1000, 1024)] +
+         [(n, 65537, k) for n in (64, 65) for k in (3, 65, 1000)])
+
+
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("n,v", [(1, 1), (3, 7), (5, 64), (4, 1256), (3, 2048), (3, 2049), (2, 8192), (2, 8193), (2, 33001), (1, 65535),
-                                 (1, 65536), (64, 65537), (65, 65537), (1, 131328), (2, 500001)])
-@pytest.mark.parametrize("k", [1, 3, 20, 64, 65, 200, 700, 1000, 1024])
+@pytest.mark.parametrize("n,v,k", SIZES)
 def test_sizes(tt, n, v, k, dtype):
-    if n > 10 and k not in (3, 65, 1000):
-        pytest.skip("many rows with three lengths of list")
     _say("top", n, v, k, dtype)
     check(tt, make(n, v, dtype), k, 1.0 + k % 2)
 
