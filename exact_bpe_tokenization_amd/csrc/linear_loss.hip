@@ -169,7 +169,7 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void k_logits(Operand w, Operand 
     __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::LDS];
     const uint32_t count = rows.head->count;
     uint32_t tm, tn;
-    if (!tile_of(blockIdx.x, m_tiles, (count + TILE::N - 1) / TILE::N, tm, tn)) return;
+    if (tile_of(blockIdx.x, m_tiles, (count + TILE::N - 1) / TILE::N, 1, tm, tn)) return;
     const uint32_t m0 = tm * TILE::M, n0 = tn * TILE::N;
     f32x4 acc[TILE::TM][TILE::TN];
     product<T, TILE, false, false>(acc, (lds_u8 *)shared, w, h, m0, n0, 0, steps, 0);
@@ -300,68 +300,64 @@ __global__ __launch_bounds__(256) void k_scale(T *__restrict__ g, uint32_t g_col
 // ---------------------------------------------------------------------------------------------
 // gradients
 
-// Four neighbouring elements of an output row, or the n that are there.
-template <class T> __device__ __forceinline__ void put4(T *to, const float (&x)[4], bool whole, uint32_t n)
-{
-    if (whole) return store4(to, x);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (k < (int)n) to[k] = (T)x[k];
-}
+// The products for dh run over all IDs, which are split where the tiles are fewer than the workgroups that run at a time.
+// How many rows take part only the device knows, so that the kernels work out the split.
+struct Split {
+    uint32_t m_tiles, n_rows_tile, blocks, most;   // tiles along m, rows of a tile, workgroups, shares at most
+    uint32_t single;                               // one piece of the vocabulary is all
+    __device__ __forceinline__ uint32_t n_tiles(uint32_t count) const { return (count + n_rows_tile - 1) / n_rows_tile; }
+    __device__ __forceinline__ uint32_t shares(uint32_t count) const
+    {
+        const uint32_t tiles = m_tiles * n_tiles(count), s = tiles ? blocks / tiles : 1;
+        return s < 1 ? 1 : s < most ? s : most;
+    }
+};
 
-// dh: columns along m, rows along n, k over the piece's IDs, of which blockIdx.y takes a share.  The sums go to `sums`
-// ([share][n_pad][dim_pad], added to where the piece is not the first), or rounded to the caller's rows if one share of one
-// piece is all.
+// dh: columns along m, rows along n, k over a share of the piece's IDs.  The sums go to `sums` ([share][n_pad][dim_pad], added
+// to where the piece is not the first), or rounded to the caller's rows if one share of one piece is all.
 template <class T, class TILE>
-__global__ __launch_bounds__(TILE::THREADS, 2) void k_grad_hidden(Operand w, Operand g, uint32_t steps, uint32_t ids, uint32_t m_tiles,
+__global__ __launch_bounds__(TILE::THREADS, 2) void k_grad_hidden(Operand w, Operand g, uint32_t steps, uint32_t ids, Split split,
                                                                   uint32_t dim, uint32_t dim_pad, uint32_t n_pad, int add, Rows rows,
-                                                                  float *__restrict__ sums, T *__restrict__ out, uint64_t stride, int whole)
+                                                                  float *__restrict__ sums, T *__restrict__ out, uint64_t stride)
 {
     __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::LDS];
-    const uint32_t count = rows.head->count;
+    const uint32_t count = rows.head->count, n_tiles = split.n_tiles(count), shares = split.shares(count);
     uint32_t tm, tn;
-    if (!tile_of(blockIdx.x, m_tiles, (count + TILE::N - 1) / TILE::N, tm, tn)) return;
-    const uint32_t m0 = tm * TILE::M, n0 = tn * TILE::N, share = (steps + gridDim.y - 1) / gridDim.y;
-    const uint32_t begin = blockIdx.y * share < steps ? blockIdx.y * share : steps, end = begin + share < steps ? begin + share : steps;
+    const uint32_t mine = tile_of(blockIdx.x, split.m_tiles, n_tiles, shares, tm, tn);
+    if (mine == NONE) return;
+    const uint32_t m0 = tm * TILE::M, n0 = tn * TILE::N, share = (steps + shares - 1) / shares;
+    const uint32_t begin = mine * share < steps ? mine * share : steps, end = begin + share < steps ? begin + share : steps;
+    if (!split.single || shares > 1) out = nullptr;
     f32x4 acc[TILE::TM][TILE::TN];
     product<T, TILE, true, false>(acc, (lds_u8 *)shared, w, g, m0, n0, begin, end, ids);
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / TILE::WN, wn = wave % TILE::WN;
-    const uint32_t m_lane = m0 + wm * TILE::TM * 16 + (lane >> 4) * 4;
-    if (!out) sums += (uint64_t)blockIdx.y * n_pad * dim_pad;
     const float unscale = rows.head->unscale;
+    sums += (uint64_t)mine * n_pad * dim_pad;
+    by_rows<TILE>(acc, (lds_u8 *)shared, [&](uint32_t n, uint32_t m, float (&x)[VEC]) {
+        n += n0;
+        m += m0;
+        if (n >= count || m >= dim) return;
+        if (out) {
 #pragma unroll
-    for (int j = 0; j < TILE::TN; ++j) {
-        const uint32_t n = n0 + (wn * TILE::TN + j) * 16 + (lane & 15);
-        if (n >= count) continue;
-        if (!out) {
-            float *to = sums + (uint64_t)n * dim_pad + m_lane;
-#pragma unroll
-            for (int i = 0; i < TILE::TM; ++i) {
-                if (m_lane + i * 16 >= dim_pad) continue;
-                f32x4 v = acc[i][j];
-                if (add) v += *(const f32x4 *)(to + i * 16);
-                *(f32x4 *)(to + i * 16) = v;
-            }
-        } else {
-            T *to = out + rows.list[n] * stride + m_lane;
-#pragma unroll
-            for (int i = 0; i < TILE::TM; ++i) {
-                const uint32_t m = m_lane + i * 16;
-                if (m >= dim) continue;
-                const float x[4] = {acc[i][j][0] * unscale, acc[i][j][1] * unscale, acc[i][j][2] * unscale, acc[i][j][3] * unscale};
-                put4(to + i * 16, x, whole && m + 4 <= dim, dim - m);
-            }
+            for (int e = 0; e < VEC; ++e) x[e] *= unscale;
+            return store_part(out + rows.list[n] * stride + m, dim - m, x);
         }
-    }
+        float *to = sums + (uint64_t)n * dim_pad + m;   // whole vectors: dim_pad is a multiple of them
+        if (add) {
+            const Vec<float> v = load_vec(to);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[e] += vec_at(v, e);
+        }
+        store_vec(to, x);
+    });
 }
 
 // The shares of dh summed, in order, and rounded.
 template <class T>
-__global__ __launch_bounds__(256) void k_finish_hidden(const float *__restrict__ sums, uint32_t shares, uint32_t n_pad, uint32_t dim,
+__global__ __launch_bounds__(256) void k_finish_hidden(const float *__restrict__ sums, Split split, uint32_t n_pad, uint32_t dim,
                                                        uint32_t dim_pad, Rows rows, T *__restrict__ out, uint64_t stride)
 {
-    const uint32_t i = blockIdx.x, r = rows.list[i];
-    if (r == NONE) return;
+    const uint32_t i = blockIdx.x, r = rows.list[i], shares = split.shares(rows.head->count);
+    if (r == NONE || (split.single && shares == 1)) return;
     const float unscale = rows.head->unscale;
     for (uint32_t j = threadIdx.x * VEC; j < dim; j += 256 * VEC) {
         float x[VEC] = {};
@@ -380,38 +376,30 @@ __global__ __launch_bounds__(256) void k_finish_hidden(const float *__restrict__
 template <class T, class TILE, class OUT>
 __global__ __launch_bounds__(TILE::THREADS, 2) void k_grad_weight(Operand h, Operand g, uint32_t m_tiles, uint32_t n_tiles, uint32_t ids,
                                                                   uint32_t dim, int accumulate, Rows rows, OUT *__restrict__ out,
-                                                                  uint64_t stride, int whole)
+                                                                  uint64_t stride)
 {
     __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::LDS];
     uint32_t tm, tn;
-    if (!tile_of(blockIdx.x, m_tiles, n_tiles, tm, tn)) return;
+    if (tile_of(blockIdx.x, m_tiles, n_tiles, 1, tm, tn)) return;
     const uint32_t m0 = tm * TILE::M, n0 = tn * TILE::N;
     f32x4 acc[TILE::TM][TILE::TN];
     product<T, TILE, true, true>(acc, (lds_u8 *)shared, h, g, m0, n0, 0, (rows.head->count + STEP_K<T> - 1) / STEP_K<T>, 0);
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / TILE::WN, wn = wave % TILE::WN;
-    const uint32_t m_lane = m0 + wm * TILE::TM * 16 + (lane >> 4) * 4;
     const float unscale = rows.head->unscale;
+    by_rows<TILE>(acc, (lds_u8 *)shared, [&](uint32_t n, uint32_t m, float (&x)[VEC]) {
+        n += n0;
+        m += m0;
+        if (n >= ids || m >= dim) return;
+        OUT *to = out + n * stride + m;
 #pragma unroll
-    for (int j = 0; j < TILE::TN; ++j) {
-        const uint32_t n = n0 + (wn * TILE::TN + j) * 16 + (lane & 15);
-        if (n >= ids) continue;
-        OUT *to = out + n * stride + m_lane;
+        for (int e = 0; e < VEC; ++e) x[e] *= unscale;
+        if (accumulate) {
+            float was[VEC];
+            load_part(to, dim - m, 0.f, was);
 #pragma unroll
-        for (int i = 0; i < TILE::TM; ++i) {
-            const uint32_t m = m_lane + i * 16;
-            if (m >= dim) continue;
-            const bool all = whole && m + 4 <= dim;
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = acc[i][j][e] * unscale;
-            if (accumulate) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (m + e < dim) x[e] += (float)to[i * 16 + e];
-            }
-            put4(to + i * 16, x, all, dim - m);
+            for (int e = 0; e < VEC; ++e) x[e] += was[e];
         }
-    }
+        store_part(to, dim - m, x);
+    });
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -427,7 +415,7 @@ uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 constexpr uint64_t KEEP_BYTES = 1ull << 30, PIECE_BYTES = 128ull << 20;
 constexpr uint32_t LEAST_IDS = 4096;
 constexpr uint32_t MOST_SHARES = 32;
-constexpr uint64_t SHARE_FLOATS = 1ull << 23;
+constexpr uint64_t SHARE_FLOATS = 1ull << 25;
 constexpr uint32_t MANY_TILES = 192;   // of 256 x 256, or of 128 x 128: enough for the CUs
 
 struct Sizes {
@@ -459,9 +447,9 @@ Sizes sizes_of(uint32_t n_rows, uint32_t n_vocab, uint32_t dim, int type, bool g
     return z;
 }
 
-typedef Tile<2, 4, 8, 4> Big;      // 256 x 256
-typedef Tile<2, 2, 4, 4> Middle;   // 128 x 128
-typedef Tile<2, 2, 2, 2> Small;    // 64 x 64
+typedef Tile<2, 4, 8, 4> Big;      // 256 x 256: one workgroup a CU
+typedef Tile<2, 2, 4, 4> Middle;   // 128 x 128: two
+typedef Tile<2, 2, 2, 2> Small;    // 64 x 64: four
 
 uint32_t tiles(uint64_t n, uint32_t of) { return (uint32_t)((n + of - 1) / of); }
 
@@ -471,6 +459,20 @@ template <class F> void with_tile(uint64_t m, uint64_t n, F f)
     if ((uint64_t)tiles(m, 256) * tiles(n, 256) >= MANY_TILES) f(Big{});
     else if ((uint64_t)tiles(m, 128) * tiles(n, 128) >= MANY_TILES) f(Middle{});
     else f(Small{});
+}
+
+// For dh, whose k is split: the largest tiles whose shares fill most of the CUs.
+template <class F> void with_split(uint32_t dim, uint32_t n_rows, uint32_t k_steps, uint64_t most, bool single, F f)
+{
+    auto of = [&](uint32_t size, uint32_t blocks) {
+        Split s{tiles(dim, size), size, blocks, (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(k_steps / 8, most)), single};
+        const uint64_t all = (uint64_t)s.m_tiles * tiles(n_rows, size), shares = std::clamp<uint64_t>(blocks / all, 1, s.most);
+        return std::pair<Split, bool>(s, all * shares * 8 >= blocks * 5);
+    };
+    const auto big = of(256, 256), middle = of(128, 512), small = of(64, 1024);
+    if (big.second) f(Big{}, big.first);
+    else if (middle.second) f(Middle{}, middle.first);
+    else f(Small{}, small.first);
 }
 
 struct Call {
@@ -572,7 +574,8 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
     const uint32_t rest = c.n_vocab > keep ? c.n_vocab - keep : 0, pieces = tiles(rest, piece);
     if (pieces) piece = (uint32_t)up(tiles(rest, pieces), PAD);
     const uint32_t all = pieces + (keep ? 1 : 0);
-    uint32_t n_shares = 1;
+    Split finish{};
+    uint32_t k_first = 0;
     for (uint32_t i = 0, first = 0; i < all; ++i) {
         const bool old = i == 0 && keep;
         const uint32_t width = old ? keep : piece, ids = std::min(width, c.n_vocab - first);
@@ -587,18 +590,16 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
                     w, h, steps, m_tiles, first, c.n_vocab, z.n_pad, rows, nullptr, g, piece);
             });
         if (c.grad_hidden && c.n_rows) {
-            with_tile(c.dim, c.n_rows, [&](auto t) {
+            const uint32_t k_steps = tiles(ids, STEP_K<T>);
+            if (i == 0) k_first = k_steps;   // the pieces' sums meet in the same places: as many shares for all
+            with_split(c.dim, c.n_rows, k_first, std::min<uint64_t>(MOST_SHARES, z.shares / 4 / ((uint64_t)z.n_pad * z.dim_pad)), all == 1,
+                       [&](auto t, Split split) {
                 using TILE = decltype(t);
-                const uint32_t m_tiles = tiles(c.dim, TILE::M), n_tiles = tiles(c.n_rows, TILE::N), k_steps = tiles(ids, STEP_K<T>);
-                if (i == 0) {
-                    const uint64_t most = z.shares / 4 / ((uint64_t)z.n_pad * z.dim_pad);
-                    n_shares = std::max(1u, std::min({512 / (m_tiles * n_tiles), k_steps / 8, (uint32_t)std::min<uint64_t>(most, MOST_SHARES)}));
-                }
-                const bool direct = all == 1 && n_shares == 1;
-                const int whole = (uintptr_t)c.grad_hidden % (4 * z.elem) == 0 && c.grad_hidden_stride % 4 == 0;
-                k_grad_hidden<T, TILE><<<dim3(tile_blocks(m_tiles, n_tiles), n_shares), TILE::THREADS, 0, s>>>(
-                    Operand{w.p, w.stride, z.dim_pad}, Operand{go, (uint64_t)width * z.elem, z.n_pad}, k_steps, ids, m_tiles, c.dim, z.dim_pad,
-                    z.n_pad, i != 0, rows, shares, direct ? (T *)c.grad_hidden : nullptr, c.grad_hidden_stride, whole);
+                finish = split;
+                const uint32_t blocks = std::max(tile_blocks(split.m_tiles, tiles(c.n_rows, TILE::N)), split.blocks);
+                k_grad_hidden<T, TILE><<<blocks, TILE::THREADS, 0, s>>>(
+                    Operand{w.p, w.stride, z.dim_pad}, Operand{go, (uint64_t)width * z.elem, z.n_pad}, k_steps, ids, split, c.dim, z.dim_pad,
+                    z.n_pad, i != 0, rows, shares, (T *)c.grad_hidden, c.grad_hidden_stride);
             });
         }
         if (c.grad_weight) {
@@ -607,10 +608,9 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
                 with_tile(c.dim, ids, [&](auto t) {
                     using TILE = decltype(t);
                     const uint32_t m_tiles = tiles(c.dim, TILE::M), n_tiles = tiles(ids, TILE::N);
-                    const int whole = (uintptr_t)c.grad_weight % (4 * sizeof(OUT)) == 0 && c.grad_weight_stride % 4 == 0;
                     k_grad_weight<T, TILE, OUT><<<tile_blocks(m_tiles, n_tiles), TILE::THREADS, 0, s>>>(
                         Operand{hidden, row, z.dim_pad}, Operand{go, (uint64_t)width * z.elem, width}, m_tiles, n_tiles, ids, c.dim, c.accumulate,
-                        rows, (OUT *)c.grad_weight + first * c.grad_weight_stride, c.grad_weight_stride, whole);
+                        rows, (OUT *)c.grad_weight + first * c.grad_weight_stride, c.grad_weight_stride);
                 });
             };
             if (c.grad_weight_type == c.type) weights(T{});
@@ -618,8 +618,8 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
         }
         first += width;
     }
-    if (c.grad_hidden && c.n_rows && !(all == 1 && n_shares == 1))
-        k_finish_hidden<T><<<z.n_pad, 256, 0, s>>>(shares, n_shares, z.n_pad, c.dim, z.dim_pad, rows, (T *)c.grad_hidden, c.grad_hidden_stride);
+    if (c.grad_hidden && c.n_rows)
+        k_finish_hidden<T><<<z.n_pad, 256, 0, s>>>(shares, finish, z.n_pad, c.dim, z.dim_pad, rows, (T *)c.grad_hidden, c.grad_hidden_stride);
 }
 
 int run(const Call &c, void *workspace, uint64_t workspace_bytes, void *stream)

@@ -265,19 +265,48 @@ __device__ __forceinline__ void product(f32x4 (&acc)[TILE::TM][TILE::TN], lds_u8
     barrier();
 }
 
-// Workgroups go round the eight XCDs, each with an L2 of its own; so that neighbours in a block of tiles share one, XCD x
-// takes the tiles from x * (all / 8) on, in bands of GROUP tiles of m that go along n.  False: no tile.
-constexpr uint32_t XCDS = 8, GROUP = 8;
-__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t m_tiles, uint32_t n_tiles, uint32_t &tm, uint32_t &tn)
+// The tile by rows of n, eight neighbours along m at a time: f(n, m, values), through LDS, 16 rows of every column of
+// wavefronts in turn.  (A lane holds four neighbours of one row, so that it would write 8 bytes in each of 16 rows, or, in
+// rows that no 8 bytes fit, element by element.)
+template <class TILE, class F> __device__ __forceinline__ void by_rows(const f32x4 (&acc)[TILE::TM][TILE::TN], lds_u8 *lds, F f)
 {
-    const uint32_t all = m_tiles * n_tiles, per = (all + XCDS - 1) / XCDS, x = id % XCDS, at = id / XCDS;
+    constexpr uint32_t STRIDE = TILE::M * 4 + 16, ROWS = TILE::WN * 16, PER_ROW = TILE::M / VEC;
+    static_assert(ROWS * STRIDE <= TILE::LDS && ROWS * PER_ROW % TILE::THREADS == 0, "a turn's rows");
+    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / TILE::WN, wn = wave % TILE::WN;
+    unrolled<TILE::TN>([&](auto turn) {
+        constexpr int j = decltype(turn)::value;
+#pragma unroll
+        for (int i = 0; i < TILE::TM; ++i)
+            *(lds_f32x4 *)(lds + (wn * 16 + (lane & 15)) * STRIDE + ((wm * TILE::TM + i) * 16 + (lane >> 4) * 4) * 4) = acc[i][j];
+        barrier();
+#pragma unroll
+        for (uint32_t k = 0; k < ROWS * PER_ROW / TILE::THREADS; ++k) {
+            const uint32_t v = k * TILE::THREADS + threadIdx.x, row = v / PER_ROW, m = v % PER_ROW * VEC;
+            const lds_u8 *from = lds + row * STRIDE + m * 4;
+            const f32x4 a = *(const lds_f32x4 *)from, b = *(const lds_f32x4 *)(from + 16);
+            float x[VEC] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+            f((row / 16 * TILE::TN + j) * 16 + row % 16, m, x);
+        }
+        barrier();
+    });
+}
+
+// Workgroups go round the eight XCDs, each with an L2 of its own; so that neighbours in a block of tiles share one, XCD x
+// takes the tiles from x * (all / 8) on, in bands of GROUP tiles of m that go along n; all tiles of a share of k (of
+// `shares`) before the next.  Returns the share, ~0 for no tile.
+constexpr uint32_t XCDS = 8, GROUP = 8;
+__device__ __forceinline__ uint32_t tile_of(uint32_t id, uint32_t m_tiles, uint32_t n_tiles, uint32_t shares, uint32_t &tm, uint32_t &tn)
+{
+    const uint32_t one = m_tiles * n_tiles, all = one * shares, per = (all + XCDS - 1) / XCDS, x = id % XCDS, at = id / XCDS;
     const uint32_t i = x * per + at;
-    if (at >= per || i >= all) return false;
-    const uint32_t band = i / (GROUP * n_tiles), in = i % (GROUP * n_tiles);
+    if (at >= per || i >= all) return ~0u;
+    const uint32_t share = i / one, tile = i % one;
+    const uint32_t band = tile / (GROUP * n_tiles), in = tile % (GROUP * n_tiles);
     const uint32_t high = m_tiles - band * GROUP < GROUP ? m_tiles - band * GROUP : GROUP;
     tm = band * GROUP + in % high;
     tn = in / high;
-    return true;
+    return share;
 }
 inline uint32_t tile_blocks(uint32_t m_tiles, uint32_t n_tiles) { return (m_tiles * n_tiles + XCDS - 1) / XCDS * XCDS; }
 
