@@ -240,24 +240,23 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void k_logits(Operand w, Operand 
     }
 }
 
-// Joins the maxima and sums over the vocabulary (`parts` of them) of 16 rows, 64 threads a row.
+// Joins the maxima and sums over the vocabulary (`parts` of them): ROWS rows a workgroup, 1024 / ROWS threads a row.
+template <uint32_t ROWS>
 __global__ __launch_bounds__(1024) void k_join(const MaxSum *__restrict__ sums, uint32_t parts, uint32_t n_pad, Rows rows,
                                                float *__restrict__ loss, float *__restrict__ lse)
 {
-    __shared__ MaxSum part[64][16];
-    const uint32_t l = threadIdx.x & 15, n = blockIdx.x * 16 + l, k = threadIdx.x >> 4;
-    if (blockIdx.x * 16 >= rows.head->count) return;
+    constexpr uint32_t PER = 1024 / ROWS;
+    __shared__ MaxSum part[16][ROWS];
+    const uint32_t l = threadIdx.x % ROWS, n = blockIdx.x * ROWS + l, k = threadIdx.x / ROWS;
+    if (blockIdx.x * ROWS >= rows.head->count) return;
     MaxSum v{NEG_INF, 0.f};
-    for (uint32_t t = k; t < parts; t += 64) v = join(v, sums[(uint64_t)t * n_pad + n]);
-    part[k][l] = v;
+    for (uint32_t t = k; t < parts; t += PER) v = join(v, sums[(uint64_t)t * n_pad + n]);
+#pragma unroll
+    for (uint32_t d = ROWS; d < 64; d *= 2) v = join(v, MaxSum{__shfl_xor(v.m, d), __shfl_xor(v.s, d)});
+    if ((threadIdx.x & 63) < ROWS) part[threadIdx.x >> 6][l] = v;
     __syncthreads();
-    if (k >= 8) return;
-    for (uint32_t i = 1; i < 8; ++i) v = join(v, part[k + 8 * i][l]);
-    // threads 0 .. 127: the first two wavefronts
-    part[k][l] = v;
-    __syncthreads();
-    if (k || n >= rows.head->count) return;
-    for (uint32_t i = 1; i < 8; ++i) v = join(v, part[i][l]);
+    if (threadIdx.x >= ROWS || n >= rows.head->count) return;
+    for (uint32_t i = 1; i < 16; ++i) v = join(v, part[i][l]);
     const bool none = empty(v);
     const float log_s = log_of(v.s);
     const uint32_t r = rows.list[n];
@@ -436,7 +435,9 @@ Sizes sizes_of(uint32_t n_rows, uint32_t n_vocab, uint32_t dim, int type, bool g
     const uint64_t row = (uint64_t)z.dim_pad * z.elem;
     z.weight = std::min(z.v_pad * row, std::max(PIECE_BYTES, PAD * row));
     // per wavefront of 128 IDs; those of 64 and 32 are for fewer than MANY_TILES tiles of 256 x 256
-    z.sums = 8 * std::max((uint64_t)z.v_pad / 128 * z.n_pad, std::min((uint64_t)z.v_pad / 32 * z.n_pad, (uint64_t)8 * 256 * MANY_TILES));
+    // or no more than PAD rows
+    z.sums = 8 * std::max({(uint64_t)z.v_pad / 128 * z.n_pad, std::min((uint64_t)z.v_pad / 32 * z.n_pad, (uint64_t)8 * 256 * MANY_TILES),
+                           (uint64_t)z.v_pad / 32 * PAD});
     if (grads) {
         z.kept = std::min((uint64_t)z.n_pad * z.v_pad * z.elem, KEEP_BYTES);
         z.g = z.elem * std::min((uint64_t)z.n_pad * z.v_pad, std::max(PIECE_BYTES / z.elem, (uint64_t)z.n_pad * LEAST_IDS));
@@ -459,6 +460,19 @@ template <class F> void with_tile(uint64_t m, uint64_t n, F f)
     if ((uint64_t)tiles(m, 256) * tiles(n, 256) >= MANY_TILES) f(Big{});
     else if ((uint64_t)tiles(m, 128) * tiles(n, 128) >= MANY_TILES) f(Middle{});
     else f(Small{});
+}
+
+typedef Tile<4, 1, 2, 2> Thin;     // 128 x 32: four
+typedef Tile<4, 1, 2, 4> Thicker;  // 128 x 64: three
+
+// For the logits; of few rows, where the table's way through the CUs is what counts: tiles that are no wider, of which
+// several run on a CU.
+template <class F> void with_logits_tile(uint64_t m, uint64_t n, F f)
+{
+    if (n <= 32) f(Thin{});
+    else if (n <= 64) f(Thicker{});
+    else if (n <= 128) f(Middle{});
+    else with_tile(m, n, f);
 }
 
 // For dh, whose k is split: the largest tiles whose shares fill most of the CUs.
@@ -541,7 +555,7 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
     uint32_t span = 0;
 
     if (forward && c.n_rows) {
-        with_tile(z.v_pad, c.n_rows, [&](auto t) {
+        with_logits_tile(z.v_pad, c.n_rows, [&](auto t) {
             using TILE = decltype(t);
             span = TILE::TM * 16;
             for (uint32_t first = 0; first < c.n_vocab;) {
@@ -557,7 +571,9 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
                     k_logits<T, TILE, SUMS><<<blocks, TILE::THREADS, 0, s>>>(w, h, steps, m_tiles, first, c.n_vocab, z.n_pad, rows, sums, nullptr, 0);
                 first += most;
             }
-            k_join<<<z.n_pad / 16, 1024, 0, s>>>(sums, tiles(c.n_vocab, TILE::TM * 16), z.n_pad, rows, c.loss, c.lse);
+            const uint32_t parts = tiles(c.n_vocab, TILE::TM * 16);
+            if (c.n_rows <= PAD) k_join<1><<<c.n_rows, 1024, 0, s>>>(sums, parts, z.n_pad, rows, c.loss, c.lse);
+            else k_join<16><<<z.n_pad / 16, 1024, 0, s>>>(sums, parts, z.n_pad, rows, c.loss, c.lse);
         });
         if (keep) {
             const uint32_t cols = (uint32_t)std::min<uint64_t>(keep, up(c.n_vocab, PAD));
@@ -582,9 +598,9 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
         const Operand w = c.n_rows ? table(first, ids) : Operand{};
         T *const go = old ? kept : g;
         if (!old && c.n_rows)
-            with_tile(ids, c.n_rows, [&](auto t) {
+            with_logits_tile(ids, std::max<uint32_t>(c.n_rows, STEP_K<T>), [&](auto t) {
                 using TILE = decltype(t);
-                // every column of G up to the piece's width is written: the products read it in whole steps
+                // every row of G up to a whole step, every column up to the piece's width is written: the products read it in steps
                 const uint32_t m_tiles = tiles(up(ids, PAD), TILE::M);
                 k_logits<T, TILE, G_AGAIN><<<tile_blocks(m_tiles, tiles(c.n_rows, TILE::N)), TILE::THREADS, 0, s>>>(
                     w, h, steps, m_tiles, first, c.n_vocab, z.n_pad, rows, nullptr, g, piece);

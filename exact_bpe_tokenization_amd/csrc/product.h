@@ -222,16 +222,16 @@ __device__ __forceinline__ void product(f32x4 (&acc)[TILE::TM][TILE::TN], lds_u8
         unrolled<CELLS>([&](auto cell) {
             constexpr int c = decltype(cell)::value, i = c / TILE::TN, j = c % TILE::TN;
             multiply<T>(fa[C][i], fb[C][j], acc[i][j]);
-            constexpr int r = (c * READS + CELLS - 1) / CELLS;   // the read that has its place here, B's first
-            if constexpr (r < READS && r * CELLS / READS == c) {
-                if constexpr (r < TILE::TN) fb[X][r] = fragment<T, TURN_B, TILE::N>(from + TILE::LDS_A, wn * TILE::TN + r, s);
+            unrolled<READS>([&](auto read) {   // those that have their place here, B's first
+                constexpr int r = decltype(read)::value;
+                if constexpr (r * CELLS / READS != c) return;
+                else if constexpr (r < TILE::TN) fb[X][r] = fragment<T, TURN_B, TILE::N>(from + TILE::LDS_A, wn * TILE::TN + r, s);
                 else fa[X][r - TILE::TN] = fragment<T, TURN_A, TILE::M>(from, wm * TILE::TM + r - TILE::TN, s);
-            }
+            });
             between(cell);
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-    static_assert(TILE::TM + TILE::TN <= CELLS && LOADS <= CELLS, "one at a time");
     // (behind the last step the fragments are read from a place that holds another's: they are not used)
     auto body = [&](uint32_t step, auto loads) {
         const uint32_t place = ((step - begin) & 1) * TILE::STAGE;
@@ -240,10 +240,11 @@ __device__ __forceinline__ void product(f32x4 (&acc)[TILE::TM][TILE::TN], lds_u8
         barrier();
         if (decltype(loads)::value) before(step + 2);
         half(std::integral_constant<int, 1>{}, lds + (place ^ TILE::STAGE), 0, [&](auto cell) {
-            if constexpr (decltype(loads)::value) {
-                constexpr int c = decltype(cell)::value, k = c * LOADS / CELLS;
-                if constexpr (k * CELLS / LOADS + CELLS / LOADS / 2 == c) load(k, place);
-            }
+            if constexpr (decltype(loads)::value)
+                unrolled<LOADS>([&](auto copy) {
+                    constexpr int k = decltype(copy)::value;
+                    if constexpr ((2 * k + 1) * CELLS / (2 * LOADS) == decltype(cell)::value) load(k, place);
+                });
         });
         if (decltype(loads)::value) after();
     };
@@ -295,7 +296,7 @@ template <class TILE, class F> __device__ __forceinline__ void by_rows(const f32
 // Workgroups go round the eight XCDs, each with an L2 of its own; so that neighbours in a block of tiles share one, XCD x
 // takes the tiles from x * (all / 8) on, in bands of GROUP tiles of m that go along n; all tiles of a share of k (of
 // `shares`) before the next.  Returns the share, ~0 for no tile.
-constexpr uint32_t XCDS = 8, GROUP = 8;
+constexpr uint32_t XCDS = 8, GROUP = 6;
 __device__ __forceinline__ uint32_t tile_of(uint32_t id, uint32_t m_tiles, uint32_t n_tiles, uint32_t shares, uint32_t &tm, uint32_t &tn)
 {
     const uint32_t one = m_tiles * n_tiles, all = one * shares, per = (all + XCDS - 1) / XCDS, x = id % XCDS, at = id / XCDS;
