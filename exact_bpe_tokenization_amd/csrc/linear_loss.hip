@@ -41,96 +41,128 @@ struct Rows {             // of the packed rows
 // ---------------------------------------------------------------------------------------------
 // rows
 
-// Numbers the rows that take part, in order, and clears what the others get.  float16's range does not hold c times a
-// small probability: G is kept times the power of two that brings the largest |c| to 2^14..2^15, so that probabilities
-// down to 2^-28 (2^-39 with fewer digits) keep their digits.
-__global__ __launch_bounds__(1024) void k_rows(const uint32_t *__restrict__ targets, uint32_t n_rows, uint32_t n_pad, uint32_t n_vocab,
-                                               const float *__restrict__ lse_in, const float *__restrict__ grad_loss, float grad_scale,
-                                               int scaled, float *loss, float *lse_out, Rows rows)
-{
-    __shared__ uint32_t part[16];
-    __shared__ uint32_t largest;
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    if (threadIdx.x == 0) largest = 0;
-    uint32_t most = 0, count = 0;
-    for (uint32_t r0 = 0; r0 < n_rows; r0 += 1024) {
-        const uint32_t r = r0 + threadIdx.x;
-        const uint32_t y = r < n_rows ? targets[r] : NONE;
-        const bool in = r < n_rows && y < n_vocab;
-        const uint64_t mask = __ballot(in);
-        __syncthreads();
-        if (lane == 0) part[wave] = __popcll(mask);
-        __syncthreads();
-        uint32_t at = count;
-        for (uint32_t w = 0; w < 16; ++w) {
-            at += w < wave ? part[w] : 0;
-            count += part[w];
-        }
-        at += __popcll(mask & ((1ull << lane) - 1));
-        if (in) {
-            float c = grad_scale * (grad_loss ? grad_loss[r] : 1.f), shift = 0.f, recip = 1.f;
-            if (lse_in) {
-                shift = lse_in[r];
-                if (shift == NEG_INF) c = shift = 0.f;   // nothing but -inf: no gradient
-            }
-            rows.list[at] = r;
-            rows.target[at] = y;
-            rows.factor[at] = c;
-            rows.shift[at] = shift;
-            rows.recip[at] = recip;
-            const uint32_t size = __builtin_bit_cast(uint32_t, c) & 0x7FFFFFFFu;
-            if (size < 0x7F800000u && size > most) most = size;
-        } else if (r < n_rows && loss) {
-            loss[r] = 0.f;
-            lse_out[r] = 0.f;
-        }
-    }
-    for (uint32_t i = count + threadIdx.x; i < n_pad; i += 1024) {
-        rows.list[i] = NONE;
-        rows.target[i] = NONE;
-        rows.factor[i] = rows.shift[i] = rows.recip[i] = 0.f;
-    }
-    __syncthreads();
-    atomicMax(&largest, most);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        float scale = 1.f;
-        const int e = (int)(largest >> 23) - 127;   // the largest |c| is 2^e .. 2^(e + 1); subnormal ones count as 2^-127
-        if (scaled && largest) scale = __builtin_amdgcn_ldexpf(1.f, 14 - e > 126 ? 126 : 14 - e);
-        rows.head->count = count;
-        rows.head->scale = scale;
-        rows.head->unscale = 1.f / scale;
-    }
-}
-
-// Copies a row of n elements to one of n_pad, zeros behind it (or throughout).
+// A row of n elements to one of n_pad, zeros behind it (or throughout), by the lanes of a wavefront.
 template <class T> __device__ __forceinline__ void copy_row(T *to, const T *from, uint32_t n, uint32_t n_pad)
 {
-    for (uint32_t j = threadIdx.x * VEC; j < n_pad; j += blockDim.x * VEC) {
+    for (uint32_t j = (threadIdx.x & 63) * VEC; j < n_pad; j += 64 * VEC) {
         float x[VEC] = {};
         if (from && j < n) load_part(from + j, n - j, 0.f, x);
         store_vec(to + j, x);
     }
 }
 
-// The packed hidden states, and zeros as the gradient of the rows that take no part.
-template <class T>
-__global__ __launch_bounds__(256) void k_pack_hidden(const T *__restrict__ hidden, uint64_t stride, uint32_t dim, uint32_t dim_pad,
-                                                     uint32_t n_rows, uint32_t n_vocab, const uint32_t *__restrict__ targets, Rows rows,
-                                                     T *__restrict__ packed, T *__restrict__ grad, uint64_t grad_stride)
+__device__ __forceinline__ float factor_of(const float *grad_loss, float grad_scale, uint32_t r)
 {
-    const uint32_t i = blockIdx.x, r = rows.list[i];
-    copy_row(packed + (uint64_t)i * dim_pad, r == NONE ? (const T *)nullptr : hidden + r * stride, dim, dim_pad);
-    if (grad && i < n_rows && targets[i] >= n_vocab) {
-        const float zero[VEC] = {};
-        for (uint32_t j = threadIdx.x * VEC; j < dim; j += 256 * VEC) store_part(grad + i * grad_stride + j, dim - j, zero);
+    return grad_scale * (grad_loss ? grad_loss[r] : 1.f);
+}
+
+// Numbers the rows that take part, in order, copies their hidden states together, and clears what the others
+// get.  Every workgroup counts through all targets, which saves a launch.
+//
+// float16's range does not hold c times a small probability: G is kept times the power of two that brings the largest |c| to
+// 2^14..2^15, so that probabilities down to 2^-28 (2^-39 with fewer digits) keep their digits.
+template <class T>
+__global__ __launch_bounds__(256) void k_gather(const T *__restrict__ hidden, uint64_t stride, uint32_t dim, uint32_t dim_pad,
+                                                const uint32_t *__restrict__ targets, uint32_t n_rows, uint32_t per, uint32_t n_vocab,
+                                                const float *__restrict__ lse_in, const float *__restrict__ grad_loss, float grad_scale,
+                                                float *loss, float *lse_out, Rows rows, T *__restrict__ packed, T *__restrict__ grad,
+                                                uint64_t grad_stride)
+{
+    constexpr bool SCALED = __is_same(T, _Float16);
+    __shared__ uint32_t part[4], befores[4], larges[4], place[256];
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, first = blockIdx.x * per, last = first + per < n_rows ? first + per : n_rows;
+    uint32_t total = 0, before = 0, large = 0;
+#pragma unroll 8
+    for (uint32_t r = threadIdx.x; r < n_rows; r += 256) {
+        const bool in = targets[r] < n_vocab;
+        total += in;
+        before += in && r < first;
+        if constexpr (SCALED) {
+            if (in) {
+                const uint32_t size = __builtin_bit_cast(uint32_t, factor_of(grad_loss, grad_scale, r)) & 0x7FFFFFFFu;
+                if (size < 0x7F800000u && size > large) large = size;
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        total += __shfl_xor(total, d);
+        before += __shfl_xor(before, d);
+        const uint32_t o = __shfl_xor(large, d);
+        large = o > large ? o : large;
+    }
+    if (lane == 0) {
+        part[wave] = total;
+        befores[wave] = before;
+        larges[wave] = large;
+    }
+    __syncthreads();
+    total = part[0] + part[1] + part[2] + part[3];
+    uint32_t at = befores[0] + befores[1] + befores[2] + befores[3];
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        for (int w = 0; w < 4; ++w) large = larges[w] > large ? larges[w] : large;
+        const int e = (int)(large >> 23) - 127;   // the largest |c| is 2^e .. 2^(e + 1); subnormal ones count as 2^-127
+        const float scale = large ? __builtin_amdgcn_ldexpf(1.f, 14 - e > 126 ? 126 : 14 - e) : 1.f;
+        rows.head->count = total;
+        rows.head->scale = scale;
+        rows.head->unscale = 1.f / scale;
+    }
+    for (uint32_t r0 = first; r0 < last; r0 += 256) {
+        const uint32_t r = r0 + threadIdx.x, y = r < last ? targets[r] : NONE;
+        const bool in = r < last && y < n_vocab;
+        const uint64_t mask = __ballot(in);
+        __syncthreads();
+        if (lane == 0) part[wave] = __popcll(mask);
+        __syncthreads();
+        uint32_t mine = at + __popcll(mask & ((1ull << lane) - 1));
+        for (uint32_t w = 0; w < 4; ++w) {
+            mine += w < wave ? part[w] : 0;
+            at += part[w];
+        }
+        if (in) {
+            float c = factor_of(grad_loss, grad_scale, r), shift = 0.f;
+            if (lse_in) {
+                shift = lse_in[r];
+                if (shift == NEG_INF) c = shift = 0.f;   // nothing but -inf: no gradient
+            }
+            rows.list[mine] = r;
+            rows.target[mine] = y;
+            rows.factor[mine] = c;
+            rows.shift[mine] = shift;
+            rows.recip[mine] = 1.f;
+        } else if (r < last && loss) {
+            loss[r] = 0.f;
+            lse_out[r] = 0.f;
+        }
+        place[threadIdx.x] = in ? mine : NONE;
+        __syncthreads();
+        for (uint32_t k = wave; k < 256 && r0 + k < last; k += 4) {
+            const uint32_t to = place[k];
+            if (to != NONE) {
+                copy_row(packed + (uint64_t)to * dim_pad, hidden + (uint64_t)(r0 + k) * stride, dim, dim_pad);
+            } else if (grad) {
+                const float zero[VEC] = {};
+                for (uint32_t j = lane * VEC; j < dim; j += 64 * VEC) store_part(grad + (uint64_t)(r0 + k) * grad_stride + j, dim - j, zero);
+            }
+        }
+    }
+    // up to the end of the last tile; what the product for dW reads in its last step as zeros
+    const uint32_t end = (total + PAD - 1) / PAD * PAD, zeros = (total + STEP_K<T> - 1) / STEP_K<T> * STEP_K<T>;
+    for (uint32_t i = total + blockIdx.x * 4 + wave; i < end; i += gridDim.x * 4) {
+        if (i < zeros) copy_row(packed + (uint64_t)i * dim_pad, (const T *)nullptr, dim, dim_pad);
+        if (lane == 0) {
+            rows.list[i] = rows.target[i] = NONE;
+            rows.factor[i] = rows.shift[i] = rows.recip[i] = 0.f;
+        }
     }
 }
 
 template <class T>
-__global__ __launch_bounds__(256) void k_pack_weight(const T *__restrict__ weight, uint64_t stride, uint32_t dim, uint32_t dim_pad, T *__restrict__ packed)
+__global__ __launch_bounds__(256) void k_pack_weight(const T *__restrict__ weight, uint64_t stride, uint32_t ids, uint32_t dim, uint32_t dim_pad,
+                                                     T *__restrict__ packed)
 {
-    copy_row(packed + (uint64_t)blockIdx.x * dim_pad, weight + blockIdx.x * stride, dim, dim_pad);
+    const uint64_t v = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (v < ids) copy_row(packed + v * dim_pad, weight + v * stride, dim, dim_pad);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -167,9 +199,10 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void k_logits(Operand w, Operand 
                                                              T *__restrict__ g, uint32_t g_cols)
 {
     __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::LDS];
-    const uint32_t count = rows.head->count;
+    // (of G every row up to a whole step of k is written: the product for dW reads it so)
+    const uint32_t count = rows.head->count, reach = USE == G_AGAIN ? (count + STEP_K<T> - 1) / STEP_K<T> * STEP_K<T> : count;
     uint32_t tm, tn;
-    if (tile_of(blockIdx.x, m_tiles, (count + TILE::N - 1) / TILE::N, 1, tm, tn)) return;
+    if (tile_of(blockIdx.x, m_tiles, (reach + TILE::N - 1) / TILE::N, 1, tm, tn)) return;
     const uint32_t m0 = tm * TILE::M, n0 = tn * TILE::N;
     f32x4 acc[TILE::TM][TILE::TN];
     product<T, TILE, false, false>(acc, (lds_u8 *)shared, w, h, m0, n0, 0, steps, 0);
@@ -240,23 +273,35 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void k_logits(Operand w, Operand 
     }
 }
 
-// Joins the maxima and sums over the vocabulary (`parts` of them): ROWS rows a workgroup, 1024 / ROWS threads a row.
-template <uint32_t ROWS>
-__global__ __launch_bounds__(1024) void k_join(const MaxSum *__restrict__ sums, uint32_t parts, uint32_t n_pad, Rows rows,
-                                               float *__restrict__ loss, float *__restrict__ lse)
-{
-    constexpr uint32_t PER = 1024 / ROWS;
-    __shared__ MaxSum part[16][ROWS];
-    const uint32_t l = threadIdx.x % ROWS, n = blockIdx.x * ROWS + l, k = threadIdx.x / ROWS;
-    if (blockIdx.x * ROWS >= rows.head->count) return;
-    MaxSum v{NEG_INF, 0.f};
-    for (uint32_t t = k; t < parts; t += PER) v = join(v, sums[(uint64_t)t * n_pad + n]);
+// Eight kept exponentials of row n into G, in place: times c exp(m - shift) recip, m the maximum that each `span` of them was
+// formed from; the target's element from its own logit, since p - 1 would show the rounding of p.  Rows and columns behind
+// the last become zeros.  (A product for them again would cost 2 dim operations an element where this moves four bytes.)
+struct Scaling {
+    uint32_t n, count, span, n_pad, n_vocab, target;
+    float c, shift, recip, at_target;
+    const MaxSum *sums;
+    template <class T> __device__ __forceinline__ void apply(T *g, uint32_t j) const
+    {
+        float x[VEC] = {};
+        if (n < count) {
+            const float f = c * exp_f(sums[(uint64_t)(j / span) * n_pad + n].m - shift) * recip * (1.f / KEPT_SCALE<T>);
+            const Vec<T> v = load_vec(g + j);
+            const uint32_t y = target - j;
 #pragma unroll
-    for (uint32_t d = ROWS; d < 64; d *= 2) v = join(v, MaxSum{__shfl_xor(v.m, d), __shfl_xor(v.s, d)});
-    if ((threadIdx.x & 63) < ROWS) part[threadIdx.x >> 6][l] = v;
-    __syncthreads();
-    if (threadIdx.x >= ROWS || n >= rows.head->count) return;
-    for (uint32_t i = 1; i < 16; ++i) v = join(v, part[i][l]);
+            for (int e = 0; e < VEC; ++e) x[e] = j + e < n_vocab ? vec_at(v, e) * f : 0.f;
+            if (y < VEC) {
+                const float own = c * (exp_f(at_target - shift) * recip - 1.f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) x[e] = y == (uint32_t)e ? own : x[e];
+            }
+        }
+        store_vec(g + j, x);
+    }
+};
+
+// A row's loss and log-sum-exp from its maximum and sum, and what G is formed with.
+__device__ __forceinline__ void put_row(MaxSum v, uint32_t n, const Rows &rows, float *loss, float *lse)
+{
     const bool none = empty(v);
     const float log_s = log_of(v.s);
     const uint32_t r = rows.list[n];
@@ -267,33 +312,53 @@ __global__ __launch_bounds__(1024) void k_join(const MaxSum *__restrict__ sums, 
     if (none) rows.factor[n] = 0.f;
 }
 
-// Kept exponentials into G, in place: a row's `cols` columns times c exp(m - shift) recip, m the maximum that each `span`
-// of them was formed from; the target's element from its own logit, since p - 1 would show the rounding of p.  (A product
-// for them again would cost 2 dim operations an element where this moves four bytes.)
+// Joins the maxima and sums over the vocabulary (`parts` of them): 16 rows a workgroup, 64 threads a row.
+__global__ __launch_bounds__(1024) void k_join(const MaxSum *__restrict__ sums, uint32_t parts, uint32_t n_pad, Rows rows,
+                                               float *__restrict__ loss, float *__restrict__ lse)
+{
+    __shared__ MaxSum part[16][16];
+    const uint32_t l = threadIdx.x & 15, n = blockIdx.x * 16 + l;
+    if (blockIdx.x * 16 >= rows.head->count) return;
+    MaxSum v{NEG_INF, 0.f};
+    for (uint32_t t = threadIdx.x >> 4; t < parts; t += 64) v = join(v, sums[(uint64_t)t * n_pad + n]);
+    v = join(v, MaxSum{__shfl_xor(v.m, 16), __shfl_xor(v.s, 16)});
+    v = join(v, MaxSum{__shfl_xor(v.m, 32), __shfl_xor(v.s, 32)});
+    if ((threadIdx.x & 63) < 16) part[threadIdx.x >> 6][l] = v;
+    __syncthreads();
+    if (threadIdx.x >= 16 || n >= rows.head->count) return;
+    for (uint32_t i = 1; i < 16; ++i) v = join(v, part[i][l]);
+    put_row(v, n, rows, loss, lse);
+}
+
 template <class T>
 __global__ __launch_bounds__(256) void k_scale(T *__restrict__ g, uint32_t g_cols, uint32_t cols, uint32_t span, const MaxSum *__restrict__ sums,
-                                               uint32_t n_pad, Rows rows, uint32_t first_row)
+                                               uint32_t n_pad, uint32_t n_vocab, Rows rows, uint32_t first_row)
 {
     const uint32_t n = first_row + blockIdx.y, count = rows.head->count;
-    if (n >= ((count + PAD - 1) / PAD) * PAD) return;
+    if (n >= (count + PAD - 1) / PAD * PAD) return;
     const uint32_t j = (blockIdx.x * 256 + threadIdx.x) * VEC;
     if (j >= cols) return;
-    T *at = g + (uint64_t)n * g_cols + j;
-    float x[VEC] = {};
+    const Scaling scaling{n, count, span, n_pad, n_vocab, rows.target[n], rows.factor[n] * rows.head->scale, rows.shift[n], rows.recip[n], rows.at_target[n], sums};
+    scaling.apply(g + (uint64_t)n * g_cols, j);
+}
+
+// Both for up to PAD rows, a workgroup a row.
+template <class T>
+__global__ __launch_bounds__(1024) void k_join_scale(const MaxSum *__restrict__ sums, uint32_t parts, uint32_t n_pad, uint32_t n_vocab, Rows rows, float *__restrict__ loss,
+                                                     float *__restrict__ lse, T *__restrict__ g, uint32_t g_cols, uint32_t cols, uint32_t span)
+{
+    __shared__ MaxSum part[16];
+    const uint32_t n = blockIdx.x, count = rows.head->count;
+    MaxSum v{NEG_INF, 0.f};
     if (n < count) {
-        const float c = rows.factor[n] * rows.head->scale, shift = rows.shift[n], r = rows.recip[n];
-        const float f = c * exp_f(sums[(uint64_t)(j / span) * n_pad + n].m - shift) * r * (1.f / KEPT_SCALE<T>);
-        const Vec<T> v = load_vec(at);
-        const uint32_t y = rows.target[n] - j;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[e] = vec_at(v, e) * f;
-        if (y < VEC) {
-            const float own = c * (exp_f(rows.at_target[n] - shift) * r - 1.f);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) x[e] = y == (uint32_t)e ? own : x[e];
-        }
+        for (uint32_t t = threadIdx.x; t < parts; t += 1024) v = join(v, sums[(uint64_t)t * n_pad + n]);
+        v = block_join<1024>(v, part);
+        if (threadIdx.x == 0) put_row(v, n, rows, loss, lse);
     }
-    store_vec(at, x);
+    const bool none = empty(v);
+    const Scaling scaling{n, count, span, n_pad, n_vocab, rows.target[n], none ? 0.f : rows.factor[n] * rows.head->scale, none ? 0.f : v.m,
+                          none ? 0.f : 1.f / v.s, rows.at_target[n], sums};
+    for (uint32_t j = threadIdx.x * VEC; j < cols; j += 1024 * VEC) scaling.apply(g + (uint64_t)n * g_cols, j);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -355,8 +420,9 @@ template <class T>
 __global__ __launch_bounds__(256) void k_finish_hidden(const float *__restrict__ sums, Split split, uint32_t n_pad, uint32_t dim,
                                                        uint32_t dim_pad, Rows rows, T *__restrict__ out, uint64_t stride)
 {
-    const uint32_t i = blockIdx.x, r = rows.list[i], shares = split.shares(rows.head->count);
-    if (r == NONE || (split.single && shares == 1)) return;
+    const uint32_t i = blockIdx.x, count = rows.head->count, shares = split.shares(count);
+    if (i >= count || (split.single && shares == 1)) return;
+    const uint32_t r = rows.list[i];
     const float unscale = rows.head->unscale;
     for (uint32_t j = threadIdx.x * VEC; j < dim; j += 256 * VEC) {
         float x[VEC] = {};
@@ -434,9 +500,9 @@ Sizes sizes_of(uint32_t n_rows, uint32_t n_vocab, uint32_t dim, int type, bool g
     z.hidden = (uint64_t)z.n_pad * z.dim_pad * z.elem;
     const uint64_t row = (uint64_t)z.dim_pad * z.elem;
     z.weight = std::min(z.v_pad * row, std::max(PIECE_BYTES, PAD * row));
-    // per wavefront of 128 IDs; those of 64 and 32 are for fewer than MANY_TILES tiles of 256 x 256
+    // per wavefront of 128 IDs; those of 64, 32 and 16 are for fewer than MANY_TILES tiles of 256 x 256
     // or no more than PAD rows
-    z.sums = 8 * std::max({(uint64_t)z.v_pad / 128 * z.n_pad, std::min((uint64_t)z.v_pad / 32 * z.n_pad, (uint64_t)8 * 256 * MANY_TILES),
+    z.sums = 8 * std::max({(uint64_t)z.v_pad / 128 * z.n_pad, std::min((uint64_t)z.v_pad / 16 * z.n_pad, (uint64_t)16 * 256 * MANY_TILES),
                            (uint64_t)z.v_pad / 32 * PAD});
     if (grads) {
         z.kept = std::min((uint64_t)z.n_pad * z.v_pad * z.elem, KEEP_BYTES);
@@ -452,6 +518,8 @@ typedef Tile<2, 4, 8, 4> Big;      // 256 x 256: one workgroup a CU
 typedef Tile<2, 2, 4, 4> Middle;   // 128 x 128: two
 typedef Tile<2, 2, 2, 2> Small;    // 64 x 64: four
 
+typedef Tile<2, 2, 1, 1> Tiny;     // 32 x 32
+
 uint32_t tiles(uint64_t n, uint32_t of) { return (uint32_t)((n + of - 1) / of); }
 
 // The largest tiles of which there are enough for the CUs.
@@ -459,7 +527,8 @@ template <class F> void with_tile(uint64_t m, uint64_t n, F f)
 {
     if ((uint64_t)tiles(m, 256) * tiles(n, 256) >= MANY_TILES) f(Big{});
     else if ((uint64_t)tiles(m, 128) * tiles(n, 128) >= MANY_TILES) f(Middle{});
-    else f(Small{});
+    else if ((uint64_t)tiles(m, 64) * tiles(n, 64) >= MANY_TILES) f(Small{});
+    else f(Tiny{});
 }
 
 typedef Tile<4, 1, 2, 2> Thin;     // 128 x 32: four
@@ -483,10 +552,11 @@ template <class F> void with_split(uint32_t dim, uint32_t n_rows, uint32_t k_ste
         const uint64_t all = (uint64_t)s.m_tiles * tiles(n_rows, size), shares = std::clamp<uint64_t>(blocks / all, 1, s.most);
         return std::pair<Split, bool>(s, all * shares * 8 >= blocks * 5);
     };
-    const auto big = of(256, 256), middle = of(128, 512), small = of(64, 1024);
+    const auto big = of(256, 256), middle = of(128, 512), small = of(64, 1024), tiny = of(32, 1024);
     if (big.second) f(Big{}, big.first);
     else if (middle.second) f(Middle{}, middle.first);
-    else f(Small{}, small.first);
+    else if (small.second) f(Small{}, small.first);
+    else f(Tiny{}, tiny.first);
 }
 
 struct Call {
@@ -523,10 +593,10 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
     const T *weight = (const T *)c.weight;
     const bool grads = c.grad_hidden || c.grad_weight, forward = c.loss != nullptr;
 
-    k_rows<<<1, 1024, 0, s>>>(c.targets, c.n_rows, z.n_pad, c.n_vocab, c.lse_in, c.grad_loss, c.grad_scale, std::is_same_v<T, _Float16>, c.loss,
-                              c.lse, rows);
-    k_pack_hidden<T><<<z.n_pad, 256, 0, s>>>((const T *)c.hidden, c.hidden_stride, c.dim, z.dim_pad, c.n_rows, c.n_vocab, c.targets, rows, hidden,
-                                             (T *)c.grad_hidden, c.grad_hidden_stride);
+    const uint32_t per = std::max(4u, tiles(c.n_rows, 512));
+    k_gather<T><<<std::max(32u, tiles(c.n_rows, per)), 256, 0, s>>>((const T *)c.hidden, c.hidden_stride, c.dim, z.dim_pad, c.targets, c.n_rows, per,
+                                                                   c.n_vocab, c.lse_in, c.grad_loss, c.grad_scale, c.loss, c.lse, rows, hidden,
+                                                                   (T *)c.grad_hidden, c.grad_hidden_stride);
 
     // The table as it lies: whole steps, aligned, a tile within 32-bit offsets.  Otherwise pieces of it are copied.
     const uint64_t w_bytes = c.weight_stride * z.elem;
@@ -540,10 +610,10 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
         const T *from = weight + first * c.weight_stride;
         if (as_is) return Operand{from, w_bytes, ids};
         if (c.n_vocab > most_packed) {
-            k_pack_weight<T><<<ids, 256, 0, s>>>(from, c.weight_stride, c.dim, z.dim_pad, packed);
+            k_pack_weight<T><<<tiles(ids, 4), 256, 0, s>>>(from, c.weight_stride, ids, c.dim, z.dim_pad, packed);
             return Operand{packed, row, ids};
         }
-        if (!copied) k_pack_weight<T><<<c.n_vocab, 256, 0, s>>>(weight, c.weight_stride, c.dim, z.dim_pad, packed);
+        if (!copied) k_pack_weight<T><<<tiles(c.n_vocab, 4), 256, 0, s>>>(weight, c.weight_stride, c.n_vocab, c.dim, z.dim_pad, packed);
         copied = true;
         return Operand{packed + (uint64_t)first * z.dim_pad, row, ids};
     };
@@ -571,14 +641,14 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
                     k_logits<T, TILE, SUMS><<<blocks, TILE::THREADS, 0, s>>>(w, h, steps, m_tiles, first, c.n_vocab, z.n_pad, rows, sums, nullptr, 0);
                 first += most;
             }
-            const uint32_t parts = tiles(c.n_vocab, TILE::TM * 16);
-            if (c.n_rows <= PAD) k_join<1><<<c.n_rows, 1024, 0, s>>>(sums, parts, z.n_pad, rows, c.loss, c.lse);
-            else k_join<16><<<z.n_pad / 16, 1024, 0, s>>>(sums, parts, z.n_pad, rows, c.loss, c.lse);
         });
-        if (keep) {
-            const uint32_t cols = (uint32_t)std::min<uint64_t>(keep, up(c.n_vocab, PAD));
-            for (uint32_t first = 0; first < z.n_pad; first += 32768)
-                k_scale<T><<<dim3(tiles(cols, 256 * VEC), std::min(32768u, z.n_pad - first)), 256, 0, s>>>(kept, keep, cols, span, sums, z.n_pad, rows,
+        const uint32_t parts = tiles(c.n_vocab, span), cols = (uint32_t)std::min<uint64_t>(keep, up(c.n_vocab, PAD));
+        if (c.n_rows <= PAD) {   // (of the loss alone: no columns)
+            k_join_scale<T><<<grads ? PAD : c.n_rows, 1024, 0, s>>>(sums, parts, z.n_pad, c.n_vocab, rows, c.loss, c.lse, kept, keep, cols, span);
+        } else {
+            k_join<<<z.n_pad / 16, 1024, 0, s>>>(sums, parts, z.n_pad, rows, c.loss, c.lse);
+            for (uint32_t first = 0; keep && first < z.n_pad; first += 32768)
+                k_scale<T><<<dim3(tiles(cols, 256 * VEC), std::min(32768u, z.n_pad - first)), 256, 0, s>>>(kept, keep, cols, span, sums, z.n_pad, c.n_vocab, rows,
                                                                                                           first);
         }
     }
@@ -598,11 +668,11 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
         const Operand w = c.n_rows ? table(first, ids) : Operand{};
         T *const go = old ? kept : g;
         if (!old && c.n_rows)
-            with_logits_tile(ids, std::max<uint32_t>(c.n_rows, STEP_K<T>), [&](auto t) {
+            with_logits_tile(ids, c.n_rows, [&](auto t) {
                 using TILE = decltype(t);
-                // every row of G up to a whole step, every column up to the piece's width is written: the products read it in steps
+                // every column of G up to the piece's width is written: the product for dh reads it in whole steps
                 const uint32_t m_tiles = tiles(up(ids, PAD), TILE::M);
-                k_logits<T, TILE, G_AGAIN><<<tile_blocks(m_tiles, tiles(c.n_rows, TILE::N)), TILE::THREADS, 0, s>>>(
+                k_logits<T, TILE, G_AGAIN><<<tile_blocks(m_tiles, tiles(up(c.n_rows, STEP_K<T>), TILE::N)), TILE::THREADS, 0, s>>>(
                     w, h, steps, m_tiles, first, c.n_vocab, z.n_pad, rows, nullptr, g, piece);
             });
         if (c.grad_hidden && c.n_rows) {
@@ -635,7 +705,7 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
         first += width;
     }
     if (c.grad_hidden && c.n_rows)
-        k_finish_hidden<T><<<z.n_pad, 256, 0, s>>>(shares, finish, z.n_pad, c.dim, z.dim_pad, rows, (T *)c.grad_hidden, c.grad_hidden_stride);
+        k_finish_hidden<T><<<c.n_rows, 256, 0, s>>>(shares, finish, z.n_pad, c.dim, z.dim_pad, rows, (T *)c.grad_hidden, c.grad_hidden_stride);
 }
 
 int run(const Call &c, void *workspace, uint64_t workspace_bytes, void *stream)

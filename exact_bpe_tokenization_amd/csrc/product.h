@@ -53,10 +53,11 @@ __device__ __forceinline__ void barrier()
 // a group of 16 lanes reads, and the groups beside it, lie apart.
 template <class T, bool TURNED, int WIDTH> __device__ __forceinline__ uint32_t swizzle(uint32_t row)
 {
+    constexpr uint32_t PIECES = WIDTH * sizeof(T) / 16;   // of a turned row
     if constexpr (!TURNED) return row & 7;
-    else if constexpr (sizeof(T) == 4) return ((row >> 2) & 3) << 2;
+    else if constexpr (sizeof(T) == 4) return (((row >> 2) & 3) << 2) & (PIECES - 1);
     else if constexpr (WIDTH >= 128) return ((row & 3) | ((row >> 3) & 1) << 2) << 1;
-    else return (((row >> 1) & 1) | ((row >> 3) & 1) << 1) << 1;
+    else return ((((row >> 1) & 1) | ((row >> 3) & 1) << 1) << 1) & (PIECES - 1);
 }
 
 // One operand's way into LDS.  Every thread copies 16-byte pieces at fixed offsets from a base that advances with k.
@@ -272,7 +273,7 @@ __device__ __forceinline__ void product(f32x4 (&acc)[TILE::TM][TILE::TN], lds_u8
 template <class TILE, class F> __device__ __forceinline__ void by_rows(const f32x4 (&acc)[TILE::TM][TILE::TN], lds_u8 *lds, F f)
 {
     constexpr uint32_t STRIDE = TILE::M * 4 + 16, ROWS = TILE::WN * 16, PER_ROW = TILE::M / VEC;
-    static_assert(ROWS * STRIDE <= TILE::LDS && ROWS * PER_ROW % TILE::THREADS == 0, "a turn's rows");
+    static_assert(ROWS * STRIDE <= TILE::LDS, "a turn's rows");
     typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / TILE::WN, wn = wave % TILE::WN;
     unrolled<TILE::TN>([&](auto turn) {
@@ -282,8 +283,9 @@ template <class TILE, class F> __device__ __forceinline__ void by_rows(const f32
             *(lds_f32x4 *)(lds + (wn * 16 + (lane & 15)) * STRIDE + ((wm * TILE::TM + i) * 16 + (lane >> 4) * 4) * 4) = acc[i][j];
         barrier();
 #pragma unroll
-        for (uint32_t k = 0; k < ROWS * PER_ROW / TILE::THREADS; ++k) {
+        for (uint32_t k = 0; k < (ROWS * PER_ROW + TILE::THREADS - 1) / TILE::THREADS; ++k) {
             const uint32_t v = k * TILE::THREADS + threadIdx.x, row = v / PER_ROW, m = v % PER_ROW * VEC;
+            if (ROWS * PER_ROW % TILE::THREADS && row >= ROWS) break;
             const lds_u8 *from = lds + row * STRIDE + m * 4;
             const f32x4 a = *(const lds_f32x4 *)from, b = *(const lds_f32x4 *)(from + 16);
             float x[VEC] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
