@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtoktier.so")
 SOURCES = ["pretok.hip", "bpe.hip", "tiles.hip", "added.hip", "toktier.hip", "repair.hip", "embed.hip", "loss.hip",
-           "sample.hip", "linear_loss.hip", "distill.hip", "top.hip"]
+           "sample.hip", "linear_loss.hip", "linear_loss_f16.hip", "linear_loss_bf16.hip", "distill.hip", "top.hip"]
 ARCH = "gfx950"
 
 

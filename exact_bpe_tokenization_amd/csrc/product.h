@@ -296,21 +296,56 @@ template <class TILE, class F> __device__ __forceinline__ void by_rows(const f32
 }
 
 // Workgroups go round the eight XCDs, each with an L2 of its own; so that neighbours in a block of tiles share one, XCD x
-// takes the tiles from x * (all / 8) on, in bands of GROUP tiles of m that go along n; all tiles of a share of k (of
-// `shares`) before the next.  Returns the share, ~0 for no tile.
-constexpr uint32_t XCDS = 8, GROUP = 6;
-__device__ __forceinline__ uint32_t tile_of(uint32_t id, uint32_t m_tiles, uint32_t n_tiles, uint32_t shares, uint32_t &tm, uint32_t &tn)
+// takes the tiles from x * (all / 8) on, in bands of GROUP tiles of m that go along n; all tiles of a share of k before
+// the next.  (Bands of 4, 6, 8, 16: loss of 8,192 rows x 131,328 x 4,096 bfloat16 6.09, 6.14, 6.40, 6.72 ms; with gradients 23.6,
+// 23.5, 23.6, 24.4.)
+constexpr uint32_t XCDS = 8, GROUP = 6, CUS = 256;
+__device__ __forceinline__ void place_of(uint32_t tile, uint32_t m_tiles, uint32_t n_tiles, uint32_t &tm, uint32_t &tn)
 {
-    const uint32_t one = m_tiles * n_tiles, all = one * shares, per = (all + XCDS - 1) / XCDS, x = id % XCDS, at = id / XCDS;
-    const uint32_t i = x * per + at;
-    if (at >= per || i >= all) return ~0u;
-    const uint32_t share = i / one, tile = i % one;
     const uint32_t band = tile / (GROUP * n_tiles), in = tile % (GROUP * n_tiles);
     const uint32_t high = m_tiles - band * GROUP < GROUP ? m_tiles - band * GROUP : GROUP;
     tm = band * GROUP + in % high;
     tn = in / high;
-    return share;
 }
-inline uint32_t tile_blocks(uint32_t m_tiles, uint32_t n_tiles) { return (m_tiles * n_tiles + XCDS - 1) / XCDS * XCDS; }
+// The workgroup's tile among `all`, ~0 for none.
+__device__ __forceinline__ uint32_t tile_of(uint32_t id, uint32_t all)
+{
+    const uint32_t per = (all + XCDS - 1) / XCDS, i = id % XCDS * per + id / XCDS;
+    return id / XCDS < per && i < all ? i : ~0u;
+}
+
+// Tiles of 256 x 256, of which one workgroup runs on a CU: up to a quarter of a round that is left at the end is cut into strips of
+// 64 along n, so that it takes the time of a strip.
+typedef Tile<2, 4, 8, 4> Big;
+typedef Tile<2, 4, 8, 1> Strip;
+constexpr uint32_t STRIPS = Big::N / Strip::N;
+
+// f(tile, m0, n0) for the workgroup's tile of m_tiles x n_tiles, if it has one.
+template <class TILE, class F> __device__ __forceinline__ void with_place(uint32_t m_tiles, uint32_t n_tiles, F f)
+{
+    uint32_t all = m_tiles * n_tiles, tm, tn;
+    if constexpr (__is_same(TILE, Big)) {
+        const uint32_t left = all % CUS;
+        if (all > CUS && left && left * STRIPS <= CUS) {
+            all -= left;
+            if (blockIdx.x >= all) {
+                const uint32_t i = blockIdx.x - all;
+                if (i >= left * STRIPS) return;
+                place_of(all + i / STRIPS, m_tiles, n_tiles, tm, tn);
+                return f(Strip{}, tm * Big::M, tn * Big::N + i % STRIPS * Strip::N);
+            }
+        }
+    }
+    const uint32_t tile = tile_of(blockIdx.x, all);
+    if (tile == ~0u) return;
+    place_of(tile, m_tiles, n_tiles, tm, tn);
+    f(TILE{}, tm * TILE::M, tn * TILE::N);
+}
+// workgroups of a launch of up to so many tiles
+template <class TILE> inline uint32_t tile_blocks(uint32_t m_tiles, uint32_t n_tiles)
+{
+    const uint32_t all = (m_tiles * n_tiles + XCDS - 1) / XCDS * XCDS;
+    return all + (__is_same(TILE, Big) && all > CUS ? CUS : 0);
+}
 
 }  // namespace tt
