@@ -1,8 +1,8 @@
 // top.hip -- the k largest logits of a row, in order, with the row's log-sum-exp.
 //
 // The row is read once for the threads' own maxima (and sums of exponentials).  Nothing below the threshold can be among
-// the first k: every wavefront takes the r-th largest of its lanes' maxima, r = k / wavefronts, and the least of those has
-// k elements at or above it.  The elements from there on are listed, from the few threads that have any, and sorted.
+// the first k: every wavefront (whose lanes all have elements) takes the r-th largest of its lanes' maxima, r = k / wavefronts,
+// and the least of those has k elements at or above it.  The elements from there on are listed, from the few threads that have any, and sorted.
 // Where they are too many, histograms over narrowing ranges of keys find the border first.
 #include <algorithm>
 #include <type_traits>
@@ -30,63 +30,120 @@ __device__ __forceinline__ float logit_of(uint32_t key)
 }
 __device__ __forceinline__ uint64_t element(float x, uint32_t id) { return (uint64_t)key_of(x) << 32 | ~id; }
 
-struct Lds {
+// A thread's vectors in groups of DEPTH, the last of GROUPS with all that are left.  (256 threads have four vectors each.)
+template <int THREADS> constexpr uint32_t GROUPS = THREADS == 256 ? 2 : 8;
+template <class T> constexpr int DEPTH = sizeof(T) == 4 ? 2 : 4;
+
+template <int THREADS> struct Lds {
     union {
-        uint64_t list[LIST];
+        uint64_t list[LIST] __attribute__((aligned(16)));
         uint32_t bins[BINS];
     };
-    uint16_t who[1024];
+    float best[GROUPS<THREADS>][THREADS];      // the groups' largest logits
+    uint16_t who[GROUPS<THREADS> * THREADS];   // groups with elements to list: group * THREADS + thread
     MaxSum sums[16];
     float bound[16];
     uint32_t part[16];
     uint32_t count, threads, found_bin, found_before;
 };
 
-// Sorts the wavefront's values, descending over the lanes, and gives the one of rank r to all.
+// At most the r-th largest of the wavefront's values: its upper 16 bits as a key, found bit by bit.
 __device__ __forceinline__ float wave_rank(float v, uint32_t r)
 {
-    const uint32_t lane = threadIdx.x & 63;
+    const uint32_t key = key_of(v);
+    uint32_t at = 0;
 #pragma unroll
-    for (uint32_t size = 2; size <= 64; size *= 2)
-#pragma unroll
-        for (uint32_t d = size / 2; d; d /= 2) {
-            const float o = __shfl_xor(v, d);
-            const bool up = (lane & size) != 0, low = (lane & d) == 0;
-            v = (low != up) ? fmaxf(v, o) : fminf(v, o);
-        }
-    return __shfl(v, r);
+    for (uint32_t bit = 0x80000000u; bit > 0x8000u; bit >>= 1) {
+        const uint32_t up = at | bit;
+        if (__popcll(__ballot(key >= up)) >= r) at = up;
+    }
+    return at <= key_of(NEG_INF) ? NEG_INF : logit_of(at);
 }
 
-// Sorts the first n (at most LIST) of list, descending; elements are all different.  Few by their ranks, each against all
-// others, more by a bitonic network.
-template <int THREADS> __device__ __forceinline__ void sort_list(uint64_t *list, uint32_t n)
+// Sorts the first n (at most LIST) of list, descending; elements are all different.
+//
+// Few by their ranks, several threads counting for an element, two elements a read.  More by a bitonic network over registers:
+// element e * THREADS + thread, so that its steps are exchanges of lanes, of wavefronts (through the list) or of a thread's own.
+// (512 elements by the network with every step through LDS took 8 us, 2,048 16 us.)
+typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+template <int THREADS> __device__ __forceinline__ void sort_by_rank(uint64_t *list, uint32_t n)
 {
-    if (n <= 256 && n <= THREADS) {
-        const uint64_t own = threadIdx.x < n ? list[threadIdx.x] : 0;
-        uint32_t rank = 0;
-        if (threadIdx.x < n)
-            for (uint32_t i = 0; i < n; ++i) rank += list[i] > own;
-        __syncthreads();
-        if (threadIdx.x < n) list[rank] = own;
-        __syncthreads();
-        return;
+    const uint32_t even = (n + 1) & ~1u;
+    uint32_t per = 1;   // threads of an element
+    while (per < 16 && 2 * per * n <= THREADS) per *= 2;
+    if (threadIdx.x == 0 && n < even) list[n] = 0;
+    __syncthreads();
+    const uint32_t e = threadIdx.x / per;
+    const uint64_t own = e < n ? list[e] : 0;
+    uint32_t rank = 0;
+    if (e < n) {
+#pragma unroll 4
+        for (uint32_t i = 2 * (threadIdx.x & (per - 1)); i < even; i += 2 * per) {
+            const u64x2 v = *(const u64x2 *)(list + i);
+            rank += (v[0] > own) + (v[1] > own);
+        }
     }
-    uint32_t all = 512;
-    while (all < n) all *= 2;
-    for (uint32_t i = n + threadIdx.x; i < all; i += THREADS) list[i] = 0;
-    for (uint32_t size = 2; size <= all; size *= 2)
+    for (uint32_t d = 1; d < per; d *= 2) rank += __shfl_xor(rank, d);
+    __syncthreads();
+    if (e < n && (threadIdx.x & (per - 1)) == 0) list[rank] = own;
+    __syncthreads();
+}
+
+__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, uint32_t d)
+{
+    return (uint64_t)(uint32_t)__shfl_xor((int)(v >> 32), d) << 32 | (uint32_t)__shfl_xor((int)v, d);
+}
+
+template <int THREADS, int EACH> __device__ __forceinline__ void sort_by_network(uint64_t *list, uint32_t n)
+{
+    constexpr uint32_t ALL = THREADS * EACH;
+    uint64_t v[EACH];
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) v[e] = e * THREADS + threadIdx.x < n ? list[e * THREADS + threadIdx.x] : 0;
+#pragma unroll
+    for (uint32_t size = 2; size <= ALL; size *= 2) {
+#pragma unroll
         for (uint32_t d = size / 2; d; d /= 2) {
-            __syncthreads();
-            for (uint32_t i = threadIdx.x; i < all / 2; i += THREADS) {
-                const uint32_t lo = 2 * i - (i & (d - 1)), hi = lo + d;
-                const uint64_t a = list[lo], b = list[hi];
-                if ((a < b) == ((lo & size) == 0)) {
-                    list[lo] = b;
-                    list[hi] = a;
+            if (d >= THREADS) {   // a thread's own: the larger at the lower index where the run descends
+#pragma unroll
+                for (uint32_t e = 0; e < EACH; ++e) {
+                    const uint32_t o = e ^ (d / THREADS);
+                    if (o < e) continue;
+                    const bool down = (e * THREADS & size) == 0;
+                    const uint64_t lo = v[e], hi = v[o];
+                    v[e] = (lo > hi) == down ? lo : hi;
+                    v[o] = (lo > hi) == down ? hi : lo;
                 }
+                continue;
+            }
+            if (d >= 64) {
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < EACH; ++e) list[e * THREADS + threadIdx.x] = v[e];
+                __syncthreads();
+            }
+#pragma unroll
+            for (uint32_t e = 0; e < EACH; ++e) {
+                const uint32_t i = e * THREADS + threadIdx.x;
+                const uint64_t o = d >= 64 ? list[i ^ d] : shfl_xor64(v[e], d);
+                const bool larger = ((i & size) == 0) == ((i & d) == 0);   // this place keeps the larger of the two
+                v[e] = (v[e] > o) == larger ? v[e] : o;
             }
         }
+    }
     __syncthreads();
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) list[e * THREADS + threadIdx.x] = v[e];
+    __syncthreads();
+}
+
+template <int THREADS> __device__ __forceinline__ void sort_list(uint64_t *list, uint32_t n)
+{
+    if (n <= (THREADS < 384 ? THREADS : 384)) sort_by_rank<THREADS>(list, n);
+    else if (THREADS == 256 && n <= 512) sort_by_network<THREADS, 512 / 256>(list, n);
+    else if (n <= 1024) sort_by_network<THREADS, 1024 / THREADS>(list, n);
+    else sort_by_network<THREADS, 2048 / THREADS>(list, n);
 }
 
 // f(first element, elements, values) for the vectors of [begin, end), dealt out to the threads
@@ -99,9 +156,78 @@ template <class T, int THREADS, class F> __device__ __forceinline__ void each_ve
     }
 }
 
+// The thread's largest logit of [begin, end), and with SUM the sum of exponentials under it, DEPTH vectors at a time with the next
+// ones on their way.  The powers are taken of x k - m k in one instruction: off by a rounding of m k, which lse = m / T + log(s)
+// has anyway.  (2,048 rows of 131,328 bfloat16, 64 listed: 149 us with rows.h's vectors, two on their way and a power's argument
+// in two instructions.)
+template <class T, int THREADS, bool SUM> __device__ __forceinline__ MaxSum largest_of(const T *x, uint32_t begin, uint32_t end, float k2, float (&best)[GROUPS<THREADS>][THREADS])
+{
+    constexpr int D = DEPTH<T>;
+    constexpr uint32_t STEP = THREADS * VEC;
+    MaxSum a{NEG_INF, 0.f};
+    float own = NEG_INF;   // of the group in work
+    auto take = [&](const auto &v, auto n) {
+        constexpr int N = decltype(n)::value;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float e = vec_at(v[i / VEC], i % VEC);
+            own = e > own ? e : own;
+        }
+        const float m = own > a.m ? own : a.m;
+        if constexpr (SUM) {
+            float s[4] = {};
+            const float from = m == NEG_INF ? 0.f : m * k2;   // nothing but -inf so far, or NaN: those are in the sums
+            if (__builtin_fabsf(from) < 1e30f) {
+                s[0] = a.s * __builtin_amdgcn_exp2f(m == NEG_INF ? 0.f : __builtin_fmaf(a.m, k2, -from));
+#pragma unroll
+                for (int i = 0; i < N; ++i) s[i & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(vec_at(v[i / VEC], i % VEC), k2, -from));
+            } else {   // the product may be beyond the type's numbers
+                s[0] = a.s * exp_f(a.m - m, k2);
+#pragma unroll
+                for (int i = 0; i < N; ++i) s[i & 3] += exp_f(vec_at(v[i / VEC], i % VEC) - m, k2);
+            }
+            a.s = (s[0] + s[1]) + (s[2] + s[3]);
+        }
+        a.m = m;
+    };
+    uint32_t j = begin + threadIdx.x * VEC, group = 0;
+    auto close = [&] {   // a group ends, the last one goes on
+        best[group][threadIdx.x] = own;
+        if (group + 1 < GROUPS<THREADS>) {
+            ++group;
+            own = NEG_INF;
+        }
+    };
+    Vec<T> v[D];
+    auto fetch = [&](uint32_t at) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) v[i] = load_vec(x + at + i * STEP);
+    };
+    constexpr uint32_t REACH = (D - 1) * STEP + VEC;
+    if (j + REACH <= end) fetch(j);
+    for (; j + REACH <= end; j += D * STEP) {
+        Vec<T> now[D];
+#pragma unroll
+        for (int i = 0; i < D; ++i) now[i] = v[i];
+        if (j + D * STEP + REACH <= end) fetch(j + D * STEP);
+        take(now, std::integral_constant<int, D * VEC>{});
+        close();
+    }
+    if (j < end) {
+        for (; j < end; j += STEP) {
+            float e8[VEC];
+            load_part(x + j, end - j, NEG_INF, e8);
+            const Vec<T> one[1] = {to_vec<T>(e8)};
+            take(one, std::integral_constant<int, VEC>{});
+        }
+        best[group][threadIdx.x] = own;
+    }
+    return a;
+}
+
 // The elements that may be among the first k, in sh.list, their number returned.  Too many: found by histograms.
 template <class T, int THREADS>
-__device__ __forceinline__ uint32_t list_by_histogram(const T *x, uint32_t begin, uint32_t end, uint32_t k, float least, float most, Lds &sh)
+__device__ __forceinline__ uint32_t list_by_histogram(const T *x, uint32_t begin, uint32_t end, uint32_t k, float least, float most, Lds<THREADS> &sh)
 {
     uint32_t lo = key_of(least), hi = key_of(most), before = 0;   // `before` elements lie above hi
     lo = lo > key_of(NEG_INF) ? lo : key_of(NEG_INF) + 1;
@@ -191,54 +317,56 @@ __device__ __forceinline__ uint32_t list_by_histogram(const T *x, uint32_t begin
 
 // The first k of [begin, end), sorted in sh.list; their number (fewer than k where there are no more) and the part's
 // maximum and sum in `all`.
-template <class T, int THREADS, int HELD, bool SUM>
-__device__ __forceinline__ uint32_t top_of(const T *x, uint32_t begin, uint32_t end, uint32_t k, float k2, Lds &sh, MaxSum &all)
+template <class T, int THREADS, bool SUM>
+__device__ __forceinline__ uint32_t top_of(const T *x, uint32_t begin, uint32_t end, uint32_t k, float k2, Lds<THREADS> &sh, MaxSum &all)
 {
     constexpr uint32_t WAVES = THREADS / 64;
     if (threadIdx.x == 0) sh.count = sh.threads = 0;
-    RowPart<T, THREADS, HELD> part{x, begin, end};
-    MaxSum a{NEG_INF, 0.f};
-    part.template each<true>(NEG_INF, [&](uint32_t, uint32_t, float (&v)[VEC]) {
-        if constexpr (SUM) {
-            add_vec(a, v, k2);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) a.m = v[e] > a.m ? v[e] : a.m;
-        }
-    });
-    if (SUM && a.s != a.s) {   // a signaling NaN may have taken the place of the maximum (fmaxf), where a comparison passes it by
-        a.m = NEG_INF;
-        part.template each<false>(NEG_INF, [&](uint32_t, uint32_t, float (&v)[VEC]) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) a.m = v[e] > a.m ? v[e] : a.m;
-        });
-    }
+    const MaxSum a = largest_of<T, THREADS, SUM>(x, begin, end, k2, sh.best);
+    // the wavefronts whose lanes all have elements
     const float mine = a.m;
-    const uint32_t rank = (k + WAVES - 1) / WAVES;
-    const float bound = rank <= 64 ? wave_rank(mine, rank - 1) : NEG_INF;
+    const uint32_t whole = (end - begin) / (64 * VEC) < WAVES ? (end - begin) / (64 * VEC) : WAVES, rank = whole ? (k + whole - 1) / whole : 65;
+    const float bound = rank > 64 ? NEG_INF : (threadIdx.x >> 6) < whole ? wave_rank(mine, rank) : -NEG_INF;
     if ((threadIdx.x & 63) == 0) sh.bound[threadIdx.x >> 6] = bound;
     all = block_join<THREADS>(a, sh.sums, k2);   // with the barrier that sh.bound needs
     float least = sh.bound[0];
 #pragma unroll
     for (uint32_t w = 1; w < WAVES; ++w) least = fminf(least, sh.bound[w]);
 
-    const uint32_t vectors = (end - begin + THREADS * VEC - 1) / (THREADS * VEC);   // of a thread, at most
+    // a group's vectors: as many as the last one may have
+    const uint32_t vectors = (end - begin + THREADS * VEC - 1) / (THREADS * VEC);
+    const uint32_t per = vectors > GROUPS<THREADS> * DEPTH<T> ? vectors - (GROUPS<THREADS> - 1) * DEPTH<T> : DEPTH<T>;
     uint32_t n = NONE;
     if (rank <= MOST_RANK || end - begin <= LIST) {
-        if (mine >= least && mine > NEG_INF) sh.who[atomicAdd(&sh.threads, 1u)] = threadIdx.x;
+        const uint32_t first = begin + threadIdx.x * VEC, own = first < end ? (end - first + THREADS * VEC - 1) / (THREADS * VEC) : 0;
+        for (uint32_t g = 0; g < GROUPS<THREADS> && g * DEPTH<T> < own; ++g) {
+            const float v = sh.best[g][threadIdx.x];
+            if (v >= least && v > NEG_INF) sh.who[atomicAdd(&sh.threads, 1u)] = g * THREADS + threadIdx.x;
+        }
         __syncthreads();
-        const uint32_t threads = sh.threads;
-        for (uint32_t i = threadIdx.x; i < threads * vectors; i += THREADS) {
-            const uint32_t v = i / threads, j = begin + (v * THREADS + sh.who[i - v * threads]) * VEC;
-            if (j >= end) continue;
-            float e8[VEC];
-            load_part(x + j, end - j, NEG_INF, e8);
+        const uint32_t all = sh.threads * per;
+        for (uint32_t i0 = threadIdx.x; i0 < all; i0 += 4 * THREADS) {   // four loads in flight
+            uint32_t at[4];
+            Vec<T> x8[4];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (e8[e] >= least && e8[e] > NEG_INF) {
-                    const uint32_t to = atomicAdd(&sh.count, 1u);
-                    if (to < LIST) sh.list[to] = element(e8[e], j + e);
+            for (int b = 0; b < 4; ++b) {
+                const uint32_t i = i0 + b * THREADS, who = i < all ? sh.who[i / per] : 0, g = who / THREADS, v = g * DEPTH<T> + i % per;
+                const uint32_t j = begin + (v * THREADS + who % THREADS) * VEC;
+                at[b] = i < all && j < end && (g + 1 == GROUPS<THREADS> || i % per < DEPTH<T>) ? j : NONE;
+                if (at[b] != NONE) x8[b] = load_some(x + j, end - j);
+            }
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (at[b] == NONE) continue;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float v = vec_at(x8[b], e);
+                    if (v >= least && v > NEG_INF && at[b] + e < end) {
+                        const uint32_t to = atomicAdd(&sh.count, 1u);
+                        if (to < LIST) sh.list[to] = element(v, at[b] + e);
+                    }
                 }
+            }
         }
         __syncthreads();
         n = sh.count;
@@ -255,14 +383,14 @@ __device__ __forceinline__ void put(uint32_t i, uint32_t n, const uint64_t *list
     logits[i] = i < n ? logit_of(list[i] >> 32) : NEG_INF;
 }
 
-template <class T, int THREADS, int HELD, bool SUM>
-__global__ __launch_bounds__(THREADS) void k_top(const T *logits, uint32_t n_vocab, uint64_t stride, uint32_t k, float inv_t, uint32_t *__restrict__ ids,
+template <class T, int THREADS, bool SUM>
+__global__ __launch_bounds__(THREADS, 8) void k_top(const T *logits, uint32_t n_vocab, uint64_t stride, uint32_t k, float inv_t, uint32_t *__restrict__ ids,
                                                  uint64_t ids_stride, float *__restrict__ out, uint64_t out_stride, float *__restrict__ lse)
 {
-    __shared__ Lds sh;
+    __shared__ Lds<THREADS> sh;
     const uint64_t row = blockIdx.x;
     MaxSum a;
-    const uint32_t n = top_of<T, THREADS, HELD, SUM>(logits + row * stride, 0, n_vocab, k, LOG2E * inv_t, sh, a);
+    const uint32_t n = top_of<T, THREADS, SUM>(logits + row * stride, 0, n_vocab, k, LOG2E * inv_t, sh, a);
     for (uint32_t i = threadIdx.x; i < k; i += THREADS) put(i, n, sh.list, ids + row * ids_stride, out + row * out_stride);
     if (SUM && threadIdx.x == 0) lse[row] = empty(a) ? NEG_INF : a.m * inv_t + log_of(a.s);
 }
@@ -272,35 +400,40 @@ template <class T, bool SUM>
 __global__ __launch_bounds__(PIECE_THREADS) void k_top_pieces(const T *logits, uint32_t n_vocab, uint64_t stride, uint32_t k, float inv_t,
                                                               uint64_t *__restrict__ lists, MaxSum *__restrict__ sums)
 {
-    __shared__ Lds sh;
+    __shared__ Lds<PIECE_THREADS> sh;
     const uint64_t row = blockIdx.y, piece = row * gridDim.x + blockIdx.x;
     const uint32_t begin = blockIdx.x * PIECE, end = n_vocab - begin < PIECE ? n_vocab : begin + PIECE;
     MaxSum a;
-    const uint32_t n = top_of<T, PIECE_THREADS, PIECE_HELD, SUM>(logits + row * stride, begin, end, k, LOG2E * inv_t, sh, a);
+    const uint32_t n = top_of<T, PIECE_THREADS, SUM>(logits + row * stride, begin, end, k, LOG2E * inv_t, sh, a);
     for (uint32_t i = threadIdx.x; i < k; i += PIECE_THREADS) lists[piece * k + i] = i < n ? sh.list[i] : 0;
     if (SUM && threadIdx.x == 0) sums[piece] = a;
 }
 
+constexpr int JOIN_THREADS = 1024;
 template <bool SUM>
-__global__ __launch_bounds__(PIECE_THREADS) void k_top_join(const uint64_t *__restrict__ lists, const MaxSum *__restrict__ sums, uint32_t pieces,
+__global__ __launch_bounds__(JOIN_THREADS) void k_top_join(const uint64_t *__restrict__ lists, const MaxSum *__restrict__ sums, uint32_t pieces,
                                                             uint32_t k, float inv_t, uint32_t *__restrict__ ids, uint64_t ids_stride,
                                                             float *__restrict__ out, uint64_t out_stride, float *__restrict__ lse)
 {
-    __shared__ Lds sh;
+    __shared__ struct {
+        uint64_t list[LIST] __attribute__((aligned(16)));
+        MaxSum sums[16];
+        uint32_t count;
+    } sh;
     const uint64_t row = blockIdx.x;
     if (threadIdx.x == 0) sh.count = 0;
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < pieces * k; i += PIECE_THREADS) {
+    for (uint32_t i = threadIdx.x; i < pieces * k; i += JOIN_THREADS) {
         const uint64_t e = lists[row * pieces * k + i];
         if (e) sh.list[atomicAdd(&sh.count, 1u)] = e;
     }
     MaxSum a{NEG_INF, 0.f};
     if (SUM && threadIdx.x < pieces) a = sums[row * pieces + threadIdx.x];
-    if (SUM) a = block_join<PIECE_THREADS>(a, sh.sums, LOG2E * inv_t);
+    if (SUM) a = block_join<JOIN_THREADS>(a, sh.sums, LOG2E * inv_t);
     __syncthreads();
     const uint32_t n = sh.count;
-    sort_list<PIECE_THREADS>(sh.list, n);
-    for (uint32_t i = threadIdx.x; i < k; i += PIECE_THREADS) put(i, n, sh.list, ids + row * ids_stride, out + row * out_stride);
+    sort_list<JOIN_THREADS>(sh.list, n);
+    for (uint32_t i = threadIdx.x; i < k; i += JOIN_THREADS) put(i, n, sh.list, ids + row * ids_stride, out + row * out_stride);
     if (SUM && threadIdx.x == 0) lse[row] = empty(a) ? NEG_INF : a.m * inv_t + log_of(a.s);
 }
 
@@ -376,19 +509,19 @@ extern "C" int toktier_top_logits(const void *logits, int type, uint32_t n_rows,
                 uint64_t *lists = (uint64_t *)workspace;
                 MaxSum *sums = (MaxSum *)((uint8_t *)workspace + L.sums);
                 k_top_pieces<T, SUM><<<dim3(L.pieces, n_rows), PIECE_THREADS, 0, s>>>(x, n_vocab, stride, k, inv_t, lists, sums);
-                k_top_join<SUM><<<n_rows, PIECE_THREADS, 0, s>>>(lists, sums, L.pieces, k, inv_t, out_ids, out_ids_stride, out_logits,
+                k_top_join<SUM><<<n_rows, JOIN_THREADS, 0, s>>>(lists, sums, L.pieces, k, inv_t, out_ids, out_ids_stride, out_logits,
                                                                  out_logits_stride, lse);
                 return;
             }
-            auto launch = [&](auto threads, auto held) {
-                constexpr int N = decltype(threads)::value, H = decltype(held)::value;
+            auto launch = [&](auto threads) {
+                constexpr int N = decltype(threads)::value;
                 in_launches(n_rows, N, [&](uint64_t r, uint32_t rows) {
-                    k_top<T, N, H, SUM><<<rows, N, 0, s>>>(x + r * stride, n_vocab, stride, k, inv_t, out_ids + r * out_ids_stride, out_ids_stride,
+                    k_top<T, N, SUM><<<rows, N, 0, s>>>(x + r * stride, n_vocab, stride, k, inv_t, out_ids + r * out_ids_stride, out_ids_stride,
                                                            out_logits + r * out_logits_stride, out_logits_stride, lse ? lse + r : nullptr);
                 });
             };
-            if (n_vocab <= 256 * VEC * 4) launch(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
-            else launch(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+            if (n_vocab <= 256 * VEC * 4) launch(std::integral_constant<int, 256>{});
+            else launch(std::integral_constant<int, 1024>{});
         };
         if (lse) with_sum(std::true_type{});
         else with_sum(std::false_type{});

@@ -31,12 +31,12 @@ def plain(logits, k, temperature=1.0):
             z = x[r] / temperature
             m = z.max()
             lse[r] = math.nan if np.isnan(m) or m == np.inf else -np.inf if m == -np.inf else m + np.log(np.exp(z - m).sum())
-            if np.isfinite(lse[r]):   # the bounds of distill_plain, of s and its logarithm
+            if np.isfinite(lse[r]):   # the bounds of distill_plain, of s and its logarithm; m k rounds, by u of |m| in the argument
                 d = np.minimum(m - z, 104)
                 p = np.exp(z - lse[r])
                 low = z[np.isfinite(z)].min()
                 rel = (p * (5 * d + 4)).sum() + 5 * min(m - low, 104) + 13 * -(-v // 2048) + 105
-                err[r] = U * (rel + 4 * (abs(lse[r] - m) + 1) + 3 * abs(m) + 2 * abs(lse[r]))
+                err[r] = U * (rel + abs(m) + 4 * (abs(lse[r] - m) + 1) + 3 * abs(m) + 2 * abs(lse[r]))
     return ids, out, lse, err
 
 
