@@ -2,7 +2,8 @@
 //
 // The row is read once for the threads' own maxima (and sums of exponentials).  Nothing below the threshold can be among
 // the first k: every wavefront (whose lanes all have elements) takes the r-th largest of its lanes' maxima, r = k / wavefronts,
-// and the least of those has k elements at or above it.  The elements from there on are listed, from the few threads that have any, and sorted.
+// and the least of those has k elements at or above it; for longer lists it is the k-th largest of the maxima of all groups of a
+// thread's vectors.  The elements from there on are listed, from the few threads that have any, and sorted.
 // Where they are too many, histograms over narrowing ranges of keys find the border first.
 #include <algorithm>
 #include <type_traits>
@@ -15,7 +16,7 @@ namespace {
 constexpr uint32_t NONE = 0xFFFFFFFFu;
 constexpr uint32_t LIST = 2048;      // listed elements
 constexpr uint32_t BINS = 2048;
-constexpr uint32_t MOST_RANK = 48;   // of a wavefront's maxima: below that too much is listed to try
+constexpr uint32_t QUICK_RANK = 16;    // of a wavefront's maxima
 
 // The order of the logits as integers, -0 equal to +0; an element is its key and the complement of its ID, so that the larger
 // of two comes first.
@@ -30,6 +31,13 @@ __device__ __forceinline__ float logit_of(uint32_t key)
 }
 __device__ __forceinline__ uint64_t element(float x, uint32_t id) { return (uint64_t)key_of(x) << 32 | ~id; }
 
+// Where sort_by_bins scatters to.
+constexpr uint32_t CROWD = 64;   // elements of a bin, at most
+struct Scatter {
+    uint32_t bins[BINS + 1], part[16], low, high, crowded;
+    uint64_t list[LIST];
+};
+
 // A thread's vectors in groups of DEPTH, the last of GROUPS with all that are left.  (256 threads have four vectors each.)
 template <int THREADS> constexpr uint32_t GROUPS = THREADS == 256 ? 2 : 8;
 template <class T> constexpr int DEPTH = sizeof(T) == 4 ? 2 : 4;
@@ -39,11 +47,14 @@ template <int THREADS> struct Lds {
         uint64_t list[LIST] __attribute__((aligned(16)));
         uint32_t bins[BINS];
     };
-    float best[GROUPS<THREADS>][THREADS];      // the groups' largest logits
+    union {
+        float best[GROUPS<THREADS>][THREADS];      // the groups' largest logits
+        Scatter scatter[THREADS == 1024];
+    };
     uint16_t who[GROUPS<THREADS> * THREADS];   // groups with elements to list: group * THREADS + thread
     MaxSum sums[16];
     float bound[16];
-    uint32_t part[16];
+    uint32_t part[16], counts[16];
     uint32_t count, threads, found_bin, found_before;
 };
 
@@ -60,11 +71,33 @@ __device__ __forceinline__ float wave_rank(float v, uint32_t r)
     return at <= key_of(NEG_INF) ? NEG_INF : logit_of(at);
 }
 
+// At most the r-th largest of all threads' values, of which thread t holds value(0) .. value(n - 1) as keys; the same way, with a
+// count over the workgroup for each bit.
+template <int THREADS, int N, class F> __device__ __forceinline__ float block_rank(uint32_t (&counts)[16], uint32_t r, F value)
+{
+    if (threadIdx.x < 16) counts[threadIdx.x] = 0;
+    uint32_t key[N], at = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = value(i);
+    __syncthreads();
+#pragma unroll 1
+    for (uint32_t b = 0; b < 16; ++b) {
+        const uint32_t up = at | 0x80000000u >> b;
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) n += __popcll(__ballot(key[i] >= up));
+        if ((threadIdx.x & 63) == 0) atomicAdd(&counts[b], n);
+        __syncthreads();
+        if (counts[b] >= r) at = up;
+    }
+    return at <= key_of(NEG_INF) ? NEG_INF : logit_of(at);
+}
+
 // Sorts the first n (at most LIST) of list, descending; elements are all different.
 //
-// Few by their ranks, several threads counting for an element, two elements a read.  More by a bitonic network over registers:
-// element e * THREADS + thread, so that its steps are exchanges of lanes, of wavefronts (through the list) or of a thread's own.
-// (512 elements by the network with every step through LDS took 8 us, 2,048 16 us.)
+// Few by their ranks, several threads counting for an element, two elements a read.  More by bins (below), or, by 256 threads
+// and where most keys are the same, by a bitonic network over registers: element e * THREADS + thread, so that its steps are
+// exchanges of lanes, of wavefronts (through the list) or of a thread's own.
 typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
 template <int THREADS> __device__ __forceinline__ void sort_by_rank(uint64_t *list, uint32_t n)
 {
@@ -138,10 +171,90 @@ template <int THREADS, int EACH> __device__ __forceinline__ void sort_by_network
     __syncthreads();
 }
 
-template <int THREADS> __device__ __forceinline__ void sort_list(uint64_t *list, uint32_t n)
+// More than a few by 1,024 threads: into bins by their keys, and in a bin by rank.  False, with the list as it was, where one
+// bin gets more than CROWD of them.
+template <int THREADS> __device__ __forceinline__ bool sort_by_bins(uint64_t *list, uint32_t n, Scatter &s)
 {
-    if (n <= (THREADS < 384 ? THREADS : 384)) sort_by_rank<THREADS>(list, n);
-    else if (THREADS == 256 && n <= 512) sort_by_network<THREADS, 512 / 256>(list, n);
+    static_assert(THREADS == 1024 && LIST == 2 * THREADS && BINS == 2 * THREADS, "two of each a thread");
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads();
+    uint64_t own[2];
+    uint32_t low = ~0u, high = 0, at[2], bin[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        own[e] = e * THREADS + threadIdx.x < n ? list[e * THREADS + threadIdx.x] : 0;
+        const uint32_t key = own[e] >> 32;
+        if (own[e]) {
+            low = key < low ? key : low;
+            high = key > high ? key : high;
+        }
+        s.bins[e * THREADS + threadIdx.x] = 0;
+    }
+    if (threadIdx.x == 0) {
+        s.low = ~0u;
+        s.high = s.crowded = 0;
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        const uint32_t l = __shfl_xor(low, d), h = __shfl_xor(high, d);
+        low = l < low ? l : low;
+        high = h > high ? h : high;
+    }
+    __syncthreads();
+    if (lane == 0) {
+        atomicMin(&s.low, low);
+        atomicMax(&s.high, high);
+    }
+    __syncthreads();
+    high = s.high;
+    const uint32_t range = high - s.low, shift = range < BINS ? 0 : 21 - __clz(range);   // BINS = 2^11
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (!own[e]) continue;
+        bin[e] = (high - (uint32_t)(own[e] >> 32)) >> shift;
+        at[e] = atomicAdd(&s.bins[bin[e]], 1u);
+        if (at[e] >= CROWD) s.crowded = 1;
+    }
+    __syncthreads();
+    if (s.crowded) return false;
+    const uint32_t c0 = s.bins[2 * threadIdx.x], c1 = s.bins[2 * threadIdx.x + 1];
+    uint32_t run = c0 + c1;
+#pragma unroll
+    for (uint32_t d = 1; d < 64; d *= 2) {
+        const uint32_t o = __shfl_up(run, d);
+        if (lane >= d) run += o;
+    }
+    if (lane == 63) s.part[wave] = run;
+    __syncthreads();
+    uint32_t before = run - c0 - c1;
+    for (uint32_t w = 0; w < wave; ++w) before += s.part[w];
+    s.bins[2 * threadIdx.x] = before;
+    s.bins[2 * threadIdx.x + 1] = before + c0;
+    if (threadIdx.x == THREADS - 1) s.bins[BINS] = n;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (own[e]) s.list[s.bins[bin[e]] + at[e]] = own[e];
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (!own[e]) continue;
+        const uint32_t first = s.bins[bin[e]], last = s.bins[bin[e] + 1];
+        uint32_t to = first;
+        for (uint32_t i = first; i < last; ++i) to += s.list[i] > own[e];
+        list[to] = own[e];
+    }
+    __syncthreads();
+    return true;
+}
+
+template <int THREADS> __device__ __forceinline__ void sort_list(uint64_t *list, uint32_t n, Scatter *scatter)
+{
+    if (n <= (THREADS < 384 ? THREADS : 384)) return sort_by_rank<THREADS>(list, n);
+    if constexpr (THREADS == 1024) {
+        if (sort_by_bins<THREADS>(list, n, *scatter)) return;
+    }
+    if (THREADS == 256 && n <= 512) sort_by_network<THREADS, 512 / 256>(list, n);
     else if (n <= 1024) sort_by_network<THREADS, 1024 / THREADS>(list, n);
     else sort_by_network<THREADS, 2048 / THREADS>(list, n);
 }
@@ -190,9 +303,10 @@ template <class T, int THREADS, bool SUM> __device__ __forceinline__ MaxSum larg
         }
         a.m = m;
     };
-    uint32_t j = begin + threadIdx.x * VEC, group = 0;
+    uint32_t j = begin + threadIdx.x * VEC, group = 0, used = 0;
     auto close = [&] {   // a group ends, the last one goes on
         best[group][threadIdx.x] = own;
+        used = group + 1;
         if (group + 1 < GROUPS<THREADS>) {
             ++group;
             own = NEG_INF;
@@ -221,7 +335,9 @@ template <class T, int THREADS, bool SUM> __device__ __forceinline__ MaxSum larg
             take(one, std::integral_constant<int, VEC>{});
         }
         best[group][threadIdx.x] = own;
+        used = group + 1;
     }
+    for (; used < GROUPS<THREADS>; ++used) best[used][threadIdx.x] = NEG_INF;
     return a;
 }
 
@@ -315,65 +431,50 @@ __device__ __forceinline__ uint32_t list_by_histogram(const T *x, uint32_t begin
     }
 }
 
-// The first k of [begin, end), sorted in sh.list; their number (fewer than k where there are no more) and the part's
-// maximum and sum in `all`.
-template <class T, int THREADS, bool SUM>
-__device__ __forceinline__ uint32_t top_of(const T *x, uint32_t begin, uint32_t end, uint32_t k, float k2, Lds<THREADS> &sh, MaxSum &all)
+// The first k of [0, n), sorted in sh.list, and their number (fewer than k where there are no more), from the elements at or above
+// `least` in the groups of vectors whose largest logits are in sh.best; address(group * THREADS + thread, i): where the group's i-th
+// vector begins, NONE for no vector; i < per.
+template <class T, int THREADS, class F>
+__device__ __forceinline__ uint32_t list_of(const T *x, uint32_t n, uint32_t k, float least, float most, uint32_t per, Lds<THREADS> &sh, F address)
 {
-    constexpr uint32_t WAVES = THREADS / 64;
-    if (threadIdx.x == 0) sh.count = sh.threads = 0;
-    const MaxSum a = largest_of<T, THREADS, SUM>(x, begin, end, k2, sh.best);
-    // the wavefronts whose lanes all have elements
-    const float mine = a.m;
-    const uint32_t whole = (end - begin) / (64 * VEC) < WAVES ? (end - begin) / (64 * VEC) : WAVES, rank = whole ? (k + whole - 1) / whole : 65;
-    const float bound = rank > 64 ? NEG_INF : (threadIdx.x >> 6) < whole ? wave_rank(mine, rank) : -NEG_INF;
-    if ((threadIdx.x & 63) == 0) sh.bound[threadIdx.x >> 6] = bound;
-    all = block_join<THREADS>(a, sh.sums, k2);   // with the barrier that sh.bound needs
-    float least = sh.bound[0];
+    for (uint32_t g = 0; g < GROUPS<THREADS>; ++g) {
+        const float v = sh.best[g][threadIdx.x];
+        if (v >= least && v > NEG_INF) sh.who[atomicAdd(&sh.threads, 1u)] = g * THREADS + threadIdx.x;
+    }
+    __syncthreads();
+    const uint32_t loads = sh.threads * per;
+    for (uint32_t i0 = threadIdx.x; i0 < loads; i0 += 4 * THREADS) {   // four loads in flight
+        uint32_t at[4];
+        Vec<T> x8[4];
 #pragma unroll
-    for (uint32_t w = 1; w < WAVES; ++w) least = fminf(least, sh.bound[w]);
-
-    // a group's vectors: as many as the last one may have
-    const uint32_t vectors = (end - begin + THREADS * VEC - 1) / (THREADS * VEC);
-    const uint32_t per = vectors > GROUPS<THREADS> * DEPTH<T> ? vectors - (GROUPS<THREADS> - 1) * DEPTH<T> : DEPTH<T>;
-    uint32_t n = NONE;
-    if (rank <= MOST_RANK || end - begin <= LIST) {
-        const uint32_t first = begin + threadIdx.x * VEC, own = first < end ? (end - first + THREADS * VEC - 1) / (THREADS * VEC) : 0;
-        for (uint32_t g = 0; g < GROUPS<THREADS> && g * DEPTH<T> < own; ++g) {
-            const float v = sh.best[g][threadIdx.x];
-            if (v >= least && v > NEG_INF) sh.who[atomicAdd(&sh.threads, 1u)] = g * THREADS + threadIdx.x;
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t i = i0 + b * THREADS, j = i < loads ? address(sh.who[i / per], i % per) : NONE;
+            at[b] = j < n ? j : NONE;
+            if (at[b] != NONE) x8[b] = load_some(x + j, n - j);
         }
-        __syncthreads();
-        const uint32_t all = sh.threads * per;
-        for (uint32_t i0 = threadIdx.x; i0 < all; i0 += 4 * THREADS) {   // four loads in flight
-            uint32_t at[4];
-            Vec<T> x8[4];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const uint32_t i = i0 + b * THREADS, who = i < all ? sh.who[i / per] : 0, g = who / THREADS, v = g * DEPTH<T> + i % per;
-                const uint32_t j = begin + (v * THREADS + who % THREADS) * VEC;
-                at[b] = i < all && j < end && (g + 1 == GROUPS<THREADS> || i % per < DEPTH<T>) ? j : NONE;
-                if (at[b] != NONE) x8[b] = load_some(x + j, end - j);
-            }
+        for (int b = 0; b < 4; ++b) {
+            if (at[b] == NONE) continue;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (at[b] == NONE) continue;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float v = vec_at(x8[b], e);
-                    if (v >= least && v > NEG_INF && at[b] + e < end) {
-                        const uint32_t to = atomicAdd(&sh.count, 1u);
-                        if (to < LIST) sh.list[to] = element(v, at[b] + e);
-                    }
+            for (int e = 0; e < VEC; ++e) {
+                const float v = vec_at(x8[b], e);
+                if (v >= least && v > NEG_INF && at[b] + e < n) {
+                    const uint32_t to = atomicAdd(&sh.count, 1u);
+                    if (to < LIST) sh.list[to] = element(v, at[b] + e);
                 }
             }
         }
-        __syncthreads();
-        n = sh.count;
     }
-    if (n > LIST) n = list_by_histogram<T, THREADS>(x, begin, end, k, least, all.m, sh);
-    sort_list<THREADS>(sh.list, n);
-    return n;
+    __syncthreads();
+    uint32_t listed = sh.count;
+    if (listed > LIST) listed = list_by_histogram<T, THREADS>(x, 0, n, k, least, most, sh);
+    sort_list<THREADS>(sh.list, listed, sh.scatter);
+    return listed;
+}
+
+template <int THREADS> __device__ __forceinline__ float least_of(uint32_t k, Lds<THREADS> &sh)
+{
+    return block_rank<THREADS, GROUPS<THREADS>>(sh.counts, k, [&](uint32_t g) { return key_of(sh.best[g][threadIdx.x]); });
 }
 
 // Place i of the answer.
@@ -384,76 +485,40 @@ __device__ __forceinline__ void put(uint32_t i, uint32_t n, const uint64_t *list
 }
 
 template <class T, int THREADS, bool SUM>
-__global__ __launch_bounds__(THREADS, 8) void k_top(const T *logits, uint32_t n_vocab, uint64_t stride, uint32_t k, float inv_t, uint32_t *__restrict__ ids,
+__global__ __launch_bounds__(THREADS, 8) void k_top(const T *logits, uint32_t n, uint64_t stride, uint32_t k, float inv_t, uint32_t *__restrict__ ids,
                                                  uint64_t ids_stride, float *__restrict__ out, uint64_t out_stride, float *__restrict__ lse)
 {
     __shared__ Lds<THREADS> sh;
+    constexpr uint32_t WAVES = THREADS / 64, STEP = THREADS * VEC;
     const uint64_t row = blockIdx.x;
-    MaxSum a;
-    const uint32_t n = top_of<T, THREADS, SUM>(logits + row * stride, 0, n_vocab, k, LOG2E * inv_t, sh, a);
-    for (uint32_t i = threadIdx.x; i < k; i += THREADS) put(i, n, sh.list, ids + row * ids_stride, out + row * out_stride);
-    if (SUM && threadIdx.x == 0) lse[row] = empty(a) ? NEG_INF : a.m * inv_t + log_of(a.s);
-}
-
-// Few long rows with a short list: every piece's first k, then the first k of those.
-template <class T, bool SUM>
-__global__ __launch_bounds__(PIECE_THREADS) void k_top_pieces(const T *logits, uint32_t n_vocab, uint64_t stride, uint32_t k, float inv_t,
-                                                              uint64_t *__restrict__ lists, MaxSum *__restrict__ sums)
-{
-    __shared__ Lds<PIECE_THREADS> sh;
-    const uint64_t row = blockIdx.y, piece = row * gridDim.x + blockIdx.x;
-    const uint32_t begin = blockIdx.x * PIECE, end = n_vocab - begin < PIECE ? n_vocab : begin + PIECE;
-    MaxSum a;
-    const uint32_t n = top_of<T, PIECE_THREADS, SUM>(logits + row * stride, begin, end, k, LOG2E * inv_t, sh, a);
-    for (uint32_t i = threadIdx.x; i < k; i += PIECE_THREADS) lists[piece * k + i] = i < n ? sh.list[i] : 0;
-    if (SUM && threadIdx.x == 0) sums[piece] = a;
-}
-
-constexpr int JOIN_THREADS = 1024;
-template <bool SUM>
-__global__ __launch_bounds__(JOIN_THREADS) void k_top_join(const uint64_t *__restrict__ lists, const MaxSum *__restrict__ sums, uint32_t pieces,
-                                                            uint32_t k, float inv_t, uint32_t *__restrict__ ids, uint64_t ids_stride,
-                                                            float *__restrict__ out, uint64_t out_stride, float *__restrict__ lse)
-{
-    __shared__ struct {
-        uint64_t list[LIST] __attribute__((aligned(16)));
-        MaxSum sums[16];
-        uint32_t count;
-    } sh;
-    const uint64_t row = blockIdx.x;
-    if (threadIdx.x == 0) sh.count = 0;
-    __syncthreads();
-    for (uint32_t i = threadIdx.x; i < pieces * k; i += JOIN_THREADS) {
-        const uint64_t e = lists[row * pieces * k + i];
-        if (e) sh.list[atomicAdd(&sh.count, 1u)] = e;
+    const T *x = logits + row * stride;
+    const float k2 = LOG2E * inv_t;
+    if (threadIdx.x == 0) sh.count = sh.threads = 0;
+    const MaxSum a = largest_of<T, THREADS, SUM>(x, 0, n, k2, sh.best);
+    // the wavefronts whose lanes all have elements
+    const uint32_t whole = n / (64 * VEC) < WAVES ? n / (64 * VEC) : WAVES, rank = whole ? (k + whole - 1) / whole : 65;
+    MaxSum all;
+    float least;
+    if (rank <= QUICK_RANK) {
+        const float bound = (threadIdx.x >> 6) < whole ? wave_rank(a.m, rank) : -NEG_INF;
+        if ((threadIdx.x & 63) == 0) sh.bound[threadIdx.x >> 6] = bound;
+        all = block_join<THREADS>(a, sh.sums, k2);   // with the barrier that sh.bound needs
+        least = sh.bound[0];
+#pragma unroll
+        for (uint32_t w = 1; w < WAVES; ++w) least = fminf(least, sh.bound[w]);
+    } else {
+        all = block_join<THREADS>(a, sh.sums, k2);
+        least = least_of<THREADS>(k, sh);
     }
-    MaxSum a{NEG_INF, 0.f};
-    if (SUM && threadIdx.x < pieces) a = sums[row * pieces + threadIdx.x];
-    if (SUM) a = block_join<JOIN_THREADS>(a, sh.sums, LOG2E * inv_t);
-    __syncthreads();
-    const uint32_t n = sh.count;
-    sort_list<JOIN_THREADS>(sh.list, n);
-    for (uint32_t i = threadIdx.x; i < k; i += JOIN_THREADS) put(i, n, sh.list, ids + row * ids_stride, out + row * out_stride);
-    if (SUM && threadIdx.x == 0) lse[row] = empty(a) ? NEG_INF : a.m * inv_t + log_of(a.s);
-}
-
-// ---------------------------------------------------------------------------------------------
-// host side
-
-constexpr uint32_t MOST_SPLIT = 64;
-struct Split {
-    uint32_t pieces;   // 0: rows are not split
-    uint64_t sums, total;
-};
-Split layout_of(uint32_t n_rows, uint32_t n_vocab, uint32_t k)
-{
-    Split L{0, 0, 256};
-    const uint32_t pieces = (n_vocab + PIECE - 1) / PIECE;
-    if (n_vocab < 8 * PIECE || n_rows > MOST_SPLIT || pieces * k > LIST) return L;
-    L.pieces = pieces;
-    L.sums = ((uint64_t)n_rows * pieces * k * 8 + 255) & ~255ull;
-    L.total = L.sums + (((uint64_t)n_rows * pieces * sizeof(MaxSum) + 255) & ~255ull);
-    return L;
+    // a group's vectors: as many as the last one may have
+    const uint32_t vectors = (n + STEP - 1) / STEP;
+    const uint32_t per = vectors > GROUPS<THREADS> * DEPTH<T> ? vectors - (GROUPS<THREADS> - 1) * DEPTH<T> : DEPTH<T>;
+    const uint32_t listed = list_of<T, THREADS>(x, n, k, least, all.m, per, sh, [&](uint32_t who, uint32_t i) {
+        const uint32_t g = who / THREADS;
+        return g + 1 == GROUPS<THREADS> || i < DEPTH<T> ? ((g * DEPTH<T> + i) * THREADS + who % THREADS) * VEC : NONE;
+    });
+    for (uint32_t i = threadIdx.x; i < k; i += THREADS) put(i, listed, sh.list, ids + row * ids_stride, out + row * out_stride);
+    if (SUM && threadIdx.x == 0) lse[row] = empty(all) ? NEG_INF : all.m * inv_t + log_of(all.s);
 }
 
 }  // namespace
@@ -461,15 +526,17 @@ Split layout_of(uint32_t n_rows, uint32_t n_vocab, uint32_t k)
 
 using namespace tt;
 
+namespace {
+// Nothing needs to be kept: a row is one workgroup's, few rows too.  (One row of 131,328 bfloat16 with its log-sum-exp, 20 listed, is 15.9 us;
+// with its maxima and sums by 17 workgroups and the rest by one it was 17.5 us, with the pieces' own lists joined 19.4.)
+constexpr uint64_t WORKSPACE = 256;
+}  // namespace
+
 extern "C" int toktier_top_logits_workspace_bytes(uint32_t n_rows, uint32_t n_vocab, uint32_t k, uint64_t *out_bytes)
 {
     if (!out_bytes || n_vocab == 0 || n_vocab > TOKTIER_MAX_VOCAB || n_rows > 0x7FFFFFFFu || k == 0 || k > TOKTIER_MAX_TOP)
         return TOKTIER_E_INVALID_ARG;
-    // what any call of up to n_rows rows, n_vocab IDs and k places needs: pieces * k <= LIST in all of them
-    const uint64_t rows = std::clamp(n_rows, 1u, MOST_SPLIT), pieces = (n_vocab + PIECE - 1) / PIECE;
-    *out_bytes = 256;
-    if (n_vocab >= 8 * PIECE)
-        *out_bytes = ((rows * std::min<uint64_t>(LIST, pieces * k) * 8 + 255) & ~255ull) + ((rows * pieces * sizeof(MaxSum) + 255) & ~255ull);
+    *out_bytes = WORKSPACE;
     return TOKTIER_OK;
 }
 
@@ -484,14 +551,13 @@ extern "C" int toktier_top_logits(const void *logits, int type, uint32_t n_rows,
     if (!matrix_ok(logits, type, n_rows, n_vocab, stride) || !matrix_ok(out_ids, TOKTIER_F32, n_rows, k, out_ids_stride) ||
         !matrix_ok(out_logits, TOKTIER_F32, n_rows, k, out_logits_stride) || !aligned4(lse) || !workspace || ((uintptr_t)workspace & 255u))
         return TOKTIER_E_INVALID_ARG;
-    const Split L = layout_of(n_rows, n_vocab, k);
-    if (workspace_bytes < L.total) return TOKTIER_E_CAPACITY;
+    if (workspace_bytes < WORKSPACE) return TOKTIER_E_CAPACITY;
     struct Area {
         const void *p;
         uint64_t n;
     };
     const Area in{logits, extent(type, n_rows, n_vocab, stride)};
-    const Area out[] = {{workspace, L.total}, {out_ids, extent(TOKTIER_F32, n_rows, k, out_ids_stride)},
+    const Area out[] = {{workspace, WORKSPACE}, {out_ids, extent(TOKTIER_F32, n_rows, k, out_ids_stride)},
                         {out_logits, extent(TOKTIER_F32, n_rows, k, out_logits_stride)}, {lse, lse ? 4ull * n_rows : 0}};
     for (int i = 0; i < 4; ++i) {
         if (!apart(out[i].p, out[i].n, in.p, in.n)) return TOKTIER_E_INVALID_ARG;
@@ -505,14 +571,6 @@ extern "C" int toktier_top_logits(const void *logits, int type, uint32_t n_rows,
         auto with_sum = [&](auto sum) {
             constexpr bool SUM = decltype(sum)::value;
             const T *x = (const T *)logits;
-            if (L.pieces) {
-                uint64_t *lists = (uint64_t *)workspace;
-                MaxSum *sums = (MaxSum *)((uint8_t *)workspace + L.sums);
-                k_top_pieces<T, SUM><<<dim3(L.pieces, n_rows), PIECE_THREADS, 0, s>>>(x, n_vocab, stride, k, inv_t, lists, sums);
-                k_top_join<SUM><<<n_rows, JOIN_THREADS, 0, s>>>(lists, sums, L.pieces, k, inv_t, out_ids, out_ids_stride, out_logits,
-                                                                 out_logits_stride, lse);
-                return;
-            }
             auto launch = [&](auto threads) {
                 constexpr int N = decltype(threads)::value;
                 in_launches(n_rows, N, [&](uint64_t r, uint32_t rows) {
@@ -520,7 +578,7 @@ extern "C" int toktier_top_logits(const void *logits, int type, uint32_t n_rows,
                                                            out_logits + r * out_logits_stride, out_logits_stride, lse ? lse + r : nullptr);
                 });
             };
-            if (n_vocab <= 256 * VEC * 4) launch(std::integral_constant<int, 256>{});
+            if (n_vocab <= 256 * VEC * 4 && k <= 256) launch(std::integral_constant<int, 256>{});
             else launch(std::integral_constant<int, 1024>{});
         };
         if (lse) with_sum(std::true_type{});
