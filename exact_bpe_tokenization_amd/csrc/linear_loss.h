@@ -605,6 +605,14 @@ template <class F> void with_split(uint32_t dim, uint32_t n_rows, uint32_t k_ste
     else f(Tiny{}, tiny.first);
 }
 
+// The IDs, in whole pads, whose tiles make up to 2^31 threads: a launch of 2^32 or more runs a part of them and reports success.
+// Other launches are far smaller, as G and the columns are.
+template <class TILE> uint32_t most_ids(uint32_t n_rows)
+{
+    const uint64_t ids = (1ull << 31) / TILE::THREADS / tiles(n_rows, TILE::N) * TILE::M;
+    return (uint32_t)std::min<uint64_t>(1u << 30, ids / PAD * PAD);
+}
+
 template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipStream_t s)
 {
     Rows rows;
@@ -658,7 +666,7 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
             using TILE = decltype(t);
             span = TILE::TM * 16;
             for (uint32_t first = 0; first < c.n_vocab;) {
-                uint32_t most = as_is ? z.v_pad : most_packed;
+                uint32_t most = std::min((uint32_t)(as_is ? z.v_pad : most_packed), most_ids<TILE>(c.n_rows));
                 if (first < keep) most = std::min(most, keep - first);
                 const uint32_t ids = std::min(most, c.n_vocab - first), m_tiles = tiles(ids, TILE::M);
                 const Operand w = table(first, ids);

@@ -281,6 +281,28 @@ def test_offsets_past_32_bits(tt):
     plain.close(gw[others], rest.expand(5, d), (e + plain.rounding(rest.abs() + e, BF16)).expand(5, d), "far zeros")
 
 
+def test_more_tiles_than_one_launch_takes(tt):
+    """2^19 rows and as many IDs that the tiles of all of them would have more than 2^32 threads."""
+    _say("linear many tiles")
+    n, v, d = 1 << 19, (1 << 20) + 300, 64
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    w = (torch.randn(v, d, generator=gen, device="cuda") * 0.3).to(BF16)
+    h = torch.randn(n, d, generator=gen, device="cuda").to(BF16)
+    y = torch.randint(0, v, (n,), generator=gen, device="cuda", dtype=torch.int32)
+    loss, lse = torch.full((n,), 7.0, device="cuda"), torch.full((n,), 7.0, device="cuda")
+    ws = torch.empty(tt.toktier_linear_cross_entropy_workspace_bytes(n, v, d, BF16, grads=False), dtype=torch.uint8,
+                     device="cuda")
+    tt.toktier_linear_cross_entropy(h, w, y, loss, lse, ws)
+    some = torch.cat([torch.arange(0, n, n // 61, device="cuda"), torch.tensor([n - 1, n - 257, n // 2 - 1], device="cuda")])
+    x = torch.mm(h[some].double(), w.double().t().contiguous())
+    z = torch.logsumexp(x, 1)
+    ref = z - x.gather(1, y[some].long().unsqueeze(1)).squeeze(1)
+    dx = (d + 1) * 2 * plain.U * torch.mm(h[some].double().abs(), w.double().abs().t().contiguous()).amax(1)
+    err = 3 * dx + plain.U * (8 * 104 + 3 * (v // 256 + 64))
+    plain.close(lse[some], z, err + 4 * plain.U * z.abs(), "many tiles lse")
+    plain.close(loss[some], ref, err + 4 * plain.U * (z.abs() + ref.abs()), "many tiles loss")
+
+
 def test_against_differences(tt):
     """The gradients' slopes along random directions against differences of the 64-bit loss."""
     _say("linear differences")
