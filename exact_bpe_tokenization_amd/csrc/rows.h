@@ -74,15 +74,19 @@ template <class T, int THREADS, int HELD> struct RowPart {
         for (int k = 0; k < VEC; ++k) x8[k] = vec_at(v, k);
         f(j, (uint32_t)VEC, x8);
     }
+    // brings what is held on its way; each<true> does so itself
+    __device__ __forceinline__ void hold()
+    {
+        const uint32_t j0 = begin + threadIdx.x * VEC;
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            if (j0 + i * STEP + VEC <= end) held[i] = load_vec(x + j0 + i * STEP);
+    }
     // f(index, elements, values): values past the row's end are `fill`
     template <bool FIRST, class F> __device__ __forceinline__ void each(float fill, F f)
     {
         const uint32_t j0 = begin + threadIdx.x * VEC;
-        if constexpr (FIRST) {
-#pragma unroll
-            for (int i = 0; i < HELD; ++i)
-                if (j0 + i * STEP + VEC <= end) held[i] = load_vec(x + j0 + i * STEP);
-        }
+        if constexpr (FIRST) hold();
 #pragma unroll
         for (int i = 0; i < HELD; ++i)
             if (j0 + i * STEP + VEC <= end) with(held[i], j0 + i * STEP, f);
