@@ -267,6 +267,16 @@ struct Logits {
     MaxSum *sums;
 };
 
+// What exp(x - m) = exp2(x log2(e) - from) takes off.  The product may be beyond the numbers of 32 bits: such an m comes off column
+// j of the logits first.
+template <class TILE> __device__ __forceinline__ float power_base(f32x4 (&acc)[TILE::TM][TILE::TN], int j, float m)
+{
+    if (__builtin_fabsf(m) < 1e38f) return m * LOG2E;
+#pragma unroll
+    for (int i = 0; i < TILE::TM; ++i) acc[i][j] -= m;
+    return 0.f;
+}
+
 template <class T, class TILE, Use USE>
 __device__ __forceinline__ void logits_tile(const Logits &a, uint32_t m0, uint32_t n0, uint32_t count, lds_u8 *lds, T *g, uint32_t g_cols)
 {
@@ -302,7 +312,7 @@ __device__ __forceinline__ void logits_tile(const Logits &a, uint32_t m0, uint32
             if (y < TILE::TM * 16 && (y & 15) < 4) rows.at_target[n] = at;
             m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
-            const float from = m == NEG_INF ? 0.f : m * LOG2E;
+            const float from = m == NEG_INF ? 0.f : power_base<TILE>(acc, j, m);
             float s = 0.f;
 #pragma unroll
             for (int i = 0; i < TILE::TM; ++i) {
@@ -321,7 +331,7 @@ __device__ __forceinline__ void logits_tile(const Logits &a, uint32_t m0, uint32
         } else {
             // padding, rows and IDs, is zeros whatever the products are: the other two products run over it
             const bool row = n < count;
-            const float c = rows.factor[n] * rows.head->scale, from = rows.shift[n] * LOG2E, r = rows.recip[n];
+            const float c = rows.factor[n] * rows.head->scale, from = power_base<TILE>(acc, j, rows.shift[n]), r = rows.recip[n];
             T *to = g + (uint64_t)n * g_cols + m_lane;
 #pragma unroll
             for (int i = 0; i < TILE::TM; ++i) {

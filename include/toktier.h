@@ -463,8 +463,10 @@ int toktier_cross_entropy_backward(const void *logits, int type, uint32_t n_rows
  * A row whose target is no ID takes no part: its hidden state is not used, its loss and lse are 0, its grad_hidden is
  * zeros, and products are formed for the other rows alone.
  * Products are summed in 32 bits; G enters the second two as numbers of `type` (for float16 times a power of two that brings
- * the largest |c_i| to 2^14 .. 2^15; what lies below 2^-39 of it is lost), each gradient is rounded once at the end.  The
- * order of every sum is fixed by the sizes, the types, the alignment of the table and the targets that are IDs.
+ * the largest |c_i| to 2^14 .. 2^15; what lies below 2^-39 of it is lost).  Where loss and gradients come from one call, the
+ * exponentials of the first IDs wait in the workspace as numbers of `type` for the row's sum, so that G is rounded twice there
+ * (but at the target).  Each gradient is rounded once at the end.  The order of every sum is fixed by the sizes, the types, the
+ * alignment of the table and the targets that are IDs.
  * Values that are not finite go through the products as products do; a row with a logit that is NaN or +inf has a NaN
  * loss, one whose logits are all -inf the loss +inf and no part in the gradients' sums beyond 0 * weight.
  *   hidden, weight  device, n_rows and n_vocab rows of dim elements of `type`; n_rows <= TOKTIER_MAX_LINEAR_ROWS,
@@ -492,7 +494,8 @@ int toktier_linear_cross_entropy(const void *hidden, int type, uint32_t n_rows, 
                                  uint64_t grad_weight_stride, int accumulate, void *workspace, uint64_t workspace_bytes,
                                  void *stream);
 
-/* The gradients alone, later, from the lse that toktier_linear_cross_entropy wrote for the same arguments. */
+/* The gradients alone, later, from the lse that toktier_linear_cross_entropy wrote for the same arguments.  A rounding of lse is
+ * relative to it, so that the probabilities are off by about |lse| 2^-24; the one call takes them from the row's maximum and sum. */
 int toktier_linear_cross_entropy_backward(const void *hidden, int type, uint32_t n_rows, uint32_t dim,
                                           uint64_t hidden_stride, const void *weight, uint32_t n_vocab,
                                           uint64_t weight_stride, const uint32_t *targets, const float *lse,

@@ -228,6 +228,36 @@ def test_sizes_of_logits(tt, dtype, size, lift):
     case.check(o, "sizes")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,v,d", [(3, 500, 64), (300, 40000, 64)])
+def test_logits_at_the_end_of_the_range(tt, n, v, d, dtype):
+    """Logits around -+3e38, whose product with log2(e) has no number: equal ones share the probability, far ones have none."""
+    _say("linear range", n, v, d, dtype)
+    h = torch.zeros(n, d, dtype=dtype, device="cuda")
+    w = torch.zeros(v, d, dtype=dtype, device="cuda")
+    big = torch.full((1,), 1.7e19, dtype=dtype, device="cuda")
+    w[:, 0], h[0, 0], h[1, 0] = -big, big, -big    # row 0: all logits -2.9e38, row 1: all 2.9e38
+    w[v // 2:, 1], h[2, 1] = -big, big             # row 2: one half 0, the other -2.9e38
+    y = torch.full((n,), 7, dtype=torch.int32, device="cuda")
+    loss, lse, gw = torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty(v, d, device="cuda")
+    ws = torch.empty(tt.toktier_linear_cross_entropy_workspace_bytes(n, v, d, dtype), dtype=torch.uint8, device="cuda")
+    tt.toktier_linear_cross_entropy(h, w, y, loss, lse, ws, grad_weight=gw, grad_scale=2.0 ** -40)
+    x = torch.zeros(n, v, dtype=torch.float64, device="cuda")
+    x[0], x[1], x[2, v // 2:] = -big.double() ** 2, big.double() ** 2, -big.double() ** 2
+    z = torch.logsumexp(x, 1)
+    plain.close(lse, z, 4 * plain.U * z.abs() + plain.U * (8 * 104 + 3 * (v // 16 + 64)), "range lse")
+    ref = (x.amax(1) - x[:, 7]) + torch.log(torch.exp(x - x.amax(1, keepdim=True)).sum(1))
+    plain.close(loss, ref, 4 * plain.U * ref.abs() + plain.U * (8 * 104 + 3 * (v // 16 + 64)), "range loss")
+    p = torch.exp(x - x.amax(1, keepdim=True))
+    g = p / p.sum(1, keepdim=True)
+    g[:, 7] -= 1.0
+    g *= 2.0 ** -40
+    ref = torch.mm(g.t().contiguous(), h.double())
+    # G is kept rounded, and so are the exponentials; the powers' and sums' errors are below 2^-12
+    err = torch.mm(g.abs().t().contiguous(), h.double().abs()) * (2 * plain.rounding(torch.ones((), dtype=torch.float64, device="cuda"), dtype) + 2.0 ** -12)
+    plain.close(gw, ref, err, "range grad_weight")
+
+
 def test_float16_keeps_small_probabilities(tt):
     """131,072 equal logits: every probability is 2^-17, and times c far below float16's numbers."""
     _say("linear float16 small")
