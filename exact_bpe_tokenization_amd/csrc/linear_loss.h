@@ -108,10 +108,18 @@ struct Rows {             // of the packed rows
 // ---------------------------------------------------------------------------------------------
 // rows
 
-// A row of n elements to one of n_pad, zeros behind it (or throughout), by the lanes of a wavefront.
-template <class T> __device__ __forceinline__ void copy_row(T *to, const T *from, uint32_t n, uint32_t n_pad)
+// A row of n elements to one of n_pad, zeros behind it (or throughout), by the lanes of a wavefront, four vectors on their way.
+template <class T> __device__ __forceinline__ void copy_row(T *__restrict__ to, const T *__restrict__ from, uint32_t n, uint32_t n_pad)
 {
-    for (uint32_t j = (threadIdx.x & 63) * VEC; j < n_pad; j += 64 * VEC) {
+    uint32_t j = (threadIdx.x & 63) * VEC;
+    for (; from && j + 3 * 64 * VEC + VEC <= n; j += 4 * 64 * VEC) {
+        Vec<T> v[4];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) v[i] = load_vec(from + j + i * 64 * VEC);
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) store_vec(to + j + i * 64 * VEC, v[i]);
+    }
+    for (; j < n_pad; j += 64 * VEC) {
         float x[VEC] = {};
         if (from && j < n) load_part(from + j, n - j, 0.f, x);
         store_vec(to + j, x);
@@ -555,7 +563,10 @@ template <class T, class TILE, class OUT> __device__ __forceinline__ void weight
 #pragma unroll
             for (int e = 0; e < VEC; ++e) x[e] += was[e];
         }
-        store_part(to, a.dim - m, x);
+        // past the caches for 16 bits (16 rows into 131,328 x 4,096 bfloat16: 420 -> 335 us; float32 loses, 128 rows into
+        // 33,024 x 1,024: 92 -> 115 us)
+        if constexpr (sizeof(OUT) == 2) stream_part(to, a.dim - m, x);
+        else store_part(to, a.dim - m, x);
     });
 }
 

@@ -57,12 +57,12 @@ template <class T> __device__ __forceinline__ Vec<T> to_vec(const float (&x)[VEC
     return v;
 }
 
-template <class T> __device__ __forceinline__ void store_vec(T *p, const float (&x)[VEC])
+template <class T> __device__ __forceinline__ void store_vec(T *p, const Vec<T> &v)
 {
-    const Vec<T> v = to_vec<T>(x);
     *(u32x4_row *)p = v.a;
     if constexpr (sizeof(T) == 4) *(u32x4_row *)(p + 4) = v.b;
 }
+template <class T> __device__ __forceinline__ void store_vec(T *p, const float (&x)[VEC]) { store_vec(p, to_vec<T>(x)); }
 
 // Up to eight elements (n of them) where a row ends inside a vector.
 template <class T> __device__ __forceinline__ void load_part(const T *p, uint32_t n, float fill, float (&x)[VEC])
