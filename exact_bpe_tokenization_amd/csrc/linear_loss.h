@@ -366,7 +366,7 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void k_logits(Logits a, uint32_t 
     __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::LDS];
     // (of G every row up to a whole step of k is written: the product for dW reads it so)
     const uint32_t count = a.rows.head->count, reach = USE == G_AGAIN ? (count + STEP_K<T> - 1) / STEP_K<T> * STEP_K<T> : count;
-    with_place<TILE>(m_tiles, (reach + TILE::N - 1) / TILE::N, [&](auto tile, uint32_t m0, uint32_t n0) {
+    with_place<TILE>(m_tiles, a.w.count * a.w.stride, reach, [&](auto tile, uint32_t m0, uint32_t n0) {
         logits_tile<T, decltype(tile), USE>(a, m0, n0, count, (lds_u8 *)shared, g, g_cols);
     });
 }
@@ -571,10 +571,10 @@ template <class T, class TILE, class OUT> __device__ __forceinline__ void weight
 }
 
 template <class T, class TILE, class OUT>
-__global__ __launch_bounds__(TILE::THREADS, 2) void k_grad_weight(Weights a, uint32_t m_tiles, uint32_t n_tiles, OUT *__restrict__ out)
+__global__ __launch_bounds__(TILE::THREADS, 2) void k_grad_weight(Weights a, uint32_t m_tiles, OUT *__restrict__ out)
 {
     __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::LDS];
-    with_place<TILE>(m_tiles, n_tiles,
+    with_place<TILE>(m_tiles, (uint64_t)a.rows.head->count * a.h.stride, a.ids,
                      [&](auto tile, uint32_t m0, uint32_t n0) { weight_tile<T, decltype(tile), OUT>(a, m0, n0, (lds_u8 *)shared, out); });
 }
 
@@ -749,11 +749,11 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
                 using OUT = decltype(o);
                 with_tile(c.dim, ids, [&](auto t) {
                     using TILE = decltype(t);
-                    const uint32_t m_tiles = tiles(c.dim, TILE::M), n_tiles = tiles(ids, TILE::N);
-                    k_grad_weight<T, TILE, OUT><<<tile_blocks<TILE>(m_tiles, n_tiles), TILE::THREADS, 0, s>>>(
+                    const uint32_t m_tiles = tiles(c.dim, TILE::M);
+                    k_grad_weight<T, TILE, OUT><<<tile_blocks<TILE>(m_tiles, tiles(ids, TILE::N)), TILE::THREADS, 0, s>>>(
                         Weights{Operand{hidden, row, z.dim_pad}, Operand{go, (uint64_t)width * z.elem, width}, ids, c.dim, c.accumulate, rows,
                                 c.grad_weight_stride},
-                        m_tiles, n_tiles, (OUT *)c.grad_weight + first * c.grad_weight_stride);
+                        m_tiles, (OUT *)c.grad_weight + first * c.grad_weight_stride);
                 });
             };
             if (c.grad_weight_type == c.type) weights(T{});

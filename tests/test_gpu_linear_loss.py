@@ -137,6 +137,25 @@ def test_large_tiles_and_pieces(tt, n, v, d, dtype):
     case.check(o, "large")
 
 
+@pytest.mark.parametrize("n,v,d,dtype", [
+    (300, 33124, 512, BF16), (300, 33124, 512, F16), (300, 33124, 256, F32),   # IDs too
+    (640, 33001, 200, F16), (385, 33024, 320, BF16),
+    (300, 131328, 768, BF16),                                                  # a table that the cache does not hold
+    (1350, 66000, 64, BF16),                                                   # strips at the end too
+])
+def test_last_tiles_that_are_half_empty(tt, n, v, d, dtype):
+    _say("linear halves", n, v, d, dtype)
+    case = Case(n, v, d, dtype, ignored=0.05)
+    ws = case.workspace(tt)
+    o = case.outputs()
+    case.forward(tt, o, ws)
+    case.check(o, "one call")
+    later = case.outputs()
+    later["loss"], later["lse"] = o["loss"], o["lse"].clone()
+    case.backward(tt, later, ws.fill_(0x5A))
+    case.check(later, "later", from_lse=True)
+
+
 def test_pieces_of_a_copied_table(tt):
     _say("linear copied pieces")
     case = Case(200, 40000, 2050, BF16, ignored=0.1, pad=1)   # 164 MB of table: two pieces for the loss
