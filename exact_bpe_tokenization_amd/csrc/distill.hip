@@ -196,8 +196,11 @@ __device__ __forceinline__ void put_grad(RowPart<T, THREADS, HELD> &part, const 
     }
 }
 
+// Wavefronts of a SIMD: all eight have 64 registers each, in which 256 threads' parts of a list and of a row of 32 bits do not find room.
+template <class T, int THREADS> constexpr int waves = sizeof(T) == 4 && THREADS == 256 ? 6 : 8;
+
 template <class T, int THREADS, int HELD>
-__global__ __launch_bounds__(THREADS, 8) void k_distill(const T *logits, uint32_t n_vocab, uint64_t stride, Teacher t, uint32_t slots, float inv_t,
+__global__ __launch_bounds__(THREADS, (waves<T, THREADS>)) void k_distill(const T *logits, uint32_t n_vocab, uint64_t stride, Teacher t, uint32_t slots, float inv_t,
                                                         float *__restrict__ loss, float *__restrict__ lse_out,
                                                         const float *__restrict__ grad_loss, float grad_scale, T *grad, uint64_t gstride)
 {
@@ -288,6 +291,7 @@ __global__ __launch_bounds__(PIECE_THREADS) void k_distill_join(const T *logits,
 // maximum and sum are formed again, by one workgroup, since in place the others would read what it has written.
 constexpr float FAR = 128.f;
 
+// (Of float32 nine registers are spilled; with six wavefronts and none spilled 2,048 rows of 131,328 take 465 us in place of 419.)
 template <class T, int THREADS>
 __global__ __launch_bounds__(THREADS, 8) void k_distill_backward(const T *logits, uint32_t n_vocab, uint64_t stride, Teacher t, uint32_t slots,
                                                                  float inv_t, float temperature, const float *__restrict__ lse,
