@@ -290,12 +290,11 @@ template <class T, int THREADS, bool SUM> __device__ __forceinline__ MaxSum larg
         if constexpr (SUM) {
             float s[4] = {};
             const float from = m == NEG_INF ? 0.f : m * k2;   // nothing but -inf so far, or NaN: those are in the sums
-            if (__builtin_fabsf(from) < 1e30f) {
-                s[0] = a.s * __builtin_amdgcn_exp2f(m == NEG_INF ? 0.f : __builtin_fmaf(a.m, k2, -from));
+            s[0] = a.s * (m == NEG_INF ? 1.f : exp_f(a.m - m, k2));   // exactly 1 where the maximum stays
+            if (__builtin_fabsf(from) < 65536.f) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) s[i & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(vec_at(v[i / VEC], i % VEC), k2, -from));
-            } else {   // the product may be beyond the type's numbers
-                s[0] = a.s * exp_f(a.m - m, k2);
+            } else {   // the rounding may be beyond a power's range, the product beyond the type's numbers
 #pragma unroll
                 for (int i = 0; i < N; ++i) s[i & 3] += exp_f(vec_at(v[i / VEC], i % VEC) - m, k2);
             }

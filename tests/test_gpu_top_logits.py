@@ -164,6 +164,14 @@ def test_strides(tt, pad, lead, dtype):
         assert bool((wide[:, :1] == 9).all()) and bool((wide[:, k + 1:] == 9).all())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("temperature", [1e-30, 1e-4, 1e4, 1e30])
+def test_temperatures_far_from_one(tt, temperature, dtype):
+    _say("top temperature", temperature, dtype)
+    check(tt, make(3, 1256, dtype), 20, temperature)
+    check(tt, make(2, 33001, dtype), 300, temperature)
+
+
 def test_no_rows_many_rows_and_far_offsets(tt):
     _say("top many rows")
     call(tt, torch.empty(0, 8, device="cuda"), 3)
