@@ -275,11 +275,11 @@ struct Logits {
     MaxSum *sums;
 };
 
-// What exp(x - m) = exp2(x log2(e) - from) takes off.  The product may be beyond the numbers of 32 bits: such an m comes off column
-// j of the logits first.
+// What exp(x - m) = exp2(x log2(e) - from) takes off.  It is off by a rounding of m log2(e), which is relative, and the product may
+// be beyond the numbers of 32 bits: a large m comes off column j of the logits first.
 template <class TILE> __device__ __forceinline__ float power_base(f32x4 (&acc)[TILE::TM][TILE::TN], int j, float m)
 {
-    if (__builtin_fabsf(m) < 1e38f) return m * LOG2E;
+    if (__builtin_fabsf(m) < 128.f) return m * LOG2E;
 #pragma unroll
     for (int i = 0; i < TILE::TM; ++i) acc[i][j] -= m;
     return 0.f;

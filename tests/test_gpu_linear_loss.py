@@ -164,6 +164,34 @@ def test_pieces_of_a_copied_table(tt):
     case.check(o, "copied pieces")
 
 
+@pytest.mark.parametrize("extra", [0, 8])
+def test_rows_four_mebibytes_apart(tt, extra):
+    """The furthest apart that a table is read where it lies, and further; both pass 2^32 bytes."""
+    _say("linear far apart", extra)
+    case = Case(70, 1100, 64, BF16, ignored=0.1)
+    flat = torch.full((1100, (1 << 21) + extra), math.nan, dtype=BF16, device="cuda")
+    flat[:, :64] = case.weight
+    case.weight = flat[:, :64]
+    o = case.outputs()
+    case.forward(tt, o, case.workspace(tt))
+    case.check(o, "far apart")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,v,d", [(5, 70, 65536), (300, 300, 16384), (70000, 300, 16)])
+def test_wide_and_tall(tt, n, v, d, dtype):
+    _say("linear wide and tall", n, v, d, dtype)
+    case = Case(n, v, d, dtype, ignored=0.3 if n > 5 else 0.0)
+    ws = case.workspace(tt)
+    o = case.outputs()
+    case.forward(tt, o, ws)
+    case.check(o, "one call")
+    later = case.outputs()
+    later["loss"], later["lse"] = o["loss"], o["lse"].clone()
+    case.backward(tt, later, ws.fill_(0x5A))
+    case.check(later, "later", from_lse=True)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_one_gradient_alone(tt, dtype):
     _say("linear one gradient", dtype)
@@ -249,12 +277,14 @@ def test_sizes_of_logits(tt, dtype, size, lift):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("n,v,d", [(3, 500, 64), (300, 40000, 64)])
-def test_logits_at_the_end_of_the_range(tt, n, v, d, dtype):
-    """Logits around -+3e38, whose product with log2(e) has no number: equal ones share the probability, far ones have none."""
-    _say("linear range", n, v, d, dtype)
+@pytest.mark.parametrize("size", [1.7e19, 3e14, 1e8, 1000.0, 200.0])
+def test_logits_at_the_end_of_the_range(tt, size, n, v, d, dtype):
+    """Logits up to -+3e38, whose product with log2(e) has no number or is off by more than a power's range: equal ones share the
+    probability, far ones have none."""
+    _say("linear range", size, n, v, d, dtype)
     h = torch.zeros(n, d, dtype=dtype, device="cuda")
     w = torch.zeros(v, d, dtype=dtype, device="cuda")
-    big = torch.full((1,), 1.7e19, dtype=dtype, device="cuda")
+    big = torch.full((1,), size, dtype=dtype, device="cuda")
     w[:, 0], h[0, 0], h[1, 0] = -big, big, -big    # row 0: all logits -2.9e38, row 1: all 2.9e38
     w[v // 2:, 1], h[2, 1] = -big, big             # row 2: one half 0, the other -2.9e38
     y = torch.full((n,), 7, dtype=torch.int32, device="cuda")
