@@ -49,7 +49,7 @@ def distill(x, ids, top, temperature, teacher_lse, c, dtype, from_lse=False):
     y = torch.where(kept, top / t, torch.full_like(top, -float("inf")))
     if teacher_lse is None:
         mt, st, _, _, relt = _parts(y, 13 * 4 + 105)
-        log_q = y - (mt + torch.log(st))
+        log_q = (y - mt) - torch.log(st)   # mt + log(st) would lose the logarithm from |mt| = 2^53 on, in 64 bits
         e_log_q = 3 * U * torch.where(torch.isinf(y), torch.zeros_like(y), (y - mt).abs()) + relt + 4 * U * (torch.log(st) + 1)
     else:
         log_q = y - teacher_lse.unsqueeze(1)
@@ -59,7 +59,7 @@ def distill(x, ids, top, temperature, teacher_lse, c, dtype, from_lse=False):
     e_log_q = e_log_q + U * log_q.abs()
     q = torch.where(some, torch.exp(log_q), torch.zeros_like(y))
     rel_q = e_log_q + U * (2 * log_q.abs().clamp(max=104) + 4)
-    log_p = torch.where(some, z.gather(1, at) - (m + log_s), torch.zeros_like(y))
+    log_p = torch.where(some, (z.gather(1, at) - m) - log_s, torch.zeros_like(y))
     e_log_p = 3 * U * torch.where(some, (m - z.gather(1, at)), torch.zeros_like(y)) + e_log_s + U * log_p.abs()
     term = torch.where(q > 0, q * (log_q - log_p), torch.zeros_like(q))
     loss = term.sum(1)

@@ -209,6 +209,17 @@ def test_rows_that_are_empty_or_not_finite(tt, v, dtype):
         assert bool(g[6].isfinite().all()) and float(g[6, int(ids[6, 3])]) < 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,v,k", [(7, 1256, 8), (3, 33001, 100), (2, 65537, 64)])
+@pytest.mark.parametrize("t", [1e-30, 1e-4, 1e4, 1e30])
+def test_temperatures_far_from_one(tt, t, n, v, k, dtype):
+    _say("distill temperature", t, n, v, k, dtype)
+    case = Case(n, v, k, dtype, t)
+    o = case.outputs()
+    case.forward(tt, o)
+    case.check(o, case.reference(), "one call")
+
+
 def test_no_rows(tt):
     e, i = torch.empty(0, 8, device="cuda"), torch.empty(0, 3, dtype=torch.int32, device="cuda")
     v, t = torch.empty(0, device="cuda"), torch.empty(0, 3, device="cuda")
