@@ -5,7 +5,7 @@
 //   G = c (exp(x - lse) - [v == y]),  dh = G W,  dW = G^T h
 //
 // One product gives every tile's maximum and sum of exponentials per row, and, for as many IDs as a gibibyte holds, leaves
-// the exponentials (in the operands' type), which become G once the rows' sums are known.  For the others the
+// the exponentials (in the operands' size), which become G once the rows' sums are known.  For the others the
 // product is formed again, a piece of the vocabulary at a time.  G goes into dh (32-bit sums over the pieces) and into
 // the pieces' rows of dW.  Positions whose target is no ID are left out of all products: the hidden states of the others
 // are copied together first, into rows that the products need not check for their ends.
@@ -254,9 +254,37 @@ enum Use {
     KEPT,    // those, and the exponentials themselves, which k_scale turns into G
     G_AGAIN  // G
 };
-// Exponentials of 16 bits are kept rounded; float16's range holds those from 2^-24 on (2^-14 with all digits), so that it
-// keeps them times 2^15.
-template <class T> constexpr float KEPT_SCALE = __is_same(T, _Float16) ? 32768.f : 1.f;
+// How exponentials wait for their row's sum: beside a 16-bit type in 16 bits of their own, since they are rounded there and once
+// more as G.  They lie in 0 .. 1, so that no bit goes to a sign and few to the exponent: of the 32-bit number the 16 bits from bit
+// SHIFT on, beside bfloat16 seven of exponent and nine of fraction (any number down to 2^-126, off by 2^-10 where G is rounded by
+// 2^-8), beside float16, times 2^-96, five and eleven (2^-12 where G is rounded by 2^-11; subnormal below 2^-30).  As numbers of the
+// type they added a whole rounding to G: it was off by up to 2^-7 and 2^-10.  NaN comes out as a number, but its row's sum is NaN.
+template <class T> constexpr int KEPT_SHIFT = __is_same(T, _Float16) ? 12 : 14;
+template <class T> constexpr float KEPT_SCALE = __is_same(T, _Float16) ? 0x1p-96f : 1.f;
+
+template <class T> __device__ __forceinline__ uint32_t keep_high(float e)   // in the upper half
+{
+    return (__builtin_bit_cast(uint32_t, e * KEPT_SCALE<T>) << (16 - KEPT_SHIFT<T>)) + 0x8000u;
+}
+// four neighbours
+template <class T> __device__ __forceinline__ void keep4(T *to, const float (&e)[4])
+{
+    if constexpr (sizeof(T) == 4) {
+        *(f32x4 *)to = f32x4{e[0], e[1], e[2], e[3]};
+    } else {
+        u32x2 v;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) v[k] = keep_high<T>(e[2 * k]) >> 16 | (keep_high<T>(e[2 * k + 1]) & 0xFFFF0000u);
+        *(u32x2 *)to = v;
+    }
+}
+// element k of a vector of them, times KEPT_SCALE
+template <class T> __device__ __forceinline__ float kept_at(const Vec<T> &v, int k)
+{
+    if constexpr (sizeof(T) == 4) return vec_at(v, k);
+    const uint32_t w = v.a[k >> 1];
+    return __builtin_bit_cast(float, ((k & 1) ? w >> 16 : w & 0xFFFFu) << KEPT_SHIFT<T>);
+}
 
 // Four neighbouring elements.
 template <class T> __device__ __forceinline__ void store4(T *to, const float (&x)[4])
@@ -334,9 +362,8 @@ __device__ __forceinline__ void logits_tile(const Logits &a, uint32_t m0, uint32
                 for (int e = 0; e < 4; ++e) {
                     x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], LOG2E, -from));
                     s += x[e];
-                    x[e] *= KEPT_SCALE<T>;
                 }
-                if constexpr (USE == KEPT) store4(g + (uint64_t)n * g_cols + m_lane + i * 16, x);
+                if constexpr (USE == KEPT) keep4(g + (uint64_t)n * g_cols + m_lane + i * 16, x);
             }
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
@@ -391,7 +418,7 @@ struct Scaling {
             const Vec<T> v = load_vec(g + j);
             const uint32_t y = target - j;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) x[e] = j + e < n_vocab ? vec_at(v, e) * f : 0.f;
+            for (int e = 0; e < VEC; ++e) x[e] = j + e < n_vocab ? kept_at(v, e) * f : 0.f;
             if (y < VEC) {
                 const float own = c * (exp_f(at_target - shift) * recip - 1.f);
 #pragma unroll

@@ -464,8 +464,9 @@ int toktier_cross_entropy_backward(const void *logits, int type, uint32_t n_rows
  * zeros, and products are formed for the other rows alone.
  * Products are summed in 32 bits; G enters the second two as numbers of `type` (for float16 times a power of two that brings
  * the largest |c_i| to 2^14 .. 2^15; what lies below 2^-39 of it is lost).  Where loss and gradients come from one call, the
- * exponentials of the first IDs wait in the workspace as numbers of `type` for the row's sum, so that G is rounded twice there
- * (but at the target).  Each gradient is rounded once at the end.  The order of every sum is fixed by the sizes, the types, the
+ * exponentials of the first IDs wait in the workspace for the row's sum, beside a 16-bit type in 16 bits as well, so that G is
+ * rounded there once more (but at the target), to ten bits beside bfloat16's eight, to twelve beside float16's eleven.  Each
+ * gradient is rounded once at the end.  The order of every sum is fixed by the sizes, the types, the
  * alignment of the table and the targets that are IDs.
  * Values that are not finite go through the products as products do; a row with a logit that is NaN or +inf has a NaN
  * loss, one whose logits are all -inf the loss +inf and no part in the gradients' sums beyond 0 * weight.
