@@ -308,14 +308,13 @@ struct Logits {
     MaxSum *sums;
 };
 
-// What exp(x - m) = exp2(x log2(e) - from) takes off.  It is off by a rounding of m log2(e), which is relative, and the product may
-// be beyond the numbers of 32 bits: a large m comes off column j of the logits first.
-template <class TILE> __device__ __forceinline__ float power_base(f32x4 (&acc)[TILE::TM][TILE::TN], int j, float m)
+// Takes m off column j of the logits, before the product with log2(e): at the maximum the power is 1 itself, so that no loss is
+// negative and a certain target's G is zero.  (In one instruction, x log2(e) - m log2(e), a power is off by the rounding of the second
+// product: by 5e-6 at logits of 127, by any factor where they are large.)
+template <class TILE> __device__ __forceinline__ void take_off(f32x4 (&acc)[TILE::TM][TILE::TN], int j, float m)
 {
-    if (__builtin_fabsf(m) < 128.f) return m * LOG2E;
 #pragma unroll
     for (int i = 0; i < TILE::TM; ++i) acc[i][j] -= m;
-    return 0.f;
 }
 
 template <class T, class TILE, Use USE>
@@ -353,14 +352,14 @@ __device__ __forceinline__ void logits_tile(const Logits &a, uint32_t m0, uint32
             if (y < TILE::TM * 16 && (y & 15) < 4) rows.at_target[n] = at;
             m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
-            const float from = m == NEG_INF ? 0.f : power_base<TILE>(acc, j, m);
+            if (m != NEG_INF) take_off<TILE>(acc, j, m);   // nothing but -inf, or NaN, stays so
             float s = 0.f;
 #pragma unroll
             for (int i = 0; i < TILE::TM; ++i) {
                 float x[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], LOG2E, -from));
+                    x[e] = exp_f(acc[i][j][e]);
                     s += x[e];
                 }
                 if constexpr (USE == KEPT) keep4(g + (uint64_t)n * g_cols + m_lane + i * 16, x);
@@ -371,14 +370,15 @@ __device__ __forceinline__ void logits_tile(const Logits &a, uint32_t m0, uint32
         } else {
             // padding, rows and IDs, is zeros whatever the products are: the other two products run over it
             const bool row = n < count;
-            const float c = rows.factor[n] * rows.head->scale, from = power_base<TILE>(acc, j, rows.shift[n]), r = rows.recip[n];
+            const float c = rows.factor[n] * rows.head->scale, r = rows.recip[n];
+            take_off<TILE>(acc, j, rows.shift[n]);
             T *to = g + (uint64_t)n * g_cols + m_lane;
 #pragma unroll
             for (int i = 0; i < TILE::TM; ++i) {
                 float x[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], LOG2E, -from)) * r;
+                    const float p = exp_f(acc[i][j][e]) * r;
                     x[e] = c * (p - (y == (uint32_t)(i * 16 + e) ? 1.f : 0.f));
                     x[e] = row ? x[e] : 0.f;
                 }

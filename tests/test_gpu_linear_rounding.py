@@ -1,5 +1,7 @@
 """How often the cross entropy from hidden states rounds: hidden states that are rows of the identity make every logit an
-element of the table, exactly, and every row of the table's gradient the rows' G, so that both can be told to the last bit."""
+element of the table, exactly, and every row of the table's gradient the rows' G, so that both can be told to the last bit; and rows whose
+target is certain."""
+import math
 
 import pytest
 import torch
@@ -70,3 +72,35 @@ def test_gradients_of_logits_are_rounded_once(tt, later, n, v, d, dtype):
     err = size * p * rel + size * (1 - hit) * (half * p + least) + 3 * U * g.abs()
     err = err + plain.HALF_STEP[dtype] * (g.abs() + err) + smallest + 2.0 ** -126
     plain.close(gw.t()[:n], g, err, "G")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,v,d", [(1, 70, 64), (16, 300, 64), (60, 5001, 64), (128, 3000, 128), (300, 9000, 320), (700, 20000, 704),
+                                   (4200, 140001, 64)])   # more than is kept
+@pytest.mark.parametrize("later", [False, True])
+def test_rows_that_are_certain(tt, later, n, v, d, dtype):
+    """All of the probability at the target, at any height of its logit: loss and gradients are zeros, not a rounding of the logit."""
+    _say("linear certain", later, n, v, d, dtype)
+    heights = torch.tensor([1.0, 5.3, 30.0, -3.7, 63.7, 100.2, 127.9, 128.5, -90.3, 1000.0, -20.1, 0.0], device="cuda")
+    top = heights[torch.arange(d, device="cuda") % 12].to(dtype)
+    w = (top.float() - 250.0).to(dtype).expand(v, d).contiguous()
+    at = (torch.arange(d, device="cuda") * 7919) % v
+    w[at, torch.arange(d, device="cuda")] = top
+    y = at[torch.arange(n, device="cuda") % d].to(torch.int32)
+    loss, lse, gh, gw = run(tt, one_hot(n, d, dtype), w, y, later=later)
+    assert torch.equal(loss, torch.zeros_like(loss)), float(loss.abs().max())
+    assert torch.equal(lse, top.float()[torch.arange(n, device="cuda") % d])
+    assert not bool(gh.any()) and not bool(gw.any()), (float(gh.abs().max()), float(gw.abs().max()))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_losses_are_not_negative(tt, dtype):
+    _say("linear not negative", dtype)
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    n, v, d = 500, 4000, 512
+    w = torch.randn(v, d, generator=gen, device="cuda").to(dtype)
+    y = torch.randint(0, v, (n,), generator=gen, device="cuda", dtype=torch.int32)
+    lift = torch.linspace(0.0, 0.24, n, device="cuda").unsqueeze(1)   # logits of the targets up to 120
+    h = (lift * w[y.long()].float()).to(dtype)
+    loss = run(tt, h, w, y)[0]
+    assert bool((loss >= 0).all()) and float(loss[-1]) < 1e-6 and math.isclose(float(loss[0]), math.log(v), rel_tol=1e-5)
