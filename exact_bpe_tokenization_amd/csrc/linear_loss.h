@@ -29,7 +29,8 @@ constexpr uint32_t PAD = 256;            // rows of the packed matrices come in 
 struct Head {
     uint32_t count;       // rows that take part
     float scale, unscale; // G is kept times `scale`
-    uint32_t pad[61];
+    uint32_t far;         // whether some row's lse_in is far from zero
+    uint32_t pad[60];
 };
 
 inline uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
@@ -149,9 +150,10 @@ __global__ __launch_bounds__(256) void k_gather(const T *__restrict__ hidden, ui
                                                 uint64_t grad_stride)
 {
     constexpr bool SCALED = __is_same(T, _Float16);
-    __shared__ uint32_t part[4], befores[4], larges[4], place[256];
+    __shared__ uint32_t part[4], befores[4], larges[4], fars[4], place[256];
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, first = blockIdx.x * per, last = first + per < n_rows ? first + per : n_rows;
     uint32_t total = 0, before = 0, large = 0;
+    bool far = false;
 #pragma unroll 8
     for (uint32_t r = threadIdx.x; r < n_rows; r += 256) {
         const bool in = targets[r] < n_vocab;
@@ -164,6 +166,10 @@ __global__ __launch_bounds__(256) void k_gather(const T *__restrict__ hidden, ui
             }
         }
     }
+    if (lse_in && blockIdx.x == 0) {   // (in the loop above it would cost the calls without it 5 us)
+#pragma unroll 8
+        for (uint32_t r = threadIdx.x; r < n_rows; r += 256) far |= targets[r] < n_vocab && lse_in[r] != NEG_INF && is_far(lse_in[r]);
+    }
 #pragma unroll
     for (int d = 32; d; d >>= 1) {
         total += __shfl_xor(total, d);
@@ -171,10 +177,12 @@ __global__ __launch_bounds__(256) void k_gather(const T *__restrict__ hidden, ui
         const uint32_t o = __shfl_xor(large, d);
         large = o > large ? o : large;
     }
+    far = __any(far);
     if (lane == 0) {
         part[wave] = total;
         befores[wave] = before;
         larges[wave] = large;
+        fars[wave] = far;
     }
     __syncthreads();
     total = part[0] + part[1] + part[2] + part[3];
@@ -184,6 +192,7 @@ __global__ __launch_bounds__(256) void k_gather(const T *__restrict__ hidden, ui
         const int e = (int)(large >> 23) - 127;   // the largest |c| is 2^e .. 2^(e + 1); subnormal ones count as 2^-127
         const float scale = large ? __builtin_amdgcn_ldexpf(1.f, 14 - e > 126 ? 126 : 14 - e) : 1.f;
         rows.head->count = total;
+        rows.head->far = fars[0] | fars[1] | fars[2] | fars[3];
         rows.head->scale = scale;
         rows.head->unscale = 1.f / scale;
     }
@@ -237,10 +246,12 @@ __global__ __launch_bounds__(256) void k_gather(const T *__restrict__ hidden, ui
     }
 }
 
+// for_far: where it is not NULL, only if there are far rows
 template <class T>
 __global__ __launch_bounds__(256) void k_pack_weight(const T *__restrict__ weight, uint64_t stride, uint32_t ids, uint32_t dim, uint32_t dim_pad,
-                                                     T *__restrict__ packed)
+                                                     T *__restrict__ packed, const Head *__restrict__ for_far)
 {
+    if (for_far && !for_far->far) return;
     const uint64_t v = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (v < ids) copy_row(packed + v * dim_pad, weight + v * stride, dim, dim_pad);
 }
@@ -250,7 +261,7 @@ __global__ __launch_bounds__(256) void k_pack_weight(const T *__restrict__ weigh
 
 // What becomes of a tile of logits, vocabulary along m, rows along n.
 enum Use {
-    SUMS,    // each row's maximum and sum of exponentials over a wavefront's IDs
+    SUMS,    // each row's maximum and sum of exponentials over a wavefront's IDs (far_only: in tiles with far rows)
     KEPT,    // those, and the exponentials themselves, which k_scale turns into G
     G_AGAIN  // G
 };
@@ -306,7 +317,17 @@ struct Logits {
     uint32_t steps, first_id, n_vocab, n_pad;
     Rows rows;
     MaxSum *sums;
+    bool far_only;
 };
+
+// Whether one of the tile's rows is far from zero; every wavefront looks at all of them.  (A reduction over the workgroup takes LDS,
+// of which four of the smallest tiles for few rows leave none.)
+template <class TILE> __device__ __forceinline__ bool far_in(const Rows &rows, uint32_t n0, uint32_t count)
+{
+    bool far = false;
+    for (uint32_t r = threadIdx.x & 63; r < TILE::N; r += 64) far |= n0 + r < count && is_far(rows.shift[n0 + r]);
+    return __any(far);
+}
 
 // Takes m off column j of the logits, before the product with log2(e): at the maximum the power is 1 itself, so that no loss is
 // negative and a certain target's G is zero.  (In one instruction, x log2(e) - m log2(e), a power is off by the rounding of the second
@@ -396,9 +417,11 @@ template <class T, class TILE, Use USE>
 __global__ __launch_bounds__(TILE::THREADS, 2) void k_logits(Logits a, uint32_t m_tiles, T *__restrict__ g, uint32_t g_cols)
 {
     __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::LDS];
+    if (USE == SUMS && a.far_only && !a.rows.head->far) return;
     // (of G every row up to a whole step of k is written: the product for dW reads it so)
     const uint32_t count = a.rows.head->count, reach = USE == G_AGAIN ? (count + STEP_K<T> - 1) / STEP_K<T> * STEP_K<T> : count;
     with_place<TILE>(m_tiles, a.w.count * a.w.stride, reach, [&](auto tile, uint32_t m0, uint32_t n0) {
+        if (USE == SUMS && a.far_only && !far_in<decltype(tile)>(a.rows, n0, count)) return;
         logits_tile<T, decltype(tile), USE>(a, m0, n0, count, (lds_u8 *)shared, g, g_cols);
     });
 }
@@ -429,33 +452,36 @@ struct Scaling {
     }
 };
 
-// A row's loss and log-sum-exp from its maximum and sum, and what G is formed with.
+// A row's loss and log-sum-exp from its maximum and sum (loss NULL: both are there), and what G is formed with.
 __device__ __forceinline__ void put_row(MaxSum v, uint32_t n, const Rows &rows, float *loss, float *lse)
 {
     const bool none = empty(v);
-    const float log_s = log_of(v.s);
-    const uint32_t r = rows.list[n];
-    lse[r] = none ? NEG_INF : v.m + log_s;
-    loss[r] = none ? -NEG_INF : (v.m - rows.at_target[n]) + log_s;
+    if (loss) {
+        const float log_s = log_of(v.s);
+        const uint32_t r = rows.list[n];
+        lse[r] = none ? NEG_INF : v.m + log_s;
+        loss[r] = none ? -NEG_INF : (v.m - rows.at_target[n]) + log_s;
+    }
     rows.shift[n] = none ? 0.f : v.m;
     rows.recip[n] = none ? 0.f : 1.f / v.s;
     if (none) rows.factor[n] = 0.f;
 }
 
-// Joins the maxima and sums over the vocabulary (`parts` of them): 16 rows a workgroup, 64 threads a row.
+// Joins the maxima and sums over the vocabulary (`parts` of them): 16 rows a workgroup, 64 threads a row.  loss NULL: of the far
+// rows.
 __global__ __launch_bounds__(1024) void k_join(const MaxSum *__restrict__ sums, uint32_t parts, uint32_t n_pad, Rows rows,
                                                float *__restrict__ loss, float *__restrict__ lse)
 {
     __shared__ MaxSum part[16][16];
     const uint32_t l = threadIdx.x & 15, n = blockIdx.x * 16 + l;
-    if (blockIdx.x * 16 >= rows.head->count) return;
+    if (blockIdx.x * 16 >= rows.head->count || (!loss && !rows.head->far)) return;
     MaxSum v{NEG_INF, 0.f};
     for (uint32_t t = threadIdx.x >> 4; t < parts; t += 64) v = join(v, sums[(uint64_t)t * n_pad + n]);
     v = join(v, MaxSum{__shfl_xor(v.m, 16), __shfl_xor(v.s, 16)});
     v = join(v, MaxSum{__shfl_xor(v.m, 32), __shfl_xor(v.s, 32)});
     if ((threadIdx.x & 63) < 16) part[threadIdx.x >> 6][l] = v;
     __syncthreads();
-    if (threadIdx.x >= 16 || n >= rows.head->count) return;
+    if (threadIdx.x >= 16 || n >= rows.head->count || (!loss && !is_far(rows.shift[n]))) return;
     for (uint32_t i = 1; i < 16; ++i) v = join(v, part[i][l]);
     put_row(v, n, rows, loss, lse);
 }
@@ -696,14 +722,14 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
     const uint32_t steps = z.dim_pad / STEP_K<T>;
     const Operand h{hidden, row, z.n_pad};
     bool copied = false;   // all of it, where that fits
-    auto table = [&](uint32_t first, uint32_t ids) {
+    auto table = [&](uint32_t first, uint32_t ids, const Head *for_far = nullptr) {
         const T *from = weight + first * c.weight_stride;
         if (as_is) return Operand{from, w_bytes, ids};
         if (c.n_vocab > most_packed) {
-            k_pack_weight<T><<<tiles(ids, 4), 256, 0, s>>>(from, c.weight_stride, ids, c.dim, z.dim_pad, packed);
+            k_pack_weight<T><<<tiles(ids, 4), 256, 0, s>>>(from, c.weight_stride, ids, c.dim, z.dim_pad, packed, for_far);
             return Operand{packed, row, ids};
         }
-        if (!copied) k_pack_weight<T><<<tiles(c.n_vocab, 4), 256, 0, s>>>(weight, c.weight_stride, c.n_vocab, c.dim, z.dim_pad, packed);
+        if (!copied) k_pack_weight<T><<<tiles(c.n_vocab, 4), 256, 0, s>>>(weight, c.weight_stride, c.n_vocab, c.dim, z.dim_pad, packed, nullptr);
         copied = true;
         return Operand{packed + (uint64_t)first * z.dim_pad, row, ids};
     };
@@ -714,7 +740,9 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
     if (!as_is && c.n_vocab > most_packed) keep = keep < most_packed ? 0 : most_packed;
     uint32_t span = 0;
 
-    if (forward && c.n_rows) {
+    // Maxima and sums.  For gradients from lse of those rows whose lse is far from zero, which the device knows: launches that find
+    // none take some 3 to 8 us (1,350 rows x 33,001 x 1,001 float16: 348 -> 355 us; with one far row 389, with all far 455).
+    if ((forward || grads) && c.n_rows) {
         with_logits_tile(z.v_pad, c.n_rows, [&](auto t) {
             using TILE = decltype(t);
             span = TILE::TM * 16;
@@ -722,16 +750,18 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
                 uint32_t most = std::min((uint32_t)(as_is ? z.v_pad : most_packed), most_ids<TILE>(c.n_rows));
                 if (first < keep) most = std::min(most, keep - first);
                 const uint32_t ids = std::min(most, c.n_vocab - first), m_tiles = tiles(ids, TILE::M);
-                const Operand w = table(first, ids);
+                const Operand w = table(first, ids, forward ? nullptr : rows.head);
                 const uint32_t blocks = tile_blocks<TILE>(m_tiles, tiles(c.n_rows, TILE::N));
-                const Logits a{w, h, steps, first, c.n_vocab, z.n_pad, rows, sums};
+                const Logits a{w, h, steps, first, c.n_vocab, z.n_pad, rows, sums, !forward};
                 if (first < keep) k_logits<T, TILE, KEPT><<<blocks, TILE::THREADS, 0, s>>>(a, m_tiles, kept + first, keep);
                 else k_logits<T, TILE, SUMS><<<blocks, TILE::THREADS, 0, s>>>(a, m_tiles, nullptr, 0);
                 first += most;
             }
         });
         const uint32_t parts = tiles(c.n_vocab, span), cols = (uint32_t)std::min<uint64_t>(keep, up(c.n_vocab, PAD));
-        if (c.n_rows <= PAD) {   // (of the loss alone: no columns)
+        if (!forward) {
+            k_join<<<z.n_pad / 16, 1024, 0, s>>>(sums, parts, z.n_pad, rows, nullptr, nullptr);
+        } else if (c.n_rows <= PAD) {   // (of the loss alone: no columns)
             k_join_scale<T><<<grads ? PAD : c.n_rows, 1024, 0, s>>>(sums, parts, z.n_pad, c.n_vocab, rows, c.loss, c.lse, kept, keep, cols, span);
         } else {
             k_join<<<z.n_pad / 16, 1024, 0, s>>>(sums, parts, z.n_pad, rows, c.loss, c.lse);
@@ -761,7 +791,7 @@ template <class T> void enqueue(const Call &c, const Sizes &z, uint8_t *ws, hipS
                 // every column of G up to the piece's width is written: the product for dh reads it in whole steps
                 const uint32_t m_tiles = tiles(up(ids, PAD), TILE::M);
                 k_logits<T, TILE, G_AGAIN><<<tile_blocks<TILE>(m_tiles, tiles(up(c.n_rows, STEP_K<T>), TILE::N)), TILE::THREADS, 0, s>>>(
-                    Logits{w, h, steps, first, c.n_vocab, z.n_pad, rows, nullptr}, m_tiles, g, piece);
+                    Logits{w, h, steps, first, c.n_vocab, z.n_pad, rows, nullptr, false}, m_tiles, g, piece);
             });
         if (c.grad_hidden && c.n_rows) {
             const uint32_t k_steps = tiles(ids, STEP_K<T>);

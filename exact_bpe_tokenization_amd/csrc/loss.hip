@@ -124,8 +124,6 @@ __global__ __launch_bounds__(PIECE_THREADS) void k_loss_join(const T *logits, ui
 // much as the power itself can be off (its exponent is rounded too, and reaches 104 before the power is zero), a row's
 // maximum and sum are formed again.  One workgroup takes such a row whole, since in place the others would read
 // what it has written.  (Two inputs in turn, 1,500 x 33,001 float16: 32 us, 51 with all rows far; 8,192 x 131,328 bfloat16: 767 and 1,216 us.)
-constexpr float FAR = 128.f;
-
 template <class T, int THREADS>
 __global__ __launch_bounds__(THREADS, 8) void k_loss_backward(const T *logits, uint32_t n_vocab, uint64_t stride,
                                                               const uint32_t *__restrict__ targets,
@@ -139,7 +137,7 @@ __global__ __launch_bounds__(THREADS, 8) void k_loss_backward(const T *logits, u
     RowPart<T, THREADS, PIECE / (THREADS * VEC)> part{logits + row * stride, begin, end};
     T *g = grad + row * gstride;
     if (z == NEG_INF || y >= n_vocab) return put_grad(part, g, true, MaxSum{z, 1.f}, c, y);
-    if (!(__builtin_fabsf(z) < FAR)) {   // NaN too
+    if (is_far(z)) {
         if (blockIdx.x) return;
         part.end = n_vocab;
         MaxSum a{NEG_INF, 0.f};

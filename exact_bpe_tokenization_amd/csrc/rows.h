@@ -107,6 +107,10 @@ template <class T, int THREADS, int HELD> struct RowPart {
     }
 };
 
+// A log-sum-exp so far from zero that its rounding, which is relative, would show in the probabilities (NaN too).
+constexpr float FAR = 128.f;
+__device__ __forceinline__ bool is_far(float lse) { return !(__builtin_fabsf(lse) < FAR); }
+
 __device__ __forceinline__ bool empty(MaxSum a) { return a.m == NEG_INF && a.s == 0.f; }   // nothing but -inf
 __device__ __forceinline__ float log_of(float s) { return LN2 * __builtin_amdgcn_logf(s); }
 

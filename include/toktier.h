@@ -495,8 +495,8 @@ int toktier_linear_cross_entropy(const void *hidden, int type, uint32_t n_rows, 
                                  uint64_t grad_weight_stride, int accumulate, void *workspace, uint64_t workspace_bytes,
                                  void *stream);
 
-/* The gradients alone, later, from the lse that toktier_linear_cross_entropy wrote for the same arguments.  A rounding of lse is
- * relative to it, so that the probabilities are off by about |lse| 2^-24; the one call takes them from the row's maximum and sum. */
+/* The gradients alone, later, from the lse that toktier_linear_cross_entropy wrote for the same arguments.  A row whose |lse| is 128
+ * or more is summed again, from products formed once more; below, the rounding of lse shows in the probabilities by up to |lse| 2^-24. */
 int toktier_linear_cross_entropy_backward(const void *hidden, int type, uint32_t n_rows, uint32_t dim,
                                           uint64_t hidden_stride, const void *weight, uint32_t n_vocab,
                                           uint64_t weight_stride, const uint32_t *targets, const float *lse,
