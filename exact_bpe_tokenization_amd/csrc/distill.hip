@@ -288,7 +288,9 @@ __global__ __launch_bounds__(PIECE_THREADS) void k_distill_join(const T *logits,
 }
 
 // The gradient from lse.  From |lse| = FAR on a row's maximum and sum are formed again, by one workgroup, since in place the others
-// would read what it has written.
+// would read what it has written.  So it is above a temperature of 2^120, where lse temperature, the maximum that a sum of one would have, or
+// a logit's distance from it might leave the range; below it a distance that does has no power.
+constexpr float HOT = 0x1p120f;
 // (Of float32 nine registers are spilled; with six wavefronts and none spilled 2,048 rows of 131,328 take 465 us in place of 419.)
 template <class T, int THREADS>
 __global__ __launch_bounds__(THREADS, 8) void k_distill_backward(const T *logits, uint32_t n_vocab, uint64_t stride, Teacher t, uint32_t slots,
@@ -304,7 +306,7 @@ __global__ __launch_bounds__(THREADS, 8) void k_distill_backward(const T *logits
     const uint32_t begin = blockIdx.x * PIECE, end = n_vocab - begin < PIECE ? n_vocab : begin + PIECE;
     constexpr int HELD = PIECE / (THREADS * VEC);
     RowPart<T, THREADS, HELD> part{logits + row * stride, begin, end};
-    const bool far = z != NEG_INF && is_far(z);
+    const bool far = z != NEG_INF && (is_far(z) || temperature > HOT);
     if (far) {
         if (blockIdx.x) return;
         part.end = n_vocab;

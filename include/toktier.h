@@ -536,7 +536,7 @@ int toktier_distill(const void *logits, int type, uint32_t n_rows, uint32_t n_vo
                     uint64_t grad_stride, void *workspace, uint64_t workspace_bytes, void *stream);
 
 /* The gradient alone, later, from the lse that toktier_distill wrote for the same arguments.  A row whose |lse| is 128 or
- * more is summed again. */
+ * more is summed again, as are all rows at temperatures above 2^120. */
 int toktier_distill_backward(const void *logits, int type, uint32_t n_rows, uint32_t n_vocab, uint64_t stride,
                              const uint32_t *top_ids, uint64_t top_ids_stride, const float *top_logits,
                              uint64_t top_logits_stride, uint32_t top_k, const float *teacher_lse, float temperature,

@@ -1,0 +1,58 @@
+"""Distillation at the ends of the range that its arguments may have: temperatures, log-sum-exps beyond 32 bits, lists with
++inf; both the one call and the gradient from lse."""
+import math
+
+import pytest
+import torch
+
+from distill_plain import vectors
+from linear_plain import U, close
+from test_gpu_distill import BF16, F16, F32, TYPES, Case
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(7, 1256, 8), (3, 33001, 100), (2, 65537, 64)]
+
+
+def _say(*a):
+    print("[gpu-case]", *a, flush=True)
+
+
+def _both(tt, case, t, what):
+    case.scale = max(t, 1.0)    # so that c / temperature is no subnormal number
+    # a temperature whose reciprocal is subnormal: half a step of that is up to 2^-22
+    subnormal = 5 * U if t > 2.0 ** 126 else 0.0
+    # a row that is summed again by 256 threads, as distill_plain counts it for large log-sum-exps
+    again = U * (13 * vectors(case.v) + 105) if t > 2.0 ** 120 else 0.0
+    p = torch.softmax(case.logits.double() / t, 1) * (case.grad_loss.double() * case.scale / t).abs().unsqueeze(1)
+    o = case.outputs()
+    case.forward(tt, o)
+    for later in (False, True):
+        if later:
+            o["grad"].fill_(3)
+            case.backward(tt, o)
+        ref = case.reference(from_lse=later)
+        ref["grad"] = ref["grad"][0], ref["grad"][1] + subnormal * ref["grad"][0].abs() + (again * p if later else 0.0)
+        case.check(o, ref, what + (" later" if later else ""), ("grad",) if later else ("loss", "lse", "grad"))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,v,k", SHAPES)
+@pytest.mark.parametrize("t", [4.3e-39, 1e-38, 1e-30, 1e-4, 1e4, 1e30, 2.0 ** 120, 1.4e36, 2e37, 1e38, 3.4e38])
+def test_temperatures(tt, t, n, v, k, dtype):
+    """Logits of the temperature's size where that is small, of ordinary size where it is large."""
+    _say("distill range temperature", t, n, v, k, dtype)
+    t = float(torch.tensor(t, dtype=torch.float32))
+    _both(tt, Case(n, v, k, dtype, t, size=2.5 * min(t, 1.0), own_lse=n == 3 and t >= 1e-4), t, "ordinary")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,v,k", SHAPES)
+@pytest.mark.parametrize("t", [1e30, 2.0 ** 120, 1e37, 2e37])
+def test_logits_of_a_large_temperatures_size(tt, t, n, v, k, dtype):
+    _say("distill range logits", t, n, v, k, dtype)
+    t = float(torch.tensor(t, dtype=torch.float32))
+    case = Case(n, v, k, dtype, t, size=2.0 * t)
+    # differences of logits have to be numbers of 32 bits
+    case.logits.clamp_(-1.6e38, 1.6e38)
+    _both(tt, case, t, "large")
