@@ -306,7 +306,7 @@ __global__ __launch_bounds__(THREADS, 8) void k_distill_backward(const T *logits
     const uint32_t begin = blockIdx.x * PIECE, end = n_vocab - begin < PIECE ? n_vocab : begin + PIECE;
     constexpr int HELD = PIECE / (THREADS * VEC);
     RowPart<T, THREADS, HELD> part{logits + row * stride, begin, end};
-    const bool far = z != NEG_INF && (is_far(z) || temperature > HOT);
+    const bool far = is_far(z) || temperature > HOT;   // -inf too: at a small temperature it may stand for a number beyond the range
     if (far) {
         if (blockIdx.x) return;
         part.end = n_vocab;
@@ -332,7 +332,7 @@ __global__ __launch_bounds__(THREADS, 8) void k_distill_backward(const T *logits
         a = block_join<THREADS>(a, lds[1], k2);
         return put_grad<T, THREADS, HELD, false>(part, list, t.k, g, empty(a), a.m, 1.f / a.s, sums.x, c, k2);
     }
-    put_grad<T, THREADS, HELD, false>(part, list, t.k, g, sums.x == 0.f || z == NEG_INF, a.m, 1.f, sums.x, c, k2);
+    put_grad<T, THREADS, HELD, false>(part, list, t.k, g, sums.x == 0.f, a.m, 1.f, sums.x, c, k2);
 }
 
 // ---------------------------------------------------------------------------------------------

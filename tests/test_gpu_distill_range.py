@@ -56,3 +56,34 @@ def test_logits_of_a_large_temperatures_size(tt, t, n, v, k, dtype):
     # differences of logits have to be numbers of 32 bits
     case.logits.clamp_(-1.6e38, 1.6e38)
     _both(tt, case, t, "large")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("v", [1256, 30000, 70000])
+@pytest.mark.parametrize("t", [1e-38, 1e-37])
+def test_log_sum_exps_beyond_32_bits(tt, t, v, dtype):
+    """lse is -inf or +inf because it has no number, not because the row is empty."""
+    _say("distill range lse", t, v, dtype)
+    n, t = 4, float(torch.tensor(t, dtype=torch.float32))
+    x = torch.full((n, v), -60.0, dtype=dtype, device="cuda")
+    x[1:, 100], x[1:, 700], x[1:, v - 1] = -50.0, -50.0, -50.0
+    x[2] = x[2] + 100
+    x[3] = -math.inf
+    ids = torch.tensor([[700, 5, -1]] * n, dtype=torch.int32, device="cuda")
+    top = torch.tensor([[1.0, 0.0, 0.0]] * n, device="cuda")
+    loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    ws = torch.empty(tt.toktier_distill_workspace_bytes(n, v, 3), dtype=torch.uint8, device="cuda")
+    one, later = torch.empty_like(x), torch.empty_like(x)
+    tt.toktier_distill(x, ids, top, loss, lse, ws, temperature=t, grad_logits=one, grad_scale=t)
+    tt.toktier_distill_backward(x, ids, top, lse, later, temperature=t, grad_scale=t)
+    assert lse.tolist() == [-math.inf, -math.inf, math.inf, -math.inf]
+    want = torch.zeros(n, v, dtype=torch.float64, device="cuda")
+    want[0] = 1.0 / v
+    want[1:3, 100], want[1:3, 700], want[1:3, v - 1] = 1 / 3, 1 / 3, 1 / 3
+    want[:3, 700] -= 1.0
+    for g in (one, later):
+        close(g, want, 2.0 ** -7 * want.abs() + (2.0 ** -24 if dtype == F16 else 0.0), "gradient")
+    x[3] = -50.0
+    here = x.clone()
+    tt.toktier_distill_backward(here, ids, top, lse, here, temperature=t, grad_scale=t)
+    assert torch.equal(here[:3], later[:3])
