@@ -88,6 +88,7 @@ __device__ __forceinline__ MaxSum read_list(const List &list, const Entries<THRE
         float v = NEG_INF, x = 0.f;
         if (id != NONE) {
             v = own.top[e];
+            if (v == -NEG_INF) v = __builtin_nanf("");   // with the teacher's own log-sum-exp too
             x = logit(i, id);
             uint32_t was = id + 1;
             for (uint32_t s = 0; s < list.slots && was != id && was != NONE; ++s)   // at most half of the slots are ever taken

@@ -87,3 +87,28 @@ def test_log_sum_exps_beyond_32_bits(tt, t, v, dtype):
     here = x.clone()
     tt.toktier_distill_backward(here, ids, top, lse, here, temperature=t, grad_scale=t)
     assert torch.equal(here[:3], later[:3])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("v", [1256, 30000, 70000])
+@pytest.mark.parametrize("own_lse", [False, True])
+def test_infinite_logits_in_a_list(tt, own_lse, v, dtype):
+    _say("distill range list", own_lse, v, dtype)
+    n = 6
+    case = Case(n, v, 20, dtype, own_lse=own_lse)
+    good = case.outputs()
+    case.forward(tt, good)
+    case.top[1, 3] = math.inf
+    case.top[2, 0] = math.nan
+    case.top[4, 19] = math.inf
+    case.ids[4, 19] = -1        # no entry, not looked at
+    o = case.outputs()
+    case.forward(tt, o)
+    for later in (False, True):
+        if later:
+            o["grad"].fill_(3)
+            case.backward(tt, o)
+        assert bool(o["loss"][1:3].isnan().all()) and bool(o["grad"][1:3].isnan().all())
+        assert torch.equal(o["lse"], good["lse"])
+        rest = torch.tensor([0, 3, 4, 5], device="cuda")
+        assert bool(o["loss"][rest].isfinite().all()) and bool(o["grad"][rest].isfinite().all())
