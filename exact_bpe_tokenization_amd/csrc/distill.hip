@@ -339,13 +339,11 @@ __global__ __launch_bounds__(THREADS, 8) void k_distill_backward(const T *logits
 // ---------------------------------------------------------------------------------------------
 // host side
 
-bool positive(float t) { return t > 0.f && t <= 3.4028234e38f && 1.f / t <= 3.4028234e38f; }
-
 int check_distill(const void *logits, int type, uint32_t n_rows, uint32_t n_vocab, uint64_t stride, const Teacher &t, float temperature,
                   const float *lse, const float *grad_loss, const void *grad, uint64_t gstride)
 {
     if (!elem_size(type) || n_vocab == 0 || n_vocab > TOKTIER_MAX_VOCAB || n_rows > 0x7FFFFFFFu || t.k == 0 || t.k > TOKTIER_MAX_TOP ||
-        !positive(temperature))
+        !temperature_ok(temperature))
         return TOKTIER_E_INVALID_ARG;
     if (n_rows == 0) return TOKTIER_OK;
     if (!matrix_ok(logits, type, n_rows, n_vocab, stride) || !matrix_ok(t.ids, TOKTIER_F32, n_rows, t.k, t.ids_stride) ||

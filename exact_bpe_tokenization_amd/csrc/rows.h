@@ -11,6 +11,9 @@ constexpr float NEG_INF = -__builtin_inff();
 // exp(x), or exp(x / temperature) with k = log2(e) / temperature
 __device__ __forceinline__ float exp_f(float x, float k = LOG2E) { return __builtin_amdgcn_exp2f(x * k); }
 
+// Temperatures whose k is a positive number: with an infinite one a distance of 0 would be NaN.
+inline bool temperature_ok(float t) { return t > 0.f && t <= 3.4028234e38f && LOG2E * (1.f / t) <= 3.4028234e38f; }
+
 // Running maximum m and sum s of exp(x - m); an empty sum is (-inf, 0).  m is only ever -inf, finite or
 // +inf; a NaN among the logits goes into s.
 struct MaxSum {

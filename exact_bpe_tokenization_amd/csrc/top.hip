@@ -547,7 +547,7 @@ extern "C" int toktier_top_logits(const void *logits, int type, uint32_t n_rows,
                                   void *workspace, uint64_t workspace_bytes, void *stream)
 {
     if (!elem_size(type) || n_vocab == 0 || n_vocab > TOKTIER_MAX_VOCAB || n_rows > 0x7FFFFFFFu || k == 0 || k > TOKTIER_MAX_TOP ||
-        !(temperature > 0.f && temperature <= 3.4028234e38f && 1.f / temperature <= 3.4028234e38f))
+        !temperature_ok(temperature))
         return TOKTIER_E_INVALID_ARG;
     if (n_rows == 0) return TOKTIER_OK;
     if (!matrix_ok(logits, type, n_rows, n_vocab, stride) || !matrix_ok(out_ids, TOKTIER_F32, n_rows, k, out_ids_stride) ||

@@ -522,7 +522,7 @@ int toktier_linear_cross_entropy_backward(const void *hidden, int type, uint32_t
  * a NaN or +inf among the logits makes lse, loss and gradient NaN, one among the list's logits loss and gradient.
  *   top_ids      device, n_rows rows of top_k uint32, top_ids_stride apart; 1 <= top_k <= TOKTIER_MAX_TOP.
  *   top_logits   device, n_rows rows of top_k float, top_logits_stride apart.
- *   teacher_lse  device, float[n_rows], or NULL.     temperature  > 0 and finite, as is its reciprocal.
+ *   teacher_lse  device, float[n_rows], or NULL.     temperature  > 0 and finite, as is log2(e) / temperature.
  *   loss, lse    device, float[n_rows].              grad_loss    device, float[n_rows], or NULL.
  *   grad_logits  device, n_rows rows of n_vocab elements of `type`, or NULL for the loss alone; may be `logits` itself with
  *                the same stride (in place), else must not overlap it.
@@ -552,7 +552,8 @@ int toktier_distill_backward(const void *logits, int type, uint32_t n_rows, uint
  *   out_ids      device, n_rows rows of k uint32, out_ids_stride apart.
  *   out_logits   device, n_rows rows of k float, out_logits_stride apart: the logits themselves.
  *   lse          device, float[n_rows], or NULL: log(sum_j exp(logits[i, j] / temperature)); -inf in a row of nothing else, NaN
- *                in one with a NaN or +inf.      temperature  > 0 and finite, as is its reciprocal.
+ *                in one with a NaN or +inf; what is beyond the range of 32 bits, differences of logits too, counts as infinite.
+ *   temperature  > 0 and finite, as is log2(e) / temperature.
  *   workspace    device, toktier_top_logits_workspace_bytes(n_rows, n_vocab, k) bytes.
  */
 int toktier_top_logits_workspace_bytes(uint32_t n_rows, uint32_t n_vocab, uint32_t k, uint64_t *out_bytes);

@@ -1,5 +1,5 @@
 """Distillation at the ends of the range that its arguments may have: temperatures, log-sum-exps beyond 32 bits, lists with
-+inf; both the one call and the gradient from lse."""
++inf; both the one call and the gradient from lse; and the top logits' temperatures."""
 import math
 
 import pytest
@@ -8,6 +8,7 @@ import torch
 from distill_plain import vectors
 from linear_plain import U, close
 from test_gpu_distill import BF16, F16, F32, TYPES, Case
+from test_gpu_top_logits import check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +113,12 @@ def test_infinite_logits_in_a_list(tt, own_lse, v, dtype):
         assert torch.equal(o["lse"], good["lse"])
         rest = torch.tensor([0, 3, 4, 5], device="cuda")
         assert bool(o["loss"][rest].isfinite().all()) and bool(o["grad"][rest].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t", [4.3e-39, 1e-38, 2.0 ** 120, 1e38, 3.4e38])
+def test_temperatures_of_top_logits(tt, t, dtype):
+    _say("top range temperature", t, dtype)
+    t = float(torch.tensor(t, dtype=torch.float32))
+    check(tt, make(3, 1256, dtype, size=2.5 * min(t, 1.0)), 20, t)
+    check(tt, make(2, 33001, dtype, size=2.5 * min(t, 1.0)), 300, t)
