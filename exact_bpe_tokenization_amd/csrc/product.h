@@ -33,7 +33,7 @@ __device__ __forceinline__ uint32_t lds_address(const lds_u8 *p) { return (uint3
 // (wait_loads) before a barrier; the compiler's own builtin would make every read of LDS wait for all of them.
 __device__ __forceinline__ void load_to_lds(uint32_t to, const void *base, uint32_t offset)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "m0", "memory");
 }
 // until at most N of them are in flight
 template <int N> __device__ __forceinline__ void wait_loads()
