@@ -542,8 +542,9 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void k_grad_hidden(Operand w, Ope
 {
     __shared__ __attribute__((aligned(16))) uint8_t shared[TILE::LDS];
     const uint32_t count = rows.head->count, n_tiles = split.n_tiles(count), shares = split.shares(count);
-    const uint32_t one = split.m_tiles * n_tiles, at = tile_of(blockIdx.x, one * shares), mine = at / one;
-    if (at == NONE) return;
+    const uint32_t one = split.m_tiles * n_tiles, at = tile_of(blockIdx.x, one * shares);
+    if (at == NONE) return;   // also where no row takes part, so that `one` is 0
+    const uint32_t mine = at / one;
     uint32_t tm, tn;
     place_of(at % one, split.m_tiles, n_tiles, tm, tn);
     const uint32_t m0 = tm * TILE::M, n0 = tn * TILE::N, share = (steps + shares - 1) / shares;
