@@ -47,13 +47,15 @@ def gradients(h, weight, x, lse, kept, at, c):
     return g, torch.mm(g, w), torch.mm(g.t().contiguous(), h)
 
 
-def bounds(h, weight, x, lse, kept, at, c, g, dtype, from_lse, base=None):
+def bounds(h, weight, x, lse, kept, at, c, g, dtype, from_lse, base=None, exact=False):
     """Bounds on the errors of (loss, lse, grad_hidden, grad_weight), of the first two where g is None; grad_weight's without its
-    rounding to the output's type."""
+    rounding to the output's type.  exact: the logits' products and sums have no roundings in 32 bits."""
     w = weight.double().abs()
     n, dim = h.shape
     v = w.size(0)
     dx = (dim + 1) * 2 * U * torch.mm(h.abs(), w.t().contiguous())
+    if exact:
+        dx = torch.zeros_like(dx)
     top = x.amax(1, keepdim=True)
     most = dx.amax(1, keepdim=True)
     away = (top - x).clamp(max=104)

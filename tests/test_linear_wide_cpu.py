@@ -1,0 +1,33 @@
+"""The bounds of the GPU tests of wide hidden states, without a GPU: at every width that those tests use, the formula's results,
+rounded, lie inside them, and wrong ones outside."""
+import pytest
+import torch
+
+import linear_exact as exact
+import linear_plain as plain
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,v,d", [(20, 3000, 4096), (300, 1256, 4096), (90, 3000, 4095), (100, 700, 4097), (60, 300, 16384), (5, 70, 65536),
+                                   (33, 300, 65536), (33, 300, 65535)])
+@pytest.mark.parametrize("from_lse", [False, True])
+def test_bounds_reject_wrong_results(from_lse, n, v, d, dtype):
+    h, w, y, c = exact.inputs(n, v, d, dtype, "cpu", ignored=0.1 if n > 5 else 0.0)
+    ref = exact.reference(h, w, y, c, dtype, from_lse)
+    for key, (value, err) in ref.items():
+        plain.close(value.to(dtype if key in ("gh", "gw") else torch.float32), value, err, key)
+    exact.reject_wrong(h, w, y, c, ref)
+    x = torch.mm(h.double(), w.double().t())
+    step = float(w.abs().max())
+    assert bool((x / step == torch.round(x / step)).all()) and float(h.shape[1]) < 2 ** 24   # exact whatever the order
+    assert 1.0 < float(x.std()) < 6.0
+
+
+@pytest.mark.parametrize("d", [4096, 65536])
+def test_bounds_of_inexact_products_would_not(d):
+    """The bounds for any inputs grow with the width, so that they tell less and less: the reason for exact ones."""
+    h, w, y, c = exact.inputs(20, 70, d, torch.float32, "cpu")
+    loss, lse, hh, x, kept, at = plain.losses(h, w, y)
+    loose = plain.bounds(hh, w, x, lse, kept, at, c, None, torch.float32, False)[0]
+    tight = plain.bounds(hh, w, x, lse, kept, at, c, None, torch.float32, False, exact=True)[0]
+    assert bool((tight < 1e-4).all()) and bool((loose > tight).all())
