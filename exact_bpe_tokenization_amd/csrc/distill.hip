@@ -361,18 +361,23 @@ int check_distill(const void *logits, int type, uint32_t n_rows, uint32_t n_voca
     return TOKTIER_OK;
 }
 
-// Few long rows are split, as for the cross entropy.
+// Few long rows are split: the more CUs against a second launch, each row read twice and its list by every piece.  So fewer rows of 32
+// bits are than of 16, and more where a row is so long that one workgroup keeps little of it.  With gradient, 64 listed, split / whole in
+// us: 131,328 bfloat16 1 row 13.0 / 22.6, 96 rows 20.7 / 23.6, 128 25.4 / 24.8, 159 30.6 / 26.2; float32 64 rows 23.0 / 26.7, 96 33.6 / 30.8;
+// 524,288 float32 64 rows 76 / 99, 128 134 / 133; 2,097,152 bfloat16 159 rows 362 / 462, float32 711 / 932; 65,536 bfloat16 16 rows 13.0 / 14.6
+// (the loss alone 12.8 / 9.8, but its bits should not depend on whether a gradient is asked for).
 constexpr uint32_t MOST_SPLIT = 159;
-bool split_rows(uint32_t n_rows, uint32_t n_vocab) { return n_vocab >= 8 * PIECE && n_rows <= MOST_SPLIT; }
+uint32_t most_split(uint32_t n_vocab, uint32_t elem) { return std::min(MOST_SPLIT, 256 / elem * std::max(1u, n_vocab >> 18)); }
+bool split_rows(uint32_t n_rows, uint32_t n_vocab, uint32_t elem) { return n_vocab >= 8 * PIECE && n_rows <= most_split(n_vocab, elem); }
 
 struct Split {
     uint32_t pieces;   // 0: rows are not split
     uint64_t kept, total;
 };
-Split layout_of(uint32_t n_rows, uint32_t n_vocab, uint32_t k)
+Split layout_of(uint32_t n_rows, uint32_t n_vocab, uint32_t k, uint32_t elem)
 {
     Split L{0, 0, 256};
-    if (!split_rows(n_rows, n_vocab)) return L;
+    if (!split_rows(n_rows, n_vocab, elem)) return L;
     L.pieces = (n_vocab + PIECE - 1) / PIECE;
     L.kept = ((uint64_t)n_rows * L.pieces * sizeof(MaxSum) + 255) & ~255ull;
     L.total = L.kept + (((uint64_t)n_rows * k * 4 + 255) & ~255ull);
@@ -388,8 +393,8 @@ extern "C" int toktier_distill_workspace_bytes(uint32_t n_rows, uint32_t n_vocab
 {
     if (!out_bytes || n_vocab == 0 || n_vocab > TOKTIER_MAX_VOCAB || n_rows > 0x7FFFFFFFu || top_k == 0 || top_k > TOKTIER_MAX_TOP)
         return TOKTIER_E_INVALID_ARG;
-    // what any call of up to n_rows rows needs: the most of those whose rows are split
-    *out_bytes = layout_of(std::clamp(n_rows, 1u, MOST_SPLIT), n_vocab, top_k).total;
+    // what any call of up to n_rows rows needs: the most of those whose rows are split, which are 16-bit ones
+    *out_bytes = layout_of(std::clamp(n_rows, 1u, most_split(n_vocab, 2)), n_vocab, top_k, 2).total;
     return TOKTIER_OK;
 }
 
@@ -402,7 +407,7 @@ extern "C" int toktier_distill(const void *logits, int type, uint32_t n_rows, ui
     int rc = check_distill(logits, type, n_rows, n_vocab, stride, t, temperature, lse, grad_loss, grad_logits, grad_stride);
     if (rc || n_rows == 0) return rc;
     if (!loss || !aligned4(loss) || !workspace || ((uintptr_t)workspace & 255u)) return TOKTIER_E_INVALID_ARG;
-    const Split L = layout_of(n_rows, n_vocab, top_k);
+    const Split L = layout_of(n_rows, n_vocab, top_k, elem_size(type));
     if (workspace_bytes < L.total) return TOKTIER_E_CAPACITY;
     struct Area {
         const void *p;
