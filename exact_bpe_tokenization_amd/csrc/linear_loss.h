@@ -11,9 +11,13 @@
 // are copied together first, into rows that the products need not check for their ends.
 //
 // Bound by the matrix cores from some 300 rows on, by the table's bytes below.  bfloat16, 8,192 rows x 131,328 x 4,096: loss 5.95 ms
-// (1,480 TFLOP/s), with gradients 23.3 ms (half of the IDs' exponentials kept, 345 us to make them G, the others' product formed
-// twice); 1,638 rows x 33,024 x 2,048: 185 and 664 us; 16 rows x 131,328 x 4,096: 218 us (4.9 TB/s) and 797.  float32, 2,048 rows x
-// 33,024 x 1,024: 1.0 to 1.1 ms and 3.2 (130 TFLOP/s).
+// (1,480 TFLOP/s), with gradients 23.2 ms (half of the IDs' exponentials kept, 345 us to make them G, the others' product formed
+// twice); 1,638 rows x 33,024 x 2,048: 184 and 655 us (as 1,638 that take part of 4,096: 690 to 706); 16 rows x 131,328 x 4,096: 218 us
+// (4.9 TB/s) and 798.  float32, 2,048 rows x 33,024 x 1,024: 1.0 ms and 3.2 (130 TFLOP/s); 16 rows x 131,328 x 4,096: 468 us (4.6 TB/s) and
+// 3,119.
+//
+// G is an operand of the type, as the matrix cores take no 32-bit one beside 16 bits: rounded once from 32 bits (and see keep_high).
+// Gradients of 16 bits are so 2.2e-3 (bfloat16) and 3.0e-4 (float16) from 64 bits, where their own rounding alone is 1.7e-3 and 2.1e-4.
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -622,8 +626,9 @@ template <class T, class TILE, class OUT> __device__ __forceinline__ void weight
 #pragma unroll
             for (int e = 0; e < VEC; ++e) x[e] += was[e];
         }
-        // past the caches for 16 bits (16 rows into 131,328 x 4,096 bfloat16: 420 -> 335 us; float32 loses, 128 rows into
-        // 33,024 x 1,024: 92 -> 115 us)
+        // past the caches for 16 bits (into 131,328 x 4,096 bfloat16, 16 rows: 420 -> 335 us; a whole call of 128 rows 1,017 -> 916, 512 1,736 ->
+        // 1,646, 2,048 5,402 -> 5,352, 8,192 as before, into 33,024 x 2,048 1,638 rows 670 -> 661; where it is added to, as before;
+        // float32 loses, 128 rows into 33,024 x 1,024: 92 -> 115 us)
         if constexpr (sizeof(OUT) == 2) stream_part(to, a.dim - m, x);
         else store_part(to, a.dim - m, x);
     });
