@@ -88,7 +88,6 @@ __device__ __forceinline__ MaxSum read_list(const List &list, const Entries<THRE
         float v = NEG_INF, x = 0.f;
         if (id != NONE) {
             v = own.top[e];
-            if (v == -NEG_INF) v = __builtin_nanf("");   // with the teacher's own log-sum-exp too
             x = logit(i, id);
             uint32_t was = id + 1;
             for (uint32_t s = 0; s < list.slots && was != id && was != NONE; ++s)   // at most half of the slots are ever taken
@@ -130,7 +129,9 @@ template <int THREADS> __device__ __forceinline__ void block_join2(MaxSum &a, Ma
 template <int THREADS>
 __device__ __forceinline__ void weigh_list(const List &list, const Teacher &t, uint64_t row, MaxSum b, MaxSum a, float inv_t, float &mass, float &loss)
 {
-    const float log_b = log_of(b.s), log_a = log_of(a.s), own = t.lse ? t.lse[row] : 0.f;
+    const float log_b = log_of(b.s), log_a = log_of(a.s);
+    // a listed +inf is NaN with the teacher's own log-sum-exp too (asked where the list is read, it spills two registers)
+    const float own = !t.lse ? 0.f : b.m == -NEG_INF ? __builtin_nanf("") : t.lse[row];
     const bool none = empty(a);
     mass = loss = 0.f;
     for (uint32_t i = threadIdx.x; i < t.k; i += THREADS) {
@@ -289,8 +290,8 @@ __global__ __launch_bounds__(PIECE_THREADS) void k_distill_join(const T *logits,
 }
 
 // The gradient from lse.  From |lse| = FAR on a row's maximum and sum are formed again, by one workgroup, since in place the others
-// would read what it has written.  So it is above a temperature of 2^120, where lse temperature, the maximum that a sum of one would have, or
-// a logit's distance from it might leave the range; below it a distance that does has no power.
+// would read what it has written.  So they are above a temperature of 2^120, where lse * temperature (the maximum that a sum of one
+// would have) or a logit's distance from it might leave the range; below, a distance that does has no power.
 constexpr float HOT = 0x1p120f;
 // (Of float32 nine registers are spilled; with six wavefronts and none spilled 2,048 rows of 131,328 take 465 us in place of 419.)
 template <class T, int THREADS>

@@ -515,11 +515,12 @@ int toktier_linear_cross_entropy_backward(const void *hidden, int type, uint32_t
  *   c_i = grad_scale * (grad_loss ? grad_loss[i] : 1)
  * Without teacher_lse q is renormalised over the list (Q = 1) and the loss is the divergence of p from it; with the teacher's
  * own log-sum-exp at the same temperature q are its probabilities, and what is not listed has no part.  (The customary factor
- * temperature squared is the caller's: grad_scale.)  An lse beyond the range of 32 bits is -inf or +inf; loss and gradient do not
- * come from it.  Differences of logits beyond that range count as infinite.  An ID may be listed twice: its entries add up.  A list without an entry,
- * or whose logits are all -inf, gives loss 0 and a gradient of zeros.  Entries of q 0 have no part in the loss.  A row of
- * logits of -inf alone has lse -inf, loss +inf and a gradient of zeros; a listed logit of -inf with q > 0 makes the loss +inf;
- * a NaN or +inf among the logits makes lse, loss and gradient NaN, one among the list's logits loss and gradient.
+ * temperature squared is the caller's: grad_scale.)  An lse beyond the range of 32 bits is -inf or +inf, which loss and gradient do
+ * not show (but a teacher_lse that is not finite is used as it is); differences of logits beyond that range count as infinite.
+ * An ID may be listed twice: its entries add up.  A list without an entry, or whose logits are all -inf, gives loss 0 and a
+ * gradient of zeros.  Entries of q 0 have no part in the loss.  A row of logits of -inf alone has lse -inf, loss +inf and a
+ * gradient of zeros; a listed logit of -inf with q > 0 makes the loss +inf; a NaN or +inf among the logits makes lse, loss and
+ * gradient NaN, one among the list's logits loss and gradient.
  *   top_ids      device, n_rows rows of top_k uint32, top_ids_stride apart; 1 <= top_k <= TOKTIER_MAX_TOP.
  *   top_logits   device, n_rows rows of top_k float, top_logits_stride apart.
  *   teacher_lse  device, float[n_rows], or NULL.     temperature  > 0 and finite, as is log2(e) / temperature.

@@ -9,7 +9,7 @@ once for float32; a sum of n products in 32 bits, in any order, is off by at mos
         would do, but a lane adds up to 32 of them and wavefronts and tiles join in turn: (32 + 8 + tiles) steps, each of
         which may rescale (2 u a unit of the maximum's growth, which is no more than the logits' range)
   G     c (p - [j = y]), rounded to the type (half a step, and the type's smallest number over the scale for float16).  Where
-        exponentials are kept, e = exp(x - m') is rounded to the type before it is multiplied by c exp(m' - m) / s: half a
+        exponentials are kept, e = exp(x - m') is rounded to no fewer digits than the type's before it is multiplied by c exp(m' - m) / s: half a
         step of c p more (and float16's smallest number over 2^15), except at the target, which has its own logit
   dh    sum_j |dG| |w| and the sum's own error over the padded IDs; then one rounding to the type
   dW    the same over the rows, plus one addition and a rounding where it accumulates."""
